@@ -269,6 +269,135 @@ topktopp_status top_k_top_p_sorted_survivors(const void* logits, topktopp_dtype 
                                              const int32_t* k, const void* min_p, int64_t cap, float* probs,
                                              int32_t* indices, int32_t* counts, void* stream);
 
+/*
+ * Beam search. A step of a search over K beams for each of N prompts takes
+ * the model's logits of the N * K rows (row i * K + b is beam b of prompt i):
+ * beam_search_select picks the continuations, beam_reorder_states makes the
+ * model's states follow them, and beam_backtrace reads the sequences out of
+ * the steps' tokens and parents at the end. Nothing waits for the host, so a
+ * step can be captured in a graph. To search among filtered tokens only, pass
+ * logits that apply_top_k_top_p has filtered: -inf is no continuation, and
+ * probabilities are those of what is left.
+ */
+#define TOPKTOPP_MAX_BEAMS 128      /* beams per prompt */
+#define TOPKTOPP_MAX_CANDIDATES 256 /* continuations picked per prompt */
+
+/*
+ * beam_search_select — the n best continuations over beams and vocabulary.
+ *
+ *   logits     [N * K, V] device buffer of `dtype`; row r starts at element
+ *              r * ld_logits (V <= ld_logits <= TOPKTOPP_MAX_LD).
+ *   scores     [N, K] fp32: the beams' accumulated log-probabilities c.
+ *   finished   [N, K] bytes, nonzero where a beam is finished, or NULL.
+ *   end_token  the token of a finished beam's continuation, >= 0 (not read
+ *              when finished is NULL).
+ *   weights    [N, K] fp32 > 0, or NULL for 1: what the beam's scores are
+ *              multiplied with for the ranking, e.g. a length normalisation.
+ *   n          continuations per prompt, 1 <= n <= TOPKTOPP_MAX_CANDIDATES.
+ *   out_scores [N, n] fp32, out_parents [N, n] int32 (beam), out_tokens
+ *              [N, n] int32, in descending rank, written completely.
+ *   workspace  beam_search_select_workspace() bytes of device memory,
+ *              16-byte aligned. It holds nothing between calls; calls that
+ *              may run at the same time need one each.
+ *
+ * The continuation of beam b with token v has the score
+ *   s = c[b] + logits[b][v] - log(sum_u exp(logits[b][u]))
+ * and the rank value s * weights[b]. A finished beam has one continuation:
+ * itself, with end_token and the score c[b]; its logits are not read. Equal
+ * rank values are ordered by beam (lower first), then by logit (larger
+ * first), then by token (lower first). Tokens with a logit of -inf are no
+ * continuations. A beam has none at all if its score is infinite or NaN, its
+ * weight is not positive and finite, or its logits hold a NaN or +inf or
+ * nothing above -inf. Ranks without a continuation hold score -inf, parent
+ * -1 and token -1.
+ *
+ * Numerics. Sums and scores are formed in 64 bits (relative error of a sum
+ * below 1e-10) and rounded once, to out_scores; order follows the 64-bit
+ * values. Results are deterministic.
+ *
+ * Errors: ERR_NULLPTR for logits (unless V is 0), scores, an output or the
+ * workspace NULL; ERR_INVALID for a dtype, N < 0, K outside
+ * [1, TOPKTOPP_MAX_BEAMS], V outside [0, TOPKTOPP_MAX_V], N * K above
+ * TOPKTOPP_MAX_B, n out of range, a stride below V, end_token < 0, a
+ * workspace that is too small or not aligned, logits not aligned to their
+ * element, or an output or the workspace overlapping anything else. N == 0
+ * is a successful no-op.
+ */
+topktopp_status beam_search_select(const void* logits, int64_t ld_logits, topktopp_dtype dtype, int64_t N, int64_t K,
+                                   int64_t V, const float* scores, const uint8_t* finished, int32_t end_token,
+                                   const float* weights, int64_t n, float* out_scores, int32_t* out_parents,
+                                   int32_t* out_tokens, void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that beam_search_select needs for these sizes (at least
+ * 16), or -1 if it would refuse them. */
+int64_t beam_search_select_workspace(topktopp_dtype dtype, int64_t N, int64_t K, int64_t V, int64_t n);
+
+/*
+ * A state whose rows follow the beams, e.g. one layer's key cache: byte b of
+ * the element at row r, indices i0, i1, i2 and position t lies at
+ *   data + r * row_stride + i0 * stride[0] + i1 * stride[1] + i2 * stride[2]
+ *        + t * position_stride + b,   0 <= b < run.
+ * All strides and the run (an element, or several that lie side by side) are
+ * in bytes; sizes are counts, 1 for an axis that is not there.
+ */
+typedef struct {
+  void* data;
+  int64_t row_stride;
+  int64_t size[3];
+  int64_t stride[3];
+  int64_t positions;
+  int64_t position_stride;
+  int64_t run;
+} topktopp_beam_state;
+
+/*
+ * beam_reorder_states — in every state, row i * K + b becomes what row
+ * i * K + parents[i][b] was before the call.
+ *
+ *   states   host array of `count` descriptions (0 <= count), read during the
+ *            call. Rows of a state: N * K. A state that shares memory with an
+ *            earlier one is moved after it.
+ *   parents  [N, K] int32 device buffer; a row whose parent lies outside
+ *            [0, K) (e.g. the -1 of a rank without a continuation) stays as
+ *            it is.
+ *   lengths  [N] int32 device buffer, or NULL: positions t < lengths[i] of
+ *            prompt i are moved, those behind are neither read nor written
+ *            (reads of a moved row may reach up to 15 bytes further).
+ *   N, K     1 <= K <= TOPKTOPP_MAX_BEAMS, N * K <= TOPKTOPP_MAX_B.
+ * ERR_NULLPTR for states, a state's data or parents NULL; ERR_INVALID for
+ * sizes out of range, negative sizes, elements of one state that share memory
+ * (a sufficient condition: in ascending order, each axis's stride reaches
+ * past all that the axes below it span), a state of more than 2^31 - 1
+ * columns per row (columns have 16 bytes where alignment allows), or parents
+ * or lengths inside a state. States with a size of 0 are skipped; nothing is
+ * moved if any argument is refused.
+ */
+topktopp_status beam_reorder_states(const topktopp_beam_state* states, int64_t count, const int32_t* parents,
+                                    int64_t N, int64_t K, const int32_t* lengths, void* stream);
+
+/*
+ * beam_backtrace — sequences out of a search's history.
+ *
+ *   tokens, parents  [T, N, K] int32: what was picked in each step; parents
+ *            of step t are beams of step t - 1 (those of step 0 are not used).
+ *   M        hypotheses per prompt, >= 0.
+ *   beams    [N, M] int32, the beam at which hypothesis m ends, or NULL for
+ *            beam m (then M <= K).
+ *   lengths  [N, M] int32, its number of steps, or NULL for T (values are
+ *            clamped to [0, T]).
+ *   out      [N, M, T] int32, written completely: out[i][m][t] is the token
+ *            of step t for t < lengths[i][m], and `pad` behind. Steps before a
+ *            beam or parent outside [0, K) hold `pad`, as that step does for
+ *            a beam outside.
+ * ERR_NULLPTR for tokens, parents or out NULL; ERR_INVALID for negative
+ * sizes, K outside [1, TOPKTOPP_MAX_BEAMS], N * K or T above 2^31 - 1, M above
+ * 2^20, M > K without beams, or out overlapping an input. N, T or M of 0 is a
+ * successful no-op.
+ */
+topktopp_status beam_backtrace(const int32_t* tokens, const int32_t* parents, int64_t T, int64_t N, int64_t K,
+                               const int32_t* beams, const int32_t* lengths, int64_t M, int32_t pad, int32_t* out,
+                               void* stream);
+
 /* Text of the most recent error on the calling thread ("" if none); the
  * counterpart of aclGetRecentErrMsg (AKP §8). Valid until the next call on
  * the same thread. */

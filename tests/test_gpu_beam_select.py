@@ -1,0 +1,229 @@
+"""beam_search_select against the plain implementation in 64 bits (needs an
+MI355X). Parents and tokens must be equal. Scores: the kernel's 64-bit value is
+within 1e-9 of the exact one (a sum's relative error is below 1e-10, and sums
+and logarithms round at 2^-53), and it is rounded once to fp32, by at most
+2^-24 of the value."""
+
+import numpy as np
+import pytest
+
+from tests import beam_ref
+from tests.gpu_util import need_gpu, say
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = {"f32": "float32", "f16": "float16", "bf16": "bfloat16"}
+
+
+def make(torch, rows, V, dtype, seed, ld=None, offset=0, scale=3.0):
+    """Logits [rows, V] as a view with row stride ld that starts `offset`
+    elements into its buffer; the buffer's other elements are NaN."""
+    ld = V if ld is None else ld
+    rng = np.random.default_rng(seed)
+    x = torch.from_numpy((rng.standard_normal((rows, V)) * scale).astype(np.float32)).to(getattr(torch, DTYPES[dtype]))
+    buf = torch.full((offset + rows * ld + 16,), float("nan"), dtype=x.dtype, device="cuda")
+    view = buf[offset:offset + rows * ld].view(rows, ld)[:, :V] if rows * ld else buf[:0].view(rows, V)
+    view.copy_(x)
+    return view
+
+
+def check(torch, logits, scores, n, finished=None, end=0, weights=None, **kw):
+    import top_logits_filtering_amd as tk
+
+    dev = lambda a, t: None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda().to(t)  # noqa: E731
+    got = tk.beam_search_select(logits, dev(scores, torch.float32), n, finished=dev(finished, torch.bool),
+                                end_token=end, weights=dev(weights, torch.float32), **kw)
+    torch.cuda.synchronize()
+    ref = beam_ref.select(logits.double().cpu().numpy(), scores, n, finished, end, weights)
+    s, p, t = (v.cpu().numpy() for v in got)
+    assert np.array_equal(p, ref[1]), (p, ref[1])
+    assert np.array_equal(t, ref[2]), (t, ref[2])
+    gone = np.isneginf(ref[0])
+    assert np.array_equal(np.isneginf(s[gone]), np.ones(gone.sum(), bool))
+    with np.errstate(over="ignore"):
+        want = ref[0].astype(np.float32)
+    inf = np.isinf(want) & ~gone  # rounds to -inf in fp32
+    assert np.array_equal(s[inf], want[inf])
+    fine = ~gone & ~inf
+    err = np.abs(s[fine].astype(np.float64) - ref[0][fine])
+    assert np.all(err <= 2.0 ** -24 * np.abs(ref[0][fine]) + 1e-9), err.max()
+    return got
+
+
+def beam_scores(N, K, seed):
+    rng = np.random.default_rng(seed + 1000)
+    return -(5 + np.cumsum(rng.exponential(0.7, (N, K)), 1)).astype(np.float32)
+
+
+SHAPES = [
+    # N, K, V, n, ld - V, offset
+    (1, 1, 1, 1, 0, 0),
+    (2, 3, 1, 4, 0, 1),
+    (2, 3, 5, 4, 0, 0),
+    (3, 2, 7, 20, 1, 3),  # fewer continuations than ranks
+    (1, 4, 1000, 8, 0, 0),
+    (4, 4, 2048, 8, 0, 0),
+    (2, 5, 2049, 3, 6, 1),
+    (3, 7, 4099, 13, 0, 5),  # rows at every alignment
+    (1, 2, 40001, 16, 3, 2),
+    (130, 1, 517, 2, 0, 0),
+    (2, 128, 300, 256, 0, 0),  # the widest beams
+    (1, 3, 151936, 6, 0, 0),
+    (90, 4, 33000, 8, 0, 0),  # enough rows for whole-register chunks
+    (1, 1, 1 << 20, 5, 0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("shape", SHAPES, ids=[str(s) for s in SHAPES])
+def test_shapes(shape, dtype):
+    torch = need_gpu()
+    N, K, V, n, more, offset = shape
+    x = make(torch, N * K, V, dtype, seed=V + n, ld=V + more, offset=offset)
+    check(torch, x, beam_scores(N, K, V), n)
+    say(f"select {shape} {dtype}")
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_finished_weights_and_dead_beams(dtype):
+    torch = need_gpu()
+    N, K, V, n = 6, 5, 3001, 12
+    rng = np.random.default_rng(5)
+    x = make(torch, N * K, V, dtype, seed=9)
+    scores = beam_scores(N, K, 3)
+    finished = rng.random((N, K)) < 0.4
+    finished[0] = True  # nothing but finished beams
+    finished[1] = False
+    weights = (0.2 + rng.random((N, K))).astype(np.float32)
+    x[finished.reshape(-1).nonzero()[0]] = float("nan")  # not read
+    check(torch, x, scores, n, finished, end=2, weights=weights)
+    scores[2, 1:] = -np.inf  # a search's first step: one live beam
+    scores[3] = -np.inf
+    scores[4, 0], scores[4, 3] = np.nan, np.inf
+    weights[5] = [0.0, -1.0, np.inf, np.nan, 1.0]
+    check(torch, x, scores, n, finished, end=2, weights=weights)
+    check(torch, x, scores, n, finished, end=V + 7)  # the end token may lie outside the vocabulary
+    scores[2, 1:] = -1e9
+    scores[3] = np.finfo(np.float32).min
+    scores[3, 2] = -1.0
+    check(torch, x, scores, n)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("V", [50, 3001, 40000])
+def test_masked_logits(V, dtype):
+    """Rows that a mask leaves nothing, one token or a few of; masks of -inf
+    and of the type's lowest value; NaN and infinities."""
+    torch = need_gpu()
+    N, K, n = 3, 4, 9
+    low = torch.finfo(getattr(torch, DTYPES[dtype])).min
+    for fill in (float("-inf"), low):
+        x = make(torch, N * K, V, dtype, seed=V)
+        rng = np.random.default_rng(V)
+        for r, left in enumerate([0, 1, 3, 8, 9, 10, V]):
+            gone = torch.from_numpy(rng.permutation(V)[left:]).cuda()
+            x[r, gone] = fill
+        x[7] = 0.0
+        x[8, V // 2] = float("nan")
+        x[9, V - 1] = float("inf")
+        x[10, 0] = -float("nan")
+        check(torch, x, beam_scores(N, K, 1), n)
+    x = make(torch, N * K, V, dtype, seed=V, scale=0.01)
+    x[0] = float("-inf")
+    x[0, V - 1] = low
+    x[1] = torch.finfo(x.dtype).max
+    x[2, 3] = torch.finfo(x.dtype).max
+    x[3] = low
+    x[4] -= 20000.0
+    x[5] += 20000.0
+    x[6, : V // 2] = float("-inf")
+    x[6, V // 2:] = low
+    x[7] = x[7].abs() * 0 - 0.0
+    x[7, ::2] = 0.0  # -0 and +0 are equal
+    check(torch, x, beam_scores(N, K, 1), n)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_ties(dtype):
+    """Equal logits, equal beams, and values in orders that defeat a bound from
+    the threads' maxima."""
+    torch = need_gpu()
+    for N, K, V, n in [(2, 4, 20000, 16), (1, 1, 9000, 256), (1, 128, 600, 256), (300, 1, 40000, 33)]:
+        rows = N * K
+        scores = beam_scores(N, K, 2)
+        x = make(torch, rows, V, dtype, seed=1)
+        x[:] = 1.5  # every continuation of a beam ties
+        check(torch, x, scores, n)
+        scores[:] = -3.0  # and the beams with each other
+        check(torch, x, scores, n)
+        x[:] = make(torch, 1, V, dtype, seed=4, scale=0.02)  # equal beams
+        check(torch, x, scores, n)
+        ramp = torch.linspace(-5, 5, V).to(x.dtype).cuda()
+        x[:] = ramp
+        check(torch, x, scores, n)
+        x[:] = ramp.flip(0)
+        check(torch, x, scores, n)
+        # all large values in the elements of one thread, many of them equal
+        P = 16 // x.element_size()
+        at = torch.arange(V, device="cuda")
+        mine = (at // P) % 256 == 77
+        x[:] = torch.where(mine, 9.0 - (at % 13).float(), -4.0).to(x.dtype)
+        check(torch, x, scores, n)
+        say(f"ties {N, K, V, n} {dtype}")
+
+
+def test_outputs_stay_inside():
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    N, K, V, n = 3, 4, 1111, 7
+    x = make(torch, N * K, V, "bf16", seed=2)
+    big = [torch.full((N * n + 64,), 77, dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32)]
+    out = tuple(b[32:32 + N * n].view(N, n) for b in big)
+    size = tk.beam_search_select_workspace(torch.bfloat16, N, K, V, n)
+    ws = torch.full((size + 64,), 77, dtype=torch.uint8, device="cuda")
+    got = check(torch, x, beam_scores(N, K, 0), n, out=out, workspace=ws[32:32 + size])
+    assert got[0].data_ptr() == out[0].data_ptr()
+    for b in big + [ws]:
+        edge = torch.cat([b[:32], b[-32:]])
+        assert bool((edge == 77).all())
+
+
+def test_streams_and_graphs():
+    """Concurrent calls on several streams; a captured call replayed between
+    other work and on new inputs, beside a second graph."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    N, K, V, n = 4, 4, 50000, 8
+    xs = [make(torch, N * K, V, "bf16", seed=i) for i in range(4)]
+    sc = [torch.from_numpy(beam_scores(N, K, i)).cuda() for i in range(4)]
+    want = [[t.clone() for t in tk.beam_search_select(x, s, n)] for x, s in zip(xs, sc)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[] for _ in xs]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            got[i].append(tk.beam_search_select(xs[i], sc[i], n, stream=st if i % 2 else st.cuda_stream))
+    torch.cuda.synchronize()
+    for i in range(4):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+    graphs, outs = [], []
+    x, s = xs[0].clone(), sc[0].clone()
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(tk.beam_search_select(x, s, n))
+        graphs.append(g)
+    for i in (0, 1, 2, 1):
+        x.copy_(xs[i])
+        s.copy_(sc[i])
+        torch.cuda.synchronize()
+        for g, o in zip(graphs, outs):
+            g.replay()
+            tk.beam_search_select(xs[3], sc[3], n)
+        torch.cuda.synchronize()
+        for o in outs:
+            assert all(torch.equal(a, b) for a, b in zip(o, want[i]))

@@ -6,6 +6,10 @@ from .binding import (  # noqa: F401
     TopKTopPError,
     apply_top_k_top_p,
     apply_top_k_top_p_with_sorted,
+    beam_backtrace,
+    beam_reorder_states,
+    beam_search_select,
+    beam_search_select_workspace,
     last_error,
     load_library,
     sample_top_k_top_p,

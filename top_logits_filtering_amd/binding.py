@@ -8,7 +8,9 @@ falling back to anything else.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -25,6 +27,10 @@ EXPORTED_SYMBOLS = (
     "apply_top_k_top_p_strided",
     "apply_top_k_top_p_with_sorted",
     "apply_top_k_top_p_with_sorted_ex",
+    "beam_backtrace",
+    "beam_reorder_states",
+    "beam_search_select",
+    "beam_search_select_workspace",
     "sample_top_k_top_p",
     "top_k_top_p_sorted_survivors",
     "topktopp_last_error",
@@ -32,6 +38,23 @@ EXPORTED_SYMBOLS = (
 )
 
 _lib = None
+
+
+TOPKTOPP_MAX_BEAMS, TOPKTOPP_MAX_CANDIDATES = 128, 256
+
+
+class BeamState(ctypes.Structure):
+    """topktopp_beam_state: a state's memory, strides and run in bytes."""
+
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("row_stride", ctypes.c_int64),
+        ("size", ctypes.c_int64 * 3),
+        ("stride", ctypes.c_int64 * 3),
+        ("positions", ctypes.c_int64),
+        ("position_stride", ctypes.c_int64),
+        ("run", ctypes.c_int64),
+    ]
 
 
 class TopKTopPError(RuntimeError):
@@ -72,6 +95,15 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.sample_top_k_top_p.restype = i32
     lib.top_k_top_p_sorted_survivors.argtypes = [vp, i32, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp]
     lib.top_k_top_p_sorted_survivors.restype = i32
+    lib.beam_search_select.argtypes = [vp, i64, i32, i64, i64, i64, vp, vp, ctypes.c_int32, vp, i64, vp, vp, vp, vp,
+                                       i64, vp]
+    lib.beam_search_select.restype = i32
+    lib.beam_search_select_workspace.argtypes = [i32, i64, i64, i64, i64]
+    lib.beam_search_select_workspace.restype = i64
+    lib.beam_reorder_states.argtypes = [vp, i64, vp, i64, i64, vp, vp]
+    lib.beam_reorder_states.restype = i32
+    lib.beam_backtrace.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, ctypes.c_int32, vp, vp]
+    lib.beam_backtrace.restype = i32
     lib.topktopp_last_error.argtypes = []
     lib.topktopp_last_error.restype = ctypes.c_char_p
     lib.topktopp_set_plan_policy.argtypes = [i32]
@@ -345,3 +377,221 @@ def top_k_top_p_sorted_survivors(logits, p=None, k=None, min_p=None, cap=1024, w
     )
     _check(status)
     return probs, indices, counts
+
+
+_NULL_SCOPE = contextlib.nullcontext()
+
+
+def _scope(stream, device):
+    """(stream handle, context): the given stream, or torch's current one of
+    the tensors' device, and the context in which buffers for it are allocated
+    and kernels launched (that stream current, and its device)."""
+    import torch
+
+    if device.type != "cuda":
+        raise ValueError("tensors must live on the GPU")
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+        if torch.cuda.current_device() == device.index:
+            return handle, _NULL_SCOPE
+        return handle, torch.cuda.device(device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if stream.device != device:
+        raise ValueError(f"the stream's device {stream.device} is not the tensors' device {device}")
+    return int(stream.cuda_stream), torch.cuda.stream(stream)
+
+
+def _check_dense(t, shape, dtype, name):
+    """None, or a contiguous tensor of `shape` and `dtype`."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got shape {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def beam_search_select_workspace(dtype, N, K, V, n=None):
+    """Bytes of the workspace that beam_search_select takes for logits
+    [N * K, V] of torch dtype `dtype` and n continuations (default K)."""
+    import torch
+
+    size = load_library().beam_search_select_workspace(
+        _dtype_code(torch.empty(0, dtype=dtype)), int(N), int(K), int(V), int(K if n is None else n))
+    if size < 0:
+        raise TopKTopPError(2, last_error())
+    return size
+
+
+def beam_search_select(logits, scores, n=None, finished=None, end_token=None, weights=None, out=None, workspace=None,
+                       stream=None):
+    """The n best continuations (default K) of each prompt over its K beams and
+    the vocabulary: (scores [N, n] float32, parents [N, n] int32, tokens [N, n]
+    int32), best first.
+
+    logits [N * K, V], rows contiguous, any row stride; scores [N, K] float32,
+    the beams' accumulated log-probabilities. A continuation of beam b with
+    token v scores scores[b] + log_softmax(logits[b])[v]. finished [N, K]
+    bool: such a beam goes on as itself only, with end_token and its score.
+    weights [N, K] float32 > 0 multiply the scores for the ranking (length
+    normalisation), not in what is returned. Beams whose score is -inf and
+    tokens whose logit is -inf are left out; ranks without a continuation hold
+    score -inf, parent -1, token -1. out: the three tensors to fill; workspace:
+    a uint8 tensor of beam_search_select_workspace() bytes, not used by any
+    other call that may run at the same time (each call allocates one else)."""
+    import torch
+
+    lib = load_library()
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [N * K, V]")
+    if scores.dim() != 2:
+        raise ValueError("scores must be 2-D [N, K]")
+    (R, V), (N, K) = logits.shape, scores.shape
+    if N * K != R:
+        raise ValueError(f"logits must have N * K = {N * K} rows, got {R}")
+    n = K if n is None else int(n)
+    dtype = _dtype_code(logits)
+    _check_dense(scores, (N, K), torch.float32, "scores")
+    if finished is not None:
+        _check_dense(finished, (N, K), torch.uint8 if finished.dtype == torch.uint8 else torch.bool, "finished")
+        if end_token is None:
+            raise ValueError("finished needs end_token")
+    _check_dense(weights, (N, K), torch.float32, "weights")
+    dev = logits.device
+    _check_device(dev, logits, scores, finished, weights)
+    xp, ldx = _rows(logits)
+    handle, scope = _scope(stream, dev)
+    with scope:
+        if out is None:
+            out = (torch.empty((N, n), dtype=torch.float32, device=dev),
+                   torch.empty((N, n), dtype=torch.int32, device=dev),
+                   torch.empty((N, n), dtype=torch.int32, device=dev))
+        o_scores, o_parents, o_tokens = out
+        _check_dense(o_scores, (N, n), torch.float32, "out scores")
+        _check_dense(o_parents, (N, n), torch.int32, "out parents")
+        _check_dense(o_tokens, (N, n), torch.int32, "out tokens")
+        if workspace is None:
+            size = lib.beam_search_select_workspace(dtype, N, K, V, n)
+            if size < 0:
+                raise TopKTopPError(2, last_error())
+            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous uint8 tensor")
+        _check_device(dev, o_scores, o_parents, o_tokens, workspace)
+        _check(lib.beam_search_select(
+            xp, ldx, dtype, N, K, V, scores.data_ptr(), None if finished is None else finished.data_ptr(),
+            0 if end_token is None else int(end_token), None if weights is None else weights.data_ptr(), n,
+            o_scores.data_ptr(), o_parents.data_ptr(), o_tokens.data_ptr(), workspace.data_ptr(), workspace.numel(),
+            handle))
+    return out
+
+
+@functools.lru_cache(maxsize=256)
+def _state_layout(shape, strides, itemsize, batch_dim, seq_dim):
+    """A tensor's axes as a BeamState has them: (row_stride, sizes, strides,
+    positions, position_stride, run), strides and run in bytes. Axes that lie
+    side by side are joined. seq_dim None: no axis is the positions."""
+    axes = sorted((strides[d] * itemsize, shape[d]) for d in range(len(shape))
+                  if d not in (batch_dim, seq_dim) and shape[d] != 1)
+    run = itemsize
+    while axes and axes[0][0] == run:
+        run *= axes.pop(0)[1]
+    joined = []
+    for stride, size in axes:
+        if joined and stride == joined[-1][0] * joined[-1][1]:
+            joined[-1] = (joined[-1][0], joined[-1][1] * size)
+        else:
+            joined.append((stride, size))
+    if len(joined) > 3:
+        raise ValueError(f"a state of shape {shape} and strides {strides} has more than three separate axes")
+    joined = [(run, 1)] * (3 - len(joined)) + joined
+    joined.reverse()  # the last of the three is the one with the smallest stride
+    positions, position_stride = (1, run) if seq_dim is None else (shape[seq_dim], strides[seq_dim] * itemsize)
+    return (strides[batch_dim] * itemsize, tuple(s for _, s in joined), tuple(s for s, _ in joined), positions,
+            position_stride, run)
+
+
+def beam_reorder_states(states, parents, batch_dim=0, seq_dim=None, lengths=None, stream=None):
+    """Every state's rows follow their beams, in place: along batch_dim (of
+    size N * K) row i * K + b becomes what row i * K + parents[i, b] was.
+
+    states: a tensor or a sequence of them (the caches of all layers, any
+    dtype and strides), all with the rows along batch_dim. parents [N, K]
+    int32; a row whose parent lies outside [0, K) stays as it is. lengths [N]
+    int32 (needs seq_dim): only positions below lengths[i] along seq_dim are
+    moved. Returns states."""
+    import torch
+
+    lib = load_library()
+    tensors = [states] if isinstance(states, torch.Tensor) else list(states)
+    if parents.dim() != 2:
+        raise ValueError("parents must be 2-D [N, K]")
+    N, K = parents.shape
+    _check_dense(parents, (N, K), torch.int32, "parents")
+    _check_dense(lengths, (N,), torch.int32, "lengths")
+    if lengths is not None and seq_dim is None:
+        raise ValueError("lengths needs seq_dim")
+    dev = parents.device
+    _check_device(dev, parents, lengths, *tensors)
+    descs = (BeamState * len(tensors))()
+    for d, t in zip(descs, tensors):
+        dims = t.dim()
+        if not -dims <= batch_dim < dims:
+            raise ValueError(f"a state of {dims} axes has no batch_dim {batch_dim}")
+        if t.shape[batch_dim] != N * K:
+            raise ValueError(f"a state must have N * K = {N * K} rows, got shape {tuple(t.shape)}")
+        seq = None
+        if lengths is not None:
+            if not -dims <= seq_dim < dims or (seq_dim - batch_dim) % dims == 0:
+                raise ValueError(f"a state of {dims} axes has no seq_dim {seq_dim} beside batch_dim {batch_dim}")
+            seq = seq_dim % dims
+        if t.is_complex() and t.is_conj() or t.is_neg():
+            raise ValueError("a state must not be a lazily conjugated or negated view")
+        if t.numel() == 0:
+            continue  # an all-zero description: nothing to move
+        d.data = t.data_ptr()
+        d.row_stride, d.size[:], d.stride[:], d.positions, d.position_stride, d.run = _state_layout(
+            tuple(t.shape), t.stride(), t.element_size(), batch_dim % dims, seq)
+    handle, scope = _scope(stream, dev)
+    with scope:
+        _check(lib.beam_reorder_states(descs, len(tensors), parents.data_ptr(), N, K,
+                                       None if lengths is None else lengths.data_ptr(), handle))
+    return states
+
+
+def beam_backtrace(tokens, parents, beams=None, lengths=None, pad=-1, out=None, stream=None):
+    """The sequences of a search's history: tokens and parents [T, N, K] int32
+    are what was picked in each step. Hypothesis m of prompt i ends after
+    lengths[i, m] steps at beam beams[i, m] (int32 [N, M]; default: every beam,
+    after all T steps). Returns int32 [N, M, T]: each step's token, `pad`
+    behind the end and before a parent outside [0, K)."""
+    import torch
+
+    lib = load_library()
+    if tokens.dim() != 3:
+        raise ValueError("tokens must be 3-D [T, N, K]")
+    T, N, K = tokens.shape
+    ends = beams if beams is not None else lengths
+    if ends is not None and ends.dim() != 2:
+        raise ValueError("beams and lengths must be 2-D [N, M]")
+    M = K if ends is None else ends.shape[1]
+    _check_dense(tokens, (T, N, K), torch.int32, "tokens")
+    _check_dense(parents, (T, N, K), torch.int32, "parents")
+    _check_dense(beams, (N, M), torch.int32, "beams")
+    _check_dense(lengths, (N, M), torch.int32, "lengths")
+    dev = tokens.device
+    _check_device(dev, tokens, parents, beams, lengths)
+    handle, scope = _scope(stream, dev)
+    with scope:
+        if out is None:
+            out = torch.empty((N, M, T), dtype=torch.int32, device=dev)
+        _check_dense(out, (N, M, T), torch.int32, "out")
+        _check_device(dev, out)
+        _check(lib.beam_backtrace(tokens.data_ptr(), parents.data_ptr(), T, N, K,
+                                  None if beams is None else beams.data_ptr(),
+                                  None if lengths is None else lengths.data_ptr(), M, int(pad), out.data_ptr(),
+                                  handle))
+    return out

@@ -11,6 +11,7 @@
 #include <string>
 
 #include "../../include/topktopp.h"
+#include "beam.h"
 #include "launch.h"
 
 namespace {
@@ -370,6 +371,219 @@ topktopp_status apply_top_k_top_p_with_sorted_ex(const void* sorted_value, int64
                                                  int64_t ld_out, void* stream) {
   return with_sorted_impl(sorted_value, ld_sorted_value, sorted_indices, ld_sorted_indices, dtype, B, V, p, k, min_p,
                           true, logits, ld_logits, out, ld_out, stream);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------ beam search ---
+
+namespace {
+
+topktopp_status check_beams(int64_t N, int64_t K) {
+  if (N < 0) return fail(TOPKTOPP_ERR_INVALID, "N=%lld is negative", (long long)N);
+  if (K < 1 || K > TOPKTOPP_MAX_BEAMS)
+    return fail(TOPKTOPP_ERR_INVALID, "K=%lld beams are outside [1, %d]", (long long)K, TOPKTOPP_MAX_BEAMS);
+  if (N > TOPKTOPP_MAX_B / K)
+    return fail(TOPKTOPP_ERR_INVALID, "N * K (%lld * %lld) exceeds the supported maximum 2^31-1", (long long)N,
+                (long long)K);
+  return TOPKTOPP_OK;
+}
+
+topktopp_status check_select(int dtype, int64_t N, int64_t K, int64_t V, int64_t n) {
+  if (!valid_dtype(dtype)) return fail(TOPKTOPP_ERR_INVALID, "dtype %d is not one of F32, F16, BF16", dtype);
+  if (topktopp_status s = check_beams(N, K)) return s;
+  if (topktopp_status s = check_shape(N * K, V)) return s;
+  if (n < 1 || n > TOPKTOPP_MAX_CANDIDATES)
+    return fail(TOPKTOPP_ERR_INVALID, "n=%lld is outside [1, %d]", (long long)n, TOPKTOPP_MAX_CANDIDATES);
+  return TOPKTOPP_OK;
+}
+
+int64_t select_workspace(int dtype, int64_t N, int64_t K, int64_t V, int64_t n) {
+  const int64_t bytes = tkp::beam_select_workspace(dtype, N, static_cast<int>(K), static_cast<int>(V), static_cast<int>(n));
+  return bytes > 16 ? bytes : 16;
+}
+
+struct Span {
+  const void* p;
+  size_t bytes;
+  const char* name;
+};
+
+// The first `outs` spans may overlap no other one.
+topktopp_status check_disjoint(const Span* spans, int count, int outs) {
+  for (int i = 0; i < outs; ++i)
+    for (int j = i + 1; j < count; ++j)
+      if (overlaps(spans[i].p, spans[i].bytes, spans[j].p, spans[j].bytes))
+        return fail(TOPKTOPP_ERR_INVALID, "%s and %s overlap", spans[i].name, spans[j].name);
+  return TOPKTOPP_OK;
+}
+
+// Bytes that a state spans from data on, or an error; 0 for a state without elements.
+topktopp_status state_span(const tkp::BeamState& s, int64_t rows, size_t* bytes) {
+  *bytes = 0;
+  const int64_t size[5] = {rows, s.size[0], s.size[1], s.size[2], s.positions};
+  const int64_t stride[5] = {s.row_stride, s.stride[0], s.stride[1], s.stride[2], s.position_stride};
+  if (s.run < 0) return fail(TOPKTOPP_ERR_INVALID, "a state's run (%lld) is negative", (long long)s.run);
+  bool empty = s.run == 0;
+  for (int i = 0; i < 5; ++i) {
+    if (size[i] < 0) return fail(TOPKTOPP_ERR_INVALID, "a state's size (%lld) is negative", (long long)size[i]);
+    if (size[i] == 0) empty = true;
+  }
+  if (empty) return TOPKTOPP_OK;
+  int order[5] = {0, 1, 2, 3, 4};
+  for (int i = 1; i < 5; ++i)
+    for (int j = i; j > 0 && stride[order[j]] < stride[order[j - 1]]; --j) {
+      const int t = order[j];
+      order[j] = order[j - 1];
+      order[j - 1] = t;
+    }
+  constexpr int64_t kMost = int64_t{1} << 46;
+  int64_t end = s.run;
+  for (int i : order) {
+    if (size[i] == 1) continue;
+    if (stride[i] < end) return fail(TOPKTOPP_ERR_INVALID, "elements of a state share memory (stride %lld below %lld)",
+                                     (long long)stride[i], (long long)end);
+    if (stride[i] > kMost || size[i] > kMost / stride[i])
+      return fail(TOPKTOPP_ERR_INVALID, "a state spans more than 2^46 bytes");
+    end += stride[i] * (size[i] - 1);
+  }
+  *bytes = static_cast<size_t>(end);
+  return TOPKTOPP_OK;
+}
+
+tkp::BeamState state_of(const topktopp_beam_state& s) {
+  return tkp::BeamState{static_cast<char*>(s.data), s.row_stride, {s.size[0], s.size[1], s.size[2]},
+                        {s.stride[0], s.stride[1], s.stride[2]}, s.positions, s.position_stride, s.run};
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t beam_search_select_workspace(topktopp_dtype dtype, int64_t N, int64_t K, int64_t V, int64_t n) {
+  g_last_error.clear();
+  if (check_select(dtype, N, K, V, n) != TOPKTOPP_OK) return -1;
+  return select_workspace(dtype, N, K, V, n);
+}
+
+topktopp_status beam_search_select(const void* logits, int64_t ld_logits, topktopp_dtype dtype, int64_t N, int64_t K,
+                                   int64_t V, const float* scores, const uint8_t* finished, int32_t end_token,
+                                   const float* weights, int64_t n, float* out_scores, int32_t* out_parents,
+                                   int32_t* out_tokens, void* workspace, int64_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (N != 0) {
+    if (logits == nullptr && V != 0) return fail(TOPKTOPP_ERR_NULLPTR, "logits is NULL");
+    if (scores == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "scores is NULL");
+    if (out_scores == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "out_scores is NULL");
+    if (out_parents == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "out_parents is NULL");
+    if (out_tokens == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "out_tokens is NULL");
+    if (workspace == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "workspace is NULL");
+  }
+  if (topktopp_status s = check_select(dtype, N, K, V, n)) return s;
+  if (N == 0) return TOPKTOPP_OK;
+  if (topktopp_status s = check_ld(ld_logits, V, "logits")) return s;
+  if (finished != nullptr && end_token < 0)
+    return fail(TOPKTOPP_ERR_INVALID, "end_token=%d is negative", (int)end_token);
+  const size_t es = elem_size(dtype);
+  if (reinterpret_cast<uintptr_t>(logits) % es != 0)
+    return fail(TOPKTOPP_ERR_INVALID, "logits is not aligned to its elements");
+  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
+    return fail(TOPKTOPP_ERR_INVALID, "workspace is not 16-byte aligned");
+  const int64_t need = select_workspace(dtype, N, K, V, n);
+  if (workspace_bytes < need)
+    return fail(TOPKTOPP_ERR_INVALID, "workspace has %lld bytes, %lld are needed", (long long)workspace_bytes,
+                (long long)need);
+  const size_t beams = static_cast<size_t>(N * K), nout = static_cast<size_t>(N * n) * 4;
+  const Span spans[] = {{out_scores, nout, "out_scores"},
+                        {out_parents, nout, "out_parents"},
+                        {out_tokens, nout, "out_tokens"},
+                        {workspace, static_cast<size_t>(need), "workspace"},
+                        {logits, V == 0 ? 0 : extent(N * K, V, ld_logits, es), "logits"},
+                        {scores, beams * 4, "scores"},
+                        {finished, beams, "finished"},
+                        {weights, beams * 4, "weights"}};
+  if (topktopp_status s = check_disjoint(spans, 8, 4)) return s;
+  const tkp::BeamSelectArgs a{logits,     ld_logits,  N,         static_cast<int>(K), static_cast<int>(V),
+                              static_cast<int>(n),    scores,    finished,            end_token,
+                              weights,    out_scores, out_parents, out_tokens,        workspace};
+  return check_launch(tkp::launch_beam_select(dtype, a, static_cast<hipStream_t>(stream)), "selection launch");
+}
+
+topktopp_status beam_reorder_states(const topktopp_beam_state* states, int64_t count, const int32_t* parents,
+                                    int64_t N, int64_t K, const int32_t* lengths, void* stream) {
+  g_last_error.clear();
+  if (count < 0) return fail(TOPKTOPP_ERR_INVALID, "count=%lld is negative", (long long)count);
+  if (topktopp_status s = check_beams(N, K)) return s;
+  if (count == 0 || N == 0) return TOPKTOPP_OK;
+  if (states == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "states is NULL");
+  if (parents == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "parents is NULL");
+  for (int64_t i = 0; i < count; ++i) {
+    const tkp::BeamState s = state_of(states[i]);
+    size_t bytes;
+    if (topktopp_status e = state_span(s, N * K, &bytes)) return e;
+    if (bytes == 0) continue;
+    if (s.data == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "data of state %lld is NULL", (long long)i);
+    if (!tkp::beam_state_fits(s, static_cast<int>(K)))
+      return fail(TOPKTOPP_ERR_INVALID, "a row of state %lld has more than 2^31-1 columns", (long long)i);
+    if (overlaps(s.data, bytes, parents, static_cast<size_t>(N * K) * 4) ||
+        overlaps(s.data, bytes, lengths, static_cast<size_t>(N) * 4))
+      return fail(TOPKTOPP_ERR_INVALID, "state %lld overlaps parents or lengths", (long long)i);
+  }
+  // states that share no memory go together, as many as a launch takes
+  tkp::BeamState batch[tkp::kMaxStates];
+  size_t spans[tkp::kMaxStates];
+  int held = 0;
+  for (int64_t i = 0; i <= count; ++i) {
+    tkp::BeamState s{};
+    size_t bytes = 0;
+    bool flush = i == count || held == tkp::kMaxStates;
+    if (i < count) {
+      s = state_of(states[i]);
+      state_span(s, N * K, &bytes);
+      for (int j = 0; j < held && bytes != 0; ++j) flush |= overlaps(s.data, bytes, batch[j].data, spans[j]);
+    }
+    if (flush && held > 0) {
+      const hipError_t e = tkp::launch_beam_reorder(batch, held, parents, N, static_cast<int>(K), lengths,
+                                                    static_cast<hipStream_t>(stream));
+      if (e != hipSuccess) return check_launch(e, "reorder launch");
+      held = 0;
+    }
+    if (bytes != 0) {
+      spans[held] = bytes;
+      batch[held++] = s;
+    }
+  }
+  return TOPKTOPP_OK;
+}
+
+topktopp_status beam_backtrace(const int32_t* tokens, const int32_t* parents, int64_t T, int64_t N, int64_t K,
+                               const int32_t* beams, const int32_t* lengths, int64_t M, int32_t pad, int32_t* out,
+                               void* stream) {
+  g_last_error.clear();
+  const bool empty = T == 0 || N == 0 || M == 0;
+  if (!empty) {
+    if (tokens == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "tokens is NULL");
+    if (parents == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "parents is NULL");
+    if (out == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "out is NULL");
+  }
+  if (topktopp_status s = check_beams(N, K)) return s;
+  if (T < 0 || T > 0x7FFFFFFFLL)
+    return fail(TOPKTOPP_ERR_INVALID, "T=%lld is outside [0, 2^31-1]", (long long)T);
+  if (M < 0 || M > (1 << 20)) return fail(TOPKTOPP_ERR_INVALID, "M=%lld is outside [0, 2^20]", (long long)M);
+  if (beams == nullptr && M > K)
+    return fail(TOPKTOPP_ERR_INVALID, "M=%lld hypotheses without beams exceed K=%lld", (long long)M, (long long)K);
+  if (empty) return TOPKTOPP_OK;
+  const size_t hist = static_cast<size_t>(T) * static_cast<size_t>(N * K) * 4;
+  const size_t paths = static_cast<size_t>(N) * static_cast<size_t>(M) * 4;
+  const Span spans[] = {{out, paths * static_cast<size_t>(T), "out"},
+                        {tokens, hist, "tokens"},
+                        {parents, hist, "parents"},
+                        {beams, paths, "beams"},
+                        {lengths, paths, "lengths"}};
+  if (topktopp_status s = check_disjoint(spans, 5, 1)) return s;
+  const tkp::BeamBacktraceArgs a{tokens, parents, beams, lengths, out, T, N, static_cast<int>(K), static_cast<int>(M),
+                                 pad};
+  return check_launch(tkp::launch_beam_backtrace(a, static_cast<hipStream_t>(stream)), "backtrace launch");
 }
 
 }  // extern "C"
