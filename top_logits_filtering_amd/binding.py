@@ -505,12 +505,14 @@ def _state_layout(shape, strides, itemsize, batch_dim, seq_dim):
             joined[-1] = (joined[-1][0], joined[-1][1] * size)
         else:
             joined.append((stride, size))
-    if len(joined) > 3:
-        raise ValueError(f"a state of shape {shape} and strides {strides} has more than three separate axes")
-    joined = [(run, 1)] * (3 - len(joined)) + joined
-    joined.reverse()  # the last of the three is the one with the smallest stride
     positions, position_stride = (1, run) if seq_dim is None else (shape[seq_dim], strides[seq_dim] * itemsize)
-    return (strides[batch_dim] * itemsize, tuple(s for _, s in joined), tuple(s for s, _ in joined), positions,
+    if seq_dim is None and len(joined) == 4:  # without lengths the positions are an axis like any other
+        position_stride, positions = joined.pop()
+    if len(joined) > 3:
+        raise ValueError(f"a state of shape {shape} and strides {strides} has too many separate axes")
+    # the last of the three has the smallest stride
+    joined = [(run, 1)] * (3 - len(joined)) + joined[::-1]
+    return (strides[batch_dim] * itemsize, tuple(n for _, n in joined), tuple(b for b, _ in joined), positions,
             position_stride, run)
 
 
