@@ -39,6 +39,9 @@ COMMON_FLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 
+# Flags of single sources. The beam selection honours NaN: a row that holds one proposes nothing.
+SOURCE_FLAGS = {"beam_select.hip": ["-fhonor-nans"]}
+
 
 def _hipcc() -> str:
     path = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -69,7 +72,7 @@ def _spills(report: str) -> list:
 
 def _compile(src: str, verbose: bool) -> str:
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-    cmd = [_hipcc(), *COMMON_FLAGS, RESOURCE_FLAG, "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [_hipcc(), *COMMON_FLAGS, *SOURCE_FLAGS.get(src, []), RESOURCE_FLAG, "-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -31,10 +31,16 @@ namespace {
 constexpr int kChunkThreads = 256;
 constexpr int kChunkWaves = kChunkThreads / kWave;
 constexpr int kChunkCap = 1024;   // candidate slots of a chunk
-constexpr int kMaxVecs = 16;      // vectors per thread at most
+constexpr int kLayers = 32;       // vectors per thread at most
+constexpr int kUnit = 2;          // vectors that share one maximum
+constexpr int kGroup = 4;         // vectors loaded ahead
+constexpr int kHits = 2048;       // pairs of vectors looked at again
+constexpr int kTargetBlocks = 1024;
 constexpr int kMergeThreads = 512;
 constexpr int kMergeCap = 2048;   // candidate slots of a prompt
-constexpr int kHeads = 512;       // group maxima that bound a prompt's candidates
+constexpr int kMergeWaves = kMergeThreads / kWave;
+constexpr uint32_t kAllRanked = 128;  // so many candidates are ranked without a bound
+constexpr int kBoundBits = 14;        // bits of the bound below the first that differs
 constexpr int kMaxBeams = 128;
 constexpr int kTokenBits = 20;
 
@@ -60,22 +66,32 @@ __device__ __forceinline__ uint64_t pack(uint32_t key, uint32_t token) {
   return (static_cast<uint64_t>(key) << 32) | (0xFFFFFFFFu - token);
 }
 
+// fma with two constants, one of which waits in a vector register: an
+// instruction reads one scalar operand at most, and the compiler would copy
+// the other one into place every time.
+__device__ __forceinline__ double fma_const(double x, double vreg, double sreg) {
+  double r;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(vreg), "s"(sreg));
+  return r;
+}
+
 // exp(y) for |y| <= 1100 (finite result for y <= 709).
 __device__ __forceinline__ double exp64(double y) {
   constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: its low bits hold rint()
-  const double nm = __builtin_fma(y, 1.4426950408889634074, kMagic);
-  const int k = static_cast<int>(__builtin_bit_cast(uint64_t, nm));
+  const double nm = fma_const(y, 1.4426950408889634074, kMagic);
+  const uint32_t k = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, nm));
   const double f = __builtin_fma(nm - kMagic, -0.69314718055994530942, y);
-  double p = 0.00019775160531026297389;
-  p = __builtin_fma(p, f, 0.0013948195139022652005);
+  double p = fma_const(f, 0.00019775160531026297389, 0.0013948195139022652005);
   p = __builtin_fma(p, f, 0.0083335611766106098887);
   p = __builtin_fma(p, f, 0.041666225250020369325);
   p = __builtin_fma(p, f, 0.16666665125242092947);
   p = __builtin_fma(p, f, 0.50000001045984631318);
   p = __builtin_fma(p, f, 1.0000000002432869351);
   p = __builtin_fma(p, f, 0.99999999996165148826);
+  // times 2^k: k added to the exponent, as one 32-bit instruction
   const uint64_t u = __builtin_bit_cast(uint64_t, p);
-  const uint32_t hi = static_cast<uint32_t>(u >> 32) + (static_cast<uint32_t>(k) << 20);
+  uint32_t hi;
+  asm("v_lshl_add_u32 %0, %1, 20, %2" : "=v"(hi) : "v"(k), "v"(static_cast<uint32_t>(u >> 32)));
   return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | static_cast<uint32_t>(u));
 }
 
@@ -112,20 +128,15 @@ __device__ __forceinline__ bool beam_alive(float c, float w) {
 
 __device__ __forceinline__ uint32_t count_ballot(bool p) { return __builtin_popcountll(__ballot(p)); }
 
-// A copy that the compiler cannot trace: what one traversal of the vectors
-// derives from them (conversions, keys) is not kept in registers for the next.
-__device__ __forceinline__ vec_t opaque(vec_t q) {
-  asm volatile("" : "+v"(q));
-  return q;
-}
-
 struct ChunkSmem {
+  float top[kLayers / kUnit][kChunkThreads];  // largest value of each thread's pairs of vectors
   uint64_t list[kChunkCap];
-  uint32_t key[kChunkThreads];
+  uint32_t half[2 * kChunkThreads];           // largest of a thread's even and of its odd pairs, as keys
   double sum[kChunkWaves];
-  uint32_t abs[kChunkWaves];
   uint32_t scan[kChunkWaves];
   uint32_t count;
+  uint32_t hits;
+  uint16_t hit[kHits];
 };
 
 // Exclusive prefix of v over the block; total: the block's sum.
@@ -145,7 +156,7 @@ __device__ __forceinline__ uint32_t block_excl(uint32_t v, uint32_t& total, Chun
   return below + incl - v;
 }
 
-template <class DT, int NV>
+template <class DT>
 __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArgs a, BeamSplit split, int64_t row0,
                                                                    ChunkStat* __restrict__ stats,
                                                                    uint64_t* __restrict__ lists) {
@@ -174,87 +185,101 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   const int first = head + v0 * P;  // token of the chunk's first vector
 
   const __amdgpu_buffer_rsrc_t rs = row_rsrc(rowp + (cnt > 0 ? first : 0), cnt * P);
-  vec_t v[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-    v[i] = __builtin_amdgcn_raw_buffer_load_b128(rs, (i * kChunkThreads + tid) * 16, 0, kLoadPolicy);
+  constexpr uint32_t kNeg = P == 4 ? static_cast<uint32_t>(DT::kNegInf)
+                                   : static_cast<uint32_t>(DT::kNegInf) * 0x00010001u;
+  // Vector i * 256 + tid; zeros behind the chunk's end.
+  auto load = [&](int i) __attribute__((always_inline)) -> vec_t {
+    return __builtin_amdgcn_raw_buffer_load_b128(rs, (i * kChunkThreads + tid) * 16, 0, kLoadPolicy);
+  };
+  // The same for a second look, with -inf behind the end.
+  auto again = [&](int at) __attribute__((always_inline)) -> vec_t {
+    const vec_t q = __builtin_amdgcn_raw_buffer_load_b128(rs, at * 16, 0, 0);
+    return at < cnt ? q : vec_t{kNeg, kNeg, kNeg, kNeg};
+  };
 
+  vec_t next[kGroup];
+#pragma unroll
+  for (int g = 0; g < kGroup; ++g) next[g] = load(g);
   int te = -1;
   if (ch == 0 && tid < head) te = tid;
   if (ch == split.chunks - 1 && tid >= 16 && tid - 16 < a.V - tail0) te = tail0 + tid - 16;
   raw_t re = DT::kNegInf;
   if (te >= 0) re = rowp[te];
-  const float xe = DT::value(re);
+  if (tid == 0) sm.count = sm.hits = 0;
 
-  if (tid == 0) sm.count = 0;
-  // One pass: the sum of exp, the largest value, the largest magnitude (for NaN).
-  constexpr uint32_t kAbs = P == 4 ? 0x7FFFFFFFu : 0x7FFF7FFFu;
-  constexpr uint32_t kNeg = P == 4 ? static_cast<uint32_t>(DT::kNegInf)
-                                   : static_cast<uint32_t>(DT::kNegInf) * 0x00010001u;
-  using pair_t = uint16_t __attribute__((ext_vector_type(2)));
-  double sum = exp_term(xe);
-  float tm = xe;
-  uint32_t am = re & kAbs;
+  // One pass: the sum of exp and the largest value of each pair of vectors.
+  // maximum() keeps a NaN, so that one shows in the chunk's maximum.
+  double sum = 0.0;
+  float half0 = -INFINITY, half1 = -INFINITY;
+  const int layers = (cnt + kChunkThreads - 1) / kChunkThreads;
+#pragma unroll 1
+  for (int i0 = 0; i0 < layers; i0 += kGroup) {
+    vec_t now[kGroup];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    if (i * kChunkThreads + tid >= cnt) v[i] = vec_t{kNeg, kNeg, kNeg, kNeg};
-    __builtin_amdgcn_sched_barrier(0);  // one vector's terms at a time, or their 64-bit values fill the registers
-    double part = 0.0;
-    const vec_t q = opaque(v[i]);
+    for (int g = 0; g < kGroup; ++g) now[g] = next[g];
+    if (i0 + kGroup < layers) {
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const float x = DT::value(lane_of<raw_t>(q, j));
-      part += exp_term(x);
-      tm = fmaxf(tm, x);
+      for (int g = 0; g < kGroup; ++g) next[g] = load(i0 + kGroup + g);
     }
-    sum += part;
+    if ((i0 + kGroup) * kChunkThreads > cnt) {  // the last group
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const uint32_t u = vword(q, w) & kAbs;
-      if constexpr (P == 4) {
-        am = am > u ? am : u;
-      } else {
-        am = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(pair_t, am),
-                                                                    __builtin_bit_cast(pair_t, u)));
+      for (int g = 0; g < kGroup; ++g)
+        if ((i0 + g) * kChunkThreads + tid >= cnt) now[g] = vec_t{kNeg, kNeg, kNeg, kNeg};
+    }
+    float tops[kGroup / kUnit];
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      __builtin_amdgcn_sched_barrier(0);  // one vector's terms at a time, or their 64-bit values fill the registers
+      double part = 0.0;
+      float m = g % kUnit == 0 ? -INFINITY : tops[g / kUnit];
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const float x = DT::value(lane_of<raw_t>(now[g], j));
+        part += exp_term(x);
+        m = __builtin_elementwise_maximum(m, x);
       }
+      tops[g / kUnit] = m;
+      sum += part;
     }
+#pragma unroll
+    for (int u = 0; u < kGroup / kUnit; ++u) sm.top[i0 / kUnit + u][tid] = tops[u];
+    half0 = __builtin_elementwise_maximum(half0, tops[0]);
+    half1 = __builtin_elementwise_maximum(half1, tops[1]);
   }
-  if constexpr (P != 4) am = (am & 0xFFFFu) > (am >> 16) ? (am & 0xFFFFu) : (am >> 16);
+  const float xe = DT::value(re);
+  sum += exp_term(xe);
+  half0 = __builtin_elementwise_maximum(half0, xe);
 
-  const uint32_t tkey = tm > -INFINITY ? order_key(tm) : 0u;
-  sm.key[tid] = tkey;
+  // Keys of NaN lie above +inf's: positive ones by order_key, negative ones by this.
+  auto key_or_nan = [](float x) -> uint32_t {
+    if ((__float_as_uint(x) & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+    return __float_as_uint(x) == 0xFF800000u ? 0u : order_key(x);
+  };
+  sm.half[tid] = key_or_nan(half0);
+  sm.half[kChunkThreads + tid] = key_or_nan(half1);
   sum = wave_sum_f64(sum);
-  am = wave_max_u32(am);
-  if (lane == 0) {
-    sm.sum[wave] = sum;
-    sm.abs[wave] = am;
-  }
+  if (lane == 0) sm.sum[wave] = sum;
   __syncthreads();
 
-  // Every wave holds all the threads' maxima, four per lane.
-  const uint4 k4 = reinterpret_cast<const uint4*>(sm.key)[lane];
-  uint32_t top = k4.x > k4.y ? k4.x : k4.y;
-  top = top > k4.z ? top : k4.z;
-  top = wave_max_u32(top > k4.w ? top : k4.w);
-  sum = 0.0;
-  am = 0;
+  // Every wave holds all the maxima, eight per lane.
+  constexpr int kHalf = 2 * kChunkThreads / kWave;
+  uint32_t k[kHalf];
+  uint32_t top = 0;
 #pragma unroll
-  for (int w = 0; w < kChunkWaves; ++w) {
-    sum += sm.sum[w];
-    am = am > sm.abs[w] ? am : sm.abs[w];
+  for (int i = 0; i < kHalf; ++i) {
+    k[i] = sm.half[i * kWave + lane];
+    top = top > k[i] ? top : k[i];
   }
-  constexpr uint32_t kInfBits = P == 4 ? 0x7F800000u : (DT::kNegInf & 0x7FFFu);
+  top = wave_max_u32(top);
+  sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < kChunkWaves; ++w) sum += sm.sum[w];
   const int64_t slot = row * split.chunks + ch;
   uint64_t* out = lists + slot * a.n;
-  if (am > kInfBits || top >= order_key(INFINITY)) {  // a NaN or +inf: the beam proposes nothing
+  if (top >= order_key(INFINITY)) {  // a NaN or +inf: the beam proposes nothing
     if (tid == 0) stats[slot] = ChunkStat{0.0, 0.0f, 1};
     return;
   }
-  // Rare paths read the chunk again rather than hold code and registers for it.
-  auto again = [&](int i) __attribute__((always_inline)) -> vec_t {
-    const vec_t q = __builtin_amdgcn_raw_buffer_load_b128(rs, (i * kChunkThreads + tid) * 16, 0, 0);
-    return i * kChunkThreads + tid < cnt ? q : vec_t{kNeg, kNeg, kNeg, kNeg};
-  };
   float ref = 0.0f;
   if (top == 0u) {
     sum = 0.0;  // nothing but -inf
@@ -262,8 +287,8 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     ref = key_value(top);
     double part = exp_below(xe, ref);
 #pragma unroll 1
-    for (int i = 0; i * kChunkThreads < cnt; ++i) {
-      const vec_t q = again(i);
+    for (int i = 0; i < layers; ++i) {
+      const vec_t q = again(i * kChunkThreads + tid);
 #pragma unroll
       for (int j = 0; j < P; ++j) part += exp_below(DT::value(lane_of<raw_t>(q, j)), ref);
     }
@@ -277,45 +302,54 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   }
   if (tid == 0) stats[slot] = ChunkStat{sum, ref, 0};
 
-  // The n-th largest of the threads' maxima is a lower bound of the chunk's
-  // n-th largest value: largest T with at least n maxima >= T, bit by bit.
+  // The n-th largest of these maxima is a lower bound of the chunk's n-th
+  // largest value: the largest T with at least n maxima >= T, bit by bit.
   const uint32_t n = static_cast<uint32_t>(a.n);
   uint32_t T = 0;
 #pragma unroll 1
   for (int bit = 31; bit >= kLow; --bit) {
     const uint32_t t = T | (1u << bit);
-    const uint32_t c = count_ballot(k4.x >= t) + count_ballot(k4.y >= t) + count_ballot(k4.z >= t) +
-                       count_ballot(k4.w >= t);
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < kHalf; ++i) c += count_ballot(k[i] >= t);
     if (c >= n) T = t;
   }
   if (T == 0u) T = order_key(-FLT_MAX);  // fewer than n maxima: all finite values
   else if (!(T & 0x80000000u)) T |= (1u << kLow) - 1u;
-  float bound = key_value(T);
+  const float bound = key_value(T);
 
+  // Pairs of vectors that reach the bound, then their elements.
+  const int units = (layers + kUnit - 1) / kUnit;
+  for (int u = 0; u < units; ++u) {
+    if (sm.top[u][tid] >= bound) {
+      const uint32_t at = atomicAdd(&sm.hits, 1u);
+      if (at < kHits) sm.hit[at] = static_cast<uint16_t>(u * kChunkThreads + tid);
+    }
+  }
   auto push = [&](float x, uint32_t token) __attribute__((always_inline)) {
     const uint32_t at = atomicAdd(&sm.count, 1u);
     if (at < kChunkCap) sm.list[at] = pack(order_key(x), token);
   };
   if (xe >= bound) push(xe, static_cast<uint32_t>(te));
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const vec_t q = opaque(v[i]);
-    float m = DT::value(lane_of<raw_t>(q, 0));
-#pragma unroll
-    for (int j = 1; j < P; ++j) m = fmaxf(m, DT::value(lane_of<raw_t>(q, j)));
-    if (m >= bound) {
-      const uint32_t token = static_cast<uint32_t>(first + (i * kChunkThreads + fresh_tid()) * P);
+  __syncthreads();
+  const uint32_t hits = sm.hits;
+  if (hits <= kHits) {
+    for (uint32_t e = tid; e < hits * kUnit; e += kChunkThreads) {
+      const int h = sm.hit[e / kUnit];
+      const int at = ((h / kChunkThreads) * kUnit + static_cast<int>(e % kUnit)) * kChunkThreads + h % kChunkThreads;
+      const vec_t q = again(at);
+      const uint32_t token = static_cast<uint32_t>(first + at * P);
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         const float x = DT::value(lane_of<raw_t>(q, j));
         if (x >= bound) push(x, token + j);
       }
     }
+    __syncthreads();
   }
-  __syncthreads();
   uint32_t M = sm.count;
 
-  if (M > kChunkCap) {
+  if (hits > kHits || M > kChunkCap) {
     // Many values at or above the bound: find the n-th largest value exactly,
     // list what lies above it, then the equal ones in the order of their tokens.
     auto key_of = [](raw_t r) -> uint32_t {
@@ -325,8 +359,8 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     auto count_from = [&](uint32_t t) __attribute__((always_inline)) -> uint32_t {
       uint32_t c = key_of(re) >= t ? 1u : 0u;
 #pragma unroll 1
-      for (int i = 0; i * kChunkThreads < cnt; ++i) {
-        const vec_t q = again(i);
+      for (int i = 0; i < layers; ++i) {
+        const vec_t q = again(i * kChunkThreads + tid);
 #pragma unroll
         for (int j = 0; j < P; ++j) c += key_of(lane_of<raw_t>(q, j)) >= t ? 1u : 0u;
       }
@@ -352,20 +386,19 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     if (tid == 0) sm.count = 0;
     __syncthreads();
     auto push_above = [&](raw_t r, uint32_t token) __attribute__((always_inline)) {
-      const uint32_t k = key_of(r);
-      if (k > T) {
+      const uint32_t key = key_of(r);
+      if (key > T) {
         const uint32_t at = atomicAdd(&sm.count, 1u);
-        if (at < kChunkCap) sm.list[at] = pack(k, token);
+        if (at < kChunkCap) sm.list[at] = pack(key, token);
       }
     };
     push_above(re, static_cast<uint32_t>(te));
 #pragma unroll 1
-    for (int i = 0; i * kChunkThreads < cnt; ++i) {
-      const vec_t q = again(i);
+    for (int i = 0; i < layers; ++i) {
+      const vec_t q = again(i * kChunkThreads + tid);
       const uint32_t token = static_cast<uint32_t>(first + (i * kChunkThreads + tid) * P);
 #pragma unroll
-      for (int j = 0; j < P; ++j)
-        push_above(lane_of<raw_t>(q, j), token + j);
+      for (int j = 0; j < P; ++j) push_above(lane_of<raw_t>(q, j), token + j);
     }
     __syncthreads();
     uint32_t have = sm.count;  // < n
@@ -380,9 +413,9 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     const bool equal_e = key_of(re) == T;
     push_equal(equal_e && te >= 0 && te < head ? 1u : 0u, static_cast<uint32_t>(te));
 #pragma unroll 1
-    for (int i = 0; i * kChunkThreads < cnt && have < n; ++i) {
+    for (int i = 0; i < layers && have < n; ++i) {
       uint32_t mask = 0;
-      const vec_t q = again(i);
+      const vec_t q = again(i * kChunkThreads + tid);
 #pragma unroll
       for (int j = 0; j < P; ++j) mask |= (key_of(lane_of<raw_t>(q, j)) == T ? 1u : 0u) << j;
       push_equal(mask, static_cast<uint32_t>(first + (i * kChunkThreads + tid) * P));
@@ -413,16 +446,59 @@ __device__ __forceinline__ bool above(const Cand& a, const Cand& b) {
 
 struct MergeSmem {
   Cand list[kMergeCap];
-  double ref[kMaxBeams];     // L = ref + rest; apart, as ref may be as large as the type goes
+  uint32_t upper[kMergeCap];  // the candidates' upper halves of hi
+  double ref[kMaxBeams];      // L = ref + rest; apart, as ref may be as large as the type goes
   double rest[kMaxBeams];
   double score[kMaxBeams];
   double weight[kMaxBeams];
-  int state[kMaxBeams];      // 0: proposes nothing, 1: its lists, 2: finished
-  uint32_t heads[kHeads];
-  Cand best[kMergeThreads / kWave];
+  int state[kMaxBeams];       // 0: proposes nothing, 1: its lists, 2: finished
+  uint32_t heads[kMergeThreads];
+  Cand best[kMergeWaves];
   uint32_t count;
-  uint32_t more;
+  uint32_t votes[2];
 };
+
+// One beam's L and state out of its chunks, held by all threads that pass the
+// same row: lane i of `lanes` takes chunks i, i + lanes, ...
+template <class Max, class Sum>
+__device__ __forceinline__ void beam_total(const ChunkStat* __restrict__ s, int C, int i, int lanes, float c, float w,
+                                           bool finished, Max max_of, Sum sum_of, double& ref, double& rest,
+                                           int& state) {
+  uint32_t rk = 0, bad = 0;
+  const bool reads = beam_alive(c, w) && !finished;
+  ref = rest = 0.0;
+  state = beam_alive(c, w) ? (finished ? 2 : 1) : 0;
+  double sum = 0.0;
+  if (C <= lanes) {
+    ChunkStat t{0.0, 0.0f, 0};
+    if (i < C) t = s[i];
+    if (reads && t.bad == 0 && t.sum > 0.0) rk = order_key(t.ref);
+    bad = max_of(static_cast<uint32_t>(t.bad));
+    rk = max_of(rk);
+    if (rk != 0) ref = key_value(rk);
+    const double d = t.ref - ref;
+    if (reads && t.bad == 0 && t.sum > 0.0) sum = d == 0.0 ? t.sum : (d < -2000.0 ? 0.0 : t.sum * exp(d));
+  } else if (reads) {
+    for (int j = i; j < C; j += lanes) {
+      const ChunkStat t = s[j];
+      bad |= static_cast<uint32_t>(t.bad);
+      if (t.sum > 0.0) rk = rk > order_key(t.ref) ? rk : order_key(t.ref);
+    }
+    bad = max_of(bad);
+    rk = max_of(rk);
+    if (rk != 0) ref = key_value(rk);
+    for (int j = i; j < C; j += lanes) {
+      const ChunkStat t = s[j];
+      const double d = t.ref - ref;
+      if (t.sum > 0.0) sum += d == 0.0 ? t.sum : (d < -2000.0 ? 0.0 : t.sum * exp(d));
+    }
+  }
+  sum = sum_of(sum);
+  if (state == 1) {
+    if (bad != 0 || !(sum > 0.0)) state = 0;
+    else rest = log(sum);
+  }
+}
 
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArgs a, int C, int64_t item0,
                                                                    const ChunkStat* __restrict__ stats,
@@ -432,130 +508,188 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
   const int64_t item = item0 + blockIdx.x;
   const int K = a.K;
   const uint32_t n = static_cast<uint32_t>(a.n);
+  const uint32_t nl = static_cast<uint32_t>(K * C);  // lists of this prompt
+  const uint64_t* __restrict__ mine = lists + item * nl * n;
 
-  // L of each beam from its chunks' sums: a wave per beam, lanes over chunks.
-  for (int b = wave; b < K; b += kMergeThreads / kWave) {
-    const int64_t row = item * K + b;
-    const float c = a.scores[row], w = a.weights != nullptr ? a.weights[row] : 1.0f;
-    int state = 0;
-    double ref = 0.0, rest = 0.0;
-    if (beam_alive(c, w)) {
-      if (a.finished != nullptr && a.finished[row] != 0) {
-        state = 2;
-      } else {
-        uint32_t rk = 0, bad = 0;
-        for (int i = lane; i < C; i += kWave) {
-          const ChunkStat s = stats[row * C + i];
-          bad |= static_cast<uint32_t>(s.bad);
-          if (s.sum > 0.0) rk = rk > order_key(s.ref) ? rk : order_key(s.ref);
-        }
-        rk = wave_max_u32(rk);
-        bad = wave_max_u32(bad);
-        ref = rk != 0 ? static_cast<double>(key_value(rk)) : 0.0;
-        double sum = 0.0;
-        for (int i = lane; i < C; i += kWave) {
-          const ChunkStat s = stats[row * C + i];
-          if (s.sum > 0.0) {
-            const double d = s.ref - ref;
-            sum += d == 0.0 ? s.sum : (d < -2000.0 ? 0.0 : s.sum * exp(d));
-          }
-        }
-        sum = wave_sum_f64(sum);
-        if (bad == 0 && sum > 0.0) {
-          state = 1;
-          rest = log(sum);
-        }
+  // The first entries of every list, `wide` of each, are under way while L is
+  // formed. (Lists of beams that propose nothing hold anything; they are not used.)
+  constexpr int kHeld = 4;
+  const uint32_t room = kHeld * kMergeThreads;
+  uint32_t wide = nl < room ? room / nl : 1u;
+  wide = wide < n ? wide : n;
+  uint64_t held[kHeld];
+#pragma unroll
+  for (int u = 0; u < kHeld; ++u) {
+    const uint32_t f = u * kMergeThreads + tid;
+    held[u] = f < nl * wide ? mine[(f / wide) * n + f % wide] : 0;
+  }
+
+  if (tid == 0) sm.count = 0;
+  if (K <= kMergeWaves) {  // a wave per beam
+    if (wave < K) {
+      const int64_t row = item * K + wave;
+      const float c = a.scores[row], w = a.weights != nullptr ? a.weights[row] : 1.0f;
+      const bool done = a.finished != nullptr && a.finished[row] != 0;
+      double ref, rest;
+      int state;
+      beam_total(stats + row * C, C, lane, kWave, c, w, done, [](uint32_t v) { return wave_max_u32(v); },
+                 [](double v) { return wave_sum_f64(v); }, ref, rest, state);
+      if (lane == 0) {
+        sm.ref[wave] = ref;
+        sm.rest[wave] = rest;
+        sm.score[wave] = c;
+        sm.weight[wave] = w;
+        sm.state[wave] = state;
       }
     }
-    if (lane == 0) {
-      sm.ref[b] = ref;
-      sm.rest[b] = rest;
-      sm.score[b] = c;
-      sm.weight[b] = w;
-      sm.state[b] = state;
-    }
-  }
-  if (tid < kHeads) sm.heads[tid] = 0;
-  if (tid == 0) {
-    sm.count = 0;
-    sm.more = 0;
+  } else if (tid < K) {  // a thread per beam
+    const int64_t row = item * K + tid;
+    const float c = a.scores[row], w = a.weights != nullptr ? a.weights[row] : 1.0f;
+    const bool done = a.finished != nullptr && a.finished[row] != 0;
+    double ref, rest;
+    int state;
+    beam_total(stats + row * C, C, 0, 1, c, w, done, [](uint32_t v) { return v; }, [](double v) { return v; }, ref,
+               rest, state);
+    sm.ref[tid] = ref;
+    sm.rest[tid] = rest;
+    sm.score[tid] = c;
+    sm.weight[tid] = w;
+    sm.state[tid] = state;
   }
   __syncthreads();
 
-  const int nl = K * C;  // lists of this prompt
-  const int64_t list0 = item * nl;
-  // Entry j of list q as a candidate; hi is 0 where there is none.
-  auto cand = [&](int q, uint32_t j) -> Cand {
-    const int b = q / C;
+  // Entry j of list q, e, as a candidate; hi is 0 where there is none.
+  auto cand = [&](uint64_t e, uint32_t q, uint32_t j) __attribute__((always_inline)) -> Cand {
+    const uint32_t b = q / static_cast<uint32_t>(C);
     const int st = sm.state[b];
-    if (st == 0) return Cand{0, 0};
     const uint64_t beam = static_cast<uint64_t>(kMaxBeams - 1 - b) << (32 + kTokenBits);
-    if (st == 2) {
-      if (j != 0 || q != b * C) return Cand{0, 0};
-      return Cand{order_key64(sm.score[b] * sm.weight[b]), beam};
-    }
-    const uint64_t e = lists[(list0 + q) * n + j];
-    if (e == 0) return Cand{0, 0};
     const uint32_t key = static_cast<uint32_t>(e >> 32);
     const uint32_t back = ((1u << kTokenBits) - 1u) - (0xFFFFFFFFu - static_cast<uint32_t>(e));
-    const double s = sm.score[b] + ((static_cast<double>(key_value(key)) - sm.ref[b]) - sm.rest[b]);
-    return Cand{order_key64(s * sm.weight[b]), beam | (static_cast<uint64_t>(key) << kTokenBits) | back};
+    double s = sm.score[b];
+    if (st == 1) s += (static_cast<double>(key_value(key)) - sm.ref[b]) - sm.rest[b];
+    const bool is = st == 1 ? e != 0 : (st == 2 && j == 0 && q == b * static_cast<uint32_t>(C));
+    const uint64_t low = st == 1 ? (static_cast<uint64_t>(key) << kTokenBits) | back : 0;
+    return is ? Cand{order_key64(s * sm.weight[b]), beam | low} : Cand{0, 0};
   };
+  auto fetch = [&](uint32_t q, uint32_t j) __attribute__((always_inline)) -> Cand { return cand(mine[q * n + j], q, j); };
 
-  // A bound: the largest T that n of the lists' first entries reach (by the
-  // upper half of the rank's image), over at most kHeads group maxima.
-  const uint32_t deep = (n + nl - 1) / nl;  // entries of each list, so that there are n
-  const uint32_t nh = deep * nl;
-  uint32_t mine = 0;
-  for (uint32_t f = tid; f < nh; f += kMergeThreads) {
-    const uint32_t h = static_cast<uint32_t>(cand(static_cast<int>(f / deep), f % deep).hi >> 32);
-    mine = mine > h ? mine : h;
-  }
-  sm.heads[tid] = mine;
-  __syncthreads();
-  uint32_t h[kHeads / kWave];
+  Cand first[kHeld];
 #pragma unroll
-  for (int i = 0; i < kHeads / kWave; ++i) h[i] = sm.heads[i * kWave + lane];
-  uint32_t T = 0;
+  for (int u = 0; u < kHeld; ++u) {
+    const uint32_t f = u * kMergeThreads + tid;
+    first[u] = f < nl * wide ? cand(held[u], f / wide, f % wide) : Cand{0, 0};
+  }
+
+  // A bound on the n-th candidate: the largest T (of the ranks' upper halves)
+  // that n of the threads' best reach; its low bits are left open. Few
+  // candidates need none.
+  uint32_t T = 1u;
+  if (nl * n > kAllRanked) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const uint32_t h = static_cast<uint32_t>(first[u].hi >> 32);
+      best = best > h ? best : h;
+    }
+    for (uint32_t q = room + tid; q < nl; q += kMergeThreads) {  // more lists than are held (wide is 1)
+      const uint32_t h = static_cast<uint32_t>(fetch(q, 0).hi >> 32);
+      best = best > h ? best : h;
+    }
+    sm.heads[tid] = best;
+    __syncthreads();
+    uint32_t h[kMergeWaves], top = 0, low = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < kMergeWaves; ++i) {
+      h[i] = sm.heads[i * kWave + lane];
+      top = top > h[i] ? top : h[i];
+      if (h[i] != 0) low = low < h[i] ? low : h[i];
+    }
+    top = wave_max_u32(top);
+    low = wave_min_u32(low);
+    T = top;
+    if (low < top) {
+      int bit = 31 - __builtin_clz(top ^ low);
+      const int stop = bit > kBoundBits ? bit - kBoundBits : 0;
+      T = top & ~((2u << bit) - 1u);
 #pragma unroll 1
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t t = T | (1u << bit);
-    uint32_t c = 0;
+      for (; bit >= stop; --bit) {
+        const uint32_t t = T | (1u << bit);
+        uint32_t c = 0;
 #pragma unroll
-    for (int i = 0; i < kHeads / kWave; ++i) c += count_ballot(h[i] >= t);
-    if (c >= n) T = t;
-  }
-  if (T == 0u) T = 1u;  // fewer than n: every candidate
-
-  // Candidates from T on, in windows of entries while a list's last one still reaches it.
-  const uint32_t window = nl < kMergeThreads ? kMergeThreads / nl : 1u;
-  for (uint32_t j0 = 0; j0 < n; j0 += window) {
-    const uint32_t wide = n - j0 < window ? n - j0 : window;
-    bool more = false;
-    for (uint32_t f = tid; f < wide * nl; f += kMergeThreads) {
-      const uint32_t j = f % wide;
-      const Cand k = cand(static_cast<int>(f / wide), j0 + j);
-      if (static_cast<uint32_t>(k.hi >> 32) >= T) {
-        const uint32_t at = atomicAdd(&sm.count, 1u);
-        if (at < kMergeCap) sm.list[at] = k;
-        more |= j == wide - 1;
+        for (int i = 0; i < kMergeWaves; ++i) c += count_ballot(h[i] >= t);
+        if (c >= n) T = t;
       }
     }
-    if (!__syncthreads_or(more)) break;
+    // fewer than n may reach even that: then every candidate counts
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < kMergeWaves; ++i) c += count_ballot(h[i] >= T && h[i] != 0);
+    if (c < n || T == 0u) T = 1u;
   }
-  __syncthreads();
-  uint32_t M = sm.count;
+
+  auto push = [&](const Cand& k) __attribute__((always_inline)) -> bool {
+    const uint32_t h = static_cast<uint32_t>(k.hi >> 32);
+    if (h < T) return false;
+    const uint32_t at = atomicAdd(&sm.count, 1u);
+    if (at < kMergeCap) {
+      sm.list[at] = k;
+      sm.upper[at] = h;
+    }
+    return true;
+  };
+  uint32_t M;
+  for (int tries = 0;; ++tries) {
+    // candidates from T on: those held, then further windows of entries while
+    // some list's last one still reaches T
+    bool more = false;
+#pragma unroll
+    for (int u = 0; u < kHeld; ++u) {
+      const uint32_t f = u * kMergeThreads + tid;
+      if (push(first[u])) more |= f % wide == wide - 1;
+    }
+    for (uint32_t q = room + tid; q < nl; q += kMergeThreads) more |= push(fetch(q, 0));
+    for (uint32_t j0 = wide; __syncthreads_or(more) && j0 < n; j0 += wide) {
+      more = false;
+      const uint32_t w = n - j0 < wide ? n - j0 : wide;
+      for (uint32_t f = tid; f < nl * w; f += kMergeThreads) {
+        const uint32_t j = f % w;
+        if (push(fetch(f / w, j0 + j))) more |= j == w - 1;
+      }
+    }
+    __syncthreads();
+    M = sm.count;
+    if (M <= kMergeCap || tries == 4) break;
+    // The list is full: the n-th best of what it holds is a better bound.
+    uint32_t better = 0;
+#pragma unroll 1
+    for (int bit = 31; bit >= 0; --bit) {
+      const uint32_t t = better | (1u << bit);
+      uint32_t c = 0;
+      if (tid == 0) sm.votes[bit & 1] = 0;
+      __syncthreads();
+      for (uint32_t e = tid; e < kMergeCap; e += kMergeThreads) c += sm.upper[e] >= t ? 1u : 0u;
+      c = wave_sum_u32(c);
+      if (lane == 0) atomicAdd(&sm.votes[bit & 1], c);
+      __syncthreads();
+      if (sm.votes[bit & 1] >= n) better = t;
+    }
+    if (better <= T) break;  // that many are equal there
+    T = better;
+    __syncthreads();
+    if (tid == 0) sm.count = 0;
+    __syncthreads();
+  }
 
   if (M > kMergeCap) {
-    // More ties in the upper half than the list holds: take the best ones one
-    // by one, each the largest candidate below the last.
+    // More candidates share an upper half than the list holds: take the best
+    // ones one by one, each the largest below the last.
     __syncthreads();
     Cand last{~0ull, ~0ull};
     uint32_t r = 0;
     for (; r < n; ++r) {
       Cand best{0, 0};
-      for (uint32_t f = tid; f < n * static_cast<uint32_t>(nl); f += kMergeThreads) {
-        const Cand k = cand(static_cast<int>(f / n), f % n);
+      for (uint32_t f = tid; f < n * nl; f += kMergeThreads) {
+        const Cand k = fetch(f / n, f % n);
         if (above(last, k) && above(k, best)) best = k;
       }
 #pragma unroll
@@ -568,10 +702,13 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       __syncthreads();
       best = sm.best[0];
 #pragma unroll
-      for (int w = 1; w < kMergeThreads / kWave; ++w)
+      for (int w = 1; w < kMergeWaves; ++w)
         if (above(sm.best[w], best)) best = sm.best[w];
       if (best.hi == 0) break;
-      if (tid == 0) sm.list[r] = best;
+      if (tid == 0) {
+        sm.list[r] = best;
+        sm.upper[r] = static_cast<uint32_t>(best.hi >> 32);
+      }
       last = best;
     }
     M = r;
@@ -580,9 +717,14 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
 
   // Ranks by counting; decode and write.
   for (uint32_t e = tid; e < M; e += kMergeThreads) {
+    const uint32_t h = sm.upper[e];
     const Cand k = sm.list[e];
     uint32_t r = 0;
-    for (uint32_t j = 0; j < M; ++j) r += above(sm.list[j], k) ? 1u : 0u;
+    for (uint32_t j = 0; j < M; ++j) {
+      const uint32_t o = sm.upper[j];
+      r += o > h ? 1u : 0u;
+      if (o == h && j != e) r += above(sm.list[j], k) ? 1u : 0u;
+    }
     if (r < n) {
       const int b = kMaxBeams - 1 - static_cast<int>(k.lo >> (32 + kTokenBits));
       double s = sm.score[b];
@@ -605,35 +747,25 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
   }
 }
 
-template <class DT, int NV>
+template <class DT>
 void launch_chunks(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t items, ChunkStat* stats,
                    uint64_t* lists, hipStream_t stream) {
   const unsigned blocks = static_cast<unsigned>(items * a.K * s.chunks);
-  hipLaunchKernelGGL((beam_chunk_kernel<DT, NV>), dim3(blocks), dim3(kChunkThreads), 0, stream, a, s, item0 * a.K,
-                     stats, lists);
-}
-
-template <class DT>
-void launch_dtype(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t items, ChunkStat* stats,
-                  uint64_t* lists, hipStream_t stream) {
-  const int per = (s.vecs + kChunkThreads - 1) / kChunkThreads;
-  if (per <= 1) launch_chunks<DT, 1>(a, s, item0, items, stats, lists, stream);
-  else if (per <= 2) launch_chunks<DT, 2>(a, s, item0, items, stats, lists, stream);
-  else if (per <= 4) launch_chunks<DT, 4>(a, s, item0, items, stats, lists, stream);
-  else if (per <= 8) launch_chunks<DT, 8>(a, s, item0, items, stats, lists, stream);
-  else launch_chunks<DT, kMaxVecs>(a, s, item0, items, stats, lists, stream);
+  hipLaunchKernelGGL(beam_chunk_kernel<DT>, dim3(blocks), dim3(kChunkThreads), 0, stream, a, s, item0 * a.K, stats,
+                     lists);
 }
 
 }  // namespace
 
-// Chunks as large as a workgroup's registers hold, but enough of them to give
-// every compute unit four workgroups when there are few rows.
+// Chunks of a few layers of vectors when there are few rows, so that every
+// compute unit gets some, and of as many as a workgroup notes maxima for when
+// there are many.
 BeamSplit beam_select_split(int dtype, int64_t rows, int V) {
   const int64_t per = dtype == 0 ? 4 : 8;
   const int64_t nv = V / per;
-  const int64_t least = (nv + kChunkThreads * kMaxVecs - 1) / (kChunkThreads * kMaxVecs);
-  const int64_t most = (nv + kChunkThreads - 1) / kChunkThreads;
-  int64_t c = rows > 0 ? 1024 / rows : 1;
+  const int64_t least = (nv + kChunkThreads * kLayers - 1) / (kChunkThreads * kLayers);
+  const int64_t most = (nv + kChunkThreads * kGroup - 1) / (kChunkThreads * kGroup);
+  int64_t c = rows > 0 ? (kTargetBlocks + rows - 1) / rows : 1;
   c = c < most ? c : most;
   c = c > least ? c : least;
   c = c > 1 ? c : 1;
@@ -653,9 +785,9 @@ hipError_t launch_beam_select(int dtype, const BeamSelectArgs& a, hipStream_t st
   const int64_t step = (int64_t{1} << 22) / (static_cast<int64_t>(a.K) * s.chunks);
   for (int64_t i = 0; i < a.N; i += step) {
     const int64_t items = a.N - i < step ? a.N - i : step;
-    if (dtype == 0) launch_dtype<F32T>(a, s, i, items, stats, lists, stream);
-    else if (dtype == 1) launch_dtype<F16T>(a, s, i, items, stats, lists, stream);
-    else launch_dtype<BF16T>(a, s, i, items, stats, lists, stream);
+    if (dtype == 0) launch_chunks<F32T>(a, s, i, items, stats, lists, stream);
+    else if (dtype == 1) launch_chunks<F16T>(a, s, i, items, stats, lists, stream);
+    else launch_chunks<BF16T>(a, s, i, items, stats, lists, stream);
     hipLaunchKernelGGL(beam_merge_kernel, dim3(static_cast<unsigned>(items)), dim3(kMergeThreads), 0, stream, a,
                        s.chunks, i, stats, lists);
     if (const hipError_t e = hipGetLastError()) return e;
