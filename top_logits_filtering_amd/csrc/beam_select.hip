@@ -31,16 +31,22 @@ namespace {
 constexpr int kChunkThreads = 256;
 constexpr int kChunkWaves = kChunkThreads / kWave;
 constexpr int kChunkCap = 1024;   // candidate slots of a chunk
+constexpr int kBoundBits = 14;    // bits of a bound from the first that differs on
 constexpr int kLayers = 32;       // vectors per thread at most
 constexpr int kUnit = 2;          // vectors that share one maximum
 constexpr int kGroup = 4;         // vectors loaded ahead
 constexpr int kHits = 2048;       // pairs of vectors looked at again
-constexpr int kTargetBlocks = 1024;
+#ifndef TB
+#define TB 1024
+#endif
+constexpr int kTargetBlocks = TB;
 constexpr int kMergeThreads = 512;
 constexpr int kMergeCap = 2048;   // candidate slots of a prompt
 constexpr int kMergeWaves = kMergeThreads / kWave;
-constexpr uint32_t kAllRanked = 128;  // so many candidates are ranked without a bound
-constexpr int kBoundBits = 14;        // bits of the bound below the first that differs
+constexpr uint32_t kWaveBound = 16;  // up to so many candidates per chunk a wave's bound is taken
+constexpr uint32_t kAllRanked = 48;  // so many candidates are ranked without a bound
+constexpr uint32_t kLongList = 96;      // a list is cut before it is ranked if it is longer
+constexpr uint32_t kMergeLists = 1024;  // lists noted as going on
 constexpr int kMaxBeams = 128;
 constexpr int kTokenBits = 20;
 
@@ -128,11 +134,45 @@ __device__ __forceinline__ bool beam_alive(float c, float w) {
 
 __device__ __forceinline__ uint32_t count_ballot(bool p) { return __builtin_popcountll(__ballot(p)); }
 
+// The largest T with at least n of the keys k (COUNT per lane; 0: none) at or
+// above it, bit by bit: not lower than `stop`, the first `bits` bits that can
+// differ. 0 if there are fewer than n keys.
+template <int COUNT>
+__device__ __forceinline__ uint32_t nth_key(const uint32_t (&k)[COUNT], uint32_t n, int bits, int stop) {
+  uint32_t top = 0, low = 0xFFFFFFFFu;
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) {
+    top = top > k[i] ? top : k[i];
+    if (k[i] != 0) low = low < k[i] ? low : k[i];
+  }
+  top = wave_max_u32(top);
+  low = wave_min_u32(low);
+  auto count = [&](uint32_t t) __attribute__((always_inline)) -> uint32_t {
+    uint32_t c = 0;
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) c += count_ballot(k[i] >= t);
+    return c;
+  };
+  if (top == 0 || count(low) < n) return 0;
+  if (low == top) return top;
+  int bit = 31 - __builtin_clz(top ^ low);
+  const int last = bit - bits + 1 > stop ? bit - bits + 1 : stop;
+  uint32_t T = top & ~((2u << bit) - 1u);
+#pragma unroll 1
+  for (; bit >= last; --bit) {
+    const uint32_t t = T | (1u << bit);
+    if (count(t) >= n) T = t;
+  }
+  return T > low ? T : low;
+}
+
 struct ChunkSmem {
   float top[kLayers / kUnit][kChunkThreads];  // largest value of each thread's pairs of vectors
-  uint64_t list[kChunkCap];
+  uint64_t list[kChunkCap + 8];
   uint32_t half[2 * kChunkThreads];           // largest of a thread's even and of its odd pairs, as keys
   double sum[kChunkWaves];
+  uint32_t wave_top[kChunkWaves];
+  uint32_t wave_bound[kChunkWaves];
   uint32_t scan[kChunkWaves];
   uint32_t count;
   uint32_t hits;
@@ -156,7 +196,9 @@ __device__ __forceinline__ uint32_t block_excl(uint32_t v, uint32_t& total, Chun
   return below + incl - v;
 }
 
-template <class DT>
+// SHORT: the chunk is one group of layers, which stays in registers; otherwise
+// groups stream through and the few vectors that matter are read again.
+template <class DT, bool SHORT>
 __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArgs a, BeamSplit split, int64_t row0,
                                                                    ChunkStat* __restrict__ stats,
                                                                    uint64_t* __restrict__ lists) {
@@ -168,8 +210,6 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int ch = static_cast<int>(blockIdx.x % static_cast<unsigned>(split.chunks));
   const int64_t row = row0 + blockIdx.x / static_cast<unsigned>(split.chunks);
-  if (!beam_alive(a.scores[row], a.weights != nullptr ? a.weights[row] : 1.0f)) return;
-  if (a.finished != nullptr && a.finished[row] != 0) return;
 
   // The row as elements before the first 16-byte boundary, whole vectors, and
   // the elements behind the last one; the few single elements are held one per
@@ -205,6 +245,9 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   if (ch == split.chunks - 1 && tid >= 16 && tid - 16 < a.V - tail0) te = tail0 + tid - 16;
   raw_t re = DT::kNegInf;
   if (te >= 0) re = rowp[te];
+  // (the first loads are under way before it is known whether the row counts)
+  if (!beam_alive(a.scores[row], a.weights != nullptr ? a.weights[row] : 1.0f)) return;
+  if (a.finished != nullptr && a.finished[row] != 0) return;
   if (tid == 0) sm.count = sm.hits = 0;
 
   // One pass: the sum of exp and the largest value of each pair of vectors.
@@ -212,21 +255,13 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   double sum = 0.0;
   float half0 = -INFINITY, half1 = -INFINITY;
   const int layers = (cnt + kChunkThreads - 1) / kChunkThreads;
-#pragma unroll 1
-  for (int i0 = 0; i0 < layers; i0 += kGroup) {
-    vec_t now[kGroup];
-#pragma unroll
-    for (int g = 0; g < kGroup; ++g) now[g] = next[g];
-    if (i0 + kGroup < layers) {
-#pragma unroll
-      for (int g = 0; g < kGroup; ++g) next[g] = load(i0 + kGroup + g);
-    }
+  float tops[kGroup / kUnit];
+  auto take = [&](int i0, vec_t (&now)[kGroup]) __attribute__((always_inline)) {
     if ((i0 + kGroup) * kChunkThreads > cnt) {  // the last group
 #pragma unroll
       for (int g = 0; g < kGroup; ++g)
         if ((i0 + g) * kChunkThreads + tid >= cnt) now[g] = vec_t{kNeg, kNeg, kNeg, kNeg};
     }
-    float tops[kGroup / kUnit];
 #pragma unroll
     for (int g = 0; g < kGroup; ++g) {
       __builtin_amdgcn_sched_barrier(0);  // one vector's terms at a time, or their 64-bit values fill the registers
@@ -241,10 +276,25 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
       tops[g / kUnit] = m;
       sum += part;
     }
-#pragma unroll
-    for (int u = 0; u < kGroup / kUnit; ++u) sm.top[i0 / kUnit + u][tid] = tops[u];
     half0 = __builtin_elementwise_maximum(half0, tops[0]);
     half1 = __builtin_elementwise_maximum(half1, tops[1]);
+  };
+  if constexpr (SHORT) {
+    take(0, next);
+  } else {
+#pragma unroll 1
+    for (int i0 = 0; i0 < layers; i0 += kGroup) {
+      vec_t now[kGroup];
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) now[g] = next[g];
+      if (i0 + kGroup < layers) {
+#pragma unroll
+        for (int g = 0; g < kGroup; ++g) next[g] = load(i0 + kGroup + g);
+      }
+      take(i0, now);
+#pragma unroll
+      for (int u = 0; u < kGroup / kUnit; ++u) sm.top[i0 / kUnit + u][tid] = tops[u];
+    }
   }
   const float xe = DT::value(re);
   sum += exp_term(xe);
@@ -255,25 +305,42 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     if ((__float_as_uint(x) & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
     return __float_as_uint(x) == 0xFF800000u ? 0u : order_key(x);
   };
-  sm.half[tid] = key_or_nan(half0);
-  sm.half[kChunkThreads + tid] = key_or_nan(half1);
-  sum = wave_sum_f64(sum);
-  if (lane == 0) sm.sum[wave] = sum;
-  __syncthreads();
+  const uint32_t n = static_cast<uint32_t>(a.n);
+  const uint32_t pair[2] = {key_or_nan(half0), key_or_nan(half1)};
 
-  // Every wave holds all the maxima, eight per lane.
-  constexpr int kHalf = 2 * kChunkThreads / kWave;
-  uint32_t k[kHalf];
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kHalf; ++i) {
-    k[i] = sm.half[i * kWave + lane];
-    top = top > k[i] ? top : k[i];
+  // The n-th largest of some maxima is a lower bound of the chunk's n-th
+  // largest value, and kBoundBits of it suffice to leave few candidates. For
+  // small n each wave finds it of its own 128 and the best of the four counts:
+  // a third of the instructions of a bound over all 512, for some candidates
+  // more.
+  uint32_t T = n <= kWaveBound ? nth_key(pair, n, kBoundBits, kLow) : 0u;
+  uint32_t top = wave_max_u32(pair[0] > pair[1] ? pair[0] : pair[1]);
+  sum = wave_sum_f64(sum);
+  if (lane == 0) {
+    sm.sum[wave] = sum;
+    sm.wave_top[wave] = top;
+    sm.wave_bound[wave] = T;
   }
-  top = wave_max_u32(top);
-  sum = 0.0;
+  // The same over all maxima, which every wave then holds, eight per lane.
+  auto block_nth = [&](int bits) __attribute__((always_inline)) -> uint32_t {
+    sm.half[tid] = pair[0];
+    sm.half[kChunkThreads + tid] = pair[1];
+    __syncthreads();
+    constexpr int kHalf = 2 * kChunkThreads / kWave;
+    uint32_t k[kHalf];
 #pragma unroll
-  for (int w = 0; w < kChunkWaves; ++w) sum += sm.sum[w];
+    for (int i = 0; i < kHalf; ++i) k[i] = sm.half[i * kWave + lane];
+    return nth_key(k, n, bits, kLow);
+  };
+  __syncthreads();
+  sum = 0.0;
+  top = 0u;
+#pragma unroll
+  for (int w = 0; w < kChunkWaves; ++w) {
+    sum += sm.sum[w];
+    top = top > sm.wave_top[w] ? top : sm.wave_top[w];
+    T = T > sm.wave_bound[w] ? T : sm.wave_bound[w];
+  }
   const int64_t slot = row * split.chunks + ch;
   uint64_t* out = lists + slot * a.n;
   if (top >= order_key(INFINITY)) {  // a NaN or +inf: the beam proposes nothing
@@ -302,51 +369,54 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   }
   if (tid == 0) stats[slot] = ChunkStat{sum, ref, 0};
 
-  // The n-th largest of these maxima is a lower bound of the chunk's n-th
-  // largest value: the largest T with at least n maxima >= T, bit by bit.
-  const uint32_t n = static_cast<uint32_t>(a.n);
-  uint32_t T = 0;
-#pragma unroll 1
-  for (int bit = 31; bit >= kLow; --bit) {
-    const uint32_t t = T | (1u << bit);
-    uint32_t c = 0;
-#pragma unroll
-    for (int i = 0; i < kHalf; ++i) c += count_ballot(k[i] >= t);
-    if (c >= n) T = t;
-  }
+  if (T == 0u) T = block_nth(kBoundBits);
   if (T == 0u) T = order_key(-FLT_MAX);  // fewer than n maxima: all finite values
   else if (!(T & 0x80000000u)) T |= (1u << kLow) - 1u;
   const float bound = key_value(T);
 
-  // Pairs of vectors that reach the bound, then their elements.
-  const int units = (layers + kUnit - 1) / kUnit;
-  for (int u = 0; u < units; ++u) {
-    if (sm.top[u][tid] >= bound) {
-      const uint32_t at = atomicAdd(&sm.hits, 1u);
-      if (at < kHits) sm.hit[at] = static_cast<uint16_t>(u * kChunkThreads + tid);
-    }
-  }
   auto push = [&](float x, uint32_t token) __attribute__((always_inline)) {
     const uint32_t at = atomicAdd(&sm.count, 1u);
     if (at < kChunkCap) sm.list[at] = pack(order_key(x), token);
   };
   if (xe >= bound) push(xe, static_cast<uint32_t>(te));
-  __syncthreads();
-  const uint32_t hits = sm.hits;
-  if (hits <= kHits) {
-    for (uint32_t e = tid; e < hits * kUnit; e += kChunkThreads) {
-      const int h = sm.hit[e / kUnit];
-      const int at = ((h / kChunkThreads) * kUnit + static_cast<int>(e % kUnit)) * kChunkThreads + h % kChunkThreads;
-      const vec_t q = again(at);
-      const uint32_t token = static_cast<uint32_t>(first + at * P);
+  uint32_t hits = 0;
+  if constexpr (SHORT) {
 #pragma unroll
-      for (int j = 0; j < P; ++j) {
-        const float x = DT::value(lane_of<raw_t>(q, j));
-        if (x >= bound) push(x, token + j);
+    for (int g = 0; g < kGroup; ++g) {
+      if (tops[g / kUnit] >= bound) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const float x = DT::value(lane_of<raw_t>(next[g], j));
+          if (x >= bound) push(x, static_cast<uint32_t>(first + (g * kChunkThreads + tid) * P + j));
+        }
+      }
+    }
+  } else {
+    // pairs of vectors that reach the bound, then their elements
+    const int units = (layers + kUnit - 1) / kUnit;
+    for (int u = 0; u < units; ++u) {
+      if (sm.top[u][tid] >= bound) {
+        const uint32_t at = atomicAdd(&sm.hits, 1u);
+        if (at < kHits) sm.hit[at] = static_cast<uint16_t>(u * kChunkThreads + tid);
       }
     }
     __syncthreads();
+    hits = sm.hits;
+    if (hits <= kHits) {
+      for (uint32_t e = tid; e < hits * kUnit; e += kChunkThreads) {
+        const int h = sm.hit[e / kUnit];
+        const int at = ((h / kChunkThreads) * kUnit + static_cast<int>(e % kUnit)) * kChunkThreads + h % kChunkThreads;
+        const vec_t q = again(at);
+        const uint32_t token = static_cast<uint32_t>(first + at * P);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          const float x = DT::value(lane_of<raw_t>(q, j));
+          if (x >= bound) push(x, token + j);
+        }
+      }
+    }
   }
+  __syncthreads();
   uint32_t M = sm.count;
 
   if (hits > kHits || M > kChunkCap) {
@@ -368,8 +438,11 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
       block_excl(c, total, sm);
       return total;
     };
-    // first whether the bound itself is that value (fewer than n above it), as
-    // where many are equal; else it is found bit by bit
+    // first whether the n-th largest maximum is that value (fewer than n above
+    // it), as where many are equal; else it is found bit by bit
+    const uint32_t exact = block_nth(32);
+    if (exact != 0) T = exact;
+    if (!(T & 0x80000000u)) T |= (1u << kLow) - 1u;
     const uint32_t bound_key = T;
 #pragma unroll 1
     for (int bit = 32; bit >= kLow; --bit) {
@@ -425,11 +498,17 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     __syncthreads();
   }
 
-  // The candidates are distinct numbers: each one's rank is the count of larger ones.
+  // The candidates are distinct numbers: each one's rank is the count of larger
+  // ones, taken eight at a time so that the reads overlap.
+  if (tid < 8 && M + tid < kChunkCap + 8) sm.list[M + tid] = 0;
+  __syncthreads();
   for (uint32_t e = tid; e < M; e += kChunkThreads) {
     const uint64_t mine = sm.list[e];
     uint32_t r = 0;
-    for (uint32_t j = 0; j < M; ++j) r += sm.list[j] > mine ? 1u : 0u;
+    for (uint32_t j = 0; j < M; j += 8) {
+#pragma unroll
+      for (uint32_t i = 0; i < 8; ++i) r += sm.list[j + i] > mine ? 1u : 0u;
+    }
     if (r < n) out[r] = mine;
   }
   for (uint32_t e = M + tid; e < n; e += kChunkThreads) out[e] = 0;
@@ -445,7 +524,7 @@ __device__ __forceinline__ bool above(const Cand& a, const Cand& b) {
 }
 
 struct MergeSmem {
-  Cand list[kMergeCap];
+  Cand list[kMergeCap + 4];
   uint32_t upper[kMergeCap];  // the candidates' upper halves of hi
   double ref[kMaxBeams];      // L = ref + rest; apart, as ref may be as large as the type goes
   double rest[kMaxBeams];
@@ -456,6 +535,8 @@ struct MergeSmem {
   Cand best[kMergeWaves];
   uint32_t count;
   uint32_t votes[2];
+  uint32_t active[2];               // lists that go on, in two turns
+  uint16_t list_of[2][kMergeLists];
 };
 
 // One beam's L and state out of its chunks, held by all threads that pass the
@@ -597,34 +678,11 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
     }
     sm.heads[tid] = best;
     __syncthreads();
-    uint32_t h[kMergeWaves], top = 0, low = 0xFFFFFFFFu;
+    uint32_t h[kMergeWaves];
 #pragma unroll
-    for (int i = 0; i < kMergeWaves; ++i) {
-      h[i] = sm.heads[i * kWave + lane];
-      top = top > h[i] ? top : h[i];
-      if (h[i] != 0) low = low < h[i] ? low : h[i];
-    }
-    top = wave_max_u32(top);
-    low = wave_min_u32(low);
-    T = top;
-    if (low < top) {
-      int bit = 31 - __builtin_clz(top ^ low);
-      const int stop = bit > kBoundBits ? bit - kBoundBits : 0;
-      T = top & ~((2u << bit) - 1u);
-#pragma unroll 1
-      for (; bit >= stop; --bit) {
-        const uint32_t t = T | (1u << bit);
-        uint32_t c = 0;
-#pragma unroll
-        for (int i = 0; i < kMergeWaves; ++i) c += count_ballot(h[i] >= t);
-        if (c >= n) T = t;
-      }
-    }
-    // fewer than n may reach even that: then every candidate counts
-    uint32_t c = 0;
-#pragma unroll
-    for (int i = 0; i < kMergeWaves; ++i) c += count_ballot(h[i] >= T && h[i] != 0);
-    if (c < n || T == 0u) T = 1u;
+    for (int i = 0; i < kMergeWaves; ++i) h[i] = sm.heads[i * kWave + lane];
+    T = nth_key(h, n, kBoundBits, 0);
+    if (T == 0u) T = 1u;  // fewer than n: every candidate counts
   }
 
   auto push = [&](const Cand& k) __attribute__((always_inline)) -> bool {
@@ -639,22 +697,37 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
   };
   uint32_t M;
   for (int tries = 0;; ++tries) {
-    // candidates from T on: those held, then further windows of entries while
-    // some list's last one still reaches T
-    bool more = false;
+    // Candidates from T on: those held, then, of the lists whose last one still
+    // reaches T, further windows of entries.
+    auto go_on = [&](int turn, uint32_t q) __attribute__((always_inline)) {
+      const uint32_t at = atomicAdd(&sm.active[turn], 1u);
+      if (at < kMergeLists) sm.list_of[turn][at] = static_cast<uint16_t>(q);
+    };
+    if (tid == 0) sm.active[0] = 0;
+    __syncthreads();
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
       const uint32_t f = u * kMergeThreads + tid;
-      if (push(first[u])) more |= f % wide == wide - 1;
+      if (push(first[u]) && f % wide == wide - 1) go_on(0, f / wide);
     }
-    for (uint32_t q = room + tid; q < nl; q += kMergeThreads) more |= push(fetch(q, 0));
-    for (uint32_t j0 = wide; __syncthreads_or(more) && j0 < n; j0 += wide) {
-      more = false;
-      const uint32_t w = n - j0 < wide ? n - j0 : wide;
-      for (uint32_t f = tid; f < nl * w; f += kMergeThreads) {
-        const uint32_t j = f % w;
-        if (push(fetch(f / w, j0 + j))) more |= j == w - 1;
+    for (uint32_t q = room + tid; q < nl; q += kMergeThreads)
+      if (push(fetch(q, 0))) go_on(0, q);
+    int turn = 0;
+    for (uint32_t j0 = wide; j0 < n; turn ^= 1) {
+      if (tid == 0) sm.active[turn ^ 1] = 0;
+      __syncthreads();
+      const uint32_t active = sm.active[turn];
+      if (active == 0) break;
+      const bool noted = active <= kMergeLists;
+      const uint32_t lists_now = noted ? active : nl;
+      uint32_t w = lists_now < room ? room / lists_now : 1u;
+      w = w < n - j0 ? w : n - j0;
+      for (uint32_t f = tid; f < lists_now * w; f += kMergeThreads) {
+        const uint32_t q = noted ? sm.list_of[turn][f / w] : f / w, j = f % w;
+        if (push(fetch(q, j0 + j)) && j == w - 1) go_on(turn ^ 1, q);
       }
+      __syncthreads();
+      j0 += w;
     }
     __syncthreads();
     M = sm.count;
@@ -715,15 +788,45 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
     __syncthreads();
   }
 
-  // Ranks by counting; decode and write.
+  // A long list is cut to what reaches the n-th of its upper halves.
+  if (M > kLongList) {
+    constexpr int kPer = kMergeCap / kWave;
+    uint32_t h[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const uint32_t e = i * kWave + lane;
+      h[i] = e < M ? sm.upper[e] : 0u;
+    }
+    const uint32_t cut = nth_key(h, n, 32, 0);
+    Cand mine[kMergeCap / kMergeThreads];
+#pragma unroll
+    for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
+      const uint32_t e = u * kMergeThreads + tid;
+      mine[u] = e < M ? sm.list[e] : Cand{0, 0};
+    }
+    __syncthreads();
+    if (tid == 0) sm.count = 0;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
+      if (mine[u].hi != 0 && static_cast<uint32_t>(mine[u].hi >> 32) >= cut) {
+        const uint32_t at = atomicAdd(&sm.count, 1u);
+        sm.list[at] = mine[u];
+      }
+    }
+    __syncthreads();
+    M = sm.count;
+  }
+
+  // Ranks by counting, four at a time so that the reads overlap. Decode and write.
+  if (tid < 4) sm.list[M + tid] = Cand{0, 0};
+  __syncthreads();
   for (uint32_t e = tid; e < M; e += kMergeThreads) {
-    const uint32_t h = sm.upper[e];
     const Cand k = sm.list[e];
     uint32_t r = 0;
-    for (uint32_t j = 0; j < M; ++j) {
-      const uint32_t o = sm.upper[j];
-      r += o > h ? 1u : 0u;
-      if (o == h && j != e) r += above(sm.list[j], k) ? 1u : 0u;
+    for (uint32_t j = 0; j < M; j += 4) {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) r += above(sm.list[j + i], k) ? 1u : 0u;
     }
     if (r < n) {
       const int b = kMaxBeams - 1 - static_cast<int>(k.lo >> (32 + kTokenBits));
@@ -751,8 +854,12 @@ template <class DT>
 void launch_chunks(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t items, ChunkStat* stats,
                    uint64_t* lists, hipStream_t stream) {
   const unsigned blocks = static_cast<unsigned>(items * a.K * s.chunks);
-  hipLaunchKernelGGL(beam_chunk_kernel<DT>, dim3(blocks), dim3(kChunkThreads), 0, stream, a, s, item0 * a.K, stats,
-                     lists);
+  if (s.vecs <= kGroup * kChunkThreads)
+    hipLaunchKernelGGL((beam_chunk_kernel<DT, true>), dim3(blocks), dim3(kChunkThreads), 0, stream, a, s, item0 * a.K,
+                       stats, lists);
+  else
+    hipLaunchKernelGGL((beam_chunk_kernel<DT, false>), dim3(blocks), dim3(kChunkThreads), 0, stream, a, s,
+                       item0 * a.K, stats, lists);
 }
 
 }  // namespace
