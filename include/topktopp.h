@@ -311,9 +311,11 @@ topktopp_status top_k_top_p_sorted_survivors(const void* logits, topktopp_dtype 
  * nothing above -inf. Ranks without a continuation hold score -inf, parent
  * -1 and token -1.
  *
- * Numerics. Sums and scores are formed in 64 bits (relative error of a sum
- * below 1e-10) and rounded once, to out_scores; order follows the 64-bit
- * values. Results are deterministic.
+ * Numerics. A sum of exp has a relative error below 3.6e-7, what follows is
+ * formed in 64 bits and rounded once, to out_scores. Where two beams'
+ * continuations come closer than that error, their sums are formed again in
+ * 64 bits (relative error below 1e-10), so the order is that of 64-bit values.
+ * Results are deterministic.
  *
  * Errors: ERR_NULLPTR for logits (unless V is 0), scores, an output or the
  * workspace NULL; ERR_INVALID for a dtype, N < 0, K outside

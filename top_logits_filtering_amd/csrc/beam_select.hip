@@ -11,13 +11,15 @@
 //   2. beam_merge_kernel, one workgroup per prompt, joins the chunks' sums to
 //      L[b] and picks the n best of all lists.
 //
-// L[b] is formed in 64 bits: parents and tokens are whole numbers whose order
-// between beams hangs on c[b] - L[b], and an error of fp32's size (1e-7)
-// would swap candidates that lie as close. FP64 vector instructions run at
-// the rate of unpacked FP32 ones on gfx950, so exp costs the same chain of
-// multiply-adds either way: exp(x) = 2^k exp(f), k = rint(x / ln 2),
-// |f| <= ln 2 / 2, and exp(f) is a polynomial of degree 7, found by Remez
-// exchange for the smallest relative error (4.0e-11).
+// Parents and tokens are whole numbers whose order between beams hangs on
+// c[b] - L[b]. The chunks' sums use the hardware's exp2 with a correction for
+// the rounding of its argument, 7 instructions an element, and are within
+// kSumError of the exact ones; where candidates of two beams come so close that
+// this could swap them, the merge sums those beams' rows again in 64 bits. So
+// the order is that of 64-bit values at the price of 32-bit ones: a sum in 64
+// bits throughout (16 instructions an element) took 30 us instead of 20 for
+// 256 rows of 151936 bf16 logits, and 110 instead of 89 for 1024 rows of
+// 128256 fp32 ones.
 
 #include <float.h>
 
@@ -36,10 +38,7 @@ constexpr int kLayers = 32;       // vectors per thread at most
 constexpr int kUnit = 2;          // vectors that share one maximum
 constexpr int kGroup = 4;         // vectors loaded ahead
 constexpr int kHits = 2048;       // pairs of vectors looked at again
-#ifndef TB
-#define TB 1024
-#endif
-constexpr int kTargetBlocks = TB;
+constexpr int kTargetBlocks = 1024;
 constexpr int kMergeThreads = 512;
 constexpr int kMergeCap = 2048;   // candidate slots of a prompt
 constexpr int kMergeWaves = kMergeThreads / kWave;
@@ -48,11 +47,12 @@ constexpr uint32_t kAllRanked = 48;  // so many candidates are ranked without a 
 constexpr uint32_t kLongList = 96;      // a list is cut before it is ranked if it is longer
 constexpr uint32_t kMergeLists = 1024;  // lists noted as going on
 constexpr int kMaxBeams = 128;
+constexpr int kMaxCandidates = 256;
 constexpr int kTokenBits = 20;
 
 // sum exp(x - ref) over a chunk; bad: a NaN or +inf was among the logits.
 struct ChunkStat {
-  double sum;
+  double sum;  // within kSumError
   float ref;
   int bad;
 };
@@ -102,21 +102,34 @@ __device__ __forceinline__ double exp64(double y) {
 }
 
 // The chunks' sums are taken of exp(x) itself while the chunk's maximum lies
-// in [kLowMax, kHighMax], which no logit of a model leaves: then no maximum is
-// needed before the sum. Terms are clamped to +-kHighMax, so 2^15 of them stay
-// finite and what the clamp adds (exp(-650), also for -inf) is below 2^-140 of
-// the largest. Other chunks are read and summed again, less their maximum.
-constexpr float kHighMax = 650.0f;
-constexpr float kLowMax = -550.0f;
+// in [kLowMax, kHighMax], which a model's logits do: then no maximum is needed
+// before the sum. Other chunks are read and summed again in 64 bits, less their
+// maximum.
+constexpr float kHighMax = 80.0f;  // eight terms of exp(80) stay finite
+constexpr float kLowMax = -40.0f;  // terms that fp32 flushes are below 2^-68 of the largest
 
-__device__ __forceinline__ double exp_term(float x) {
-  return exp64(static_cast<double>(__builtin_amdgcn_fmed3f(x, -kHighMax, kHighMax)));
+// A part of exp(x) = 2^t * 2^lo, t = x log2(e) rounded and lo what that lost:
+// returns 2^t and adds lo * 2^t to `rest`, which counts times ln 2.
+__device__ __forceinline__ float exp_parts(float x, float& rest) {
+  constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.925963033500e-8f;
+  const float xc = __builtin_amdgcn_fmed3f(x, -104.0f, 104.0f);  // finite, also for -inf
+  const float t = xc * kLog2e;
+  const float lo = __builtin_fmaf(xc, kLog2eLow, __builtin_fmaf(xc, kLog2e, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  rest = __builtin_fmaf(e, lo, rest);
+  return e;
 }
 
-// exp(x - ref) for x <= ref, both finite, or x = -inf.
+// Relative error of a chunk's sum: 8.5e-8 of exp2 (the most over all arguments
+// in +-[2^-10, 120), measured), three additions and a multiply-add in fp32 at
+// 2^-24 each, and less than 1e-10 of what follows in 64 bits.
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr double kSumError = 3.5e-7;
+
+// exp(x - ref) for x - ref below 700, or x = -inf.
 __device__ __forceinline__ double exp_below(float x, float ref) {
   const double y = static_cast<double>(x) - static_cast<double>(ref);
-  return y < -kHighMax ? 0.0 : exp64(y);
+  return y < -700.0 ? 0.0 : exp64(y);
 }
 
 // Key bits that tell this dtype's values apart; the bits below them are all
@@ -264,17 +277,21 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     }
 #pragma unroll
     for (int g = 0; g < kGroup; ++g) {
-      __builtin_amdgcn_sched_barrier(0);  // one vector's terms at a time, or their 64-bit values fill the registers
-      double part = 0.0;
       float m = g % kUnit == 0 ? -INFINITY : tops[g / kUnit];
+      float e[P], rest = 0.0f;
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         const float x = DT::value(lane_of<raw_t>(now[g], j));
-        part += exp_term(x);
+        e[j] = exp_parts(x, rest);
         m = __builtin_elementwise_maximum(m, x);
       }
       tops[g / kUnit] = m;
-      sum += part;
+#pragma unroll
+      for (int d = 1; d < P; d *= 2) {
+#pragma unroll
+        for (int j = 0; j < P; j += 2 * d) e[j] += e[j + d];
+      }
+      sum += static_cast<double>(__builtin_fmaf(rest, kLn2, e[0]));
     }
     half0 = __builtin_elementwise_maximum(half0, tops[0]);
     half1 = __builtin_elementwise_maximum(half1, tops[1]);
@@ -297,7 +314,11 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     }
   }
   const float xe = DT::value(re);
-  sum += exp_term(xe);
+  {
+    float rest = 0.0f;
+    const float e = exp_parts(xe, rest);
+    sum += static_cast<double>(__builtin_fmaf(rest, kLn2, e));
+  }
   half0 = __builtin_elementwise_maximum(half0, xe);
 
   // Keys of NaN lie above +inf's: positive ones by order_key, negative ones by this.
@@ -519,18 +540,24 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
 struct Cand {
   uint64_t hi, lo;
 };
+__device__ __forceinline__ int beam_of(const Cand& k) {
+  return kMaxBeams - 1 - static_cast<int>(k.lo >> (32 + kTokenBits));
+}
 __device__ __forceinline__ bool above(const Cand& a, const Cand& b) {
   return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
 }
 
 struct MergeSmem {
   Cand list[kMergeCap + 4];
+  Cand sorted[kMaxCandidates + 2];  // the first n + 1
   uint32_t upper[kMergeCap];  // the candidates' upper halves of hi
   double ref[kMaxBeams];      // L = ref + rest; apart, as ref may be as large as the type goes
   double rest[kMaxBeams];
   double score[kMaxBeams];
   double weight[kMaxBeams];
   int state[kMaxBeams];       // 0: proposes nothing, 1: its lists, 2: finished
+  int close[kMaxBeams];       // 1: a candidate comes too close to another beam's, 2: summed in 64 bits
+  double part[kMergeWaves];
   uint32_t heads[kMergeThreads];
   Cand best[kMergeWaves];
   uint32_t count;
@@ -581,6 +608,44 @@ __device__ __forceinline__ void beam_total(const ChunkStat* __restrict__ s, int 
   }
 }
 
+// sum exp(x - ref) over a whole row in 64 bits, by all threads.
+template <class DT>
+__device__ double row_sum(const BeamSelectArgs& a, int64_t row, float ref, MergeSmem& sm) {
+  using raw_t = typename DT::raw_t;
+  constexpr int P = DT::kPerVec;
+  const int tid = threadIdx.x;
+  const raw_t* rowp = static_cast<const raw_t*>(a.logits) + row * a.ld;
+  int head = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(rowp) & 15u)) & 15u) / static_cast<int>(sizeof(raw_t));
+  head = head < a.V ? head : a.V;
+  const int nfull = (a.V - head) / P;
+  double sum = 0.0;
+  for (int i = tid; i < head; i += kMergeThreads) sum += exp_below(DT::value(rowp[i]), ref);
+  for (int i = head + nfull * P + tid; i < a.V; i += kMergeThreads) sum += exp_below(DT::value(rowp[i]), ref);
+  const vec_t* v = reinterpret_cast<const vec_t*>(rowp + head);
+  for (int i = tid; i < nfull; i += kMergeThreads) {
+    const vec_t q = v[i];
+#pragma unroll 1  // seldom run: kept small in registers
+    for (int j = 0; j < P; ++j) sum += exp_below(DT::value(lane_of_dyn<raw_t>(q, j)), ref);
+  }
+  sum = wave_sum_f64(sum);
+  __syncthreads();
+  if (tid % kWave == 0) sm.part[tid / kWave] = sum;
+  __syncthreads();
+  sum = 0.0;
+#pragma unroll
+  for (int w = 0; w < kMergeWaves; ++w) sum += sm.part[w];
+  return sum;
+}
+
+// The upper half of the image of a rank value by `margin` below T's.
+__device__ __forceinline__ uint32_t lowered(uint32_t T, double margin) {
+  const uint64_t u = static_cast<uint64_t>(T) << 32;
+  const uint64_t bits = (u >> 63) ? u & 0x7FFFFFFFFFFFFFFFull : ~u;
+  const uint32_t t = static_cast<uint32_t>(order_key64(__builtin_bit_cast(double, bits) - margin) >> 32);
+  return t < T && t > 0u ? t : T;
+}
+
+template <class DT>
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArgs a, int C, int64_t item0,
                                                                    const ChunkStat* __restrict__ stats,
                                                                    const uint64_t* __restrict__ lists) {
@@ -637,7 +702,17 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
     sm.weight[tid] = w;
     sm.state[tid] = state;
   }
+  if (tid < K) sm.close[tid] = 0;
   __syncthreads();
+
+  // Ranks of two beams may be off against each other by this.
+  double margin = 2.0 * kSumError;
+  if (a.weights != nullptr) {
+    uint32_t most = 0;
+    for (int b = lane; b < K; b += kWave)
+      if (sm.state[b] != 0) most = most > __float_as_uint(sm.weight[b]) ? most : __float_as_uint(sm.weight[b]);
+    margin *= __uint_as_float(wave_max_u32(most));
+  }
 
   // Entry j of list q, e, as a candidate; hi is 0 where there is none.
   auto cand = [&](uint64_t e, uint32_t q, uint32_t j) __attribute__((always_inline)) -> Cand {
@@ -654,212 +729,247 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
   };
   auto fetch = [&](uint32_t q, uint32_t j) __attribute__((always_inline)) -> Cand { return cand(mine[q * n + j], q, j); };
 
-  Cand first[kHeld];
-#pragma unroll
-  for (int u = 0; u < kHeld; ++u) {
-    const uint32_t f = u * kMergeThreads + tid;
-    first[u] = f < nl * wide ? cand(held[u], f / wide, f % wide) : Cand{0, 0};
-  }
-
-  // A bound on the n-th candidate: the largest T (of the ranks' upper halves)
-  // that n of the threads' best reach; its low bits are left open. Few
-  // candidates need none.
-  uint32_t T = 1u;
-  if (nl * n > kAllRanked) {
-    uint32_t best = 0;
-#pragma unroll
-    for (int u = 0; u < kHeld; ++u) {
-      const uint32_t h = static_cast<uint32_t>(first[u].hi >> 32);
-      best = best > h ? best : h;
-    }
-    for (uint32_t q = room + tid; q < nl; q += kMergeThreads) {  // more lists than are held (wide is 1)
-      const uint32_t h = static_cast<uint32_t>(fetch(q, 0).hi >> 32);
-      best = best > h ? best : h;
-    }
-    sm.heads[tid] = best;
-    __syncthreads();
-    uint32_t h[kMergeWaves];
-#pragma unroll
-    for (int i = 0; i < kMergeWaves; ++i) h[i] = sm.heads[i * kWave + lane];
-    T = nth_key(h, n, kBoundBits, 0);
-    if (T == 0u) T = 1u;  // fewer than n: every candidate counts
-  }
-
-  auto push = [&](const Cand& k) __attribute__((always_inline)) -> bool {
-    const uint32_t h = static_cast<uint32_t>(k.hi >> 32);
-    if (h < T) return false;
-    const uint32_t at = atomicAdd(&sm.count, 1u);
-    if (at < kMergeCap) {
-      sm.list[at] = k;
-      sm.upper[at] = h;
-    }
-    return true;
-  };
+  // Once with the chunks' sums; and, if candidates come too close, once more.
   uint32_t M;
-  for (int tries = 0;; ++tries) {
-    // Candidates from T on: those held, then, of the lists whose last one still
-    // reaches T, further windows of entries.
-    auto go_on = [&](int turn, uint32_t q) __attribute__((always_inline)) {
-      const uint32_t at = atomicAdd(&sm.active[turn], 1u);
-      if (at < kMergeLists) sm.list_of[turn][at] = static_cast<uint16_t>(q);
-    };
-    if (tid == 0) sm.active[0] = 0;
-    __syncthreads();
+  for (bool last = false;; last = true) {
+    Cand first[kHeld];
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
       const uint32_t f = u * kMergeThreads + tid;
-      if (push(first[u]) && f % wide == wide - 1) go_on(0, f / wide);
+      first[u] = f < nl * wide ? cand(held[u], f / wide, f % wide) : Cand{0, 0};
     }
-    for (uint32_t q = room + tid; q < nl; q += kMergeThreads)
-      if (push(fetch(q, 0))) go_on(0, q);
-    int turn = 0;
-    for (uint32_t j0 = wide; j0 < n; turn ^= 1) {
-      if (tid == 0) sm.active[turn ^ 1] = 0;
+
+    // A bound on the n-th candidate: the largest T (of the ranks' upper halves)
+    // that n of the threads' best reach; its low bits are left open. Few
+    // candidates need none.
+    uint32_t T = 1u;
+    if (nl * n > kAllRanked) {
+      uint32_t best = 0;
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        const uint32_t h = static_cast<uint32_t>(first[u].hi >> 32);
+        best = best > h ? best : h;
+      }
+      for (uint32_t q = room + tid; q < nl; q += kMergeThreads) {  // more lists than are held (wide is 1)
+        const uint32_t h = static_cast<uint32_t>(fetch(q, 0).hi >> 32);
+        best = best > h ? best : h;
+      }
+      sm.heads[tid] = best;
       __syncthreads();
-      const uint32_t active = sm.active[turn];
-      if (active == 0) break;
-      const bool noted = active <= kMergeLists;
-      const uint32_t lists_now = noted ? active : nl;
-      uint32_t w = lists_now < room ? room / lists_now : 1u;
-      w = w < n - j0 ? w : n - j0;
-      for (uint32_t f = tid; f < lists_now * w; f += kMergeThreads) {
-        const uint32_t q = noted ? sm.list_of[turn][f / w] : f / w, j = f % w;
-        if (push(fetch(q, j0 + j)) && j == w - 1) go_on(turn ^ 1, q);
+      uint32_t h[kMergeWaves];
+#pragma unroll
+      for (int i = 0; i < kMergeWaves; ++i) h[i] = sm.heads[i * kWave + lane];
+      T = nth_key(h, n, kBoundBits, 0);
+      T = T == 0u ? 1u : lowered(T, margin);  // fewer than n: every candidate counts
+    }
+
+    auto push = [&](const Cand& k) __attribute__((always_inline)) -> bool {
+      const uint32_t h = static_cast<uint32_t>(k.hi >> 32);
+      if (h < T) return false;
+      const uint32_t at = atomicAdd(&sm.count, 1u);
+      if (at < kMergeCap) {
+        sm.list[at] = k;
+        sm.upper[at] = h;
+      }
+      return true;
+    };
+    for (int tries = 0;; ++tries) {
+      // Candidates from T on: those held, then, of the lists whose last one still
+      // reaches T, further windows of entries.
+      auto go_on = [&](int turn, uint32_t q) __attribute__((always_inline)) {
+        const uint32_t at = atomicAdd(&sm.active[turn], 1u);
+        if (at < kMergeLists) sm.list_of[turn][at] = static_cast<uint16_t>(q);
+      };
+      if (tid == 0) sm.active[0] = 0;
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kHeld; ++u) {
+        const uint32_t f = u * kMergeThreads + tid;
+        if (push(first[u]) && f % wide == wide - 1) go_on(0, f / wide);
+      }
+      for (uint32_t q = room + tid; q < nl; q += kMergeThreads)
+        if (push(fetch(q, 0))) go_on(0, q);
+      int turn = 0;
+      for (uint32_t j0 = wide; j0 < n; turn ^= 1) {
+        if (tid == 0) sm.active[turn ^ 1] = 0;
+        __syncthreads();
+        const uint32_t active = sm.active[turn];
+        if (active == 0) break;
+        const bool noted = active <= kMergeLists;
+        const uint32_t lists_now = noted ? active : nl;
+        uint32_t w = lists_now < room ? room / lists_now : 1u;
+        w = w < n - j0 ? w : n - j0;
+        for (uint32_t f = tid; f < lists_now * w; f += kMergeThreads) {
+          const uint32_t q = noted ? sm.list_of[turn][f / w] : f / w, j = f % w;
+          if (push(fetch(q, j0 + j)) && j == w - 1) go_on(turn ^ 1, q);
+        }
+        __syncthreads();
+        j0 += w;
       }
       __syncthreads();
-      j0 += w;
-    }
-    __syncthreads();
-    M = sm.count;
-    if (M <= kMergeCap || tries == 4) break;
-    // The list is full: the n-th best of what it holds is a better bound.
-    uint32_t better = 0;
+      M = sm.count;
+      if (M <= kMergeCap || tries == 4) break;
+      // The list is full: the n-th best of what it holds is a better bound.
+      uint32_t better = 0;
 #pragma unroll 1
-    for (int bit = 31; bit >= 0; --bit) {
-      const uint32_t t = better | (1u << bit);
-      uint32_t c = 0;
-      if (tid == 0) sm.votes[bit & 1] = 0;
+      for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t t = better | (1u << bit);
+        uint32_t c = 0;
+        if (tid == 0) sm.votes[bit & 1] = 0;
+        __syncthreads();
+        for (uint32_t e = tid; e < kMergeCap; e += kMergeThreads) c += sm.upper[e] >= t ? 1u : 0u;
+        c = wave_sum_u32(c);
+        if (lane == 0) atomicAdd(&sm.votes[bit & 1], c);
+        __syncthreads();
+        if (sm.votes[bit & 1] >= n) better = t;
+      }
+      better = lowered(better, margin);
+      if (better <= T) break;  // that many are equal there
+      T = better;
       __syncthreads();
-      for (uint32_t e = tid; e < kMergeCap; e += kMergeThreads) c += sm.upper[e] >= t ? 1u : 0u;
-      c = wave_sum_u32(c);
-      if (lane == 0) atomicAdd(&sm.votes[bit & 1], c);
+      if (tid == 0) sm.count = 0;
       __syncthreads();
-      if (sm.votes[bit & 1] >= n) better = t;
     }
-    if (better <= T) break;  // that many are equal there
-    T = better;
+
+    if (M > kMergeCap) {
+      // More candidates share an upper half than the list holds: take the best
+      // ones one by one, each the largest below the last.
+      __syncthreads();
+      Cand prev{~0ull, ~0ull};
+      uint32_t r = 0;
+      for (; r <= n; ++r) {
+        Cand best{0, 0};
+        for (uint32_t f = tid; f < n * nl; f += kMergeThreads) {
+          const Cand k = fetch(f / n, f % n);
+          if (above(prev, k) && above(k, best)) best = k;
+        }
+#pragma unroll
+        for (int d = 1; d < kWave; d *= 2) {
+          const Cand o{__shfl_xor(best.hi, d), __shfl_xor(best.lo, d)};
+          if (above(o, best)) best = o;
+        }
+        __syncthreads();
+        if (lane == 0) sm.best[wave] = best;
+        __syncthreads();
+        best = sm.best[0];
+#pragma unroll
+        for (int w = 1; w < kMergeWaves; ++w)
+          if (above(sm.best[w], best)) best = sm.best[w];
+        if (best.hi == 0) break;
+        if (tid == 0) {
+          sm.list[r] = best;
+          sm.upper[r] = static_cast<uint32_t>(best.hi >> 32);
+        }
+        prev = best;
+      }
+      M = r;
+      __syncthreads();
+    }
+
+    // A long list is cut to what reaches the n-th of its upper halves.
+    if (M > kLongList) {
+      constexpr int kPer = kMergeCap / kWave;
+      uint32_t h[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const uint32_t e = i * kWave + lane;
+        h[i] = e < M ? sm.upper[e] : 0u;
+      }
+      const uint32_t cut = lowered(nth_key(h, n, 32, 0), margin);
+      Cand mine[kMergeCap / kMergeThreads];
+#pragma unroll
+      for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
+        const uint32_t e = u * kMergeThreads + tid;
+        mine[u] = e < M ? sm.list[e] : Cand{0, 0};
+      }
+      __syncthreads();
+      if (tid == 0) sm.count = 0;
+      __syncthreads();
+#pragma unroll
+      for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
+        if (mine[u].hi != 0 && static_cast<uint32_t>(mine[u].hi >> 32) >= cut) {
+          const uint32_t at = atomicAdd(&sm.count, 1u);
+          sm.list[at] = mine[u];
+        }
+      }
+      __syncthreads();
+      M = sm.count;
+    }
+
+    // Ranks by counting, four at a time so that the reads overlap. Decode and write.
+    if (tid < 4) sm.list[M + tid] = Cand{0, 0};
     __syncthreads();
+    for (uint32_t e = tid; e < M; e += kMergeThreads) {
+      const Cand k = sm.list[e];
+      uint32_t r = 0;
+      for (uint32_t j = 0; j < M; j += 4) {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) r += above(sm.list[j + i], k) ? 1u : 0u;
+      }
+      if (r <= n) sm.sorted[r] = k;
+    }
+    __syncthreads();
+    if (last) break;
+
+    // Neighbours of different beams that lie closer than the sums are exact
+    // (equal ones are beams alike): those beams' sums are formed again.
+    auto value = [](const Cand& k) -> double {
+      return __builtin_bit_cast(double, (k.hi >> 63) ? k.hi & 0x7FFFFFFFFFFFFFFFull : ~k.hi);
+    };
+    bool again = false;
+    if (static_cast<uint32_t>(tid) < n && static_cast<uint32_t>(tid) + 1u < M) {
+      const Cand p = sm.sorted[tid], q = sm.sorted[tid + 1];
+      const int bp = beam_of(p), bq = beam_of(q);
+      if (bp != bq && p.hi != q.hi && value(p) - value(q) <= margin) {
+        again = sm.state[bp] == 1 || sm.state[bq] == 1;
+        sm.close[bp] = sm.close[bq] = 1;
+      }
+    }
+    if (!__syncthreads_or(again)) break;
+    for (int b = 0; b < K; ++b) {
+      if (sm.close[b] == 0 || sm.state[b] != 1) continue;
+      const double sum = row_sum<DT>(a, item * K + b, static_cast<float>(sm.ref[b]), sm);
+      if (tid == 0) sm.rest[b] = log(sum);
+    }
     if (tid == 0) sm.count = 0;
     __syncthreads();
   }
 
-  if (M > kMergeCap) {
-    // More candidates share an upper half than the list holds: take the best
-    // ones one by one, each the largest below the last.
-    __syncthreads();
-    Cand last{~0ull, ~0ull};
-    uint32_t r = 0;
-    for (; r < n; ++r) {
-      Cand best{0, 0};
-      for (uint32_t f = tid; f < n * nl; f += kMergeThreads) {
-        const Cand k = fetch(f / n, f % n);
-        if (above(last, k) && above(k, best)) best = k;
-      }
-#pragma unroll
-      for (int d = 1; d < kWave; d *= 2) {
-        const Cand o{__shfl_xor(best.hi, d), __shfl_xor(best.lo, d)};
-        if (above(o, best)) best = o;
-      }
-      __syncthreads();
-      if (lane == 0) sm.best[wave] = best;
-      __syncthreads();
-      best = sm.best[0];
-#pragma unroll
-      for (int w = 1; w < kMergeWaves; ++w)
-        if (above(sm.best[w], best)) best = sm.best[w];
-      if (best.hi == 0) break;
-      if (tid == 0) {
-        sm.list[r] = best;
-        sm.upper[r] = static_cast<uint32_t>(best.hi >> 32);
-      }
-      last = best;
-    }
-    M = r;
-    __syncthreads();
-  }
-
-  // A long list is cut to what reaches the n-th of its upper halves.
-  if (M > kLongList) {
-    constexpr int kPer = kMergeCap / kWave;
-    uint32_t h[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const uint32_t e = i * kWave + lane;
-      h[i] = e < M ? sm.upper[e] : 0u;
-    }
-    const uint32_t cut = nth_key(h, n, 32, 0);
-    Cand mine[kMergeCap / kMergeThreads];
-#pragma unroll
-    for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
-      const uint32_t e = u * kMergeThreads + tid;
-      mine[u] = e < M ? sm.list[e] : Cand{0, 0};
-    }
-    __syncthreads();
-    if (tid == 0) sm.count = 0;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
-      if (mine[u].hi != 0 && static_cast<uint32_t>(mine[u].hi >> 32) >= cut) {
-        const uint32_t at = atomicAdd(&sm.count, 1u);
-        sm.list[at] = mine[u];
-      }
-    }
-    __syncthreads();
-    M = sm.count;
-  }
-
-  // Ranks by counting, four at a time so that the reads overlap. Decode and write.
-  if (tid < 4) sm.list[M + tid] = Cand{0, 0};
-  __syncthreads();
-  for (uint32_t e = tid; e < M; e += kMergeThreads) {
-    const Cand k = sm.list[e];
-    uint32_t r = 0;
-    for (uint32_t j = 0; j < M; j += 4) {
-#pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) r += above(sm.list[j + i], k) ? 1u : 0u;
-    }
-    if (r < n) {
-      const int b = kMaxBeams - 1 - static_cast<int>(k.lo >> (32 + kTokenBits));
+  if (tid < static_cast<int>(n)) {
+    const int64_t o = item * n + tid;
+    if (static_cast<uint32_t>(tid) < M) {
+      const Cand k = sm.sorted[tid];
+      const int b = beam_of(k);
       double s = sm.score[b];
       int32_t token = a.end_token;
       if (sm.state[b] == 1) {
         s += (static_cast<double>(key_value(static_cast<uint32_t>(k.lo >> kTokenBits))) - sm.ref[b]) - sm.rest[b];
         token = static_cast<int32_t>(((1u << kTokenBits) - 1u) - (static_cast<uint32_t>(k.lo) & ((1u << kTokenBits) - 1u)));
       }
-      const int64_t o = item * n + r;
       a.out_scores[o] = static_cast<float>(s);
       a.out_parents[o] = b;
       a.out_tokens[o] = token;
+    } else {
+      a.out_scores[o] = -INFINITY;
+      a.out_parents[o] = -1;
+      a.out_tokens[o] = -1;
     }
-  }
-  for (uint32_t e = M + tid; e < n; e += kMergeThreads) {
-    const int64_t o = item * n + e;
-    a.out_scores[o] = -INFINITY;
-    a.out_parents[o] = -1;
-    a.out_tokens[o] = -1;
   }
 }
 
 template <class DT>
-void launch_chunks(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t items, ChunkStat* stats,
+void launch_both(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t items, ChunkStat* stats,
                    uint64_t* lists, hipStream_t stream) {
   const unsigned blocks = static_cast<unsigned>(items * a.K * s.chunks);
+  // few layers: they stay in registers
   if (s.vecs <= kGroup * kChunkThreads)
     hipLaunchKernelGGL((beam_chunk_kernel<DT, true>), dim3(blocks), dim3(kChunkThreads), 0, stream, a, s, item0 * a.K,
                        stats, lists);
   else
     hipLaunchKernelGGL((beam_chunk_kernel<DT, false>), dim3(blocks), dim3(kChunkThreads), 0, stream, a, s,
                        item0 * a.K, stats, lists);
+  hipLaunchKernelGGL(beam_merge_kernel<DT>, dim3(static_cast<unsigned>(items)), dim3(kMergeThreads), 0, stream, a,
+                     s.chunks, item0, stats, lists);
 }
 
 }  // namespace
@@ -892,11 +1002,9 @@ hipError_t launch_beam_select(int dtype, const BeamSelectArgs& a, hipStream_t st
   const int64_t step = (int64_t{1} << 22) / (static_cast<int64_t>(a.K) * s.chunks);
   for (int64_t i = 0; i < a.N; i += step) {
     const int64_t items = a.N - i < step ? a.N - i : step;
-    if (dtype == 0) launch_chunks<F32T>(a, s, i, items, stats, lists, stream);
-    else if (dtype == 1) launch_chunks<F16T>(a, s, i, items, stats, lists, stream);
-    else launch_chunks<BF16T>(a, s, i, items, stats, lists, stream);
-    hipLaunchKernelGGL(beam_merge_kernel, dim3(static_cast<unsigned>(items)), dim3(kMergeThreads), 0, stream, a,
-                       s.chunks, i, stats, lists);
+    if (dtype == 0) launch_both<F32T>(a, s, i, items, stats, lists, stream);
+    else if (dtype == 1) launch_both<F16T>(a, s, i, items, stats, lists, stream);
+    else launch_both<BF16T>(a, s, i, items, stats, lists, stream);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
