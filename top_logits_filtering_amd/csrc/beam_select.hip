@@ -43,6 +43,9 @@ constexpr int kMergeThreads = 512;
 constexpr int kMergeCap = 2048;   // candidate slots of a prompt
 constexpr int kMergeWaves = kMergeThreads / kWave;
 constexpr uint32_t kWaveBound = 16;  // up to so many candidates per chunk a wave's bound is taken
+constexpr uint32_t kMergeWaveBound = 32;  // the same in the merge
+constexpr int kHeld = 4;                  // list entries a thread of the merge holds from the start
+constexpr uint32_t kRoom = kHeld * kMergeThreads;
 constexpr uint32_t kAllRanked = 48;  // so many candidates are ranked without a bound
 constexpr uint32_t kLongList = 96;      // a list is cut before it is ranked if it is longer
 constexpr uint32_t kMergeLists = 1024;  // lists noted as going on
@@ -646,31 +649,30 @@ __device__ __forceinline__ uint32_t lowered(uint32_t T, double margin) {
 }
 
 template <class DT>
-__global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArgs a, int C, int64_t item0,
-                                                                   const ChunkStat* __restrict__ stats,
+__global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArgs a, Div chunks, Div window,
+                                                                   int64_t item0, const ChunkStat* __restrict__ stats,
                                                                    const uint64_t* __restrict__ lists) {
   __shared__ MergeSmem sm;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int64_t item = item0 + blockIdx.x;
   const int K = a.K;
   const uint32_t n = static_cast<uint32_t>(a.n);
+  const int C = static_cast<int>(chunks.d);
   const uint32_t nl = static_cast<uint32_t>(K * C);  // lists of this prompt
   const uint64_t* __restrict__ mine = lists + item * nl * n;
 
   // The first entries of every list, `wide` of each, are under way while L is
   // formed. (Lists of beams that propose nothing hold anything; they are not used.)
-  constexpr int kHeld = 4;
-  const uint32_t room = kHeld * kMergeThreads;
-  uint32_t wide = nl < room ? room / nl : 1u;
-  wide = wide < n ? wide : n;
+  const uint32_t wide = window.d, heldn = nl * wide < kRoom ? nl * wide : kRoom;
   uint64_t held[kHeld];
 #pragma unroll
   for (int u = 0; u < kHeld; ++u) {
-    const uint32_t f = u * kMergeThreads + tid;
-    held[u] = f < nl * wide ? mine[(f / wide) * n + f % wide] : 0;
+    const uint32_t f = u * kMergeThreads + tid, q = quotient(f, window);
+    held[u] = 0;
+    if (u * kMergeThreads < heldn && f < heldn) held[u] = mine[q * n + (f - q * wide)];
   }
 
-  if (tid == 0) sm.count = 0;
+  if (tid == 0) sm.count = sm.active[0] = 0;
   if (K <= kMergeWaves) {  // a wave per beam
     if (wave < K) {
       const int64_t row = item * K + wave;
@@ -716,7 +718,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
 
   // Entry j of list q, e, as a candidate; hi is 0 where there is none.
   auto cand = [&](uint64_t e, uint32_t q, uint32_t j) __attribute__((always_inline)) -> Cand {
-    const uint32_t b = q / static_cast<uint32_t>(C);
+    const uint32_t b = quotient(q, chunks);
     const int st = sm.state[b];
     const uint64_t beam = static_cast<uint64_t>(kMaxBeams - 1 - b) << (32 + kTokenBits);
     const uint32_t key = static_cast<uint32_t>(e >> 32);
@@ -735,8 +737,9 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
     Cand first[kHeld];
 #pragma unroll
     for (int u = 0; u < kHeld; ++u) {
-      const uint32_t f = u * kMergeThreads + tid;
-      first[u] = f < nl * wide ? cand(held[u], f / wide, f % wide) : Cand{0, 0};
+      const uint32_t f = u * kMergeThreads + tid, q = quotient(f, window);
+      first[u] = Cand{0, 0};
+      if (u * kMergeThreads < heldn && f < heldn) first[u] = cand(held[u], q, f - q * wide);
     }
 
     // A bound on the n-th candidate: the largest T (of the ranks' upper halves)
@@ -750,16 +753,27 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
         const uint32_t h = static_cast<uint32_t>(first[u].hi >> 32);
         best = best > h ? best : h;
       }
-      for (uint32_t q = room + tid; q < nl; q += kMergeThreads) {  // more lists than are held (wide is 1)
+      for (uint32_t q = kRoom + tid; q < nl; q += kMergeThreads) {  // more lists than are held (wide is 1)
         const uint32_t h = static_cast<uint32_t>(fetch(q, 0).hi >> 32);
         best = best > h ? best : h;
       }
-      sm.heads[tid] = best;
-      __syncthreads();
-      uint32_t h[kMergeWaves];
+      if (n <= kMergeWaveBound) {  // the best of the waves' own bounds, as in the chunks
+        const uint32_t own[1] = {best};
+        const uint32_t t = nth_key(own, n, kBoundBits, 0);
+        if (lane == 0) sm.heads[wave] = t;
+        __syncthreads();
 #pragma unroll
-      for (int i = 0; i < kMergeWaves; ++i) h[i] = sm.heads[i * kWave + lane];
-      T = nth_key(h, n, kBoundBits, 0);
+        for (int w = 0; w < kMergeWaves; ++w) T = T > sm.heads[w] ? T : sm.heads[w];
+      }
+      if (T <= 1u) {
+        __syncthreads();
+        sm.heads[tid] = best;
+        __syncthreads();
+        uint32_t h[kMergeWaves];
+#pragma unroll
+        for (int i = 0; i < kMergeWaves; ++i) h[i] = sm.heads[i * kWave + lane];
+        T = nth_key(h, n, kBoundBits, 0);
+      }
       T = T == 0u ? 1u : lowered(T, margin);  // fewer than n: every candidate counts
     }
 
@@ -780,14 +794,14 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
         const uint32_t at = atomicAdd(&sm.active[turn], 1u);
         if (at < kMergeLists) sm.list_of[turn][at] = static_cast<uint16_t>(q);
       };
-      if (tid == 0) sm.active[0] = 0;
-      __syncthreads();
 #pragma unroll
       for (int u = 0; u < kHeld; ++u) {
-        const uint32_t f = u * kMergeThreads + tid;
-        if (push(first[u]) && f % wide == wide - 1) go_on(0, f / wide);
+        if (u * kMergeThreads < heldn && push(first[u]) && wide < n) {
+          const uint32_t f = u * kMergeThreads + tid, q = quotient(f, window);
+          if (f - q * wide == wide - 1) go_on(0, q);
+        }
       }
-      for (uint32_t q = room + tid; q < nl; q += kMergeThreads)
+      for (uint32_t q = kRoom + tid; q < nl; q += kMergeThreads)
         if (push(fetch(q, 0))) go_on(0, q);
       int turn = 0;
       for (uint32_t j0 = wide; j0 < n; turn ^= 1) {
@@ -797,7 +811,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
         if (active == 0) break;
         const bool noted = active <= kMergeLists;
         const uint32_t lists_now = noted ? active : nl;
-        uint32_t w = lists_now < room ? room / lists_now : 1u;
+        uint32_t w = lists_now < kRoom ? kRoom / lists_now : 1u;
         w = w < n - j0 ? w : n - j0;
         for (uint32_t f = tid; f < lists_now * w; f += kMergeThreads) {
           const uint32_t q = noted ? sm.list_of[turn][f / w] : f / w, j = f % w;
@@ -827,7 +841,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       if (better <= T) break;  // that many are equal there
       T = better;
       __syncthreads();
-      if (tid == 0) sm.count = 0;
+      if (tid == 0) sm.count = sm.active[0] = 0;
       __syncthreads();
     }
 
@@ -896,20 +910,39 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       M = sm.count;
     }
 
-    // Ranks by counting, four at a time so that the reads overlap. Decode and write.
-    if (tid < 4) sm.list[M + tid] = Cand{0, 0};
-    __syncthreads();
+    // Ranks by counting, four at a time so that the reads overlap (what lies
+    // behind the list does not count). Decode and write.
     for (uint32_t e = tid; e < M; e += kMergeThreads) {
       const Cand k = sm.list[e];
       uint32_t r = 0;
       for (uint32_t j = 0; j < M; j += 4) {
 #pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) r += above(sm.list[j + i], k) ? 1u : 0u;
+        for (uint32_t i = 0; i < 4; ++i) r += above(sm.list[j + i], k) && j + i < M ? 1u : 0u;
       }
       if (r <= n) sm.sorted[r] = k;
+      if (r < n) {
+        const int b = beam_of(k);
+        double s = sm.score[b];
+        int32_t token = a.end_token;
+        if (sm.state[b] == 1) {
+          const uint32_t low = static_cast<uint32_t>(k.lo) & ((1u << kTokenBits) - 1u);
+          s += (static_cast<double>(key_value(static_cast<uint32_t>(k.lo >> kTokenBits))) - sm.ref[b]) - sm.rest[b];
+          token = static_cast<int32_t>(((1u << kTokenBits) - 1u) - low);
+        }
+        const int64_t o = item * n + r;
+        a.out_scores[o] = static_cast<float>(s);
+        a.out_parents[o] = b;
+        a.out_tokens[o] = token;
+      }
     }
+    for (uint32_t e = M + tid; e < n; e += kMergeThreads) {
+      const int64_t o = item * n + e;
+      a.out_scores[o] = -INFINITY;
+      a.out_parents[o] = -1;
+      a.out_tokens[o] = -1;
+    }
+    if (last || K == 1) break;
     __syncthreads();
-    if (last) break;
 
     // Neighbours of different beams that lie closer than the sums are exact
     // (equal ones are beams alike): those beams' sums are formed again.
@@ -931,29 +964,8 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       const double sum = row_sum<DT>(a, item * K + b, static_cast<float>(sm.ref[b]), sm);
       if (tid == 0) sm.rest[b] = log(sum);
     }
-    if (tid == 0) sm.count = 0;
+    if (tid == 0) sm.count = sm.active[0] = 0;
     __syncthreads();
-  }
-
-  if (tid < static_cast<int>(n)) {
-    const int64_t o = item * n + tid;
-    if (static_cast<uint32_t>(tid) < M) {
-      const Cand k = sm.sorted[tid];
-      const int b = beam_of(k);
-      double s = sm.score[b];
-      int32_t token = a.end_token;
-      if (sm.state[b] == 1) {
-        s += (static_cast<double>(key_value(static_cast<uint32_t>(k.lo >> kTokenBits))) - sm.ref[b]) - sm.rest[b];
-        token = static_cast<int32_t>(((1u << kTokenBits) - 1u) - (static_cast<uint32_t>(k.lo) & ((1u << kTokenBits) - 1u)));
-      }
-      a.out_scores[o] = static_cast<float>(s);
-      a.out_parents[o] = b;
-      a.out_tokens[o] = token;
-    } else {
-      a.out_scores[o] = -INFINITY;
-      a.out_parents[o] = -1;
-      a.out_tokens[o] = -1;
-    }
   }
 }
 
@@ -968,8 +980,12 @@ void launch_both(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t it
   else
     hipLaunchKernelGGL((beam_chunk_kernel<DT, false>), dim3(blocks), dim3(kChunkThreads), 0, stream, a, s,
                        item0 * a.K, stats, lists);
+  // the window of entries that the merge holds of every list
+  const uint32_t nl = static_cast<uint32_t>(a.K) * static_cast<uint32_t>(s.chunks);
+  uint32_t wide = nl < kRoom ? kRoom / nl : 1u;
+  wide = wide < static_cast<uint32_t>(a.n) ? wide : static_cast<uint32_t>(a.n);
   hipLaunchKernelGGL(beam_merge_kernel<DT>, dim3(static_cast<unsigned>(items)), dim3(kMergeThreads), 0, stream, a,
-                     s.chunks, item0, stats, lists);
+                     make_div(static_cast<uint32_t>(s.chunks)), make_div(wide), item0, stats, lists);
 }
 
 }  // namespace

@@ -17,21 +17,6 @@ namespace {
 
 constexpr int kMoveThreads = 256;
 
-// Quotients of 31-bit numbers by a fixed divisor: floor(x * m / 2^(31 + s))
-// with m = ceil(2^(31 + s) / d), 2^s >= d. The error of m, below 1 in d's
-// share of 2^(31 + s), moves the quotient of x < 2^31 by less than 1 / d.
-struct Div {
-  uint32_t d, m, s;
-};
-Div make_div(uint32_t d) {
-  uint32_t s = 0;
-  while ((uint64_t{1} << s) < d) ++s;
-  return Div{d, static_cast<uint32_t>(((uint64_t{1} << (31 + s)) + d - 1) / d), s};
-}
-__device__ __forceinline__ uint32_t quotient(uint32_t x, const Div& v) {
-  return static_cast<uint32_t>((static_cast<uint64_t>(x) * v.m) >> (31 + v.s));
-}
-
 // A state cut into panels (one index of each of the three axes) of columns.
 struct MoveState {
   char* data;
