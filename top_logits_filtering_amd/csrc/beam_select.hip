@@ -23,6 +23,8 @@
 
 #include <float.h>
 
+#include <type_traits>
+
 #include "beam.h"
 #include "device_common.h"
 #include "reg_tile.h"
@@ -32,23 +34,22 @@ namespace {
 
 constexpr int kChunkThreads = 256;
 constexpr int kChunkWaves = kChunkThreads / kWave;
-constexpr int kChunkCap = 1024;   // candidate slots of a chunk
-constexpr int kBoundBits = 14;    // bits of a bound from the first that differs on
-constexpr int kLayers = 32;       // vectors per thread at most
-constexpr int kUnit = 2;          // vectors that share one maximum
-constexpr int kGroup = 4;         // vectors loaded ahead
-constexpr int kHits = 2048;       // pairs of vectors looked at again
+constexpr int kChunkCap = 1024;  // candidate slots of a chunk
+constexpr int kLayers = 32;      // vectors per thread at most
+constexpr int kUnit = 2;         // vectors that share one maximum
+constexpr int kGroup = 4;        // vectors loaded ahead
+constexpr int kHits = 1024;      // pairs of vectors that may reach the bound
 constexpr int kTargetBlocks = 1024;
 constexpr int kMergeThreads = 512;
-constexpr int kMergeCap = 2048;   // candidate slots of a prompt
 constexpr int kMergeWaves = kMergeThreads / kWave;
-constexpr uint32_t kWaveBound = 16;  // up to so many candidates per chunk a wave's bound is taken
-constexpr uint32_t kMergeWaveBound = 32;  // the same in the merge
-constexpr int kHeld = 4;                  // list entries a thread of the merge holds from the start
+constexpr int kMergeCap = 2048;  // candidate slots of a prompt
+constexpr int kHeld = 4;         // list entries a thread of the merge holds from the start
 constexpr uint32_t kRoom = kHeld * kMergeThreads;
-constexpr uint32_t kAllRanked = 48;  // so many candidates are ranked without a bound
-constexpr uint32_t kLongList = 96;      // a list is cut before it is ranked if it is longer
 constexpr uint32_t kMergeLists = 1024;  // lists noted as going on
+constexpr uint32_t kGroupBound = 32;    // up to so many candidates 64 maxima give the bound
+constexpr int kBoundBits = 14;          // bits of a bound from the first that differs on
+constexpr uint32_t kAllRanked = 48;     // so many candidates are ranked without a bound
+constexpr uint32_t kLongList = 160;     // a longer list is cut before it is ranked
 constexpr int kMaxBeams = 128;
 constexpr int kMaxCandidates = 256;
 constexpr int kTokenBits = 20;
@@ -182,17 +183,59 @@ __device__ __forceinline__ uint32_t nth_key(const uint32_t (&k)[COUNT], uint32_t
   return T > low ? T : low;
 }
 
+// The maximum over groups of SIZE (4 or 8) neighbouring lanes, in all of them.
+template <int SIZE>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  auto most = [](uint32_t x, uint32_t y) { return x > y ? x : y; };
+  v = most(v, dpp_u32<dpp::kQuad1032>(v, 0u));
+  v = most(v, dpp_u32<dpp::kQuad2301>(v, 0u));
+  if constexpr (SIZE == 8) v = most(v, dpp_u32<dpp::kRowHalfMirror>(v, 0u));
+  return v;
+}
+
+// rank[e] = how many of list[0, M) rank above list[e]. The threads share each
+// entry's comparisons, so that short lists take few steps. (Reads up to three
+// entries behind the list, which do not count.)
+template <int THREADS, class Item, class Above>
+__device__ __forceinline__ void count_ranks(const Item* list, uint32_t* rank, uint32_t M, Above above) {
+  const uint32_t tid = threadIdx.x;
+  for (uint32_t e = tid; e < M; e += THREADS) rank[e] = 0;
+  lds_barrier();
+  uint32_t span = kWave;
+  while (span < M && span < THREADS) span *= 2;
+  const uint32_t parts = THREADS / span, part = tid / span;
+  const uint32_t seg = ((M + parts - 1) / parts + 3u) & ~3u;
+  const uint32_t j0 = part * seg, j1 = j0 + seg < M ? j0 + seg : M;
+  for (uint32_t e = tid & (span - 1u); e < M; e += span) {
+    const Item mine = list[e];
+    uint32_t r = 0;
+    for (uint32_t j = j0; j < j1; j += 4) {
+#pragma unroll
+      for (uint32_t i = 0; i < 4; ++i) r += above(list[j + i], mine) && j + i < j1 ? 1u : 0u;
+    }
+    if (r != 0) atomicAdd(&rank[e], r);
+  }
+  lds_barrier();
+}
+
 struct ChunkSmem {
-  float top[kLayers / kUnit][kChunkThreads];  // largest value of each thread's pairs of vectors
-  uint64_t list[kChunkCap + 8];
-  uint32_t half[2 * kChunkThreads];           // largest of a thread's even and of its odd pairs, as keys
+  uint64_t list[kChunkCap + 4];
+  uint32_t rank[kChunkCap];
+  uint32_t half[2 * kChunkThreads];  // largest of a thread's even and of its odd pairs of vectors, as keys
   double sum[kChunkWaves];
   uint32_t wave_top[kChunkWaves];
-  uint32_t wave_bound[kChunkWaves];
+  uint32_t group[kWave];
   uint32_t scan[kChunkWaves];
   uint32_t count;
   uint32_t hits;
-  uint16_t hit[kHits];
+  uint16_t hit[kHits];               // pairs of vectors that reach the bound: unit * 256 + thread
+};
+// What finds the elements of those pairs: the pairs themselves, or every pair's maximum.
+struct ShortSmem : ChunkSmem {
+  vec_t pair[kHits][kUnit];
+};
+struct LongSmem : ChunkSmem {
+  float top[kLayers / kUnit][kChunkThreads];
 };
 
 // Exclusive prefix of v over the block; total: the block's sum.
@@ -221,7 +264,7 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   using raw_t = typename DT::raw_t;
   constexpr int P = DT::kPerVec;
   constexpr int kLow = key_low_bits<DT>();
-  __shared__ ChunkSmem sm;
+  __shared__ std::conditional_t<SHORT, ShortSmem, LongSmem> sm;
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int ch = static_cast<int>(blockIdx.x % static_cast<unsigned>(split.chunks));
@@ -331,39 +374,46 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   };
   const uint32_t n = static_cast<uint32_t>(a.n);
   const uint32_t pair[2] = {key_or_nan(half0), key_or_nan(half1)};
+  const uint32_t own = pair[0] > pair[1] ? pair[0] : pair[1];
 
   // The n-th largest of some maxima is a lower bound of the chunk's n-th
-  // largest value, and kBoundBits of it suffice to leave few candidates. For
-  // small n each wave finds it of its own 128 and the best of the four counts:
-  // a third of the instructions of a bound over all 512, for some candidates
-  // more.
-  uint32_t T = n <= kWaveBound ? nth_key(pair, n, kBoundBits, kLow) : 0u;
-  uint32_t top = wave_max_u32(pair[0] > pair[1] ? pair[0] : pair[1]);
+  // largest value; kBoundBits of it suffice to leave few candidates. For small n
+  // of the maxima of 64 groups of threads, one per lane.
+  const bool grouped = n <= kGroupBound;
+  uint32_t top = wave_max_u32(own);
   sum = wave_sum_f64(sum);
+  if (grouped) {
+    const uint32_t g = group_max<kChunkThreads / kWave>(own);
+    if (tid % (kChunkThreads / kWave) == 0) sm.group[tid / (kChunkThreads / kWave)] = g;
+  }
   if (lane == 0) {
     sm.sum[wave] = sum;
     sm.wave_top[wave] = top;
-    sm.wave_bound[wave] = T;
   }
-  // The same over all maxima, which every wave then holds, eight per lane.
+  // For larger n of two maxima of each thread, which every wave then holds,
+  // eight per lane.
   auto block_nth = [&](int bits) __attribute__((always_inline)) -> uint32_t {
     sm.half[tid] = pair[0];
     sm.half[kChunkThreads + tid] = pair[1];
-    __syncthreads();
+    lds_barrier();
     constexpr int kHalf = 2 * kChunkThreads / kWave;
     uint32_t k[kHalf];
 #pragma unroll
     for (int i = 0; i < kHalf; ++i) k[i] = sm.half[i * kWave + lane];
     return nth_key(k, n, bits, kLow);
   };
-  __syncthreads();
+  lds_barrier();
   sum = 0.0;
   top = 0u;
 #pragma unroll
   for (int w = 0; w < kChunkWaves; ++w) {
     sum += sm.sum[w];
     top = top > sm.wave_top[w] ? top : sm.wave_top[w];
-    T = T > sm.wave_bound[w] ? T : sm.wave_bound[w];
+  }
+  uint32_t T = 0u;
+  if (grouped) {
+    const uint32_t g[1] = {sm.group[lane]};
+    T = nth_key(g, n, kBoundBits, kLow);
   }
   const int64_t slot = row * split.chunks + ch;
   uint64_t* out = lists + slot * a.n;
@@ -391,8 +441,6 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
 #pragma unroll
     for (int w = 0; w < kChunkWaves; ++w) sum += sm.sum[w];
   }
-  if (tid == 0) stats[slot] = ChunkStat{sum, ref, 0};
-
   if (T == 0u) T = block_nth(kBoundBits);
   if (T == 0u) T = order_key(-FLT_MAX);  // fewer than n maxima: all finite values
   else if (!(T & 0x80000000u)) T |= (1u << kLow) - 1u;
@@ -403,44 +451,49 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     if (at < kChunkCap) sm.list[at] = pack(order_key(x), token);
   };
   if (xe >= bound) push(xe, static_cast<uint32_t>(te));
-  uint32_t hits = 0;
+
+  // Pairs of vectors that reach the bound, then their elements, a thread each.
+  auto hit = [&](int u, bool is) __attribute__((always_inline)) -> uint32_t {
+    if (!is) return kHits;
+    const uint32_t at = atomicAdd(&sm.hits, 1u);
+    if (at < kHits) sm.hit[at] = static_cast<uint16_t>(u * kChunkThreads + tid);
+    return at;
+  };
   if constexpr (SHORT) {
 #pragma unroll
-    for (int g = 0; g < kGroup; ++g) {
-      if (tops[g / kUnit] >= bound) {
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          const float x = DT::value(lane_of<raw_t>(next[g], j));
-          if (x >= bound) push(x, static_cast<uint32_t>(first + (g * kChunkThreads + tid) * P + j));
-        }
+    for (int u = 0; u < kGroup / kUnit; ++u) {
+      const uint32_t at = hit(u, tops[u] >= bound);
+      if (at < kHits) {
+        sm.pair[at][0] = next[u * kUnit];
+        sm.pair[at][1] = next[u * kUnit + 1];
       }
     }
   } else {
-    // pairs of vectors that reach the bound, then their elements
     const int units = (layers + kUnit - 1) / kUnit;
-    for (int u = 0; u < units; ++u) {
-      if (sm.top[u][tid] >= bound) {
-        const uint32_t at = atomicAdd(&sm.hits, 1u);
-        if (at < kHits) sm.hit[at] = static_cast<uint16_t>(u * kChunkThreads + tid);
-      }
-    }
-    __syncthreads();
-    hits = sm.hits;
-    if (hits <= kHits) {
-      for (uint32_t e = tid; e < hits * kUnit; e += kChunkThreads) {
-        const int h = sm.hit[e / kUnit];
-        const int at = ((h / kChunkThreads) * kUnit + static_cast<int>(e % kUnit)) * kChunkThreads + h % kChunkThreads;
-        const vec_t q = again(at);
-        const uint32_t token = static_cast<uint32_t>(first + at * P);
+    for (int u = 0; u < units; ++u) hit(u, sm.top[u][tid] >= bound);
+  }
+  lds_barrier();
+  const uint32_t hits = sm.hits;
+  if (hits <= kHits) {
+    constexpr int kQuads = kUnit * P / 4;  // four elements a thread
+    struct Quad {
+      raw_t r[4];
+    };
+    for (uint32_t e = tid; e < hits * kQuads; e += kChunkThreads) {
+      const int h = sm.hit[e / kQuads], part = static_cast<int>(e % kQuads) * 4;
+      const int at = ((h / kChunkThreads) * kUnit + part / P) * kChunkThreads + h % kChunkThreads;
+      const uint32_t token = static_cast<uint32_t>(first + at * P + part % P);
+      Quad q{{DT::kNegInf, DT::kNegInf, DT::kNegInf, DT::kNegInf}};
+      if constexpr (SHORT) q = reinterpret_cast<const Quad*>(&sm.pair[0][0])[e];
+      else if (at < cnt) q = *reinterpret_cast<const Quad*>(rowp + token);
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-          const float x = DT::value(lane_of<raw_t>(q, j));
-          if (x >= bound) push(x, token + j);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float x = DT::value(q.r[j]);
+        if (x >= bound) push(x, token + j);
       }
     }
   }
-  __syncthreads();
+  lds_barrier();
   uint32_t M = sm.count;
 
   if (hits > kHits || M > kChunkCap) {
@@ -522,20 +575,14 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     __syncthreads();
   }
 
-  // The candidates are distinct numbers: each one's rank is the count of larger
-  // ones, taken eight at a time so that the reads overlap.
-  if (tid < 8 && M + tid < kChunkCap + 8) sm.list[M + tid] = 0;
-  __syncthreads();
+  // The candidates are distinct numbers: each one's place is its rank.
+  count_ranks<kChunkThreads>(sm.list, sm.rank, M, [](uint64_t x, uint64_t y) { return x > y; });
   for (uint32_t e = tid; e < M; e += kChunkThreads) {
-    const uint64_t mine = sm.list[e];
-    uint32_t r = 0;
-    for (uint32_t j = 0; j < M; j += 8) {
-#pragma unroll
-      for (uint32_t i = 0; i < 8; ++i) r += sm.list[j + i] > mine ? 1u : 0u;
-    }
-    if (r < n) out[r] = mine;
+    const uint32_t r = sm.rank[e];
+    if (r < n) out[r] = sm.list[e];
   }
   for (uint32_t e = M + tid; e < n; e += kChunkThreads) out[e] = 0;
+  if (tid == 0) stats[slot] = ChunkStat{sum, ref, 0};
 }
 
 // A candidate of a prompt: the rank value's image, then beam, logit and token
@@ -554,12 +601,14 @@ struct MergeSmem {
   Cand list[kMergeCap + 4];
   Cand sorted[kMaxCandidates + 2];  // the first n + 1
   uint32_t upper[kMergeCap];  // the candidates' upper halves of hi
+  uint32_t rank[kMergeCap];
   double ref[kMaxBeams];      // L = ref + rest; apart, as ref may be as large as the type goes
   double rest[kMaxBeams];
   double score[kMaxBeams];
   double weight[kMaxBeams];
   int state[kMaxBeams];       // 0: proposes nothing, 1: its lists, 2: finished
-  int close[kMaxBeams];       // 1: a candidate comes too close to another beam's, 2: summed in 64 bits
+  int close[kMaxBeams];       // a candidate comes too close to another beam's
+  int again;                  // some do
   double part[kMergeWaves];
   uint32_t heads[kMergeThreads];
   Cand best[kMergeWaves];
@@ -672,7 +721,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
     if (u * kMergeThreads < heldn && f < heldn) held[u] = mine[q * n + (f - q * wide)];
   }
 
-  if (tid == 0) sm.count = sm.active[0] = 0;
+  if (tid == 0) sm.count = sm.active[0] = sm.again = 0;
   if (K <= kMergeWaves) {  // a wave per beam
     if (wave < K) {
       const int64_t row = item * K + wave;
@@ -705,7 +754,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
     sm.state[tid] = state;
   }
   if (tid < K) sm.close[tid] = 0;
-  __syncthreads();
+  lds_barrier();
 
   // Ranks of two beams may be off against each other by this.
   double margin = 2.0 * kSumError;
@@ -757,18 +806,18 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
         const uint32_t h = static_cast<uint32_t>(fetch(q, 0).hi >> 32);
         best = best > h ? best : h;
       }
-      if (n <= kMergeWaveBound) {  // the best of the waves' own bounds, as in the chunks
-        const uint32_t own[1] = {best};
-        const uint32_t t = nth_key(own, n, kBoundBits, 0);
-        if (lane == 0) sm.heads[wave] = t;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kMergeWaves; ++w) T = T > sm.heads[w] ? T : sm.heads[w];
+      T = 0u;
+      if (n <= kGroupBound) {  // as in the chunks
+        const uint32_t g = group_max<kMergeThreads / kWave>(best);
+        if (tid % (kMergeThreads / kWave) == 0) sm.heads[tid / (kMergeThreads / kWave)] = g;
+        lds_barrier();
+        const uint32_t mine[1] = {sm.heads[lane]};
+        T = nth_key(mine, n, kBoundBits, 0);
+        lds_barrier();
       }
-      if (T <= 1u) {
-        __syncthreads();
+      if (T == 0u) {
         sm.heads[tid] = best;
-        __syncthreads();
+        lds_barrier();
         uint32_t h[kMergeWaves];
 #pragma unroll
         for (int i = 0; i < kMergeWaves; ++i) h[i] = sm.heads[i * kWave + lane];
@@ -806,7 +855,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       int turn = 0;
       for (uint32_t j0 = wide; j0 < n; turn ^= 1) {
         if (tid == 0) sm.active[turn ^ 1] = 0;
-        __syncthreads();
+        lds_barrier();
         const uint32_t active = sm.active[turn];
         if (active == 0) break;
         const bool noted = active <= kMergeLists;
@@ -817,10 +866,10 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
           const uint32_t q = noted ? sm.list_of[turn][f / w] : f / w, j = f % w;
           if (push(fetch(q, j0 + j)) && j == w - 1) go_on(turn ^ 1, q);
         }
-        __syncthreads();
+        lds_barrier();
         j0 += w;
       }
-      __syncthreads();
+      lds_barrier();
       M = sm.count;
       if (M <= kMergeCap || tries == 4) break;
       // The list is full: the n-th best of what it holds is a better bound.
@@ -882,14 +931,20 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
 
     // A long list is cut to what reaches the n-th of its upper halves.
     if (M > kLongList) {
-      constexpr int kPer = kMergeCap / kWave;
-      uint32_t h[kPer];
+      uint32_t cut = 0;
+      if (M <= 8 * kWave) {
+        uint32_t h[8];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const uint32_t e = i * kWave + lane;
-        h[i] = e < M ? sm.upper[e] : 0u;
+        for (int i = 0; i < 8; ++i) h[i] = static_cast<uint32_t>(i * kWave + lane) < M ? sm.upper[i * kWave + lane] : 0u;
+        cut = nth_key(h, n, kBoundBits, 0);
+      } else {
+        uint32_t h[kMergeCap / kWave];
+#pragma unroll
+        for (int i = 0; i < kMergeCap / kWave; ++i)
+          h[i] = static_cast<uint32_t>(i * kWave + lane) < M ? sm.upper[i * kWave + lane] : 0u;
+        cut = nth_key(h, n, kBoundBits, 0);
       }
-      const uint32_t cut = lowered(nth_key(h, n, 32, 0), margin);
+      if (cut != 0u) cut = lowered(cut, margin);
       Cand mine[kMergeCap / kMergeThreads];
 #pragma unroll
       for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
@@ -910,15 +965,11 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       M = sm.count;
     }
 
-    // Ranks by counting, four at a time so that the reads overlap (what lies
-    // behind the list does not count). Decode and write.
+    // Decode and write.
+    count_ranks<kMergeThreads>(sm.list, sm.rank, M, [](const Cand& x, const Cand& y) { return above(x, y); });
     for (uint32_t e = tid; e < M; e += kMergeThreads) {
       const Cand k = sm.list[e];
-      uint32_t r = 0;
-      for (uint32_t j = 0; j < M; j += 4) {
-#pragma unroll
-        for (uint32_t i = 0; i < 4; ++i) r += above(sm.list[j + i], k) && j + i < M ? 1u : 0u;
-      }
+      const uint32_t r = sm.rank[e];
       if (r <= n) sm.sorted[r] = k;
       if (r < n) {
         const int b = beam_of(k);
@@ -942,23 +993,24 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       a.out_tokens[o] = -1;
     }
     if (last || K == 1) break;
-    __syncthreads();
+    lds_barrier();
 
     // Neighbours of different beams that lie closer than the sums are exact
     // (equal ones are beams alike): those beams' sums are formed again.
     auto value = [](const Cand& k) -> double {
       return __builtin_bit_cast(double, (k.hi >> 63) ? k.hi & 0x7FFFFFFFFFFFFFFFull : ~k.hi);
     };
-    bool again = false;
     if (static_cast<uint32_t>(tid) < n && static_cast<uint32_t>(tid) + 1u < M) {
       const Cand p = sm.sorted[tid], q = sm.sorted[tid + 1];
       const int bp = beam_of(p), bq = beam_of(q);
       if (bp != bq && p.hi != q.hi && value(p) - value(q) <= margin) {
-        again = sm.state[bp] == 1 || sm.state[bq] == 1;
+        if (sm.state[bp] == 1 || sm.state[bq] == 1) sm.again = 1;
         sm.close[bp] = sm.close[bq] = 1;
       }
     }
-    if (!__syncthreads_or(again)) break;
+    lds_barrier();
+    if (sm.again == 0) break;
+    __syncthreads();  // what this round wrote lies before what the next one writes
     for (int b = 0; b < K; ++b) {
       if (sm.close[b] == 0 || sm.state[b] != 1) continue;
       const double sum = row_sum<DT>(a, item * K + b, static_cast<float>(sm.ref[b]), sm);
