@@ -35,10 +35,8 @@ namespace {
 constexpr int kChunkThreads = 256;
 constexpr int kChunkWaves = kChunkThreads / kWave;
 constexpr int kChunkCap = 1024;  // candidate slots of a chunk
-constexpr int kLayers = 32;      // vectors per thread at most
-constexpr int kUnit = 2;         // vectors that share one maximum
-constexpr int kGroup = 4;        // vectors loaded ahead
-constexpr int kHits = 1024;      // pairs of vectors that may reach the bound
+constexpr int kUnits = 16;       // units of a thread at most
+constexpr int kHits = 1024;      // units that may reach the bound
 constexpr int kTargetBlocks = 1024;
 constexpr int kMergeThreads = 512;
 constexpr int kMergeWaves = kMergeThreads / kWave;
@@ -53,6 +51,14 @@ constexpr uint32_t kLongList = 160;     // a longer list is cut before it is ran
 constexpr int kMaxBeams = 128;
 constexpr int kMaxCandidates = 256;
 constexpr int kTokenBits = 20;
+
+// A thread's vectors: 16 elements make a unit, which shares one maximum, and 32
+// a group, which is loaded while the one before is summed (for fp32 groups of
+// half the size took 90 us instead of 84 for 1024 rows of 128256).
+template <class DT>
+constexpr int kUnitOf = 16 / DT::kPerVec;
+template <class DT>
+constexpr int kGroupOf = 32 / DT::kPerVec;
 
 // sum exp(x - ref) over a chunk; bad: a NaN or +inf was among the logits.
 struct ChunkStat {
@@ -221,21 +227,22 @@ __device__ __forceinline__ void count_ranks(const Item* list, uint32_t* rank, ui
 struct ChunkSmem {
   uint64_t list[kChunkCap + 4];
   uint32_t rank[kChunkCap];
-  uint32_t half[2 * kChunkThreads];  // largest of a thread's even and of its odd pairs of vectors, as keys
+  uint32_t half[2 * kChunkThreads];  // largest of a thread's even and of its odd units, as keys
   double sum[kChunkWaves];
   uint32_t wave_top[kChunkWaves];
   uint32_t group[kWave];
   uint32_t scan[kChunkWaves];
   uint32_t count;
   uint32_t hits;
-  uint16_t hit[kHits];               // pairs of vectors that reach the bound: unit * 256 + thread
+  uint16_t hit[kHits];               // units that reach the bound: unit * 256 + thread
 };
-// What finds the elements of those pairs: the pairs themselves, or every pair's maximum.
+// What finds the elements of those units: the units themselves, or every unit's maximum.
+template <class DT>
 struct ShortSmem : ChunkSmem {
-  vec_t pair[kHits][kUnit];
+  vec_t unit[2 * kChunkThreads][kUnitOf<DT>];  // a thread of a short chunk has two
 };
 struct LongSmem : ChunkSmem {
-  float top[kLayers / kUnit][kChunkThreads];
+  float top[kUnits][kChunkThreads];
 };
 
 // Exclusive prefix of v over the block; total: the block's sum.
@@ -264,7 +271,8 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   using raw_t = typename DT::raw_t;
   constexpr int P = DT::kPerVec;
   constexpr int kLow = key_low_bits<DT>();
-  __shared__ std::conditional_t<SHORT, ShortSmem, LongSmem> sm;
+  constexpr int kUnit = kUnitOf<DT>, kGroup = kGroupOf<DT>;
+  __shared__ std::conditional_t<SHORT, ShortSmem<DT>, LongSmem> sm;
 
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int ch = static_cast<int>(blockIdx.x % static_cast<unsigned>(split.chunks));
@@ -309,7 +317,7 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   if (a.finished != nullptr && a.finished[row] != 0) return;
   if (tid == 0) sm.count = sm.hits = 0;
 
-  // One pass: the sum of exp and the largest value of each pair of vectors.
+  // One pass: the sum of exp and the largest value of each unit.
   // maximum() keeps a NaN, so that one shows in the chunk's maximum.
   double sum = 0.0;
   float half0 = -INFINITY, half1 = -INFINITY;
@@ -339,8 +347,11 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
       }
       sum += static_cast<double>(__builtin_fmaf(rest, kLn2, e[0]));
     }
-    half0 = __builtin_elementwise_maximum(half0, tops[0]);
-    half1 = __builtin_elementwise_maximum(half1, tops[1]);
+#pragma unroll
+    for (int u = 0; u < kGroup / kUnit; u += 2) {
+      half0 = __builtin_elementwise_maximum(half0, tops[u]);
+      half1 = __builtin_elementwise_maximum(half1, tops[u + 1]);
+    }
   };
   if constexpr (SHORT) {
     take(0, next);
@@ -452,7 +463,7 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   };
   if (xe >= bound) push(xe, static_cast<uint32_t>(te));
 
-  // Pairs of vectors that reach the bound, then their elements, a thread each.
+  // Units that reach the bound, then their elements, four a thread.
   auto hit = [&](int u, bool is) __attribute__((always_inline)) -> uint32_t {
     if (!is) return kHits;
     const uint32_t at = atomicAdd(&sm.hits, 1u);
@@ -463,9 +474,9 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
 #pragma unroll
     for (int u = 0; u < kGroup / kUnit; ++u) {
       const uint32_t at = hit(u, tops[u] >= bound);
-      if (at < kHits) {
-        sm.pair[at][0] = next[u * kUnit];
-        sm.pair[at][1] = next[u * kUnit + 1];
+      if (at < 2 * kChunkThreads) {
+#pragma unroll
+        for (int g = 0; g < kUnit; ++g) sm.unit[at][g] = next[u * kUnit + g];
       }
     }
   } else {
@@ -475,7 +486,7 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   lds_barrier();
   const uint32_t hits = sm.hits;
   if (hits <= kHits) {
-    constexpr int kQuads = kUnit * P / 4;  // four elements a thread
+    constexpr int kQuads = kUnit * P / 4;
     struct Quad {
       raw_t r[4];
     };
@@ -484,7 +495,7 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
       const int at = ((h / kChunkThreads) * kUnit + part / P) * kChunkThreads + h % kChunkThreads;
       const uint32_t token = static_cast<uint32_t>(first + at * P + part % P);
       Quad q{{DT::kNegInf, DT::kNegInf, DT::kNegInf, DT::kNegInf}};
-      if constexpr (SHORT) q = reinterpret_cast<const Quad*>(&sm.pair[0][0])[e];
+      if constexpr (SHORT) q = reinterpret_cast<const Quad*>(sm.unit[e / kQuads])[e % kQuads];
       else if (at < cnt) q = *reinterpret_cast<const Quad*>(rowp + token);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -1026,7 +1037,7 @@ void launch_both(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t it
                    uint64_t* lists, hipStream_t stream) {
   const unsigned blocks = static_cast<unsigned>(items * a.K * s.chunks);
   // few layers: they stay in registers
-  if (s.vecs <= kGroup * kChunkThreads)
+  if (s.vecs <= kGroupOf<DT> * kChunkThreads)
     hipLaunchKernelGGL((beam_chunk_kernel<DT, true>), dim3(blocks), dim3(kChunkThreads), 0, stream, a, s, item0 * a.K,
                        stats, lists);
   else
@@ -1048,8 +1059,9 @@ void launch_both(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t it
 BeamSplit beam_select_split(int dtype, int64_t rows, int V) {
   const int64_t per = dtype == 0 ? 4 : 8;
   const int64_t nv = V / per;
-  const int64_t least = (nv + kChunkThreads * kLayers - 1) / (kChunkThreads * kLayers);
-  const int64_t most = (nv + kChunkThreads * kGroup - 1) / (kChunkThreads * kGroup);
+  const int64_t largest = kChunkThreads * kUnits * 16 / per, smallest = kChunkThreads * 32 / per;
+  const int64_t least = (nv + largest - 1) / largest;
+  const int64_t most = (nv + smallest - 1) / smallest;
   int64_t c = rows > 0 ? (kTargetBlocks + rows - 1) / rows : 1;
   c = c < most ? c : most;
   c = c > least ? c : least;
