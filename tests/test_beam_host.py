@@ -191,14 +191,17 @@ def test_state_layout_addresses_every_element(shape, view, seq):
     row_stride, size, stride, positions, position_stride, run = _state_layout(tuple(t.shape), t.stride(), 4, 0, seq)
     flat = torch.arange(int(np.prod(shape)))
     for r in range(t.shape[0]):
+        seen = []
         for pos in range(positions):
-            seen = []
+            here = []
             for i in itertools.product(*(range(n) for n in size)):
                 at = r * row_stride + sum(a * b for a, b in zip(i, stride)) + pos * position_stride
                 assert at % 4 == 0 and run % 4 == 0
-                seen += flat[t.storage_offset() + at // 4:][:run // 4].tolist()
-            want = t[r] if seq is None else t[r].select(seq - 1, pos)
-            assert sorted(seen) == sorted(want.reshape(-1).tolist())
+                here += flat[t.storage_offset() + at // 4:][:run // 4].tolist()
+            if seq is not None:
+                assert sorted(here) == sorted(t[r].select(seq - 1, pos).reshape(-1).tolist())
+            seen += here
+        assert sorted(seen) == sorted(t[r].reshape(-1).tolist())
     real = [s for s, n in zip(stride, size) if n != 1]
     assert real == sorted(real, reverse=True) and list(size)[:3 - len(real)] == [1] * (3 - len(real))
 

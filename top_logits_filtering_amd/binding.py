@@ -402,16 +402,17 @@ def _scope(stream, device):
     return int(stream.cuda_stream), torch.cuda.stream(stream)
 
 
-def _check_dense(t, shape, dtype, name):
-    """None, or a contiguous tensor of `shape` and `dtype`."""
-    if t is None:
-        return
+def _check_dense(t, shape, dtype, name, device):
+    """A contiguous tensor of `shape` and `dtype` on the GPU of index `device`
+    (-1: the CPU, where nothing runs)."""
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got shape {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    if t.get_device() != device:
+        raise ValueError(f"tensors must share one device: {name} is on {t.device}")
 
 
 def beam_search_select_workspace(dtype, N, K, V, n=None):
@@ -444,7 +445,7 @@ def beam_search_select(logits, scores, n=None, finished=None, end_token=None, we
     other call that may run at the same time (each call allocates one else)."""
     import torch
 
-    lib = load_library()
+    lib = _lib or load_library()
     if logits.dim() != 2:
         raise ValueError("logits must be 2-D [N * K, V]")
     if scores.dim() != 2:
@@ -452,40 +453,47 @@ def beam_search_select(logits, scores, n=None, finished=None, end_token=None, we
     (R, V), (N, K) = logits.shape, scores.shape
     if N * K != R:
         raise ValueError(f"logits must have N * K = {N * K} rows, got {R}")
+    ldx, step = logits.stride()
+    if step != 1 and V > 1:
+        raise ValueError("rows must be contiguous (stride 1 along the last dimension)")
+    if R <= 1:
+        ldx = V
     n = K if n is None else int(n)
     dtype = _dtype_code(logits)
-    _check_dense(scores, (N, K), torch.float32, "scores")
+    dev = logits.get_device()
+    _check_dense(scores, (N, K), torch.float32, "scores", dev)
+    p_finished = p_weights = None
     if finished is not None:
-        _check_dense(finished, (N, K), torch.uint8 if finished.dtype == torch.uint8 else torch.bool, "finished")
+        _check_dense(finished, (N, K), torch.uint8 if finished.dtype == torch.uint8 else torch.bool, "finished", dev)
         if end_token is None:
             raise ValueError("finished needs end_token")
-    _check_dense(weights, (N, K), torch.float32, "weights")
-    dev = logits.device
-    _check_device(dev, logits, scores, finished, weights)
-    xp, ldx = _rows(logits)
-    handle, scope = _scope(stream, dev)
+        p_finished = finished.data_ptr()
+    if weights is not None:
+        _check_dense(weights, (N, K), torch.float32, "weights", dev)
+        p_weights = weights.data_ptr()
+    handle, scope = _scope(stream, logits.device)
     with scope:
         if out is None:
-            out = (torch.empty((N, n), dtype=torch.float32, device=dev),
-                   torch.empty((N, n), dtype=torch.int32, device=dev),
-                   torch.empty((N, n), dtype=torch.int32, device=dev))
+            out = (torch.empty((N, n), dtype=torch.float32, device=logits.device),
+                   torch.empty((N, n), dtype=torch.int32, device=logits.device),
+                   torch.empty((N, n), dtype=torch.int32, device=logits.device))
         o_scores, o_parents, o_tokens = out
-        _check_dense(o_scores, (N, n), torch.float32, "out scores")
-        _check_dense(o_parents, (N, n), torch.int32, "out parents")
-        _check_dense(o_tokens, (N, n), torch.int32, "out tokens")
+        _check_dense(o_scores, (N, n), torch.float32, "out scores", dev)
+        _check_dense(o_parents, (N, n), torch.int32, "out parents", dev)
+        _check_dense(o_tokens, (N, n), torch.int32, "out tokens", dev)
         if workspace is None:
             size = lib.beam_search_select_workspace(dtype, N, K, V, n)
             if size < 0:
                 raise TopKTopPError(2, last_error())
-            workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-        elif workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous uint8 tensor")
-        _check_device(dev, o_scores, o_parents, o_tokens, workspace)
-        _check(lib.beam_search_select(
-            xp, ldx, dtype, N, K, V, scores.data_ptr(), None if finished is None else finished.data_ptr(),
-            0 if end_token is None else int(end_token), None if weights is None else weights.data_ptr(), n,
-            o_scores.data_ptr(), o_parents.data_ptr(), o_tokens.data_ptr(), workspace.data_ptr(), workspace.numel(),
-            handle))
+            workspace = torch.empty(size, dtype=torch.uint8, device=logits.device)
+        else:
+            size = workspace.numel()
+            _check_dense(workspace, workspace.shape, torch.uint8, "workspace", dev)
+        status = lib.beam_search_select(
+            logits.data_ptr(), ldx, dtype, N, K, V, scores.data_ptr(), p_finished,
+            0 if end_token is None else int(end_token), p_weights, n, o_scores.data_ptr(), o_parents.data_ptr(),
+            o_tokens.data_ptr(), workspace.data_ptr(), size, handle)
+    _check(status)
     return out
 
 
@@ -527,20 +535,22 @@ def beam_reorder_states(states, parents, batch_dim=0, seq_dim=None, lengths=None
     moved. Returns states."""
     import torch
 
-    lib = load_library()
+    lib = _lib or load_library()
     tensors = [states] if isinstance(states, torch.Tensor) else list(states)
     if parents.dim() != 2:
         raise ValueError("parents must be 2-D [N, K]")
     N, K = parents.shape
-    _check_dense(parents, (N, K), torch.int32, "parents")
-    _check_dense(lengths, (N,), torch.int32, "lengths")
-    if lengths is not None and seq_dim is None:
-        raise ValueError("lengths needs seq_dim")
-    dev = parents.device
-    _check_device(dev, parents, lengths, *tensors)
+    dev = parents.get_device()
+    _check_dense(parents, (N, K), torch.int32, "parents", dev)
+    if lengths is not None:
+        _check_dense(lengths, (N,), torch.int32, "lengths", dev)
+        if seq_dim is None:
+            raise ValueError("lengths needs seq_dim")
     descs = (BeamState * len(tensors))()
     for d, t in zip(descs, tensors):
         dims = t.dim()
+        if t.get_device() != dev:
+            raise ValueError(f"tensors must share one device: a state is on {t.device}")
         if not -dims <= batch_dim < dims:
             raise ValueError(f"a state of {dims} axes has no batch_dim {batch_dim}")
         if t.shape[batch_dim] != N * K:
@@ -557,10 +567,11 @@ def beam_reorder_states(states, parents, batch_dim=0, seq_dim=None, lengths=None
         d.data = t.data_ptr()
         d.row_stride, d.size[:], d.stride[:], d.positions, d.position_stride, d.run = _state_layout(
             tuple(t.shape), t.stride(), t.element_size(), batch_dim % dims, seq)
-    handle, scope = _scope(stream, dev)
+    handle, scope = _scope(stream, parents.device)
     with scope:
-        _check(lib.beam_reorder_states(descs, len(tensors), parents.data_ptr(), N, K,
-                                       None if lengths is None else lengths.data_ptr(), handle))
+        status = lib.beam_reorder_states(descs, len(tensors), parents.data_ptr(), N, K,
+                                         None if lengths is None else lengths.data_ptr(), handle)
+    _check(status)
     return states
 
 
@@ -572,7 +583,7 @@ def beam_backtrace(tokens, parents, beams=None, lengths=None, pad=-1, out=None, 
     behind the end and before a parent outside [0, K)."""
     import torch
 
-    lib = load_library()
+    lib = _lib or load_library()
     if tokens.dim() != 3:
         raise ValueError("tokens must be 3-D [T, N, K]")
     T, N, K = tokens.shape
@@ -580,20 +591,21 @@ def beam_backtrace(tokens, parents, beams=None, lengths=None, pad=-1, out=None, 
     if ends is not None and ends.dim() != 2:
         raise ValueError("beams and lengths must be 2-D [N, M]")
     M = K if ends is None else ends.shape[1]
-    _check_dense(tokens, (T, N, K), torch.int32, "tokens")
-    _check_dense(parents, (T, N, K), torch.int32, "parents")
-    _check_dense(beams, (N, M), torch.int32, "beams")
-    _check_dense(lengths, (N, M), torch.int32, "lengths")
-    dev = tokens.device
-    _check_device(dev, tokens, parents, beams, lengths)
-    handle, scope = _scope(stream, dev)
+    dev = tokens.get_device()
+    _check_dense(tokens, (T, N, K), torch.int32, "tokens", dev)
+    _check_dense(parents, (T, N, K), torch.int32, "parents", dev)
+    if beams is not None:
+        _check_dense(beams, (N, M), torch.int32, "beams", dev)
+    if lengths is not None:
+        _check_dense(lengths, (N, M), torch.int32, "lengths", dev)
+    handle, scope = _scope(stream, tokens.device)
     with scope:
         if out is None:
-            out = torch.empty((N, M, T), dtype=torch.int32, device=dev)
-        _check_dense(out, (N, M, T), torch.int32, "out")
-        _check_device(dev, out)
-        _check(lib.beam_backtrace(tokens.data_ptr(), parents.data_ptr(), T, N, K,
-                                  None if beams is None else beams.data_ptr(),
-                                  None if lengths is None else lengths.data_ptr(), M, int(pad), out.data_ptr(),
-                                  handle))
+            out = torch.empty((N, M, T), dtype=torch.int32, device=tokens.device)
+        _check_dense(out, (N, M, T), torch.int32, "out", dev)
+        status = lib.beam_backtrace(tokens.data_ptr(), parents.data_ptr(), T, N, K,
+                                    None if beams is None else beams.data_ptr(),
+                                    None if lengths is None else lengths.data_ptr(), M, int(pad), out.data_ptr(),
+                                    handle)
+    _check(status)
     return out
