@@ -12,6 +12,7 @@ import contextlib
 import ctypes
 import functools
 import os
+import struct
 from typing import Optional
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
@@ -379,6 +380,7 @@ def top_k_top_p_sorted_survivors(logits, p=None, k=None, min_p=None, cap=1024, w
     return probs, indices, counts
 
 
+_pack_pointer = struct.Struct("=Q").pack
 _NULL_SCOPE = contextlib.nullcontext()
 
 
@@ -524,6 +526,25 @@ def _state_layout(shape, strides, itemsize, batch_dim, seq_dim):
             position_stride, run)
 
 
+@functools.lru_cache(maxsize=256)
+def _state_bytes(shape, strides, itemsize, batch_dim, seq_dim, rows):
+    """A BeamState as bytes, without the data pointer it begins with."""
+    dims = len(shape)
+    if not -dims <= batch_dim < dims:
+        raise ValueError(f"a state of {dims} axes has no batch_dim {batch_dim}")
+    if shape[batch_dim] != rows:
+        raise ValueError(f"a state must have N * K = {rows} rows, got shape {tuple(shape)}")
+    if seq_dim is not None:
+        if not -dims <= seq_dim < dims or (seq_dim - batch_dim) % dims == 0:
+            raise ValueError(f"a state of {dims} axes has no seq_dim {seq_dim} beside batch_dim {batch_dim}")
+        seq_dim %= dims
+    if 0 in shape:
+        return bytes(ctypes.sizeof(BeamState) - 8)  # nothing to move
+    row_stride, sizes, steps, positions, step, run = _state_layout(tuple(shape), strides, itemsize, batch_dim % dims,
+                                                                   seq_dim)
+    return struct.pack("=10q", row_stride, *sizes, *steps, positions, step, run)
+
+
 def beam_reorder_states(states, parents, batch_dim=0, seq_dim=None, lengths=None, stream=None):
     """Every state's rows follow their beams, in place: along batch_dim (of
     size N * K) row i * K + b becomes what row i * K + parents[i, b] was.
@@ -546,27 +567,16 @@ def beam_reorder_states(states, parents, batch_dim=0, seq_dim=None, lengths=None
         _check_dense(lengths, (N,), torch.int32, "lengths", dev)
         if seq_dim is None:
             raise ValueError("lengths needs seq_dim")
-    descs = (BeamState * len(tensors))()
-    for d, t in zip(descs, tensors):
-        dims = t.dim()
+    seq = None if lengths is None else seq_dim
+    descs = []
+    for t in tensors:
         if t.get_device() != dev:
             raise ValueError(f"tensors must share one device: a state is on {t.device}")
-        if not -dims <= batch_dim < dims:
-            raise ValueError(f"a state of {dims} axes has no batch_dim {batch_dim}")
-        if t.shape[batch_dim] != N * K:
-            raise ValueError(f"a state must have N * K = {N * K} rows, got shape {tuple(t.shape)}")
-        seq = None
-        if lengths is not None:
-            if not -dims <= seq_dim < dims or (seq_dim - batch_dim) % dims == 0:
-                raise ValueError(f"a state of {dims} axes has no seq_dim {seq_dim} beside batch_dim {batch_dim}")
-            seq = seq_dim % dims
-        if t.is_complex() and t.is_conj() or t.is_neg():
+        if t.is_neg() or (t.is_complex() and t.is_conj()):
             raise ValueError("a state must not be a lazily conjugated or negated view")
-        if t.numel() == 0:
-            continue  # an all-zero description: nothing to move
-        d.data = t.data_ptr()
-        d.row_stride, d.size[:], d.stride[:], d.positions, d.position_stride, d.run = _state_layout(
-            tuple(t.shape), t.stride(), t.element_size(), batch_dim % dims, seq)
+        descs.append(_pack_pointer(t.data_ptr()))
+        descs.append(_state_bytes(t.shape, t.stride(), t.element_size(), batch_dim, seq, N * K))
+    descs = b"".join(descs)
     handle, scope = _scope(stream, parents.device)
     with scope:
         status = lib.beam_reorder_states(descs, len(tensors), parents.data_ptr(), N, K,

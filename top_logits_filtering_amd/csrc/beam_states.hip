@@ -28,15 +28,13 @@ struct MoveState {
   Div run;             // columns per run; run.d == 0: positions are contiguous
   uint32_t columns;    // panels * columns per panel
   uint32_t run_bytes;  // bytes of a position, for the length's end
-  int64_t block0;      // first block of this state
 };
 
 struct MoveArgs {
+  uint32_t first[kMaxStates];  // each state's first block; the largest number behind the last state
   MoveState state[kMaxStates];
-  int count;
+  Div items;
   int K;
-  int64_t N;
-  int64_t block0;
   const int32_t* parents;
   const int32_t* lengths;
 };
@@ -56,13 +54,13 @@ struct Column<1> { using type = uint8_t; };
 template <int KMAX, int W, int U>
 __global__ __launch_bounds__(kMoveThreads) void beam_move_kernel(const MoveArgs a) {
   using col_t = typename Column<W>::type;
-  const int64_t block = a.block0 + blockIdx.x;
   int si = 0;
-  while (si + 1 < a.count && block >= a.state[si + 1].block0) ++si;
+#pragma unroll
+  for (int i = 1; i < kMaxStates; ++i) si += blockIdx.x >= a.first[i] ? 1 : 0;
   const MoveState& s = a.state[si];
-  const int64_t local = block - s.block0;
-  const int64_t item = local % a.N;
-  const int64_t tile = local / a.N;
+  const uint32_t local = blockIdx.x - a.first[si];
+  const uint32_t tile = quotient(local, a.items);
+  const int64_t item = local - tile * a.items.d;
 
   const int32_t* __restrict__ parents = a.parents + item * a.K;
   const int64_t len = a.lengths != nullptr ? a.lengths[item] : INT64_MAX;
@@ -73,12 +71,12 @@ __global__ __launch_bounds__(kMoveThreads) void beam_move_kernel(const MoveArgs 
   int live[U];
 #pragma unroll
   for (int u = 0; u < U; ++u) {
-    const uint64_t c = static_cast<uint64_t>(tile) * (kMoveThreads * U) + u * kMoveThreads + threadIdx.x;
+    const uint32_t c = tile * (kMoveThreads * U) + u * kMoveThreads + threadIdx.x;
     live[u] = 0;
     off[u] = 0;
     if (c < s.columns) {
-      const uint32_t p = quotient(static_cast<uint32_t>(c), s.panel);
-      const uint32_t j = static_cast<uint32_t>(c) - p * s.panel.d;
+      const uint32_t p = quotient(c, s.panel);
+      const uint32_t j = c - p * s.panel.d;
       const uint32_t p2 = quotient(p, s.size2), i2 = p - p2 * s.size2.d;
       const uint32_t i0 = quotient(p2, s.size1), i1 = p2 - i0 * s.size1.d;
       off[u] = i0 * s.stride[0] + i1 * s.stride[1] + i2 * s.stride[2];
@@ -161,18 +159,40 @@ uint64_t row_bytes(const BeamState& s) {
   return n;
 }
 
+// Launches a.state[0, count) for all N prompts, as many of them at a time as
+// keep a grid below 2^32 threads.
 template <int KMAX, int W, int U>
-hipError_t move_all(MoveArgs& a, hipStream_t stream) {
-  int64_t blocks = 0;
-  for (int i = 0; i < a.count; ++i) {
-    a.state[i].block0 = blocks;
-    blocks += (static_cast<int64_t>(a.state[i].columns) + kMoveThreads * U - 1) / (kMoveThreads * U) * a.N;
+hipError_t move_all(const MoveArgs& a, int count, int64_t N, hipStream_t stream) {
+  constexpr int64_t kMost = int64_t{1} << 23;
+  int64_t tiles[kMaxStates], sum = 0;
+  for (int i = 0; i < count; ++i) {
+    tiles[i] = (static_cast<int64_t>(a.state[i].columns) + kMoveThreads * U - 1) / (kMoveThreads * U);
+    sum += tiles[i];
   }
-  const int64_t step = int64_t{1} << 23;  // a grid holds below 2^32 threads
-  for (a.block0 = 0; a.block0 < blocks; a.block0 += step) {
-    const int64_t n = blocks - a.block0 < step ? blocks - a.block0 : step;
-    hipLaunchKernelGGL((beam_move_kernel<KMAX, W, U>), dim3(static_cast<unsigned>(n)), dim3(kMoveThreads), 0, stream,
-                       a);
+  if (sum > kMost && count > 1) {
+    for (int i = 0; i < count; ++i) {
+      MoveArgs one = a;
+      one.state[0] = a.state[i];
+      if (const hipError_t e = move_all<KMAX, W, U>(one, 1, N, stream)) return e;
+    }
+    return hipSuccess;
+  }
+  const int64_t step = kMost / sum;  // tiles of one state are below 2^23
+  for (int64_t n0 = 0; n0 < N; n0 += step) {
+    const int64_t n = N - n0 < step ? N - n0 : step;
+    MoveArgs b = a;
+    int64_t blocks = 0;
+    for (int i = 0; i < kMaxStates; ++i) {
+      b.first[i] = i < count ? static_cast<uint32_t>(blocks) : 0xFFFFFFFFu;
+      if (i >= count) continue;
+      b.state[i].data += n0 * a.K * a.state[i].row_stride;
+      blocks += tiles[i] * n;
+    }
+    b.items = make_div(static_cast<uint32_t>(n));
+    b.parents += n0 * a.K;
+    if (b.lengths != nullptr) b.lengths += n0;
+    hipLaunchKernelGGL((beam_move_kernel<KMAX, W, U>), dim3(static_cast<unsigned>(blocks)), dim3(kMoveThreads), 0,
+                       stream, b);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
@@ -190,10 +210,11 @@ hipError_t launch_beam_reorder(const BeamState* states, int count, const int32_t
   // states of one column width share a launch
   for (const int w : {16, 4, 2, 1}) {
     MoveArgs a{};
+    int held = 0;
     for (int i = 0; i < count; ++i) {
       const BeamState& s = states[i];
       if (column_bytes(s, K) != w) continue;
-      MoveState& m = a.state[a.count++];
+      MoveState& m = a.state[held++];
       m.data = s.data;
       m.row_stride = s.row_stride;
       for (int k = 0; k < 3; ++k) m.stride[k] = s.stride[k];
@@ -207,21 +228,20 @@ hipError_t launch_beam_reorder(const BeamState* states, int count, const int32_t
       m.columns = static_cast<uint32_t>(per * static_cast<uint64_t>(s.size[0] * s.size[1] * s.size[2]));
       m.run_bytes = static_cast<uint32_t>(s.run);
     }
-    if (a.count == 0) continue;
-    a.N = N;
+    if (held == 0) continue;
     a.K = K;
     a.parents = parents;
     a.lengths = lengths;
     hipError_t e;
     if (w == 16) {
-      if (K <= 4) e = move_all<4, 16, 4>(a, stream);
-      else if (K <= 8) e = move_all<8, 16, 2>(a, stream);
-      else if (K <= 16) e = move_all<16, 16, 1>(a, stream);
-      else e = move_all<32, 16, 1>(a, stream);
+      if (K <= 4) e = move_all<4, 16, 4>(a, held, N, stream);
+      else if (K <= 8) e = move_all<8, 16, 2>(a, held, N, stream);
+      else if (K <= 16) e = move_all<16, 16, 1>(a, held, N, stream);
+      else e = move_all<32, 16, 1>(a, held, N, stream);
     } else if (w == 4) {
-      e = K <= 32 ? move_all<32, 4, 1>(a, stream) : move_all<128, 4, 1>(a, stream);
+      e = K <= 32 ? move_all<32, 4, 1>(a, held, N, stream) : move_all<128, 4, 1>(a, held, N, stream);
     } else {
-      e = w == 2 ? move_all<128, 2, 1>(a, stream) : move_all<128, 1, 1>(a, stream);
+      e = w == 2 ? move_all<128, 2, 1>(a, held, N, stream) : move_all<128, 1, 1>(a, held, N, stream);
     }
     if (e != hipSuccess) return e;
   }
