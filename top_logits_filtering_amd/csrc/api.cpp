@@ -517,11 +517,13 @@ topktopp_status beam_reorder_states(const topktopp_beam_state* states, int64_t c
   if (count == 0 || N == 0) return TOPKTOPP_OK;
   if (states == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "states is NULL");
   if (parents == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "parents is NULL");
+  int64_t total = 0;
   for (int64_t i = 0; i < count; ++i) {
     const tkp::BeamState s = state_of(states[i]);
     size_t bytes;
     if (topktopp_status e = state_span(s, N * K, &bytes)) return e;
     if (bytes == 0) continue;
+    total += static_cast<int64_t>(bytes);
     if (s.data == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "data of state %lld is NULL", (long long)i);
     if (!tkp::beam_state_fits(s, static_cast<int>(K)))
       return fail(TOPKTOPP_ERR_INVALID, "a row of state %lld has more than 2^31-1 columns", (long long)i);
@@ -544,7 +546,7 @@ topktopp_status beam_reorder_states(const topktopp_beam_state* states, int64_t c
     }
     if (flush && held > 0) {
       const hipError_t e = tkp::launch_beam_reorder(batch, held, parents, N, static_cast<int>(K), lengths,
-                                                    static_cast<hipStream_t>(stream));
+                                                    total, static_cast<hipStream_t>(stream));
       if (e != hipSuccess) return check_launch(e, "reorder launch");
       held = 0;
     }

@@ -63,9 +63,10 @@ constexpr int kMaxStates = 24;
 
 // Whether launch_beam_reorder takes the state: its units per row stay below 2^31.
 bool beam_state_fits(const BeamState& s, int K);
-// count <= kMaxStates states whose memory is disjoint.
+// count <= kMaxStates states whose memory is disjoint; bytes: what all states
+// of the call hold together.
 hipError_t launch_beam_reorder(const BeamState* states, int count, const int32_t* parents, int64_t N, int K,
-                               const int32_t* lengths, hipStream_t stream);
+                               const int32_t* lengths, int64_t bytes, hipStream_t stream);
 
 struct BeamBacktraceArgs {
   const int32_t* tokens;   // [T, N, K]
