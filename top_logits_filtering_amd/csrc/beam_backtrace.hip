@@ -17,32 +17,37 @@
 namespace tkp {
 namespace {
 
-constexpr int kTraceThreads = 512;
-constexpr int kSegment = 16;       // steps of a segment, and segments of a group
-constexpr int kTracePaths = 32;    // hypotheses of a workgroup at most
-constexpr int kTraceBytes = 49152; // parents and paths of a piece
-constexpr int kMapBytes = kTraceBytes / kSegment + 512;
+constexpr int kTraceThreads = 1024;
+constexpr int kSegment = 16;        // steps of a segment, and segments of a group
+constexpr int kTracePaths = 32;     // hypotheses of a workgroup at most
+constexpr int kTraceBytes = 49152;  // parents and paths of a piece
 constexpr int kTraceBeams = 128;
+constexpr int kRowMost = kTraceBeams + 4;
+constexpr int kMapBytes = kTraceBytes / kSegment + kSegment * kRowMost;
+constexpr int kGroupBytes = kMapBytes / kSegment + kRowMost;
+constexpr int kTraceUnroll = 4;
+constexpr int kTraceTarget = 256;   // workgroups wanted
 constexpr int kDies = 8;
-constexpr int kTraceUnroll = 8;
-constexpr int kTraceTarget = 256;  // workgroups wanted
-constexpr uint8_t kNowhere = 255;
+
+// Bytes of a step's parents: K beams, and at K the beam "nowhere", which stays nowhere.
+__host__ __device__ constexpr int row_bytes_of(int K) { return (K + 4) & ~3; }
 
 struct TraceSmem {
-  uint8_t bytes[kTraceBytes];
+  alignas(16) uint8_t bytes[kTraceBytes];
   // beam before a segment (a group), by the beam in its last step
-  uint8_t map[kMapBytes];
-  uint8_t group_map[kMapBytes / kSegment + kTraceBeams];
-  // a path's beam in the last step of a segment (a group), or where it begins
+  alignas(16) uint8_t map[kMapBytes];
+  uint8_t group_map[kGroupBytes];
+  // a path's beam in the last step of a segment (a group); nowhere where it has not begun
   uint8_t entry[kMapBytes];
-  uint8_t group_entry[kMapBytes / kSegment + kTracePaths];
+  uint8_t group_entry[kGroupBytes];
   uint8_t begin[kTracePaths];  // the beam at which a path begins
-  uint8_t at[kTracePaths];     // its beam before the segment, the group, the piece where it was last
+  uint8_t at[kTracePaths];     // its beam before what was passed last
   int end[kTracePaths];        // its last step
 };
 
-__global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBacktraceArgs a, Div beams, Div tiles,
-                                                                       int paths, int steps, int64_t step_stride) {
+__global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBacktraceArgs a, Div beams, Div quads,
+                                                                       Div tiles, int paths, int steps,
+                                                                       int64_t step_stride) {
   __shared__ TraceSmem sm;
   const int tid = threadIdx.x;
   // Neighbouring prompts share cache lines of the history, and workgroups go to
@@ -53,9 +58,9 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
   const int64_t item = item32;
   const int m0 = static_cast<int>(block - item32 * tiles.d) * paths;
   const int M = a.M - m0 < paths ? a.M - m0 : paths;
-  const int K = a.K, T = static_cast<int>(a.T);
-  uint8_t* parent = sm.bytes;            // [steps][K]
-  uint8_t* path = sm.bytes + steps * K;  // [M][steps]
+  const int K = a.K, T = static_cast<int>(a.T), row = row_bytes_of(K);
+  uint8_t* parent = sm.bytes;              // [steps][row]
+  uint8_t* path = sm.bytes + steps * row;  // [M][steps]
   const int64_t at0 = item * K;
 
   if (tid < M) {
@@ -64,72 +69,104 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
     len = len < 0 ? 0 : (len > T ? T : len);
     const int b = a.beams != nullptr ? a.beams[h] : m0 + tid;
     sm.end[tid] = len - 1;
-    sm.begin[tid] = b >= 0 && b < K ? static_cast<uint8_t>(b) : kNowhere;
-    sm.at[tid] = kNowhere;
+    sm.begin[tid] = static_cast<uint8_t>(b >= 0 && b < K ? b : K);
+    sm.at[tid] = static_cast<uint8_t>(K);
   }
 
-  for (int t1 = T; t1 > 0; t1 -= steps) {  // the piece [t0, t1)
+  for (int t1 = T; t1 > 0; t1 -= steps) {  // the piece [t0, t1), filled up with steps that change nothing
     const int t0 = t1 > steps ? t1 - steps : 0;
     const int n = t1 - t0;
     const int segs = (n + kSegment - 1) / kSegment, groups = (segs + kSegment - 1) / kSegment;
-    auto last_of = [&](int s) { return ((s + 1) * kSegment < n ? (s + 1) * kSegment : n) - 1; };
-    auto last_seg = [&](int g) { return ((g + 1) * kSegment < segs ? (g + 1) * kSegment : segs) - 1; };
     lds_barrier();
     const int32_t* __restrict__ from = a.parents + t0 * step_stride + at0;
-    for (int f0 = tid; f0 < n * K; f0 += kTraceUnroll * kTraceThreads) {
-      int p[kTraceUnroll];
+    auto byte_of = [&](int p) -> uint32_t { return p >= 0 && p < K ? p : K; };
+    if (quads.d != 0) {  // four beams at a time: their addresses are aligned
+      const int count = n * static_cast<int>(quads.d);
+      for (int f0 = tid; f0 < count; f0 += kTraceUnroll * kTraceThreads) {
+        int4 p[kTraceUnroll];
 #pragma unroll
-      for (int u = 0; u < kTraceUnroll; ++u) {
-        const int f = f0 + u * kTraceThreads;
-        const int t = static_cast<int>(quotient(static_cast<uint32_t>(f), beams));
-        p[u] = f < n * K ? from[t * step_stride + (f - t * K)] : -1;
+        for (int u = 0; u < kTraceUnroll; ++u) {
+          const int f = f0 + u * kTraceThreads;
+          const int t = static_cast<int>(quotient(static_cast<uint32_t>(f), quads));
+          p[u] = int4{0, 0, 0, 0};
+          if (f < count)
+            p[u] = *reinterpret_cast<const int4*>(from + t * step_stride + (f - t * static_cast<int>(quads.d)) * 4);
+        }
+#pragma unroll
+        for (int u = 0; u < kTraceUnroll; ++u) {
+          const int f = f0 + u * kTraceThreads;
+          const int t = static_cast<int>(quotient(static_cast<uint32_t>(f), quads));
+          if (f < count)
+            *reinterpret_cast<uint32_t*>(parent + t * row + (f - t * static_cast<int>(quads.d)) * 4) =
+                byte_of(p[u].x) | byte_of(p[u].y) << 8 | byte_of(p[u].z) << 16 | byte_of(p[u].w) << 24;
+        }
       }
+    } else {
+      for (int f0 = tid; f0 < n * K; f0 += kTraceUnroll * kTraceThreads) {
+        int p[kTraceUnroll];
 #pragma unroll
-      for (int u = 0; u < kTraceUnroll; ++u) {
-        const int f = f0 + u * kTraceThreads;
-        if (f < n * K) parent[f] = p[u] >= 0 && p[u] < K ? static_cast<uint8_t>(p[u]) : kNowhere;
+        for (int u = 0; u < kTraceUnroll; ++u) {
+          const int f = f0 + u * kTraceThreads;
+          const int t = static_cast<int>(quotient(static_cast<uint32_t>(f), beams));
+          p[u] = f < n * K ? from[t * step_stride + (f - t * K)] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < kTraceUnroll; ++u) {
+          const int f = f0 + u * kTraceThreads;
+          const int t = static_cast<int>(quotient(static_cast<uint32_t>(f), beams));
+          if (f < n * K) parent[t * row + (f - t * K)] = static_cast<uint8_t>(byte_of(p[u]));
+        }
       }
     }
+    for (int t = tid; t < segs * kSegment; t += kTraceThreads) {
+      if (t < n) {
+        parent[t * row + K] = static_cast<uint8_t>(K);
+      } else {
+        for (int k = 0; k <= K; ++k) parent[t * row + k] = static_cast<uint8_t>(k);
+      }
+    }
+    for (int s = segs + tid; s < groups * kSegment; s += kTraceThreads)
+      for (int k = 0; k <= K; ++k) sm.map[s * row + k] = static_cast<uint8_t>(k);
     lds_barrier();
 
-    // the segments' maps; and where the paths that begin in this piece are before their first segment
+    // the segments' maps, and each path's beam before the segment in which it begins
     for (int f = tid; f < segs * K + M; f += kTraceThreads) {
-      if (f < segs * K) {
-        const int s = static_cast<int>(quotient(static_cast<uint32_t>(f), beams));
-        int b = f - s * K;
-        for (int t = last_of(s); t >= s * kSegment && b != kNowhere; --t) b = parent[t * K + b];
-        sm.map[f] = static_cast<uint8_t>(b);
-      } else {
-        const int m = f - segs * K, e = sm.end[m] - t0;
-        if (e >= 0 && e < n) {
-          int b = sm.begin[m];
-          for (int t = e; t >= e / kSegment * kSegment && b != kNowhere; --t) b = parent[t * K + b];
-          sm.at[m] = static_cast<uint8_t>(b);
-        }
+      const bool own = f >= segs * K;
+      const int m = f - segs * K, e = own ? sm.end[m] - t0 : -1;
+      if (own && (e < 0 || e >= n)) continue;
+      const int s = own ? e / kSegment : static_cast<int>(quotient(static_cast<uint32_t>(f), beams));
+      const int k = f - s * K, begin = own ? sm.begin[m] : K;
+      int b = own ? K : k;
+#pragma unroll
+      for (int i = kSegment - 1; i >= 0; --i) {
+        if (s * kSegment + i == e) b = begin;
+        b = parent[(s * kSegment + i) * row + b];
       }
+      if (own) sm.at[m] = static_cast<uint8_t>(b);
+      else sm.map[s * row + k] = static_cast<uint8_t>(b);
     }
+    for (int s = tid; s < segs; s += kTraceThreads) sm.map[s * row + K] = static_cast<uint8_t>(K);
     lds_barrier();
-    // the same with groups
+    // the same with groups, whose steps are segments
     for (int f = tid; f < groups * K + M; f += kTraceThreads) {
-      if (f < groups * K) {
-        const int g = static_cast<int>(quotient(static_cast<uint32_t>(f), beams));
-        int b = f - g * K;
-        for (int s = last_seg(g); s >= g * kSegment && b != kNowhere; --s) b = sm.map[s * K + b];
-        sm.group_map[f] = static_cast<uint8_t>(b);
-      } else {
-        const int m = f - groups * K, e = sm.end[m] - t0;
-        if (e >= 0 && e < n) {
-          const int first = e / kSegment;
-          int b = sm.at[m];
-          sm.entry[first * M + m] = sm.begin[m];
-          for (int s = first - 1; s >= first / kSegment * kSegment; --s) {
-            sm.entry[s * M + m] = static_cast<uint8_t>(b);
-            if (b != kNowhere) b = sm.map[s * K + b];
-          }
-          sm.at[m] = static_cast<uint8_t>(b);
-        }
+      const bool own = f >= groups * K;
+      const int m = f - groups * K, e = own ? sm.end[m] - t0 : -1;
+      if (own && (e < 0 || e >= n)) continue;
+      const int s = own ? e / kSegment : -1;
+      const int g = own ? s / kSegment : static_cast<int>(quotient(static_cast<uint32_t>(f), beams));
+      const int k = f - g * K, begin = own ? sm.at[m] : K;
+      int b = own ? K : k;
+#pragma unroll
+      for (int i = kSegment - 1; i >= 0; --i) {
+        const int q = g * kSegment + i;
+        const int next = sm.map[q * row + b];
+        if (own && q < segs) sm.entry[q * M + m] = static_cast<uint8_t>(b);
+        b = q == s ? begin : next;
       }
+      if (own) sm.at[m] = static_cast<uint8_t>(b);
+      else sm.group_map[g * row + k] = static_cast<uint8_t>(b);
     }
+    for (int g = tid; g < groups; g += kTraceThreads) sm.group_map[g * row + K] = static_cast<uint8_t>(K);
     lds_barrier();
     // a path's way through the groups that it passes from end to end
     if (tid < M) {
@@ -138,7 +175,7 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
       int b = sm.at[tid];
       for (; g >= 0; --g) {
         sm.group_entry[g * M + tid] = static_cast<uint8_t>(b);
-        if (b != kNowhere) b = sm.group_map[g * K + b];
+        b = sm.group_map[g * row + b];
       }
       sm.at[tid] = static_cast<uint8_t>(b);
     }
@@ -148,20 +185,25 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
       const int g = f / M, m = f - g * M, e = sm.end[m] - t0;
       if (e >= n || e / (kSegment * kSegment) > g) {
         int b = sm.group_entry[g * M + m];
-        for (int s = last_seg(g); s >= g * kSegment; --s) {
-          sm.entry[s * M + m] = static_cast<uint8_t>(b);
-          if (b != kNowhere) b = sm.map[s * K + b];
+#pragma unroll
+        for (int i = kSegment - 1; i >= 0; --i) {
+          const int q = g * kSegment + i;
+          if (q < segs) sm.entry[q * M + m] = static_cast<uint8_t>(b);
+          b = sm.map[q * row + b];
         }
       }
     }
     lds_barrier();
     // and through their steps
     for (int f = tid; f < segs * M; f += kTraceThreads) {
-      const int s = f / M, m = f - s * M, e = sm.end[m] - t0;
-      int b = e >= s * kSegment ? sm.entry[s * M + m] : kNowhere;
-      for (int t = last_of(s); t >= s * kSegment; --t) {
-        path[m * steps + t] = t > e ? kNowhere : static_cast<uint8_t>(b);
-        if (t <= e && b != kNowhere) b = parent[t * K + b];
+      const int s = f / M, m = f - s * M, e = sm.end[m] - t0, begin = sm.begin[m];
+      int b = e >= (s + 1) * kSegment ? sm.entry[s * M + m] : K;
+#pragma unroll
+      for (int i = kSegment - 1; i >= 0; --i) {
+        const int t = s * kSegment + i;
+        if (t == e) b = begin;
+        if (t < n) path[m * steps + t] = static_cast<uint8_t>(b);
+        b = parent[t * row + b];
       }
     }
     lds_barrier();
@@ -174,8 +216,8 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
 #pragma unroll
         for (int u = 0; u < kTraceUnroll; ++u) {
           const int t = s0 + u * kTraceThreads;
-          const int b = t < n ? path[m * steps + t] : kNowhere;
-          v[u] = b != kNowhere ? tokens[t * step_stride + b] : a.pad;
+          const int b = t < n ? path[m * steps + t] : K;
+          v[u] = b < K ? tokens[t * step_stride + b] : a.pad;
         }
 #pragma unroll
         for (int u = 0; u < kTraceUnroll; ++u)
@@ -194,8 +236,12 @@ hipError_t launch_beam_backtrace(const BeamBacktraceArgs& a, hipStream_t stream)
   paths = paths < kTracePaths ? paths : kTracePaths;
   paths = paths < a.M ? paths : a.M;
   const int tiles = static_cast<int>((a.M + paths - 1) / paths);
-  const int64_t fit = kTraceBytes / (a.K + paths) / kSegment * kSegment;
-  const int steps = static_cast<int>(a.T < fit ? a.T : fit);
+  // steps of a piece, whole segments
+  const int64_t fit = kTraceBytes / (row_bytes_of(a.K) + paths) / kSegment * kSegment;
+  const int64_t whole = (a.T + kSegment - 1) / kSegment * kSegment;
+  const int steps = static_cast<int>(whole < fit ? whole : fit);
+  const bool aligned = a.K % 4 == 0 && reinterpret_cast<uintptr_t>(a.parents) % 16 == 0;
+  const Div quads = aligned ? make_div(static_cast<uint32_t>(a.K / 4)) : Div{0, 0, 0};
   const int64_t most = int64_t{1} << 22;  // a grid holds below 2^32 threads
   const int64_t per = most / tiles > 0 ? most / tiles : 1;
   for (int64_t i = 0; i < a.N; i += per) {
@@ -209,7 +255,7 @@ hipError_t launch_beam_backtrace(const BeamBacktraceArgs& a, hipStream_t stream)
     b.out += i * a.M * a.T;
     hipLaunchKernelGGL(beam_backtrace_kernel, dim3(static_cast<unsigned>((items * tiles + kDies - 1) / kDies * kDies)),
                        dim3(kTraceThreads), 0,
-                       stream, b, make_div(static_cast<uint32_t>(a.K)), make_div(static_cast<uint32_t>(tiles)),
+                       stream, b, make_div(static_cast<uint32_t>(a.K)), quads, make_div(static_cast<uint32_t>(tiles)),
                        static_cast<int>(paths), steps, a.N * a.K);
     if (const hipError_t e = hipGetLastError()) return e;
   }
