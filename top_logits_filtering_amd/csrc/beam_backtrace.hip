@@ -46,7 +46,7 @@ struct TraceSmem {
 };
 
 __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBacktraceArgs a, Div beams, Div quads,
-                                                                       Div tiles, int paths, int steps,
+                                                                       Div tiles, int paths, Div piece,
                                                                        int64_t step_stride) {
   __shared__ TraceSmem sm;
   const int tid = threadIdx.x;
@@ -59,6 +59,7 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
   const int m0 = static_cast<int>(block - item32 * tiles.d) * paths;
   const int M = a.M - m0 < paths ? a.M - m0 : paths;
   const int K = a.K, T = static_cast<int>(a.T), row = row_bytes_of(K);
+  const int steps = static_cast<int>(piece.d);
   uint8_t* parent = sm.bytes;              // [steps][row]
   uint8_t* path = sm.bytes + steps * row;  // [M][steps]
   const int64_t at0 = item * K;
@@ -209,19 +210,21 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
     lds_barrier();
 
     const int32_t* __restrict__ tokens = a.tokens + t0 * step_stride + at0;
-    for (int m = 0; m < M; ++m) {
-      int32_t* __restrict__ out = a.out + (item * a.M + m0 + m) * a.T + t0;
-      for (int s0 = tid; s0 < n; s0 += kTraceUnroll * kTraceThreads) {
-        int32_t v[kTraceUnroll];
+    int32_t* __restrict__ out = a.out + (item * a.M + m0) * a.T + t0;
+    for (int f0 = tid; f0 < M * steps; f0 += kTraceUnroll * kTraceThreads) {
+      int32_t v[kTraceUnroll];
 #pragma unroll
-        for (int u = 0; u < kTraceUnroll; ++u) {
-          const int t = s0 + u * kTraceThreads;
-          const int b = t < n ? path[m * steps + t] : K;
-          v[u] = b < K ? tokens[t * step_stride + b] : a.pad;
-        }
+      for (int u = 0; u < kTraceUnroll; ++u) {
+        const int f = f0 + u * kTraceThreads, m = static_cast<int>(quotient(static_cast<uint32_t>(f), piece));
+        const int t = f - m * steps;
+        const int b = f < M * steps && t < n ? path[f] : K;
+        v[u] = b < K ? tokens[t * step_stride + b] : a.pad;
+      }
 #pragma unroll
-        for (int u = 0; u < kTraceUnroll; ++u)
-          if (s0 + u * kTraceThreads < n) out[s0 + u * kTraceThreads] = v[u];
+      for (int u = 0; u < kTraceUnroll; ++u) {
+        const int f = f0 + u * kTraceThreads, m = static_cast<int>(quotient(static_cast<uint32_t>(f), piece));
+        const int t = f - m * steps;
+        if (f < M * steps && t < n) out[m * a.T + t] = v[u];
       }
     }
   }
@@ -256,7 +259,7 @@ hipError_t launch_beam_backtrace(const BeamBacktraceArgs& a, hipStream_t stream)
     hipLaunchKernelGGL(beam_backtrace_kernel, dim3(static_cast<unsigned>((items * tiles + kDies - 1) / kDies * kDies)),
                        dim3(kTraceThreads), 0,
                        stream, b, make_div(static_cast<uint32_t>(a.K)), quads, make_div(static_cast<uint32_t>(tiles)),
-                       static_cast<int>(paths), steps, a.N * a.K);
+                       static_cast<int>(paths), make_div(static_cast<uint32_t>(steps)), a.N * a.K);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
