@@ -314,7 +314,7 @@ topktopp_status top_k_top_p_sorted_survivors(const void* logits, topktopp_dtype 
  * Numerics. A sum of exp has a relative error below 3.6e-7, what follows is
  * formed in 64 bits and rounded once, to out_scores. Where two beams'
  * continuations come closer than that error, their sums are formed again in
- * 64 bits (relative error below 1e-10), so the order is that of 64-bit values.
+ * 64 bits, so the order is that of 64-bit values.
  * Results are deterministic.
  *
  * Errors: ERR_NULLPTR for logits (unless V is 0), scores, an output or the

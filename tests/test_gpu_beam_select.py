@@ -205,6 +205,22 @@ def test_beams_closer_than_a_32_bit_sum(V, dtype):
     check(torch, x, scores, 5, finished, end=3)
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_equal_beams_at_unequal_addresses(dtype):
+    """Beams with the same logits and scores tie, also where their rows begin at
+    different offsets from 16 bytes and are summed in another order."""
+    torch = need_gpu()
+    N, K, V = 2, 9, 30001
+    x = make(torch, N * K, V, dtype, seed=1, ld=V + 6)
+    x[:] = x[:1].clone()
+    scores = np.full((N, K), -1.25, np.float32)
+    check(torch, x, scores, 40)
+    x[:] = torch.linspace(-9, 9, V, device="cuda").to(x.dtype)
+    check(torch, x, scores, 40)
+    scores[:, 4] += 1e-7  # and with one that is a step of fp32 better
+    check(torch, x, scores, 40)
+
+
 def test_outputs_stay_inside():
     torch = need_gpu()
     import top_logits_filtering_amd as tk

@@ -82,35 +82,6 @@ __device__ __forceinline__ uint64_t pack(uint32_t key, uint32_t token) {
   return (static_cast<uint64_t>(key) << 32) | (0xFFFFFFFFu - token);
 }
 
-// fma with two constants, one of which waits in a vector register: an
-// instruction reads one scalar operand at most, and the compiler would copy
-// the other one into place every time.
-__device__ __forceinline__ double fma_const(double x, double vreg, double sreg) {
-  double r;
-  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(r) : "v"(x), "v"(vreg), "s"(sreg));
-  return r;
-}
-
-// exp(y) for |y| <= 1100 (finite result for y <= 709).
-__device__ __forceinline__ double exp64(double y) {
-  constexpr double kMagic = 6755399441055744.0;  // 1.5 * 2^52: its low bits hold rint()
-  const double nm = fma_const(y, 1.4426950408889634074, kMagic);
-  const uint32_t k = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, nm));
-  const double f = __builtin_fma(nm - kMagic, -0.69314718055994530942, y);
-  double p = fma_const(f, 0.00019775160531026297389, 0.0013948195139022652005);
-  p = __builtin_fma(p, f, 0.0083335611766106098887);
-  p = __builtin_fma(p, f, 0.041666225250020369325);
-  p = __builtin_fma(p, f, 0.16666665125242092947);
-  p = __builtin_fma(p, f, 0.50000001045984631318);
-  p = __builtin_fma(p, f, 1.0000000002432869351);
-  p = __builtin_fma(p, f, 0.99999999996165148826);
-  // times 2^k: k added to the exponent, as one 32-bit instruction
-  const uint64_t u = __builtin_bit_cast(uint64_t, p);
-  uint32_t hi;
-  asm("v_lshl_add_u32 %0, %1, 20, %2" : "=v"(hi) : "v"(k), "v"(static_cast<uint32_t>(u >> 32)));
-  return __builtin_bit_cast(double, (static_cast<uint64_t>(hi) << 32) | static_cast<uint32_t>(u));
-}
-
 // The chunks' sums are taken of exp(x) itself while the chunk's maximum lies
 // in [kLowMax, kHighMax], which a model's logits do: then no maximum is needed
 // before the sum. Other chunks are read and summed again in 64 bits, less their
@@ -136,10 +107,9 @@ __device__ __forceinline__ float exp_parts(float x, float& rest) {
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr double kSumError = 3.5e-7;
 
-// exp(x - ref) for x - ref below 700, or x = -inf.
+// exp(x - ref) in 64 bits, for finite ref and x below ref + 700 or -inf.
 __device__ __forceinline__ double exp_below(float x, float ref) {
-  const double y = static_cast<double>(x) - static_cast<double>(ref);
-  return y < -700.0 ? 0.0 : exp64(y);
+  return exp(static_cast<double>(x) - static_cast<double>(ref));
 }
 
 // Key bits that tell this dtype's values apart; the bits below them are all
@@ -147,6 +117,14 @@ __device__ __forceinline__ double exp_below(float x, float ref) {
 template <class DT>
 constexpr int key_low_bits() {
   return DT::kPerVec == 4 ? 0 : (DT::kNegInf == 0xFF80u ? 16 : 13);
+}
+
+// Elements of a row of V before its first 16-byte boundary.
+template <class raw_t>
+__device__ __forceinline__ int head_of(const raw_t* row, int V) {
+  const int bytes = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(row) & 15u)) & 15u);
+  const int head = bytes / static_cast<int>(sizeof(raw_t));
+  return head < V ? head : V;
 }
 
 // A beam whose score or weight rules it out proposes nothing.
@@ -282,8 +260,7 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   // the elements behind the last one; the few single elements are held one per
   // thread, in the first and the last chunk.
   const raw_t* rowp = static_cast<const raw_t*>(a.logits) + row * a.ld;
-  int head = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(rowp) & 15u)) & 15u) / static_cast<int>(sizeof(raw_t));
-  head = head < a.V ? head : a.V;
+  const int head = head_of(rowp, a.V);
   const int nfull = (a.V - head) / P;
   const int tail0 = head + nfull * P;
   const int v0 = ch * split.vecs;
@@ -610,7 +587,7 @@ __device__ __forceinline__ bool above(const Cand& a, const Cand& b) {
 
 struct MergeSmem {
   Cand list[kMergeCap + 4];
-  Cand sorted[kMaxCandidates + 2];  // the first n + 1
+  Cand sorted[kMaxCandidates];
   uint32_t upper[kMergeCap];  // the candidates' upper halves of hi
   uint32_t rank[kMergeCap];
   double ref[kMaxBeams];      // L = ref + rest; apart, as ref may be as large as the type goes
@@ -620,7 +597,7 @@ struct MergeSmem {
   int state[kMaxBeams];       // 0: proposes nothing, 1: its lists, 2: finished
   int close[kMaxBeams];       // a candidate comes too close to another beam's
   int again;                  // some do
-  double part[kMergeWaves];
+  uint64_t part[2][kMergeWaves];
   uint32_t heads[kMergeThreads];
   Cand best[kMergeWaves];
   uint32_t count;
@@ -671,33 +648,51 @@ __device__ __forceinline__ void beam_total(const ChunkStat* __restrict__ s, int 
   }
 }
 
-// sum exp(x - ref) over a whole row in 64 bits, by all threads.
+// A sum of terms in [0, 1] that does not depend on their order, so that beams
+// with the same logits get the same sum wherever their rows begin: two integers,
+// in steps of 2^-42 and of 2^-84, exact for 2^20 terms.
+struct ExactSum {
+  int64_t high = 0, low = 0;
+  __device__ __forceinline__ void add(double t) {
+    const double scaled = t * 0x1p42, whole = rint(scaled);
+    high += static_cast<int64_t>(whole);
+    low += static_cast<int64_t>(rint((scaled - whole) * 0x1p42));
+  }
+};
+
+// sum exp(x - top) over a whole row in 64 bits, by all threads; top: its maximum.
 template <class DT>
-__device__ double row_sum(const BeamSelectArgs& a, int64_t row, float ref, MergeSmem& sm) {
+__device__ double row_sum(const BeamSelectArgs& a, int64_t row, float top, MergeSmem& sm) {
   using raw_t = typename DT::raw_t;
   constexpr int P = DT::kPerVec;
   const int tid = threadIdx.x;
   const raw_t* rowp = static_cast<const raw_t*>(a.logits) + row * a.ld;
-  int head = static_cast<int>((16u - (reinterpret_cast<uintptr_t>(rowp) & 15u)) & 15u) / static_cast<int>(sizeof(raw_t));
-  head = head < a.V ? head : a.V;
-  const int nfull = (a.V - head) / P;
-  double sum = 0.0;
-  for (int i = tid; i < head; i += kMergeThreads) sum += exp_below(DT::value(rowp[i]), ref);
-  for (int i = head + nfull * P + tid; i < a.V; i += kMergeThreads) sum += exp_below(DT::value(rowp[i]), ref);
+  const int head = head_of(rowp, a.V), nfull = (a.V - head) / P;
+  ExactSum sum;
+  for (int i = tid; i < head; i += kMergeThreads) sum.add(exp_below(DT::value(rowp[i]), top));
+  for (int i = head + nfull * P + tid; i < a.V; i += kMergeThreads) sum.add(exp_below(DT::value(rowp[i]), top));
   const vec_t* v = reinterpret_cast<const vec_t*>(rowp + head);
   for (int i = tid; i < nfull; i += kMergeThreads) {
     const vec_t q = v[i];
 #pragma unroll 1  // seldom run: kept small in registers
-    for (int j = 0; j < P; ++j) sum += exp_below(DT::value(lane_of_dyn<raw_t>(q, j)), ref);
+    for (int j = 0; j < P; ++j) sum.add(exp_below(DT::value(lane_of_dyn<raw_t>(q, j)), top));
   }
-  sum = wave_sum_f64(sum);
+  const uint64_t high = wave_sum_u64(static_cast<uint64_t>(sum.high));
+  const uint64_t low = wave_sum_u64(static_cast<uint64_t>(sum.low));
   __syncthreads();
-  if (tid % kWave == 0) sm.part[tid / kWave] = sum;
+  if (tid % kWave == 0) {
+    sm.part[0][tid / kWave] = high;
+    sm.part[1][tid / kWave] = low;
+  }
   __syncthreads();
-  sum = 0.0;
+  uint64_t h = 0, l = 0;
 #pragma unroll
-  for (int w = 0; w < kMergeWaves; ++w) sum += sm.part[w];
-  return sum;
+  for (int w = 0; w < kMergeWaves; ++w) {
+    h += sm.part[0][w];
+    l += sm.part[1][w];
+  }
+  const double rest = static_cast<double>(static_cast<int64_t>(l)) * 0x1p-42;
+  return (static_cast<double>(static_cast<int64_t>(h)) + rest) * 0x1p-42;
 }
 
 // The upper half of the image of a rank value by `margin` below T's.
@@ -789,7 +784,9 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
     const uint64_t low = st == 1 ? (static_cast<uint64_t>(key) << kTokenBits) | back : 0;
     return is ? Cand{order_key64(s * sm.weight[b]), beam | low} : Cand{0, 0};
   };
-  auto fetch = [&](uint32_t q, uint32_t j) __attribute__((always_inline)) -> Cand { return cand(mine[q * n + j], q, j); };
+  auto fetch = [&](uint32_t q, uint32_t j) __attribute__((always_inline)) -> Cand {
+    return cand(mine[q * n + j], q, j);
+  };
 
   // Once with the chunks' sums; and, if candidates come too close, once more.
   uint32_t M;
@@ -905,127 +902,147 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       __syncthreads();
     }
 
-    if (M > kMergeCap) {
-      // More candidates share an upper half than the list holds: take the best
-      // ones one by one, each the largest below the last.
+    if (M > kMergeCap && !last && K > 1) {
+      // More candidates share an upper half than the list holds, and which of
+      // them are close is not seen: every sum is formed again.
       __syncthreads();
-      Cand prev{~0ull, ~0ull};
-      uint32_t r = 0;
-      for (; r <= n; ++r) {
-        Cand best{0, 0};
-        for (uint32_t f = tid; f < n * nl; f += kMergeThreads) {
-          const Cand k = fetch(f / n, f % n);
-          if (above(prev, k) && above(k, best)) best = k;
-        }
+      if (tid < K) sm.close[tid] = 1;
+      __syncthreads();
+    } else {
+      if (M > kMergeCap) {
+        // Take the best ones one by one, each the largest below the last.
+        __syncthreads();
+        Cand prev{~0ull, ~0ull};
+        uint32_t r = 0;
+        for (; r < n; ++r) {
+          Cand best{0, 0};
+          for (uint32_t f = tid; f < n * nl; f += kMergeThreads) {
+            const Cand k = fetch(f / n, f % n);
+            if (above(prev, k) && above(k, best)) best = k;
+          }
 #pragma unroll
-        for (int d = 1; d < kWave; d *= 2) {
-          const Cand o{__shfl_xor(best.hi, d), __shfl_xor(best.lo, d)};
-          if (above(o, best)) best = o;
+          for (int d = 1; d < kWave; d *= 2) {
+            const Cand o{__shfl_xor(best.hi, d), __shfl_xor(best.lo, d)};
+            if (above(o, best)) best = o;
+          }
+          __syncthreads();
+          if (lane == 0) sm.best[wave] = best;
+          __syncthreads();
+          best = sm.best[0];
+#pragma unroll
+          for (int w = 1; w < kMergeWaves; ++w)
+            if (above(sm.best[w], best)) best = sm.best[w];
+          if (best.hi == 0) break;
+          if (tid == 0) {
+            sm.list[r] = best;
+            sm.upper[r] = static_cast<uint32_t>(best.hi >> 32);
+          }
+          prev = best;
+        }
+        M = r;
+        __syncthreads();
+      }
+
+      // A long list is cut to what reaches the n-th of its upper halves.
+      if (M > kLongList) {
+        uint32_t cut = 0;
+        if (M <= 8 * kWave) {
+          uint32_t h[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            h[i] = static_cast<uint32_t>(i * kWave + lane) < M ? sm.upper[i * kWave + lane] : 0u;
+          cut = nth_key(h, n, kBoundBits, 0);
+        } else {
+          uint32_t h[kMergeCap / kWave];
+#pragma unroll
+          for (int i = 0; i < kMergeCap / kWave; ++i)
+            h[i] = static_cast<uint32_t>(i * kWave + lane) < M ? sm.upper[i * kWave + lane] : 0u;
+          cut = nth_key(h, n, kBoundBits, 0);
+        }
+        if (cut != 0u) cut = lowered(cut, margin);
+        Cand mine[kMergeCap / kMergeThreads];
+#pragma unroll
+        for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
+          const uint32_t e = u * kMergeThreads + tid;
+          mine[u] = e < M ? sm.list[e] : Cand{0, 0};
         }
         __syncthreads();
-        if (lane == 0) sm.best[wave] = best;
+        if (tid == 0) sm.count = 0;
         __syncthreads();
-        best = sm.best[0];
 #pragma unroll
-        for (int w = 1; w < kMergeWaves; ++w)
-          if (above(sm.best[w], best)) best = sm.best[w];
-        if (best.hi == 0) break;
-        if (tid == 0) {
-          sm.list[r] = best;
-          sm.upper[r] = static_cast<uint32_t>(best.hi >> 32);
+        for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
+          if (mine[u].hi != 0 && static_cast<uint32_t>(mine[u].hi >> 32) >= cut) {
+            const uint32_t at = atomicAdd(&sm.count, 1u);
+            sm.list[at] = mine[u];
+          }
         }
-        prev = best;
+        __syncthreads();
+        M = sm.count;
       }
-      M = r;
-      __syncthreads();
-    }
 
-    // A long list is cut to what reaches the n-th of its upper halves.
-    if (M > kLongList) {
-      uint32_t cut = 0;
-      if (M <= 8 * kWave) {
-        uint32_t h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = static_cast<uint32_t>(i * kWave + lane) < M ? sm.upper[i * kWave + lane] : 0u;
-        cut = nth_key(h, n, kBoundBits, 0);
-      } else {
-        uint32_t h[kMergeCap / kWave];
-#pragma unroll
-        for (int i = 0; i < kMergeCap / kWave; ++i)
-          h[i] = static_cast<uint32_t>(i * kWave + lane) < M ? sm.upper[i * kWave + lane] : 0u;
-        cut = nth_key(h, n, kBoundBits, 0);
-      }
-      if (cut != 0u) cut = lowered(cut, margin);
-      Cand mine[kMergeCap / kMergeThreads];
-#pragma unroll
-      for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
-        const uint32_t e = u * kMergeThreads + tid;
-        mine[u] = e < M ? sm.list[e] : Cand{0, 0};
-      }
-      __syncthreads();
-      if (tid == 0) sm.count = 0;
-      __syncthreads();
-#pragma unroll
-      for (int u = 0; u < kMergeCap / kMergeThreads; ++u) {
-        if (mine[u].hi != 0 && static_cast<uint32_t>(mine[u].hi >> 32) >= cut) {
-          const uint32_t at = atomicAdd(&sm.count, 1u);
-          sm.list[at] = mine[u];
+      // Decode and write.
+      count_ranks<kMergeThreads>(sm.list, sm.rank, M, [](const Cand& x, const Cand& y) { return above(x, y); });
+      for (uint32_t e = tid; e < M; e += kMergeThreads) {
+        const Cand k = sm.list[e];
+        const uint32_t r = sm.rank[e];
+        if (r < n) {
+          sm.sorted[r] = k;
+          const int b = beam_of(k);
+          double s = sm.score[b];
+          int32_t token = a.end_token;
+          if (sm.state[b] == 1) {
+            const uint32_t low = static_cast<uint32_t>(k.lo) & ((1u << kTokenBits) - 1u);
+            s += (static_cast<double>(key_value(static_cast<uint32_t>(k.lo >> kTokenBits))) - sm.ref[b]) - sm.rest[b];
+            token = static_cast<int32_t>(((1u << kTokenBits) - 1u) - low);
+          }
+          const int64_t o = item * n + r;
+          a.out_scores[o] = static_cast<float>(s);
+          a.out_parents[o] = b;
+          a.out_tokens[o] = token;
         }
       }
-      __syncthreads();
-      M = sm.count;
-    }
+      for (uint32_t e = M + tid; e < n; e += kMergeThreads) {
+        const int64_t o = item * n + e;
+        a.out_scores[o] = -INFINITY;
+        a.out_parents[o] = -1;
+        a.out_tokens[o] = -1;
+      }
+      if (last || K == 1) break;
+      lds_barrier();
 
-    // Decode and write.
-    count_ranks<kMergeThreads>(sm.list, sm.rank, M, [](const Cand& x, const Cand& y) { return above(x, y); });
-    for (uint32_t e = tid; e < M; e += kMergeThreads) {
-      const Cand k = sm.list[e];
-      const uint32_t r = sm.rank[e];
-      if (r <= n) sm.sorted[r] = k;
-      if (r < n) {
-        const int b = beam_of(k);
-        double s = sm.score[b];
-        int32_t token = a.end_token;
-        if (sm.state[b] == 1) {
-          const uint32_t low = static_cast<uint32_t>(k.lo) & ((1u << kTokenBits) - 1u);
-          s += (static_cast<double>(key_value(static_cast<uint32_t>(k.lo >> kTokenBits))) - sm.ref[b]) - sm.rest[b];
-          token = static_cast<int32_t>(((1u << kTokenBits) - 1u) - low);
+      // Neighbours of different beams that lie closer than the sums are exact, and
+      // what lies so close behind the n-th: those beams' sums are formed again. (If
+      // all such are equal, they are of beams alike, and stand.)
+      auto value = [](const Cand& k) -> double {
+        return __builtin_bit_cast(double, (k.hi >> 63) ? k.hi & 0x7FFFFFFFFFFFFFFFull : ~k.hi);
+      };
+      auto compare = [&](const Cand& p, const Cand& q) __attribute__((always_inline)) {
+        const int bp = beam_of(p), bq = beam_of(q);
+        if (bp != bq && value(p) - value(q) <= margin) {
+          if (p.hi != q.hi && (sm.state[bp] == 1 || sm.state[bq] == 1)) sm.again = 1;
+          sm.close[bp] = sm.close[bq] = 1;
         }
-        const int64_t o = item * n + r;
-        a.out_scores[o] = static_cast<float>(s);
-        a.out_parents[o] = b;
-        a.out_tokens[o] = token;
-      }
+      };
+      if (static_cast<uint32_t>(tid) + 1u < (M < n ? M : n)) compare(sm.sorted[tid], sm.sorted[tid + 1]);
+      for (uint32_t e = tid; e < M; e += kMergeThreads)
+        if (sm.rank[e] >= n) compare(sm.sorted[n - 1], sm.list[e]);
+      lds_barrier();
+      if (sm.again == 0) break;
+      __syncthreads();  // what this round wrote lies before what the next one writes
     }
-    for (uint32_t e = M + tid; e < n; e += kMergeThreads) {
-      const int64_t o = item * n + e;
-      a.out_scores[o] = -INFINITY;
-      a.out_parents[o] = -1;
-      a.out_tokens[o] = -1;
-    }
-    if (last || K == 1) break;
-    lds_barrier();
-
-    // Neighbours of different beams that lie closer than the sums are exact
-    // (equal ones are beams alike): those beams' sums are formed again.
-    auto value = [](const Cand& k) -> double {
-      return __builtin_bit_cast(double, (k.hi >> 63) ? k.hi & 0x7FFFFFFFFFFFFFFFull : ~k.hi);
-    };
-    if (static_cast<uint32_t>(tid) < n && static_cast<uint32_t>(tid) + 1u < M) {
-      const Cand p = sm.sorted[tid], q = sm.sorted[tid + 1];
-      const int bp = beam_of(p), bq = beam_of(q);
-      if (bp != bq && p.hi != q.hi && value(p) - value(q) <= margin) {
-        if (sm.state[bp] == 1 || sm.state[bq] == 1) sm.again = 1;
-        sm.close[bp] = sm.close[bq] = 1;
-      }
-    }
-    lds_barrier();
-    if (sm.again == 0) break;
-    __syncthreads();  // what this round wrote lies before what the next one writes
     for (int b = 0; b < K; ++b) {
       if (sm.close[b] == 0 || sm.state[b] != 1) continue;
-      const double sum = row_sum<DT>(a, item * K + b, static_cast<float>(sm.ref[b]), sm);
-      if (tid == 0) sm.rest[b] = log(sum);
+      uint64_t most = 0;  // the row's maximum heads one of its lists
+      for (int i = 0; i < C; ++i) {
+        const uint64_t e = mine[static_cast<uint32_t>(b * C + i) * n];
+        most = most > e ? most : e;
+      }
+      const float top = key_value(static_cast<uint32_t>(most >> 32));
+      const double sum = row_sum<DT>(a, item * K + b, top, sm);
+      if (tid == 0) {
+        sm.ref[b] = top;
+        sm.rest[b] = log(sum);
+      }
     }
     if (tid == 0) sm.count = sm.active[0] = 0;
     __syncthreads();
