@@ -192,6 +192,23 @@ def test_backtrace(shape):
     say(f"backtrace {shape}")
 
 
+def test_backtrace_ends_around_pieces():
+    """A history longer than a workgroup holds is taken in pieces from its end;
+    paths that end at every step near where one piece meets the next."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    T, N, K = 1267, 2, 86
+    rng = np.random.default_rng(4)
+    tokens = rng.integers(0, 50000, (T, N, K)).astype(np.int32)
+    parents = rng.integers(0, K, (T, N, K)).astype(np.int32)
+    lengths = np.stack([np.r_[140:220, 690:780], np.r_[1097:1267]]).astype(np.int32)
+    beams = rng.integers(0, K, lengths.shape).astype(np.int32)
+    got = tk.beam_backtrace(*(torch.from_numpy(a).cuda() for a in (tokens, parents, beams, lengths)))
+    torch.cuda.synchronize()
+    assert np.array_equal(got.cpu().numpy(), beam_ref.backtrace(tokens, parents, beams, lengths))
+
+
 def test_backtrace_out_and_graph():
     torch = need_gpu()
     import top_logits_filtering_amd as tk

@@ -197,7 +197,9 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
     lds_barrier();
     // and through their steps
     for (int f = tid; f < segs * M; f += kTraceThreads) {
-      const int s = f / M, m = f - s * M, e = sm.end[m] - t0, begin = sm.begin[m];
+      const int s = f / M, m = f - s * M, begin = sm.begin[m];
+      int e = sm.end[m] - t0;
+      if (e >= n) e = INT32_MAX;  // it begins behind the piece, not in the steps that fill it up
       int b = e >= (s + 1) * kSegment ? sm.entry[s * M + m] : K;
 #pragma unroll
       for (int i = kSegment - 1; i >= 0; --i) {
