@@ -47,7 +47,8 @@ constexpr uint32_t kMergeLists = 1024;  // lists noted as going on
 constexpr uint32_t kGroupBound = 32;    // up to so many candidates 64 maxima give the bound
 constexpr int kBoundBits = 14;          // bits of a bound from the first that differs on
 constexpr uint32_t kAllRanked = 48;     // so many candidates are ranked without a bound
-constexpr uint32_t kLongList = 160;     // a longer list is cut before it is ranked
+constexpr uint32_t kLongList = 320;     // a longer list is cut before it is ranked
+constexpr int kQuadStep = 2;            // reads of four elements that overlap
 constexpr int kMaxBeams = 128;
 constexpr int kMaxCandidates = 256;
 constexpr int kTokenBits = 20;
@@ -178,9 +179,9 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
 }
 
 // rank[e] = how many of list[0, M) rank above list[e]. The threads share each
-// entry's comparisons, so that short lists take few steps. (Reads up to three
-// entries behind the list, which do not count.)
-template <int THREADS, class Item, class Above>
+// entry's comparisons, so that short lists take few steps. (Reads up to
+// STEP - 1 entries behind the list, which do not count.)
+template <int THREADS, uint32_t STEP, class Item, class Above>
 __device__ __forceinline__ void count_ranks(const Item* list, uint32_t* rank, uint32_t M, Above above) {
   const uint32_t tid = threadIdx.x;
   for (uint32_t e = tid; e < M; e += THREADS) rank[e] = 0;
@@ -188,14 +189,14 @@ __device__ __forceinline__ void count_ranks(const Item* list, uint32_t* rank, ui
   uint32_t span = kWave;
   while (span < M && span < THREADS) span *= 2;
   const uint32_t parts = THREADS / span, part = tid / span;
-  const uint32_t seg = ((M + parts - 1) / parts + 3u) & ~3u;
+  const uint32_t seg = (M + parts - 1) / parts;
   const uint32_t j0 = part * seg, j1 = j0 + seg < M ? j0 + seg : M;
   for (uint32_t e = tid & (span - 1u); e < M; e += span) {
     const Item mine = list[e];
     uint32_t r = 0;
-    for (uint32_t j = j0; j < j1; j += 4) {
+    for (uint32_t j = j0; j < j1; j += STEP) {
 #pragma unroll
-      for (uint32_t i = 0; i < 4; ++i) r += above(list[j + i], mine) && j + i < j1 ? 1u : 0u;
+      for (uint32_t i = 0; i < STEP; ++i) r += above(list[j + i], mine) && j + i < j1 ? 1u : 0u;
     }
     if (r != 0) atomicAdd(&rank[e], r);
   }
@@ -203,7 +204,7 @@ __device__ __forceinline__ void count_ranks(const Item* list, uint32_t* rank, ui
 }
 
 struct ChunkSmem {
-  uint64_t list[kChunkCap + 4];
+  uint64_t list[kChunkCap + 8];
   uint32_t rank[kChunkCap];
   uint32_t half[2 * kChunkThreads];  // largest of a thread's even and of its odd units, as keys
   double sum[kChunkWaves];
@@ -467,17 +468,31 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
     struct Quad {
       raw_t r[4];
     };
-    for (uint32_t e = tid; e < hits * kQuads; e += kChunkThreads) {
-      const int h = sm.hit[e / kQuads], part = static_cast<int>(e % kQuads) * 4;
-      const int at = ((h / kChunkThreads) * kUnit + part / P) * kChunkThreads + h % kChunkThreads;
-      const uint32_t token = static_cast<uint32_t>(first + at * P + part % P);
-      Quad q{{DT::kNegInf, DT::kNegInf, DT::kNegInf, DT::kNegInf}};
-      if constexpr (SHORT) q = reinterpret_cast<const Quad*>(sm.unit[e / kQuads])[e % kQuads];
-      else if (at < cnt) q = *reinterpret_cast<const Quad*>(rowp + token);
+    const uint32_t total = hits * kQuads;
+    for (uint32_t e0 = tid; e0 < total; e0 += kQuadStep * kChunkThreads) {
+      Quad q[kQuadStep];
+      uint32_t token[kQuadStep];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = DT::value(q.r[j]);
-        if (x >= bound) push(x, token + j);
+      for (int u = 0; u < kQuadStep; ++u) {
+        q[u] = Quad{{DT::kNegInf, DT::kNegInf, DT::kNegInf, DT::kNegInf}};
+        token[u] = 0;
+        const uint32_t e = e0 + u * kChunkThreads;
+        if (u * kChunkThreads < total && e < total) {
+          const int h = sm.hit[e / kQuads], part = static_cast<int>(e % kQuads) * 4;
+          const int at = ((h / kChunkThreads) * kUnit + part / P) * kChunkThreads + h % kChunkThreads;
+          token[u] = static_cast<uint32_t>(first + at * P + part % P);
+          if constexpr (SHORT) q[u] = reinterpret_cast<const Quad*>(sm.unit[e / kQuads])[e % kQuads];
+          else if (at < cnt) q[u] = *reinterpret_cast<const Quad*>(rowp + token[u]);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kQuadStep; ++u) {
+        if (u * kChunkThreads >= total) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float x = DT::value(q[u].r[j]);
+          if (x >= bound) push(x, token[u] + j);
+        }
       }
     }
   }
@@ -564,7 +579,7 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   }
 
   // The candidates are distinct numbers: each one's place is its rank.
-  count_ranks<kChunkThreads>(sm.list, sm.rank, M, [](uint64_t x, uint64_t y) { return x > y; });
+  count_ranks<kChunkThreads, 8>(sm.list, sm.rank, M, [](uint64_t x, uint64_t y) { return x > y; });
   for (uint32_t e = tid; e < M; e += kChunkThreads) {
     const uint32_t r = sm.rank[e];
     if (r < n) out[r] = sm.list[e];
@@ -981,7 +996,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       }
 
       // Decode and write.
-      count_ranks<kMergeThreads>(sm.list, sm.rank, M, [](const Cand& x, const Cand& y) { return above(x, y); });
+      count_ranks<kMergeThreads, 4>(sm.list, sm.rank, M, [](const Cand& x, const Cand& y) { return above(x, y); });
       for (uint32_t e = tid; e < M; e += kMergeThreads) {
         const Cand k = sm.list[e];
         const uint32_t r = sm.rank[e];
