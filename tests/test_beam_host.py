@@ -144,6 +144,8 @@ def test_binding_refusals():
         (TypeError, (x, c), dict(finished=c, end_token=1)),
         (ValueError, (x, c), dict(finished=torch.zeros(2, 3, dtype=torch.bool))),
         (ValueError, (x, c), dict(finished=torch.zeros(3, 2, dtype=torch.bool), end_token=1)),
+        (ValueError, (x, c), dict(finished=torch.zeros(2, 3, dtype=torch.bool), end_token=2 ** 31)),
+        (ValueError, (x, c), dict(finished=torch.zeros(2, 3, dtype=torch.bool), end_token=-1)),
         (TypeError, (x, c), dict(weights=c.double())), (ValueError, (x, c), dict(weights=torch.zeros(2, 4))),
     ):
         with pytest.raises(err):
@@ -169,6 +171,7 @@ def test_binding_refusals():
         (ValueError, (h, h), dict(beams=torch.zeros(2, **i32))),
         (ValueError, (h, h), dict(beams=torch.zeros(2, 4, **i32), lengths=torch.zeros(2, 3, **i32))),
         (TypeError, (h, h), dict(lengths=torch.zeros(2, 4))),
+        (ValueError, (h, h), dict(pad=2 ** 31)), (ValueError, (h, h), dict(pad=-2 ** 31 - 1)),
     ):
         with pytest.raises(err):
             tk.beam_backtrace(*args, **kw)

@@ -276,3 +276,84 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         for o in outs:
             assert all(torch.equal(a, b) for a, b in zip(o, want[i]))
+
+
+def test_handle_of_the_default_stream():
+    """A stream handle of 0 is the default stream, whichever stream is current."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+    from top_logits_filtering_amd.binding import _scope
+
+    N, K, V = 2, 3, 5000
+    x = make(torch, N * K, V, "f16", seed=8)
+    c = torch.from_numpy(beam_scores(N, K, 8)).cuda()
+    want = [t.clone() for t in tk.beam_search_select(x, c)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        assert _scope(None, x.device)[0] == side.cuda_stream != 0
+        handle, scope = _scope(0, x.device)
+        with scope:
+            assert handle == 0 and torch.cuda.current_stream() == torch.cuda.default_stream()
+        got = tk.beam_search_select(x, c, stream=0)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_one_workspace_for_successive_calls():
+    """It holds nothing between calls: calls of several shapes take the same one in turn."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    shapes = [(3, 4, 9001, 8, "bf16"), (1, 2, 40001, 16, "f32"), (2, 20, 600, 100, "f16"), (3, 4, 9001, 8, "bf16")]
+    size = max(tk.beam_search_select_workspace(getattr(torch, DTYPES[d]), N, K, V, n) for N, K, V, n, d in shapes)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    for i, (N, K, V, n, d) in enumerate(shapes):
+        fin = np.random.default_rng(i).random((N, K)) < 0.3
+        check(torch, make(torch, N * K, V, d, seed=i), beam_scores(N, K, i), n, finished=fin, end=3, workspace=ws)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_subnormal_logits(dtype):
+    """Values that differ by subnormal steps are ranked as they are."""
+    torch = need_gpu()
+    N, K, V, n = 1, 2, 12000, 12
+    step = {"f32": 2.0 ** -149, "f16": 2.0 ** -24, "bf16": 2.0 ** -133}[dtype]
+    rng = np.random.default_rng(5)
+    for low, high in ((-40, 40), (-40, -1), (-3, -1), (-1, 0)):
+        k = rng.integers(low, high + 1, (N * K, V)).astype(np.float64)
+        x = torch.from_numpy((k * step).astype(np.float32)).to(getattr(torch, DTYPES[dtype])).cuda()
+        assert np.array_equal(x.double().cpu().numpy(), k * step)
+        check(torch, x, np.array([[-1.0, -1.5]], np.float32), n)
+
+
+@pytest.mark.parametrize("equal", [False, True])
+def test_widest_beams_and_rows(equal):
+    """128 beams of 2^20 tokens: as many lists as a prompt can have."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    K, V, n = 128, 1 << 20, 256
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    x = torch.zeros((K, V), device="cuda") if equal else torch.randn((K, V), generator=g, device="cuda")
+    # beams that lie well apart (equal: the first has all ranks), or all within reach of each other
+    c = torch.arange(K, device="cuda", dtype=torch.float32).neg().view(1, K) * (1.0 if equal else 0.001)
+    scores, parents, tokens = tk.beam_search_select(x, c, n)
+    torch.cuda.synchronize()
+    best, beam, token = [], [], []
+    for b in range(K):
+        row = x[b].double()
+        if equal:
+            val, tok = row[:n], torch.arange(n, device="cuda")
+        else:
+            val, tok = row.topk(n)  # distinct enough: equal ones do not matter below
+        best.append((val - torch.logsumexp(row, 0) + c[0, b].double()).cpu().numpy())
+        beam.append(np.full(n, b))
+        token.append(tok.cpu().numpy())
+    best, beam, token = (np.concatenate(v) for v in (best, beam, token))
+    pick = np.lexsort((token, beam, -best))[:n]
+    assert np.array_equal(parents[0].cpu().numpy(), beam[pick])
+    assert np.array_equal(tokens[0].cpu().numpy(), token[pick])
+    err = np.abs(scores[0].double().cpu().numpy() - best[pick])
+    assert np.all(err <= 2.0 ** -24 * np.abs(best[pick]) + SUM_ERROR)

@@ -229,3 +229,19 @@ def test_backtrace_out_and_graph():
         torch.cuda.synchronize()
         assert np.array_equal(out.cpu().numpy(), beam_ref.backtrace(tokens.cpu().numpy(), parents.cpu().numpy()))
     assert bool((big[:32] == 5).all()) and bool((big[-32:] == 5).all())
+
+
+def test_backtrace_of_many_prompts():
+    """More prompts than one grid holds workgroups."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    T, N, K = 2, (1 << 21) + 5, 2
+    rng = np.random.default_rng(6)
+    tokens = rng.integers(0, 50000, (T, N, K)).astype(np.int32)
+    parents = rng.integers(-1, K, (T, N, K)).astype(np.int32)
+    got = tk.beam_backtrace(torch.from_numpy(tokens).cuda(), torch.from_numpy(parents).cuda())
+    torch.cuda.synchronize()
+    first = np.take_along_axis(tokens[0], np.maximum(parents[1], 0), 1)
+    want = np.stack([np.where(parents[1] < 0, -1, first), tokens[1]], 2)
+    assert np.array_equal(got.cpu().numpy(), want)

@@ -397,8 +397,8 @@ def _scope(stream, device):
         if torch.cuda.current_device() == device.index:
             return handle, _NULL_SCOPE
         return handle, torch.cuda.device(device)
-    if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    if not hasattr(stream, "cuda_stream"):  # a handle; 0 is the default stream's
+        stream = torch.cuda.ExternalStream(int(stream), device=device) if stream else torch.cuda.default_stream(device)
     if stream.device != device:
         raise ValueError(f"the stream's device {stream.device} is not the tensors' device {device}")
     return int(stream.cuda_stream), torch.cuda.stream(stream)
@@ -435,7 +435,7 @@ def beam_search_select(logits, scores, n=None, finished=None, end_token=None, we
     the vocabulary: (scores [N, n] float32, parents [N, n] int32, tokens [N, n]
     int32), best first.
 
-    logits [N * K, V], rows contiguous, any row stride; scores [N, K] float32,
+    logits [N * K, V], rows contiguous, any row stride from V on; scores [N, K] float32,
     the beams' accumulated log-probabilities. A continuation of beam b with
     token v scores scores[b] + log_softmax(logits[b])[v]. finished [N, K]
     bool: such a beam goes on as itself only, with end_token and its score.
@@ -469,6 +469,8 @@ def beam_search_select(logits, scores, n=None, finished=None, end_token=None, we
         _check_dense(finished, (N, K), torch.uint8 if finished.dtype == torch.uint8 else torch.bool, "finished", dev)
         if end_token is None:
             raise ValueError("finished needs end_token")
+        if not 0 <= end_token < 2 ** 31:
+            raise ValueError(f"end_token must be an int32 >= 0, got {end_token}")
         p_finished = finished.data_ptr()
     if weights is not None:
         _check_dense(weights, (N, K), torch.float32, "weights", dev)
@@ -493,7 +495,7 @@ def beam_search_select(logits, scores, n=None, finished=None, end_token=None, we
             _check_dense(workspace, workspace.shape, torch.uint8, "workspace", dev)
         status = lib.beam_search_select(
             logits.data_ptr(), ldx, dtype, N, K, V, scores.data_ptr(), p_finished,
-            0 if end_token is None else int(end_token), p_weights, n, o_scores.data_ptr(), o_parents.data_ptr(),
+            0 if finished is None else int(end_token), p_weights, n, o_scores.data_ptr(), o_parents.data_ptr(),
             o_tokens.data_ptr(), workspace.data_ptr(), size, handle)
     _check(status)
     return out
@@ -601,6 +603,8 @@ def beam_backtrace(tokens, parents, beams=None, lengths=None, pad=-1, out=None, 
     if ends is not None and ends.dim() != 2:
         raise ValueError("beams and lengths must be 2-D [N, M]")
     M = K if ends is None else ends.shape[1]
+    if not -2 ** 31 <= pad < 2 ** 31:
+        raise ValueError(f"pad must be an int32, got {pad}")
     dev = tokens.get_device()
     _check_dense(tokens, (T, N, K), torch.int32, "tokens", dev)
     _check_dense(parents, (T, N, K), torch.int32, "parents", dev)

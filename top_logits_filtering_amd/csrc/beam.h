@@ -42,7 +42,7 @@ struct BeamSplit {
   int chunks;
   int vecs;
 };
-BeamSplit beam_select_split(int dtype, int64_t rows, int V);
+BeamSplit beam_select_split(int dtype, int64_t rows, int V, int n);
 int64_t beam_select_workspace(int dtype, int64_t N, int K, int V, int n);
 hipError_t launch_beam_select(int dtype, const BeamSelectArgs& a, hipStream_t stream);
 

@@ -247,7 +247,7 @@ hipError_t launch_beam_backtrace(const BeamBacktraceArgs& a, hipStream_t stream)
   const int steps = static_cast<int>(whole < fit ? whole : fit);
   const bool aligned = a.K % 4 == 0 && reinterpret_cast<uintptr_t>(a.parents) % 16 == 0;
   const Div quads = aligned ? make_div(static_cast<uint32_t>(a.K / 4)) : Div{0, 0, 0};
-  const int64_t most = int64_t{1} << 22;  // a grid holds below 2^32 threads
+  const int64_t most = int64_t{1} << 21;  // a grid holds below 2^32 threads
   const int64_t per = most / tiles > 0 ? most / tiles : 1;
   for (int64_t i = 0; i < a.N; i += per) {
     const int64_t items = a.N - i < per ? a.N - i : per;

@@ -16,10 +16,16 @@
 // the rounding of its argument, 7 instructions an element, and are within
 // kSumError of the exact ones; where candidates of two beams come so close that
 // this could swap them, the merge sums those beams' rows again in 64 bits. So
-// the order is that of 64-bit values at the price of 32-bit ones: a sum in 64
-// bits throughout (16 instructions an element) took 30 us instead of 20 for
-// 256 rows of 151936 bf16 logits, and 110 instead of 89 for 1024 rows of
-// 128256 fp32 ones.
+// the order is that of 64-bit values at the price of 32-bit ones: with sums in
+// 64 bits throughout (16 instructions an element) the chunks of 256 rows of
+// 151936 bf16 logits took 30 us against 20, and those of 1024 rows of 128256
+// fp32 ones 110 us against 89 (84 today).
+//
+// The logits have to be read once and nothing else is of their size. Times on
+// one MI355X, chunks + merge, V tokens: a prompt of 4 beams, V 151936 bf16: 5.9 +
+// 6.1 us, chains of dependent steps; 64 such prompts: 21 + 6 us (3.7 TB/s); 128
+// prompts of 8 beams, V 128256 fp32: 85 + 9 us (6.2 TB/s); 2 prompts of 64 beams,
+// V 151936 bf16, 128 continuations: 24 + 17 us.
 
 #include <float.h>
 
@@ -37,25 +43,45 @@ constexpr int kChunkWaves = kChunkThreads / kWave;
 constexpr int kChunkCap = 1024;  // candidate slots of a chunk
 constexpr int kUnits = 16;       // units of a thread at most
 constexpr int kHits = 1024;      // units that may reach the bound
-constexpr int kTargetBlocks = 1024;
+// Chunks wanted where rows are few. Each adds a list of n for the merge to go
+// through, so half of them for many candidates. Against 1024 chunks: 2 prompts of
+// 64 beams, n 128: 45 -> 41 us, 4 of 100 beams, n 200: 84 -> 54 us; n <= 32 the
+// same (up to 1 us either way), and with 256 40 prompts of 4 beams, V 100000
+// fp32, 25 us against 23 to 24.
+constexpr int kTargetBlocks = 512;
 constexpr int kMergeThreads = 512;
 constexpr int kMergeWaves = kMergeThreads / kWave;
 constexpr int kMergeCap = 2048;  // candidate slots of a prompt
 constexpr int kHeld = 4;         // list entries a thread of the merge holds from the start
 constexpr uint32_t kRoom = kHeld * kMergeThreads;
-constexpr uint32_t kMergeLists = 1024;  // lists noted as going on
-constexpr uint32_t kGroupBound = 32;    // up to so many candidates 64 maxima give the bound
+// Up to so many candidates a chunk takes its bound from 64 maxima, which is 1.4
+// us less than from 512. For more of them it would leave ever longer lists.
+constexpr uint32_t kGroupBound = 32;
+// The same for the merge, whose entries are sorted by list, so that large ones lie
+// in one group: 2 prompts of 64 beams with n 24 take 23 us like this and 30 with
+// the bound of the chunks, 64 of 16 with n 32 27.5 and 31.6; but one prompt of 4
+// beams with n 32 15.4 and 14.0. With n 16 64 maxima are up to 3 us faster.
+constexpr uint32_t kMergeGroupBound = 16;
 constexpr int kBoundBits = 14;          // bits of a bound from the first that differs on
-constexpr uint32_t kAllRanked = 48;     // so many candidates are ranked without a bound
-constexpr uint32_t kLongList = 320;     // a longer list is cut before it is ranked
-constexpr int kQuadStep = 2;            // reads of four elements that overlap
+// So many candidates are ranked without a bound, which takes 4.6 us instead of
+// 7.3 for 32 of them, 1 us less for 128, and 4 us more for 256 and 128 prompts.
+constexpr uint32_t kAllRanked = 128;
+// A longer list is cut to few more than n before it is ranked in time M^2: n 200
+// takes 37 us so and 143 without; cut from 64 on, n 8 10.6 instead of 8.8.
+constexpr uint32_t kLongList = 320;
+constexpr int kQuadStep = 2;  // reads of four elements that overlap; 6.5 us instead of 7.5 for one
 constexpr int kMaxBeams = 128;
 constexpr int kMaxCandidates = 256;
 constexpr int kTokenBits = 20;
+// A prompt has no more lists than the merge holds the first entries of: few rows
+// are split into kTargetBlocks chunks together, and many beams' rows into as many
+// as the longest row needs.
+static_assert(kTargetBlocks + kMaxBeams <= kRoom);
+static_assert(((1 << kTokenBits) / (kChunkThreads * kUnits * 16)) * kMaxBeams <= kRoom);
 
 // A thread's vectors: 16 elements make a unit, which shares one maximum, and 32
-// a group, which is loaded while the one before is summed (for fp32 groups of
-// half the size took 90 us instead of 84 for 1024 rows of 128256).
+// a group, which is loaded while the one before is summed (fp32 groups of half
+// the size took 90 us instead of 84 for 1024 rows of 128256).
 template <class DT>
 constexpr int kUnitOf = 16 / DT::kPerVec;
 template <class DT>
@@ -241,8 +267,17 @@ __device__ __forceinline__ uint32_t block_excl(uint32_t v, uint32_t& total, Chun
   return below + incl - v;
 }
 
-// SHORT: the chunk is one group of layers, which stays in registers; otherwise
-// groups stream through and the few vectors that matter are read again.
+// One chunk: its sum of exp and its n best. Each thread reads its vectors once,
+// the next group of them in flight while one is summed, past the caches (525 MB:
+// 96 us in all, 103 through them), and notes a maximum per unit. The n-th largest
+// of some of these maxima bounds the n-th largest element from below, so only
+// units that reach it, a few more than n, are looked at again; their elements
+// that reach it are ranked against each other. What bounds it: memory for fp32
+// (6.2 TB/s at 525 MB); for 16-bit types the seven instructions an element and,
+// with few chunks, the 4 us from the last load to the last store.
+// SHORT: the chunk is one group of layers, which stays in registers (6.5 us
+// instead of 6.8 for 64 rows of 32000 fp16); otherwise groups stream through and
+// the few vectors that matter are read again.
 template <class DT, bool SHORT>
 __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArgs a, BeamSplit split, int64_t row0,
                                                                    ChunkStat* __restrict__ stats,
@@ -618,7 +653,7 @@ struct MergeSmem {
   uint32_t count;
   uint32_t votes[2];
   uint32_t active[2];               // lists that go on, in two turns
-  uint16_t list_of[2][kMergeLists];
+  uint16_t list_of[2][kRoom];
 };
 
 // One beam's L and state out of its chunks, held by all threads that pass the
@@ -718,6 +753,13 @@ __device__ __forceinline__ uint32_t lowered(uint32_t T, double margin) {
   return t < T && t > 0u ? t : T;
 }
 
+// One prompt: L of its beams out of their chunks' sums, then the n best of all
+// lists. The lists' first entries are held in registers from the start; the n-th
+// of the threads' best bounds the n-th candidate, lists whose last entry held
+// still reaches the bound are read on, and what reaches it is ranked. A chain of
+// some ten dependent steps in shared memory, 4.6 to 9 us for up to 16
+// candidates, and 17 us for 128 of 64 beams: more workgroups than one to a prompt
+// would have to meet again at its end.
 template <class DT>
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArgs a, Div chunks, Div window,
                                                                    int64_t item0, const ChunkStat* __restrict__ stats,
@@ -743,7 +785,9 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
   }
 
   if (tid == 0) sm.count = sm.active[0] = sm.again = 0;
-  if (K <= kMergeWaves) {  // a wave per beam
+  // A wave per beam, whose lanes take its chunks side by side (19 of them: 6.1 us
+  // in all instead of 12.6); a thread per beam where there are more beams.
+  if (K <= kMergeWaves) {
     if (wave < K) {
       const int64_t row = item * K + wave;
       const float c = a.scores[row], w = a.weights != nullptr ? a.weights[row] : 1.0f;
@@ -760,7 +804,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
         sm.state[wave] = state;
       }
     }
-  } else if (tid < K) {  // a thread per beam
+  } else if (tid < K) {
     const int64_t row = item * K + tid;
     const float c = a.scores[row], w = a.weights != nullptr ? a.weights[row] : 1.0f;
     const bool done = a.finished != nullptr && a.finished[row] != 0;
@@ -825,12 +869,8 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
         const uint32_t h = static_cast<uint32_t>(first[u].hi >> 32);
         best = best > h ? best : h;
       }
-      for (uint32_t q = kRoom + tid; q < nl; q += kMergeThreads) {  // more lists than are held (wide is 1)
-        const uint32_t h = static_cast<uint32_t>(fetch(q, 0).hi >> 32);
-        best = best > h ? best : h;
-      }
       T = 0u;
-      if (n <= kGroupBound) {  // as in the chunks
+      if (n <= kMergeGroupBound) {
         const uint32_t g = group_max<kMergeThreads / kWave>(best);
         if (tid % (kMergeThreads / kWave) == 0) sm.heads[tid / (kMergeThreads / kWave)] = g;
         lds_barrier();
@@ -864,7 +904,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       // reaches T, further windows of entries.
       auto go_on = [&](int turn, uint32_t q) __attribute__((always_inline)) {
         const uint32_t at = atomicAdd(&sm.active[turn], 1u);
-        if (at < kMergeLists) sm.list_of[turn][at] = static_cast<uint16_t>(q);
+        sm.list_of[turn][at] = static_cast<uint16_t>(q);
       };
 #pragma unroll
       for (int u = 0; u < kHeld; ++u) {
@@ -873,20 +913,16 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
           if (f - q * wide == wide - 1) go_on(0, q);
         }
       }
-      for (uint32_t q = kRoom + tid; q < nl; q += kMergeThreads)
-        if (push(fetch(q, 0))) go_on(0, q);
       int turn = 0;
       for (uint32_t j0 = wide; j0 < n; turn ^= 1) {
         if (tid == 0) sm.active[turn ^ 1] = 0;
         lds_barrier();
         const uint32_t active = sm.active[turn];
         if (active == 0) break;
-        const bool noted = active <= kMergeLists;
-        const uint32_t lists_now = noted ? active : nl;
-        uint32_t w = lists_now < kRoom ? kRoom / lists_now : 1u;
+        uint32_t w = kRoom / active;
         w = w < n - j0 ? w : n - j0;
-        for (uint32_t f = tid; f < lists_now * w; f += kMergeThreads) {
-          const uint32_t q = noted ? sm.list_of[turn][f / w] : f / w, j = f % w;
+        for (uint32_t f = tid; f < active * w; f += kMergeThreads) {
+          const uint32_t q = sm.list_of[turn][f / w], j = f % w;
           if (push(fetch(q, j0 + j)) && j == w - 1) go_on(turn ^ 1, q);
         }
         lds_barrier();
@@ -1066,7 +1102,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
 
 template <class DT>
 void launch_both(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t items, ChunkStat* stats,
-                   uint64_t* lists, hipStream_t stream) {
+                 uint64_t* lists, hipStream_t stream) {
   const unsigned blocks = static_cast<unsigned>(items * a.K * s.chunks);
   // few layers: they stay in registers
   if (s.vecs <= kGroupOf<DT> * kChunkThreads)
@@ -1077,7 +1113,7 @@ void launch_both(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t it
                        item0 * a.K, stats, lists);
   // the window of entries that the merge holds of every list
   const uint32_t nl = static_cast<uint32_t>(a.K) * static_cast<uint32_t>(s.chunks);
-  uint32_t wide = nl < kRoom ? kRoom / nl : 1u;
+  uint32_t wide = kRoom / nl;
   wide = wide < static_cast<uint32_t>(a.n) ? wide : static_cast<uint32_t>(a.n);
   hipLaunchKernelGGL(beam_merge_kernel<DT>, dim3(static_cast<unsigned>(items)), dim3(kMergeThreads), 0, stream, a,
                      make_div(static_cast<uint32_t>(s.chunks)), make_div(wide), item0, stats, lists);
@@ -1085,16 +1121,17 @@ void launch_both(const BeamSelectArgs& a, BeamSplit s, int64_t item0, int64_t it
 
 }  // namespace
 
-// Chunks of a few layers of vectors when there are few rows, so that every
-// compute unit gets some, and of as many as a workgroup notes maxima for when
-// there are many.
-BeamSplit beam_select_split(int dtype, int64_t rows, int V) {
+// Chunks of one group of layers or more when there are few rows, so that every
+// compute unit gets some, and of as many layers as a workgroup notes maxima for
+// when there are many.
+BeamSplit beam_select_split(int dtype, int64_t rows, int V, int n) {
   const int64_t per = dtype == 0 ? 4 : 8;
   const int64_t nv = V / per;
   const int64_t largest = kChunkThreads * kUnits * 16 / per, smallest = kChunkThreads * 32 / per;
   const int64_t least = (nv + largest - 1) / largest;
   const int64_t most = (nv + smallest - 1) / smallest;
-  int64_t c = rows > 0 ? (kTargetBlocks + rows - 1) / rows : 1;
+  const int64_t target = n <= static_cast<int>(kGroupBound) ? kTargetBlocks : kTargetBlocks / 2;
+  int64_t c = rows > 0 ? (target + rows - 1) / rows : 1;
   c = c < most ? c : most;
   c = c > least ? c : least;
   c = c > 1 ? c : 1;
@@ -1102,12 +1139,12 @@ BeamSplit beam_select_split(int dtype, int64_t rows, int V) {
 }
 
 int64_t beam_select_workspace(int dtype, int64_t N, int K, int V, int n) {
-  const BeamSplit s = beam_select_split(dtype, N * K, V);
+  const BeamSplit s = beam_select_split(dtype, N * K, V, n);
   return N * K * s.chunks * (static_cast<int64_t>(sizeof(ChunkStat)) + 8 * static_cast<int64_t>(n));
 }
 
 hipError_t launch_beam_select(int dtype, const BeamSelectArgs& a, hipStream_t stream) {
-  const BeamSplit s = beam_select_split(dtype, a.N * a.K, a.V);
+  const BeamSplit s = beam_select_split(dtype, a.N * a.K, a.V, a.n);
   ChunkStat* stats = static_cast<ChunkStat*>(a.workspace);
   uint64_t* lists = reinterpret_cast<uint64_t*>(stats + a.N * a.K * s.chunks);
   // a launch holds at most 2^22 workgroups of 256 threads
