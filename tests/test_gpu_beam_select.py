@@ -1,8 +1,8 @@
 """beam_search_select against the plain implementation in 64 bits (needs an
 MI355X). Parents and tokens must be equal. Scores: a sum of exp is off by at most
 3.5e-7 of itself (hardware exp2 8.5e-8, measured over all arguments that occur;
-three additions and a multiply-add in fp32 at 2^-24 = 6.0e-8 each; everything
-else is in 64 bits and below 1e-9), so its logarithm is by less than 3.6e-7; the
+three additions in fp32 at 2^-24 = 6.0e-8 each, and a multiply-add at as much or,
+for 16-bit logits, 1e-8 of a series that is cut short; everything else is in 64 bits and below 1e-9), so its logarithm is by less than 3.6e-7; the
 score is rounded once to fp32, by at most 2^-24 of its value."""
 
 import numpy as np
@@ -357,3 +357,18 @@ def test_widest_beams_and_rows(equal):
     assert np.array_equal(tokens[0].cpu().numpy(), token[pick])
     err = np.abs(scores[0].double().cpu().numpy() - best[pick])
     assert np.all(err <= 2.0 ** -24 * np.abs(best[pick]) + SUM_ERROR)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_logits_far_from_zero(dtype):
+    """Rows that lie high or low, up to and past where the sums are formed less
+    their maximum; few tokens have most of the weight, so that scores are small
+    and show the sum's error."""
+    torch = need_gpu()
+    N, K, V = 6, 5, 30001
+    rng = np.random.default_rng(9)
+    x = rng.standard_normal((N * K, V)) - 14.0
+    x[:, 100:104] += rng.uniform(9.0, 16.0, (N * K, 4))
+    x += np.repeat([-30.0, -8.0, 12.0, 40.0, 74.0, 100.0], K)[:, None]
+    x = torch.from_numpy(x.astype(np.float32)).to(getattr(torch, DTYPES[dtype])).cuda()
+    check(torch, x, np.tile(-np.arange(K, dtype=np.float32) / 64, (N, 1)), 2 * K)

@@ -13,19 +13,19 @@
 //
 // Parents and tokens are whole numbers whose order between beams hangs on
 // c[b] - L[b]. The chunks' sums use the hardware's exp2 with a correction for
-// the rounding of its argument, 7 instructions an element, and are within
+// the rounding of its argument, 7 or 8 instructions an element, and are within
 // kSumError of the exact ones; where candidates of two beams come so close that
 // this could swap them, the merge sums those beams' rows again in 64 bits. So
 // the order is that of 64-bit values at the price of 32-bit ones: with sums in
 // 64 bits throughout (16 instructions an element) the chunks of 256 rows of
 // 151936 bf16 logits took 30 us against 20, and those of 1024 rows of 128256
-// fp32 ones 110 us against 89 (84 today).
+// fp32 ones 110 us against 89 (85 today).
 //
 // The logits have to be read once and nothing else is of their size. Times on
 // one MI355X, chunks + merge, V tokens: a prompt of 4 beams, V 151936 bf16: 5.9 +
-// 6.1 us, chains of dependent steps; 64 such prompts: 21 + 6 us (3.7 TB/s); 128
+// 6.1 us, chains of dependent steps; 64 such prompts: 20 + 6 us (3.9 TB/s); 128
 // prompts of 8 beams, V 128256 fp32: 85 + 9 us (6.2 TB/s); 2 prompts of 64 beams,
-// V 151936 bf16, 128 continuations: 24 + 17 us.
+// V 151936 bf16, 128 continuations: 22 + 17 us.
 
 #include <float.h>
 
@@ -116,22 +116,53 @@ __device__ __forceinline__ uint64_t pack(uint32_t key, uint32_t token) {
 constexpr float kHighMax = 80.0f;  // eight terms of exp(80) stay finite
 constexpr float kLowMax = -40.0f;  // terms that fp32 flushes are below 2^-68 of the largest
 
-// A part of exp(x) = 2^t * 2^lo, t = x log2(e) rounded and lo what that lost:
-// returns 2^t and adds lo * 2^t to `rest`, which counts times ln 2.
+constexpr float kLn2 = 0.693147180559945309417f;
+
+// exp(x) = 2^t * 2^lo with t as the hardware's exp2 takes it: returns 2^t and
+// adds to `rest` what the sum needs for 2^lo (sum_of).
+// fp32: t = x log2(e) rounded, lo what that lost; rest is the sum of lo * 2^t.
+// 16-bit types, whose values have at most 8 or 11 bits: t = x * log2_high(),
+// which has so few that the product is exact; rest is the sum of x * 2^t.
+template <class DT>
+constexpr float log2_high() {
+  return DT::kNegInf == 0xFF80u ? 47274.0f / 32768 : 5909.0f / 4096;
+}
+template <class DT>
 __device__ __forceinline__ float exp_parts(float x, float& rest) {
   constexpr float kLog2e = 1.44269502162933349609375f, kLog2eLow = 1.925963033500e-8f;
   const float xc = __builtin_amdgcn_fmed3f(x, -104.0f, 104.0f);  // finite, also for -inf
-  const float t = xc * kLog2e;
-  const float lo = __builtin_fmaf(xc, kLog2eLow, __builtin_fmaf(xc, kLog2e, -t));
-  const float e = __builtin_amdgcn_exp2f(t);
-  rest = __builtin_fmaf(e, lo, rest);
-  return e;
+  if constexpr (DT::kPerVec == 4) {
+    const float t = xc * kLog2e;
+    const float lo = __builtin_fmaf(xc, kLog2eLow, __builtin_fmaf(xc, kLog2e, -t));
+    const float e = __builtin_amdgcn_exp2f(t);
+    rest = __builtin_fmaf(e, lo, rest);
+    return e;
+  } else {
+    const float e = __builtin_amdgcn_exp2f(xc * log2_high<DT>());
+    rest = __builtin_fmaf(e, xc, rest);
+    return e;
+  }
+}
+
+// The sum of exp(x) out of the sums of 2^t and rest.
+// fp32: 2^lo = 1 + lo ln 2, as lo is below 2^-17.
+// 16-bit types: exp(x) = 2^t * exp(kx) with k = 1 - log2_high() ln 2, 4.9e-6 or
+// 4.7e-5. With m the mean of x under the weights 2^t the sum is
+// sum * exp(km) * (1 + k^2 var / 2 + ...). The variance of 257 elements, as many
+// as a thread has, is at most 9 (255 of them lie about 6 below the others), so
+// what is left out is below 1e-8; |km| is below 5e-3.
+template <class DT>
+__device__ __forceinline__ double sum_of(double sum, double rest) {
+  if constexpr (DT::kPerVec == 4) return sum + rest * kLn2;
+  constexpr double kRate = 1.0 - log2_high<DT>() * 0.693147180559945309417;
+  const double y = rest * kRate, z = y * __builtin_amdgcn_rcp(sum + 0x1p-1000);
+  return sum + y * (1.0 + z * (0.5 + z * (1.0 / 6)));
 }
 
 // Relative error of a chunk's sum: 8.5e-8 of exp2 (the most over all arguments
-// in +-[2^-10, 120), measured), three additions and a multiply-add in fp32 at
-// 2^-24 each, and less than 1e-10 of what follows in 64 bits.
-constexpr float kLn2 = 0.693147180559945309417f;
+// in +-[2^-10, 120), measured), three additions in fp32 at 2^-24 each, and either
+// a multiply-add at 2^-24 or the 1e-8 of sum_of; less than 1e-10 of what
+// follows in 64 bits.
 constexpr double kSumError = 3.5e-7;
 
 // exp(x - ref) in 64 bits, for finite ref and x below ref + 700 or -inf.
@@ -273,8 +304,10 @@ __device__ __forceinline__ uint32_t block_excl(uint32_t v, uint32_t& total, Chun
 // of some of these maxima bounds the n-th largest element from below, so only
 // units that reach it, a few more than n, are looked at again; their elements
 // that reach it are ranked against each other. What bounds it: memory for fp32
-// (6.2 TB/s at 525 MB); for 16-bit types the seven instructions an element and,
-// with few chunks, the 4 us from the last load to the last store.
+// (6.2 TB/s at 525 MB); for 16-bit types the seven instructions an element beside
+// it (with the correction that fp32 needs, two more, 256 rows of 151936 bf16 take
+// 21.6 us instead of 19.8), and with few chunks the 4 us from the last load to
+// the last store.
 // SHORT: the chunk is one group of layers, which stays in registers (6.5 us
 // instead of 6.8 for 64 rows of 32000 fp16); otherwise groups stream through and
 // the few vectors that matter are read again.
@@ -332,7 +365,7 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
 
   // One pass: the sum of exp and the largest value of each unit.
   // maximum() keeps a NaN, so that one shows in the chunk's maximum.
-  double sum = 0.0;
+  double sum = 0.0, sum_rest = 0.0;
   float half0 = -INFINITY, half1 = -INFINITY;
   const int layers = (cnt + kChunkThreads - 1) / kChunkThreads;
   float tops[kGroup / kUnit];
@@ -349,7 +382,7 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
 #pragma unroll
       for (int j = 0; j < P; ++j) {
         const float x = DT::value(lane_of<raw_t>(now[g], j));
-        e[j] = exp_parts(x, rest);
+        e[j] = exp_parts<DT>(x, rest);
         m = __builtin_elementwise_maximum(m, x);
       }
       tops[g / kUnit] = m;
@@ -358,7 +391,12 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
 #pragma unroll
         for (int j = 0; j < P; j += 2 * d) e[j] += e[j + d];
       }
-      sum += static_cast<double>(__builtin_fmaf(rest, kLn2, e[0]));
+      if constexpr (P == 4) {
+        sum += static_cast<double>(__builtin_fmaf(rest, kLn2, e[0]));
+      } else {
+        sum += static_cast<double>(e[0]);
+        sum_rest += static_cast<double>(rest);
+      }
     }
 #pragma unroll
     for (int u = 0; u < kGroup / kUnit; u += 2) {
@@ -386,8 +424,9 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   const float xe = DT::value(re);
   {
     float rest = 0.0f;
-    const float e = exp_parts(xe, rest);
-    sum += static_cast<double>(__builtin_fmaf(rest, kLn2, e));
+    sum += static_cast<double>(exp_parts<DT>(xe, rest));
+    sum_rest += static_cast<double>(rest);
+    sum = sum_of<DT>(sum, sum_rest);  // (fp32: of this element alone)
   }
   half0 = __builtin_elementwise_maximum(half0, xe);
 
