@@ -2,8 +2,9 @@
 MI355X). Parents and tokens must be equal. Scores: a sum of exp is off by at most
 3.5e-7 of itself (hardware exp2 8.5e-8, measured over all arguments that occur;
 three additions in fp32 at 2^-24 = 6.0e-8 each, and a multiply-add at as much or,
-for 16-bit logits, 1e-8 of a series that is cut short; everything else is in 64 bits and below 1e-9), so its logarithm is by less than 3.6e-7; the
-score is rounded once to fp32, by at most 2^-24 of its value."""
+for 16-bit logits, 1e-8 of a series that is cut short; everything else is in 64
+bits and below 1e-9), so its logarithm is by less than 3.6e-7; the score is
+rounded once to fp32, by at most 2^-24 of its value."""
 
 import numpy as np
 import pytest

@@ -10,6 +10,12 @@
 // chains of about 16 reads of bytes in shared memory instead of one of T. Tokens are
 // fetched at the end, side by side. A history that does not fit is taken in
 // pieces from its end.
+//
+// Dependent steps bound it, not its bytes: 100 steps of 4 prompts and 4 beams take
+// 7.4 us on one MI355X; 2048 steps of 64 prompts and 8 beams (10.5 MB) 14.6, where
+// a first form with one level of maps, formed from loads one at a time, took 45. A
+// row of that history is 2 KB of which a prompt has 32 bytes, so a workgroup reads
+// 2048 cache lines for its parents and again for its tokens.
 
 #include "beam.h"
 #include "device_common.h"
@@ -51,7 +57,7 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
   __shared__ TraceSmem sm;
   const int tid = threadIdx.x;
   // Neighbouring prompts share cache lines of the history, and workgroups go to
-  // the 8 dies in turn: each die takes a run of prompts.
+  // the 8 dies in turn: each die takes a run of prompts (14.6 us; 20.0 in turn).
   const uint32_t block = (blockIdx.x % kDies) * (gridDim.x / kDies) + blockIdx.x / kDies;
   const uint32_t item32 = quotient(block, tiles);
   if (item32 >= a.N) return;
@@ -81,7 +87,7 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
     lds_barrier();
     const int32_t* __restrict__ from = a.parents + t0 * step_stride + at0;
     auto byte_of = [&](int p) -> uint32_t { return p >= 0 && p < K ? p : K; };
-    if (quads.d != 0) {  // four beams at a time: their addresses are aligned
+    if (quads.d != 0) {  // four beams at a time, if aligned: 14.6 us, 16.0 one at a time
       const int count = n * static_cast<int>(quads.d);
       for (int f0 = tid; f0 < count; f0 += kTraceUnroll * kTraceThreads) {
         int4 p[kTraceUnroll];
@@ -236,7 +242,8 @@ __global__ __launch_bounds__(kTraceThreads) void beam_backtrace_kernel(BeamBackt
 
 hipError_t launch_beam_backtrace(const BeamBacktraceArgs& a, hipStream_t stream) {
   // Few prompts: their hypotheses are spread over more workgroups, each of
-  // which forms the maps again (they come from the same cache lines).
+  // which forms the maps again (they come from the same cache lines). 64 prompts of
+  // 8: 64 workgroups 19.8 us, 128 15.6, 256 14.6, 512 23.7.
   int64_t paths = (a.N * a.M + kTraceTarget - 1) / kTraceTarget;
   paths = paths < kTracePaths ? paths : kTracePaths;
   paths = paths < a.M ? paths : a.M;

@@ -8,6 +8,11 @@
 // into a new tensor and copying it back moves twice that. Rows that stay are
 // not touched. The K values wait in registers, so wide beams take narrower
 // columns.
+//
+// Memory bounds it: each changed row written once and each of their parents read
+// once. On one MI355X, rates of those bytes: 4 beams 2.4 GB in 409 us (5.9 TB/s),
+// 6 beams 219 MB in one state 38 us (5.7), 16 to 32 beams 5.3 to 5.5 TB/s, 64 and
+// 128 beams 4.3 and 4.7. Four small states of one prompt take 4.2 us.
 
 #include "beam.h"
 #include "device_common.h"
@@ -51,8 +56,10 @@ struct Column<2> { using type = uint16_t; };
 template <>
 struct Column<1> { using type = uint8_t; };
 
-// KMAX: beams held; W: bytes of a column; NT: reads that leave no copy in the
-// caches. Writes never do: the rows are next read by another step.
+// One tile of 256 columns of one state and prompt. KMAX: beams held; W: bytes of
+// a column; NT: reads that leave no copy in the caches. Writes never do: the rows
+// are next read by another step. (A thread with 2, 4 or 8 columns, to read the
+// parents' numbers less often, took 425, 456 and 482 us where this takes 411.)
 template <int KMAX, int W, bool NT>
 __global__ __launch_bounds__(kMoveThreads) void beam_move_kernel(const MoveArgs a) {
   using col_t = typename Column<W>::type;
@@ -131,7 +138,8 @@ __global__ __launch_bounds__(kMoveThreads) void beam_move_kernel(const MoveArgs 
 int64_t low_bit(int64_t x) { return x & -x; }
 
 // Bytes of a column: what every address is aligned to, at most 16, and for
-// wide beams what fits the registers. Columns of 16 bytes may reach past the
+// wide beams what fits the registers (2.4 GB of 4 beams take 410 us in columns of
+// 16 bytes, 1170 in columns of 4). Columns of 16 bytes may reach past the
 // length inside a piece of whole words; smaller ones never do.
 int column_bytes(const BeamState& s, int K) {
   int64_t w = 16 | reinterpret_cast<int64_t>(s.data) | s.row_stride;
@@ -237,17 +245,12 @@ hipError_t launch_beam_reorder(const BeamState* states, int count, const int32_t
       // Calls on more than the last-level cache holds read past it: 2.1 GB in
       // 32 states take 410 us so and 448 us otherwise, 194 MB in one state 48
       // and 39 us.
-      if (streamed) {
-        if (K <= 4) e = move_all<4, 16, true>(a, held, N, stream);
-        else if (K <= 8) e = move_all<8, 16, true>(a, held, N, stream);
-        else if (K <= 16) e = move_all<16, 16, true>(a, held, N, stream);
-        else e = move_all<32, 16, true>(a, held, N, stream);
-      } else {
-        if (K <= 4) e = move_all<4, 16, false>(a, held, N, stream);
-        else if (K <= 8) e = move_all<8, 16, false>(a, held, N, stream);
-        else if (K <= 16) e = move_all<16, 16, false>(a, held, N, stream);
-        else e = move_all<32, 16, false>(a, held, N, stream);
-      }
+      // Room for 16 beams costs 4 nothing (411 us either way), room for 32 leaves
+      // fewer waves (562 us).
+      if (streamed)
+        e = K <= 16 ? move_all<16, 16, true>(a, held, N, stream) : move_all<32, 16, true>(a, held, N, stream);
+      else
+        e = K <= 16 ? move_all<16, 16, false>(a, held, N, stream) : move_all<32, 16, false>(a, held, N, stream);
     } else if (w == 4) {
       e = K <= 32 ? move_all<32, 4, false>(a, held, N, stream) : move_all<128, 4, false>(a, held, N, stream);
     } else {
