@@ -25,7 +25,7 @@
 // one MI355X, chunks + merge, V tokens: a prompt of 4 beams, V 151936 bf16: 5.9 +
 // 6.1 us, chains of dependent steps; 64 such prompts: 20 + 6 us (3.9 TB/s); 128
 // prompts of 8 beams, V 128256 fp32: 85 + 9 us (6.2 TB/s); 2 prompts of 64 beams,
-// V 151936 bf16, 128 continuations: 22 + 17 us.
+// V 151936 bf16, 128 continuations: 20 + 16 us.
 
 #include <float.h>
 
@@ -70,6 +70,7 @@ constexpr uint32_t kAllRanked = 128;
 // takes 37 us so and 143 without; cut from 64 on, n 8 10.6 instead of 8.8.
 constexpr uint32_t kLongList = 320;
 constexpr int kQuadStep = 2;  // reads of four elements that overlap; 6.5 us instead of 7.5 for one
+constexpr uint32_t kChunkStep = 8, kMergeStep = 4;  // comparisons side by side
 constexpr int kMaxBeams = 128;
 constexpr int kMaxCandidates = 256;
 constexpr int kTokenBits = 20;
@@ -236,24 +237,25 @@ __device__ __forceinline__ uint32_t group_max(uint32_t v) {
 }
 
 // rank[e] = how many of list[0, M) rank above list[e]. The threads share each
-// entry's comparisons, so that short lists take few steps. (Reads up to
-// STEP - 1 entries behind the list, which do not count.)
+// entry's comparisons, so that short lists take few steps. The list has room for
+// STEP more entries, which become Item{}, above no other.
 template <int THREADS, uint32_t STEP, class Item, class Above>
-__device__ __forceinline__ void count_ranks(const Item* list, uint32_t* rank, uint32_t M, Above above) {
+__device__ __forceinline__ void count_ranks(Item* list, uint32_t* rank, uint32_t M, Above above) {
   const uint32_t tid = threadIdx.x;
   for (uint32_t e = tid; e < M; e += THREADS) rank[e] = 0;
+  if (tid < STEP) list[M + tid] = Item{};
   lds_barrier();
   uint32_t span = kWave;
   while (span < M && span < THREADS) span *= 2;
   const uint32_t parts = THREADS / span, part = tid / span;
-  const uint32_t seg = (M + parts - 1) / parts;
+  const uint32_t seg = (M + parts * STEP - 1) / (parts * STEP) * STEP;
   const uint32_t j0 = part * seg, j1 = j0 + seg < M ? j0 + seg : M;
   for (uint32_t e = tid & (span - 1u); e < M; e += span) {
     const Item mine = list[e];
     uint32_t r = 0;
     for (uint32_t j = j0; j < j1; j += STEP) {
 #pragma unroll
-      for (uint32_t i = 0; i < STEP; ++i) r += above(list[j + i], mine) && j + i < j1 ? 1u : 0u;
+      for (uint32_t i = 0; i < STEP; ++i) r += above(list[j + i], mine) ? 1u : 0u;
     }
     if (r != 0) atomicAdd(&rank[e], r);
   }
@@ -261,7 +263,7 @@ __device__ __forceinline__ void count_ranks(const Item* list, uint32_t* rank, ui
 }
 
 struct ChunkSmem {
-  uint64_t list[kChunkCap + 8];
+  uint64_t list[kChunkCap + kChunkStep];
   uint32_t rank[kChunkCap];
   uint32_t half[2 * kChunkThreads];  // largest of a thread's even and of its odd units, as keys
   double sum[kChunkWaves];
@@ -653,7 +655,7 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   }
 
   // The candidates are distinct numbers: each one's place is its rank.
-  count_ranks<kChunkThreads, 8>(sm.list, sm.rank, M, [](uint64_t x, uint64_t y) { return x > y; });
+  count_ranks<kChunkThreads, kChunkStep>(sm.list, sm.rank, M, [](uint64_t x, uint64_t y) { return x > y; });
   for (uint32_t e = tid; e < M; e += kChunkThreads) {
     const uint32_t r = sm.rank[e];
     if (r < n) out[r] = sm.list[e];
@@ -675,7 +677,7 @@ __device__ __forceinline__ bool above(const Cand& a, const Cand& b) {
 }
 
 struct MergeSmem {
-  Cand list[kMergeCap + 4];
+  Cand list[kMergeCap + kMergeStep];
   Cand sorted[kMaxCandidates];
   uint32_t upper[kMergeCap];  // the candidates' upper halves of hi
   uint32_t rank[kMergeCap];
@@ -797,7 +799,7 @@ __device__ __forceinline__ uint32_t lowered(uint32_t T, double margin) {
 // of the threads' best bounds the n-th candidate, lists whose last entry held
 // still reaches the bound are read on, and what reaches it is ranked. A chain of
 // some ten dependent steps in shared memory, 4.6 to 9 us for up to 16
-// candidates, and 17 us for 128 of 64 beams: more workgroups than one to a prompt
+// candidates, and 16 us for 128 of 64 beams: more workgroups than one to a prompt
 // would have to meet again at its end.
 template <class DT>
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArgs a, Div chunks, Div window,
@@ -1071,7 +1073,8 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       }
 
       // Decode and write.
-      count_ranks<kMergeThreads, 4>(sm.list, sm.rank, M, [](const Cand& x, const Cand& y) { return above(x, y); });
+      count_ranks<kMergeThreads, kMergeStep>(sm.list, sm.rank, M,
+                                             [](const Cand& x, const Cand& y) { return above(x, y); });
       for (uint32_t e = tid; e < M; e += kMergeThreads) {
         const Cand k = sm.list[e];
         const uint32_t r = sm.rank[e];
