@@ -373,3 +373,18 @@ def test_logits_far_from_zero(dtype):
     x += np.repeat([-30.0, -8.0, 12.0, 40.0, 74.0, 100.0], K)[:, None]
     x = torch.from_numpy(x.astype(np.float32)).to(getattr(torch, DTYPES[dtype])).cuda()
     check(torch, x, np.tile(-np.arange(K, dtype=np.float32) / 64, (N, 1)), 2 * K)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("V", [3, 40, 30001])
+def test_beams_alike_but_for_one_logit(V, dtype):
+    """Rows that differ in one small logit, the first, last or any other: their
+    sums differ by less than a 32-bit one shows, and rank the beams."""
+    torch = need_gpu()
+    N, K = 2, 8
+    x = make(torch, N * K, V, dtype, seed=12, ld=V + 5, offset=1, scale=1.0)
+    x[:] = x[:1].clone()
+    for i, at in enumerate((0, V - 1, V // 2, 1, V - 2, V - 1)):
+        for row in (i + 1, K + (i * 3) % K):
+            x[row, at] = -9.0 - 0.25 * i
+    check(torch, x, np.full((N, K), -0.5, np.float32), min(3 * K, K * V))
