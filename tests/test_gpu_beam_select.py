@@ -388,3 +388,57 @@ def test_beams_alike_but_for_one_logit(V, dtype):
         for row in (i + 1, K + (i * 3) % K):
             x[row, at] = -9.0 - 0.25 * i
     check(torch, x, np.full((N, K), -0.5, np.float32), min(3 * K, K * V))
+
+
+def unlike_rows(torch, dtype, V, at, value):
+    """Rows [len(value), V] that differ in one logit: element `at` + 1 of a row
+    is its `value`, which lies 18 or more below the row's largest logit, `at`, in
+    the same 16 bytes. What it adds to their sum is lost in fp32 but not in 64
+    bits, in which it ranks the beams."""
+    x = make(torch, 1, V, dtype, seed=21, scale=1.0).repeat(len(value), 1)
+    assert at % 4 == 0 and x.data_ptr() % 16 == 0 and V * x.element_size() % 16 == 0
+    x[:, at] = 15.0
+    x[:, at + 1] = torch.tensor(value, device="cuda").to(x.dtype)
+    return x
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("V", [8, 40, 1600, 40000])
+def test_unlike_beams_whose_32_bit_sums_agree(V, dtype):
+    """Beams of equal scores whose rows differ by one logit far below the
+    largest of its 16 bytes: 32-bit sums are the same to the last bit, 64-bit
+    ones rank the beams, the one that has a token banned first."""
+    torch = need_gpu()
+    inf = float("inf")
+    at = V // 2 // 8 * 8
+    value = [-4.5, -3.0, -inf, -6.0, -3.0, -inf, -9.0, -4.5]
+    K = len(value)
+    one = np.full((1, K), -1.5, np.float32)
+    for order in (list(range(K)), list(range(K))[::-1], [0, 2], [1, 5, 0]):
+        x = unlike_rows(torch, dtype, V, at, [value[b] for b in order])
+        k = len(order)
+        for n in (1, k, min(3 * k + 1, k * V)):
+            check(torch, x, one[:, :k], n)
+            check(torch, x, one[:, :k], n, weights=np.full((1, k), 0.375, np.float32))
+    # pairs of like rows, and with the same rows in several prompts, one of them like throughout
+    x = torch.cat([unlike_rows(torch, dtype, V, at, v) for v in ([-4.5, -6.0] * 4, [-6.0] * 8, sorted(value))])
+    for n in (1, 5, 20):
+        check(torch, x, np.full((3, K), -0.25, np.float32), n)
+
+
+@pytest.mark.parametrize("K", [2, 5])
+def test_finished_beam_that_32_bits_tie_with_another(K):
+    """A finished beam's score is exact. An unfinished one whose best token has
+    all but 1.5e-8 of the weight scores less, which only 64 bits show."""
+    torch = need_gpu()
+    V = 4096
+    x = torch.full((K, V), float("-inf"), device="cuda")
+    x[:, 400] = 0.0
+    x[:, 401] = -18.0
+    scores = np.full((1, K), -0.125, np.float32)
+    finished = np.zeros((1, K), bool)
+    finished[0, K - 1] = True
+    for n in (1, 2, K + 3):
+        check(torch, x, scores, n, finished, end=7)
+        check(torch, x, scores, n, finished[:, ::-1], end=7)
+        check(torch, x, scores, n, np.ones((1, K), bool), end=7)

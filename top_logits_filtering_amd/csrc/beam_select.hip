@@ -687,7 +687,9 @@ struct MergeSmem {
   double weight[kMaxBeams];
   int state[kMaxBeams];       // 0: proposes nothing, 1: its lists, 2: finished
   int close[kMaxBeams];       // a candidate comes too close to another beam's
-  int again;                  // some do
+  int like[kMaxBeams];        // of those, the first beam found to have the same row
+  int again;                  // some come too close and may be in the wrong order
+  int equal;                  // some are equal, and in the right order if their rows are
   uint64_t part[2][kMergeWaves];
   uint32_t heads[kMergeThreads];
   Cand best[kMergeWaves];
@@ -850,7 +852,7 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
     if (u * kMergeThreads < heldn && f < heldn) held[u] = mine[q * n + (f - q * wide)];
   }
 
-  if (tid == 0) sm.count = sm.active[0] = sm.again = 0;
+  if (tid == 0) sm.count = sm.active[0] = sm.again = sm.equal = 0;
   // A wave per beam, whose lanes take its chunks side by side (19 of them: 6.1 us
   // in all instead of 12.6); a thread per beam where there are more beams.
   if (K <= kMergeWaves) {
@@ -1129,27 +1131,57 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       lds_barrier();
 
       // Neighbours of different beams that lie closer than the sums are exact, and
-      // what lies so close behind the n-th: those beams' sums are formed again. (If
-      // all such are equal, they are of beams alike, and stand.)
+      // what lies so close behind the n-th: those beams' sums are formed again.
+      // Equal ranks do not show that the sums are: a logit far below another one is
+      // lost in 32 bits. But of the same score, weight, logit and row they tie.
+      auto pairs = [&](auto compare) __attribute__((always_inline)) {
+        if (static_cast<uint32_t>(tid) + 1u < (M < n ? M : n)) compare(sm.sorted[tid], sm.sorted[tid + 1]);
+        for (uint32_t e = tid; e < M; e += kMergeThreads)
+          if (sm.rank[e] >= n) compare(sm.sorted[n - 1], sm.list[e]);
+      };
       auto value = [](const Cand& k) -> double {
         return __builtin_bit_cast(double, (k.hi >> 63) ? k.hi & 0x7FFFFFFFFFFFFFFFull : ~k.hi);
       };
-      auto compare = [&](const Cand& p, const Cand& q) __attribute__((always_inline)) {
+      pairs([&](const Cand& p, const Cand& q) __attribute__((always_inline)) {
         const int bp = beam_of(p), bq = beam_of(q);
-        if (bp != bq && value(p) - value(q) <= margin) {
-          if (p.hi != q.hi && (sm.state[bp] == 1 || sm.state[bq] == 1)) sm.again = 1;
-          sm.close[bp] = sm.close[bq] = 1;
-        }
-      };
-      if (static_cast<uint32_t>(tid) + 1u < (M < n ? M : n)) compare(sm.sorted[tid], sm.sorted[tid + 1]);
-      for (uint32_t e = tid; e < M; e += kMergeThreads)
-        if (sm.rank[e] >= n) compare(sm.sorted[n - 1], sm.list[e]);
+        if (bp == bq || (sm.state[bp] == 2 && sm.state[bq] == 2) || value(p) - value(q) > margin) return;
+        const bool tie = p.hi == q.hi && sm.state[bp] == sm.state[bq] && sm.score[bp] == sm.score[bq] &&
+                         sm.weight[bp] == sm.weight[bq] && ((p.lo ^ q.lo) >> kTokenBits & 0xFFFFFFFFu) == 0;
+        (tie ? sm.equal : sm.again) = 1;
+        sm.close[bp] = sm.close[bq] = 1;
+      });
       lds_barrier();
-      if (sm.again == 0) break;
+      if (sm.again == 0) {
+        if (sm.equal == 0) break;
+        // Rows are compared where their sums are equal, until two of them differ all
+        // the same: 4 beams with the same row of 151936 bf16 take 31 us so, 64 of them
+        // 0.85 ms. (Like rows at different offsets from 16 bytes may have unequal sums.)
+        bool differ = false;
+        for (int b = 0; b < K && !differ; ++b) {
+          if (sm.close[b] == 0) continue;
+          int like = 0;
+          while (like < b && !(sm.close[like] != 0 && sm.like[like] == like && sm.ref[like] == sm.ref[b] &&
+                               sm.rest[like] == sm.rest[b]))
+            ++like;
+          differ = like < b && !rows_alike<DT>(a, item * K + like, item * K + b);
+          if (tid == 0) sm.like[b] = like;
+          lds_barrier();
+        }
+        if (differ && tid == 0) sm.again = 1;
+        pairs([&](const Cand& p, const Cand& q) __attribute__((always_inline)) {
+          const int bp = beam_of(p), bq = beam_of(q);
+          if (!differ && sm.close[bp] != 0 && sm.close[bq] != 0 && sm.like[bp] != sm.like[bq] &&
+              value(p) - value(q) <= margin)
+            sm.again = 1;
+        });
+        lds_barrier();
+        if (sm.again == 0) break;
+      }
       __syncthreads();  // what this pass wrote lies before what the next one writes
     }
-    // Rows alike have one sum: 64 beams with the same row of 151936 take 1.0 ms so
-    // and 5.0 with a sum each, 4 of them 114 us and 309.
+    // A row with the bits of the last one summed has its sum: 64 beams with the same
+    // row of 151937 bf16, at all offsets from 16 bytes, take 0.95 ms so and 4.9 with a
+    // sum each, 4 of them 115 us and 306. (Like rows in turn with others are summed.)
     int before = -1;
     for (int b = 0; b < K; ++b) {
       if (sm.close[b] == 0 || sm.state[b] != 1) continue;
