@@ -442,3 +442,21 @@ def test_finished_beam_that_32_bits_tie_with_another(K):
         check(torch, x, scores, n, finished, end=7)
         check(torch, x, scores, n, finished[:, ::-1], end=7)
         check(torch, x, scores, n, np.ones((1, K), bool), end=7)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("score", [-3e7, -1e9, -1e10, -3e12, 2e10])
+def test_scores_whose_steps_exceed_a_sum_s_error(score, dtype):
+    """Scores so large that ranks have coarse steps even in 64 bits: rows with
+    the same logits in another order tie there, and their 32-bit sums, which
+    differ, may round to different steps."""
+    torch = need_gpu()
+    N, K, V = 60, 4, 24
+    rng = np.random.default_rng(17)
+    base = (rng.standard_normal((N, 1, V)) * 3).astype(np.float32)
+    x = make(torch, N * K, V, dtype, seed=0)
+    x.copy_(torch.from_numpy(rng.permuted(np.broadcast_to(base, (N, K, V)), axis=2).reshape(N * K, V)))
+    scores = np.full((N, K), score, np.float32)
+    for n in (1, 7, 60):
+        check(torch, x, scores, n)
+        check(torch, x, scores, n, weights=np.full((N, K), 0.75, np.float32))

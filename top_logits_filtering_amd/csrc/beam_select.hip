@@ -165,6 +165,10 @@ __device__ __forceinline__ double sum_of(double sum, double rest) {
 // a multiply-add at 2^-24 or the 1e-8 of sum_of; less than 1e-10 of what
 // follows in 64 bits.
 constexpr double kSumError = 3.5e-7;
+// A rank is rounded four times, x - ref, less rest, plus c and times w, all but the
+// last to numbers below |s| + |c|: with and without kSumError, and of two ranks, by
+// less than 2^-49 |s w| + 2^-50 |c w| together. That shows with scores from 1e9 on.
+constexpr double kRounding = 0x1p-48;
 
 // exp(x - ref) in 64 bits, for finite ref and x below ref + 700 or -inf.
 __device__ __forceinline__ double exp_below(float x, float ref) {
@@ -676,6 +680,10 @@ __device__ __forceinline__ bool above(const Cand& a, const Cand& b) {
   return a.hi > b.hi || (a.hi == b.hi && a.lo > b.lo);
 }
 
+// Candidates of two beams come too close and may be in the wrong order; or they are
+// equal and in the right order if the beams' rows are alike.
+constexpr int kAgain = 1, kEqual = 2;
+
 struct MergeSmem {
   Cand list[kMergeCap + kMergeStep];
   Cand sorted[kMaxCandidates];
@@ -688,8 +696,7 @@ struct MergeSmem {
   int state[kMaxBeams];       // 0: proposes nothing, 1: its lists, 2: finished
   int close[kMaxBeams];       // a candidate comes too close to another beam's
   int like[kMaxBeams];        // of those, the first beam found to have the same row
-  int again;                  // some come too close and may be in the wrong order
-  int equal;                  // some are equal, and in the right order if their rows are
+  int again;                  // kAgain and kEqual
   uint64_t part[2][kMergeWaves];
   uint32_t heads[kMergeThreads];
   Cand best[kMergeWaves];
@@ -813,11 +820,12 @@ __device__ bool rows_alike(const BeamSelectArgs& a, int64_t row0, int64_t row1) 
   return !__syncthreads_or(static_cast<int>(differ != 0));
 }
 
-// The upper half of the image of a rank value by `margin` below T's.
+// The upper half of the image of a rank value by `margin` and its rounding below T's.
 __device__ __forceinline__ uint32_t lowered(uint32_t T, double margin) {
   const uint64_t u = static_cast<uint64_t>(T) << 32;
   const uint64_t bits = (u >> 63) ? u & 0x7FFFFFFFFFFFFFFFull : ~u;
-  const uint32_t t = static_cast<uint32_t>(order_key64(__builtin_bit_cast(double, bits) - margin) >> 32);
+  const double value = __builtin_bit_cast(double, bits);
+  const uint32_t t = static_cast<uint32_t>(order_key64(value - (margin + kRounding * fabs(value))) >> 32);
   return t < T && t > 0u ? t : T;
 }
 
@@ -852,7 +860,20 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
     if (u * kMergeThreads < heldn && f < heldn) held[u] = mine[q * n + (f - q * wide)];
   }
 
-  if (tid == 0) sm.count = sm.active[0] = sm.again = sm.equal = 0;
+  // Ranks of two beams may be off against each other by this and kRounding of the rank.
+  uint32_t most_w = 0, most_c = 0;  // the largest weight, and the upper half of the largest |c w|
+  for (int b = lane; b < K; b += kWave) {
+    const float c = a.scores[item * K + b], w = a.weights != nullptr ? a.weights[item * K + b] : 1.0f;
+    if (!beam_alive(c, w)) continue;
+    const double cw = fabs(static_cast<double>(c) * static_cast<double>(w));
+    const uint32_t upper = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, cw) >> 32);
+    most_w = most_w > __float_as_uint(w) ? most_w : __float_as_uint(w);
+    most_c = most_c > upper ? most_c : upper;
+  }
+  const double margin = 2.0 * kSumError * __uint_as_float(wave_max_u32(most_w)) +
+                        kRounding * __builtin_bit_cast(double, static_cast<uint64_t>(wave_max_u32(most_c) + 1u) << 32);
+
+  if (tid == 0) sm.count = sm.active[0] = sm.again = 0;
   // A wave per beam, whose lanes take its chunks side by side (19 of them: 6.1 us
   // in all instead of 12.6); a thread per beam where there are more beams.
   if (K <= kMergeWaves) {
@@ -888,15 +909,6 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
   }
   if (tid < K) sm.close[tid] = 0;
   lds_barrier();
-
-  // Ranks of two beams may be off against each other by this.
-  double margin = 2.0 * kSumError;
-  if (a.weights != nullptr) {
-    uint32_t most = 0;
-    for (int b = lane; b < K; b += kWave)
-      if (sm.state[b] != 0) most = most > __float_as_uint(sm.weight[b]) ? most : __float_as_uint(sm.weight[b]);
-    margin *= __uint_as_float(wave_max_u32(most));
-  }
 
   // Entry j of list q, e, as a candidate; hi is 0 where there is none.
   auto cand = [&](uint64_t e, uint32_t q, uint32_t j) __attribute__((always_inline)) -> Cand {
@@ -1142,17 +1154,21 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
       auto value = [](const Cand& k) -> double {
         return __builtin_bit_cast(double, (k.hi >> 63) ? k.hi & 0x7FFFFFFFFFFFFFFFull : ~k.hi);
       };
+      auto near = [&](const Cand& p, const Cand& q) -> bool {
+        return value(p) - value(q) <= margin + kRounding * fabs(value(q));
+      };
       pairs([&](const Cand& p, const Cand& q) __attribute__((always_inline)) {
         const int bp = beam_of(p), bq = beam_of(q);
-        if (bp == bq || (sm.state[bp] == 2 && sm.state[bq] == 2) || value(p) - value(q) > margin) return;
+        if (bp == bq || !near(p, q) || (sm.state[bp] == 2 && sm.state[bq] == 2)) return;
         const bool tie = p.hi == q.hi && sm.state[bp] == sm.state[bq] && sm.score[bp] == sm.score[bq] &&
                          sm.weight[bp] == sm.weight[bq] && ((p.lo ^ q.lo) >> kTokenBits & 0xFFFFFFFFu) == 0;
-        (tie ? sm.equal : sm.again) = 1;
+        atomicOr(&sm.again, tie ? kEqual : kAgain);
         sm.close[bp] = sm.close[bq] = 1;
       });
       lds_barrier();
-      if (sm.again == 0) {
-        if (sm.equal == 0) break;
+      const int again = sm.again;
+      if (again == 0) break;
+      if (again == kEqual) {
         // Rows are compared where their sums are equal, until two of them differ all
         // the same: 4 beams with the same row of 151936 bf16 take 31 us so, 64 of them
         // 0.85 ms. (Like rows at different offsets from 16 bytes may have unequal sums.)
@@ -1167,15 +1183,13 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
           if (tid == 0) sm.like[b] = like;
           lds_barrier();
         }
-        if (differ && tid == 0) sm.again = 1;
         pairs([&](const Cand& p, const Cand& q) __attribute__((always_inline)) {
           const int bp = beam_of(p), bq = beam_of(q);
-          if (!differ && sm.close[bp] != 0 && sm.close[bq] != 0 && sm.like[bp] != sm.like[bq] &&
-              value(p) - value(q) <= margin)
-            sm.again = 1;
+          if (!differ && sm.close[bp] != 0 && sm.close[bq] != 0 && sm.like[bp] != sm.like[bq] && near(p, q))
+            sm.again = kAgain;
         });
         lds_barrier();
-        if (sm.again == 0) break;
+        if (!differ && sm.again == kEqual) break;
       }
       __syncthreads();  // what this pass wrote lies before what the next one writes
     }
