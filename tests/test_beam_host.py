@@ -232,3 +232,13 @@ def test_plain_forms_by_hand():
     assert beam_ref.backtrace(tokens, parents).tolist() == [[[1, 5, 6], [0, 3, 7], [1, 5, 8]]]
     assert beam_ref.reorder(np.array([[1], [2], [3]]), np.array([[2, 0, -1]]), 0).tolist() == [[3], [1], [3]]
     assert ctypes.sizeof(BeamState) == 88
+
+
+def test_reorder_refuses_states_that_record_gradients():
+    leaf = torch.zeros(6, 5, requires_grad=True)
+    parents = torch.zeros(2, 3, dtype=torch.int32)
+    for state in (leaf, leaf[:, :3], leaf * 2, [torch.zeros(6, 2), leaf]):
+        with pytest.raises(ValueError, match="requires grad"):
+            tk.beam_reorder_states(state, parents)
+        with torch.no_grad(), pytest.raises(ValueError, match="GPU"):  # that of tensors on the CPU
+            tk.beam_reorder_states(state, parents)

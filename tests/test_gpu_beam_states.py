@@ -245,3 +245,42 @@ def test_backtrace_of_many_prompts():
     first = np.take_along_axis(tokens[0], np.maximum(parents[1], 0), 1)
     want = np.stack([np.where(parents[1] < 0, -1, first), tokens[1]], 2)
     assert np.array_equal(got.cpu().numpy(), want)
+
+
+def test_reorder_counts_as_a_modification():
+    """A state saved for a backward pass must not change unnoticed; a parameter
+    may be reordered under no_grad, as may tensors of inference mode."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    N, K = 2, 3
+    parents = torch.tensor([[1, 0, 2], [0, 0, 0]], dtype=torch.int32, device="cuda")
+    x = torch.ones((N * K, 4), device="cuda", requires_grad=True)
+    states = [torch.rand((N * K, 4), device="cuda"), torch.rand((N * K, 4), device="cuda")]
+    before = [s._version for s in states]
+    y = (x * states[1]).sum()
+    tk.beam_reorder_states(states, parents)
+    assert all(s._version > v for s, v in zip(states, before))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    base = torch.rand((N * K, 8), device="cuda")
+    seen = base._version
+    tk.beam_reorder_states(base[:, :4], parents)
+    assert base._version > seen  # a view's memory is its base's
+    tk.beam_reorder_states([], parents)
+
+    leaf = torch.rand((N * K, 4), device="cuda", requires_grad=True)
+    now, want = leaf._version, beam_ref.reorder(leaf.detach().cpu().numpy(), parents.cpu().numpy(), 0)
+    with pytest.raises(ValueError, match="requires grad"):
+        tk.beam_reorder_states(leaf, parents)
+    with torch.no_grad():
+        tk.beam_reorder_states(leaf, parents)
+    assert leaf._version > now and np.array_equal(leaf.detach().cpu().numpy(), want)
+    with torch.inference_mode():
+        cache = torch.rand((N * K, 4), device="cuda")
+        want = beam_ref.reorder(cache.cpu().numpy(), parents.cpu().numpy(), 0)
+        tk.beam_reorder_states(cache, parents)
+    assert np.array_equal(cache.cpu().numpy(), want)
+    tk.beam_reorder_states(cache, parents)  # and outside of it
+    torch.cuda.synchronize()
+    assert np.array_equal(cache.cpu().numpy(), beam_ref.reorder(want, parents.cpu().numpy(), 0))

@@ -394,7 +394,7 @@ def _scope(stream, device):
         raise ValueError("tensors must live on the GPU")
     if stream is None:
         handle = torch._C._cuda_getCurrentRawStream(device.index)
-        if torch.cuda.current_device() == device.index:
+        if torch._C._cuda_getDevice() == device.index:
             return handle, _NULL_SCOPE
         return handle, torch.cuda.device(device)
     if not hasattr(stream, "cuda_stream"):  # a handle; 0 is the default stream's
@@ -555,7 +555,9 @@ def beam_reorder_states(states, parents, batch_dim=0, seq_dim=None, lengths=None
     dtype and strides), all with the rows along batch_dim. parents [N, K]
     int32; a row whose parent lies outside [0, K) stays as it is. lengths [N]
     int32 (needs seq_dim): only positions below lengths[i] along seq_dim are
-    moved. Returns states."""
+    moved. Returns states. Gradients do not flow through the move: a state that
+    requires grad is refused unless under no_grad, and one that was saved for a
+    backward pass counts as modified, as with torch's in-place operations."""
     import torch
 
     lib = _lib or load_library()
@@ -576,6 +578,8 @@ def beam_reorder_states(states, parents, batch_dim=0, seq_dim=None, lengths=None
             raise ValueError(f"tensors must share one device: a state is on {t.device}")
         if t.is_neg() or (t.is_complex() and t.is_conj()):
             raise ValueError("a state must not be a lazily conjugated or negated view")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("a state that requires grad can only be reordered under no_grad")
         descs.append(_pack_pointer(t.data_ptr()))
         descs.append(_state_bytes(t.shape, t.stride(), t.element_size(), batch_dim, seq, N * K))
     descs = b"".join(descs)
@@ -584,6 +588,7 @@ def beam_reorder_states(states, parents, batch_dim=0, seq_dim=None, lengths=None
         status = lib.beam_reorder_states(descs, len(tensors), parents.data_ptr(), N, K,
                                          None if lengths is None else lengths.data_ptr(), handle)
     _check(status)
+    torch.autograd.graph.increment_version(tensors)
     return states
 
 
