@@ -175,3 +175,44 @@ def test_reorder_more_than_the_cache(K):
             want = torch.where(moved[r], keep[source[r]], keep[r])
             assert torch.equal(state[0][r], want), (axis, r)
         del keep
+
+
+def test_given_outputs_count_as_modified():
+    """Outputs that the caller gives are written in place: what was saved of
+    them for a backward pass must not change unnoticed."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    N, K, V, T = 2, 3, 50, 4
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    logits = torch.randn((N * K, V), generator=g, device="cuda", requires_grad=True)
+    scores = torch.zeros((N, K), device="cuda")
+    want = tk.beam_search_select(logits, scores)
+    assert not any(t.requires_grad for t in want)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    out = (torch.zeros((N, K), device="cuda"), torch.zeros((N, K), **i32), torch.zeros((N, K), **i32))
+    seen = [t._version for t in out]
+    x = torch.ones((N, K), device="cuda", requires_grad=True)
+    y = (x * out[0]).sum() + torch.index_select(x, 1, out[1].view(-1)).sum()
+    got = tk.beam_search_select(logits, scores, out=out)
+    assert all(a is b for a, b in zip(got, out)) and all(torch.equal(a, b) for a, b in zip(out, want))
+    assert all(t._version > v for t, v in zip(out, seen))
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+
+    leaf = torch.zeros((N, K), device="cuda", requires_grad=True)
+    with pytest.raises(ValueError, match="require grad"):
+        tk.beam_search_select(logits, scores, out=(leaf, *out[1:]))
+    with torch.no_grad():
+        tk.beam_search_select(logits, scores, out=(leaf, *out[1:]))
+    assert torch.equal(leaf.detach(), want[0])
+
+    tokens, parents = (torch.zeros((T, N, K), **i32) for _ in range(2))
+    paths = torch.ones((N, K, T), **i32)
+    seen = paths._version
+    assert tk.beam_backtrace(tokens, parents, out=paths) is paths and paths._version > seen
+    with torch.inference_mode():
+        paths = torch.ones((N, K, T), **i32)
+    tk.beam_backtrace(tokens, parents, out=paths)
+    assert not bool(paths.any())

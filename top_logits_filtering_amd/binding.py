@@ -444,7 +444,9 @@ def beam_search_select(logits, scores, n=None, finished=None, end_token=None, we
     tokens whose logit is -inf are left out; ranks without a continuation hold
     score -inf, parent -1, token -1. out: the three tensors to fill; workspace:
     a uint8 tensor of beam_search_select_workspace() bytes, not used by any
-    other call that may run at the same time (each call allocates one else)."""
+    other call that may run at the same time (each call allocates one else).
+    No gradients: what is returned does not depend on logits or scores for
+    autograd, whether or not these require grad."""
     import torch
 
     lib = _lib or load_library()
@@ -476,8 +478,9 @@ def beam_search_select(logits, scores, n=None, finished=None, end_token=None, we
         _check_dense(weights, (N, K), torch.float32, "weights", dev)
         p_weights = weights.data_ptr()
     handle, scope = _scope(stream, logits.device)
+    given = out is not None
     with scope:
-        if out is None:
+        if not given:
             out = (torch.empty((N, n), dtype=torch.float32, device=logits.device),
                    torch.empty((N, n), dtype=torch.int32, device=logits.device),
                    torch.empty((N, n), dtype=torch.int32, device=logits.device))
@@ -485,6 +488,8 @@ def beam_search_select(logits, scores, n=None, finished=None, end_token=None, we
         _check_dense(o_scores, (N, n), torch.float32, "out scores", dev)
         _check_dense(o_parents, (N, n), torch.int32, "out parents", dev)
         _check_dense(o_tokens, (N, n), torch.int32, "out tokens", dev)
+        if o_scores.requires_grad and torch.is_grad_enabled():
+            raise ValueError("out scores that require grad can only be written under no_grad")
         if workspace is None:
             size = lib.beam_search_select_workspace(dtype, N, K, V, n)
             if size < 0:
@@ -498,6 +503,8 @@ def beam_search_select(logits, scores, n=None, finished=None, end_token=None, we
             0 if finished is None else int(end_token), p_weights, n, o_scores.data_ptr(), o_parents.data_ptr(),
             o_tokens.data_ptr(), workspace.data_ptr(), size, handle)
     _check(status)
+    if given:
+        torch.autograd.graph.increment_version(out)
     return out
 
 
@@ -618,8 +625,9 @@ def beam_backtrace(tokens, parents, beams=None, lengths=None, pad=-1, out=None, 
     if lengths is not None:
         _check_dense(lengths, (N, M), torch.int32, "lengths", dev)
     handle, scope = _scope(stream, tokens.device)
+    given = out is not None
     with scope:
-        if out is None:
+        if not given:
             out = torch.empty((N, M, T), dtype=torch.int32, device=tokens.device)
         _check_dense(out, (N, M, T), torch.int32, "out", dev)
         status = lib.beam_backtrace(tokens.data_ptr(), parents.data_ptr(), T, N, K,
@@ -627,4 +635,6 @@ def beam_backtrace(tokens, parents, beams=None, lengths=None, pad=-1, out=None, 
                                     None if lengths is None else lengths.data_ptr(), M, int(pad), out.data_ptr(),
                                     handle)
     _check(status)
+    if given:
+        torch.autograd.graph.increment_version(out)
     return out
