@@ -284,3 +284,66 @@ def test_reorder_counts_as_a_modification():
     tk.beam_reorder_states(cache, parents)  # and outside of it
     torch.cuda.synchronize()
     assert np.array_equal(cache.cpu().numpy(), beam_ref.reorder(want, parents.cpu().numpy(), 0))
+
+
+@pytest.mark.parametrize("K", [4, 8, 12, 128])
+def test_backtrace_of_unaligned_histories(K):
+    """Numbers of beams that are read four at a time, in histories that begin at
+    any multiple of 4 bytes."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    T, N, M = 75, 3, 9
+    rng = np.random.default_rng(K)
+    tokens = rng.integers(0, 50000, (T, N, K)).astype(np.int32)
+    parents = rng.integers(-1, K + 1, (T, N, K)).astype(np.int32)
+    parents[rng.random((T, N, K)) < 0.8] = 1
+    beams = rng.integers(0, K, (N, M)).astype(np.int32)
+    lengths = rng.integers(0, T + 1, (N, M)).astype(np.int32)
+    want = beam_ref.backtrace(tokens, parents, beams, lengths)
+    for shift in range(5):
+        buf = torch.full((2, T * N * K + 8), 10 ** 9, dtype=torch.int32, device="cuda")
+        history = [b[shift:shift + T * N * K].view(T, N, K) for b in buf]
+        for view, a in zip(history, (tokens, parents)):
+            view.copy_(torch.from_numpy(a))
+        assert history[1].data_ptr() % 16 == 4 * shift % 16
+        got = tk.beam_backtrace(*history, *(torch.from_numpy(a).cuda() for a in (beams, lengths)))
+        torch.cuda.synchronize()
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
+NARROW = [
+    # N, K, shape around the rows (R), bytes, seq_dim
+    (3, 4, ("R", 4, 64, 515), 2, 3),  # keys held transposed, an odd number of positions
+    (3, 4, ("R", 4, 64, 512), 2, 3),
+    (3, 4, ("R", 2, 64, 513), 1, 3),
+    (3, 4, ("R", 4, 300, 75), 2, 2),  # an odd head size
+    (3, 6, ("R", 300, 3, 75), 2, 1),
+    (3, 40, ("R", 999, 6), 2, 1),
+    (3, 5, ("R", 70001), 2, 1),  # words by position
+    (3, 5, ("R", 4, 200, 33), 4, 2),
+]
+
+
+@pytest.mark.parametrize("case", NARROW, ids=[str(c) for c in NARROW])
+def test_reorder_of_narrow_runs(case):
+    """States whose positions are a few bytes that follow each other, at more
+    than a workgroup's size, with lengths that end at every byte of a word."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    N, K, shape, es, sd = case
+    shape = tuple(N * K if s == "R" else s for s in shape)
+    dtype = {1: torch.uint8, 2: torch.bfloat16, 4: torch.float32}[es]
+    parents = parents_of(N, K, 2)
+    dev_p = torch.from_numpy(parents).cuda()
+    T = shape[sd]
+    start = filled(torch, shape, dtype, 11)
+    for least in range(0, 18, 3):
+        lengths = np.array([T - 1 - least, T // 2 + least, least], np.int32)
+        state = start.clone()
+        want = beam_ref.reorder(bits(state), parents, 0, sd, lengths)
+        tk.beam_reorder_states(state, dev_p, seq_dim=sd, lengths=torch.from_numpy(lengths).cuda())
+        torch.cuda.synchronize()
+        assert np.array_equal(bits(state), want), lengths
+    say(f"reorder {case}")
