@@ -303,7 +303,7 @@ topktopp_status top_k_top_p_sorted_survivors(const void* logits, topktopp_dtype 
  * The continuation of beam b with token v has the score
  *   s = c[b] + logits[b][v] - log(sum_u exp(logits[b][u]))
  * and the rank value s * weights[b]. A finished beam has one continuation:
- * itself, with end_token and the score c[b]; its logits are not read. Equal
+ * itself, with end_token and the score c[b], whatever its logits hold. Equal
  * rank values are ordered by beam (lower first), then by logit (larger
  * first), then by token (lower first). Tokens with a logit of -inf are no
  * continuations. A beam has none at all if its score is infinite or NaN, its
@@ -313,8 +313,10 @@ topktopp_status top_k_top_p_sorted_survivors(const void* logits, topktopp_dtype 
  *
  * Numerics. A sum of exp has a relative error below 3.6e-7, what follows is
  * formed in 64 bits and rounded once, to out_scores. Where two beams'
- * continuations come closer than that error, their sums are formed again in
- * 64 bits, so the order is that of 64-bit values.
+ * continuations come closer than that error and the roundings of their rank
+ * values, or tie, their sums are formed again in 64 bits (or found to be those
+ * of rows with the same bits), so the order is that of 64-bit values. Of two
+ * that only the roundings of 64 bits tell apart, either may come first.
  * Results are deterministic.
  *
  * Errors: ERR_NULLPTR for logits (unless V is 0), scores, an output or the
@@ -354,7 +356,12 @@ typedef struct {
 
 /*
  * beam_reorder_states — in every state, row i * K + b becomes what row
- * i * K + parents[i][b] was before the call.
+ * i * K + parents[i][b] was before the call. Columns of the rows are moved, of
+ * 16 bytes where all strides, the data and a row's pieces allow it, else of 4, 2
+ * or 1 bytes, which is slower. Positions that follow each other without a gap
+ * (position_stride == run) take columns of 2 bytes or 1 where the run is no
+ * multiple of 4, so that a length may end anywhere; a state that is moved whole
+ * is better described without positions, as longer runs.
  *
  *   states   host array of `count` descriptions (0 <= count), read during the
  *            call. Rows of a state: N * K. A state that shares memory with an

@@ -22,10 +22,10 @@
 // fp32 ones 110 us against 89 (85 today).
 //
 // The logits have to be read once and nothing else is of their size. Times on
-// one MI355X, chunks + merge, V tokens: a prompt of 4 beams, V 151936 bf16: 5.9 +
-// 6.1 us, chains of dependent steps; 64 such prompts: 20 + 6 us (3.9 TB/s); 128
-// prompts of 8 beams, V 128256 fp32: 85 + 9 us (6.2 TB/s); 2 prompts of 64 beams,
-// V 151936 bf16, 128 continuations: 20 + 16 us.
+// one MI355X, chunks + merge, V tokens: a prompt of 4 beams, V 151936 bf16: 5.8 +
+// 6.3 us, chains of dependent steps; 64 such prompts: 20 + 6 us (3.9 TB/s); 128
+// prompts of 8 beams, V 128256 fp32: 85 to 88 + 9 us (6.0 to 6.2 TB/s); 2 prompts of
+// 64 beams, V 151936 bf16, 128 continuations: 21 + 17 us.
 
 #include <float.h>
 
@@ -115,7 +115,7 @@ __device__ __forceinline__ uint64_t pack(uint32_t key, uint32_t token) {
 // before the sum. Other chunks are read and summed again in 64 bits, less their
 // maximum.
 constexpr float kHighMax = 80.0f;  // eight terms of exp(80) stay finite
-constexpr float kLowMax = -40.0f;  // terms that fp32 flushes are below 2^-68 of the largest
+constexpr float kLowMax = -40.0f;  // terms that exp2 flushes are below 2^-68 of the largest
 
 constexpr float kLn2 = 0.693147180559945309417f;
 
@@ -161,9 +161,9 @@ __device__ __forceinline__ double sum_of(double sum, double rest) {
 }
 
 // Relative error of a chunk's sum: 8.5e-8 of exp2 (the most over all arguments
-// in +-[2^-10, 120), measured), three additions in fp32 at 2^-24 each, and either
-// a multiply-add at 2^-24 or the 1e-8 of sum_of; less than 1e-10 of what
-// follows in 64 bits.
+// from -126 to 126, measured; below them it gives 0), three additions in fp32 at
+// 2^-24 each, and either a multiply-add at 2^-24 or the 1e-8 of sum_of; less than
+// 1e-10 of what follows in 64 bits.
 constexpr double kSumError = 3.5e-7;
 // A rank is rounded four times, x - ref, less rest, plus c and times w, all but the
 // last to numbers below |s| + |c|: with and without kSumError, and of two ranks, by
@@ -310,10 +310,11 @@ __device__ __forceinline__ uint32_t block_excl(uint32_t v, uint32_t& total, Chun
 // of some of these maxima bounds the n-th largest element from below, so only
 // units that reach it, a few more than n, are looked at again; their elements
 // that reach it are ranked against each other. What bounds it: memory for fp32
-// (6.2 TB/s at 525 MB); for 16-bit types the seven instructions an element beside
-// it (with the correction that fp32 needs, two more, 256 rows of 151936 bf16 take
-// 21.6 us instead of 19.8), and with few chunks the 4 us from the last load to
-// the last store.
+// (6.0 to 6.2 TB/s at 525 MB); for 256 rows of 151936 16-bit logits (3.9 TB/s) the seven
+// instructions an element in part (with the correction that fp32 needs, two more,
+// they take 21.6 us instead of 19.8), and that all 768 workgroups start and end
+// together, so that none's 4 us from the last load to the last store are hidden;
+// with few chunks those 4 us.
 // SHORT: the chunk is one group of layers, which stays in registers (6.5 us
 // instead of 6.8 for 64 rows of 32000 fp16); otherwise groups stream through and
 // the few vectors that matter are read again.
@@ -364,7 +365,9 @@ __global__ __launch_bounds__(kChunkThreads) void beam_chunk_kernel(BeamSelectArg
   if (ch == split.chunks - 1 && tid >= 16 && tid - 16 < a.V - tail0) te = tail0 + tid - 16;
   raw_t re = DT::kNegInf;
   if (te >= 0) re = rowp[te];
-  // (the first loads are under way before it is known whether the row counts)
+  // (the first loads are under way before it is known whether the row counts: of 64
+  // rows of 32000 fp16 that are short chunks throughout, 16 of them finished, all are
+  // read, 4.6 MB with the lists where the other 48 have 3.1)
   if (!beam_alive(a.scores[row], a.weights != nullptr ? a.weights[row] : 1.0f)) return;
   if (a.finished != nullptr && a.finished[row] != 0) return;
   if (tid == 0) sm.count = sm.hits = 0;
@@ -833,8 +836,8 @@ __device__ __forceinline__ uint32_t lowered(uint32_t T, double margin) {
 // lists. The lists' first entries are held in registers from the start; the n-th
 // of the threads' best bounds the n-th candidate, lists whose last entry held
 // still reaches the bound are read on, and what reaches it is ranked. A chain of
-// some ten dependent steps in shared memory, 4.6 to 9 us for up to 16
-// candidates, and 16 us for 128 of 64 beams: more workgroups than one to a prompt
+// some ten dependent steps in shared memory, 5 to 9.6 us for up to 16
+// candidates, and 17 us for 128 of 64 beams: more workgroups than one to a prompt
 // would have to meet again at its end.
 template <class DT>
 __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArgs a, Div chunks, Div window,

@@ -10,9 +10,13 @@
 // columns.
 //
 // Memory bounds it: each changed row written once and each of their parents read
-// once. On one MI355X, rates of those bytes: 4 beams 2.4 GB in 409 us (5.9 TB/s),
-// 6 beams 219 MB in one state 38 us (5.7), 16 to 32 beams 5.3 to 5.5 TB/s, 64 and
-// 128 beams 4.3 and 4.7. Four small states of one prompt take 4.2 us.
+// once. On one MI355X, rates of those bytes in columns of 16 bytes: 4 beams 2.4 GB
+// in 410 us (5.9 TB/s), 6 beams 219 MB in one state 38 us (5.7), 17 and 32 beams 5.4
+// and 5.1 TB/s; 64 and 128 beams, in columns of 4, 3.8 and 4.2, and 2.5 and 2.9
+// where the length ends halfway. Few beams in narrow columns are bound by the number
+// of loads and stores: 4 beams in columns of 4 bytes 2.0 to 2.7 TB/s, of 2 and of 1,
+// which take the registers of 128 beams, 0.25 to 0.34 and 0.17. Four small states of
+// one prompt take 4.2 us.
 
 #include "beam.h"
 #include "device_common.h"
@@ -140,7 +144,9 @@ int64_t low_bit(int64_t x) { return x & -x; }
 // Bytes of a column: what every address is aligned to, at most 16, and for
 // wide beams what fits the registers (2.4 GB of 4 beams take 410 us in columns of
 // 16 bytes, 1170 in columns of 4). Columns of 16 bytes may reach past the
-// length inside a piece of whole words; smaller ones never do.
+// length inside a piece of whole words; smaller ones never do, so that a piece whose
+// positions follow each other in runs that are no whole words (keys held transposed
+// in 16 bits, an odd head size) is moved 2 bytes or 1 at a time up to the length.
 int column_bytes(const BeamState& s, int K) {
   int64_t w = 16 | reinterpret_cast<int64_t>(s.data) | s.row_stride;
   for (int i = 0; i < 3; ++i)
