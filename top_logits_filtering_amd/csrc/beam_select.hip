@@ -166,8 +166,9 @@ __device__ __forceinline__ double sum_of(double sum, double rest) {
 // 1e-10 of what follows in 64 bits.
 constexpr double kSumError = 3.5e-7;
 // A rank is rounded four times, x - ref, less rest, plus c and times w, all but the
-// last to numbers below |s| + |c|: with and without kSumError, and of two ranks, by
-// less than 2^-49 |s w| + 2^-50 |c w| together. That shows with scores from 1e9 on.
+// last to numbers below |s|, or for positive c below |s| + 2c: with and without
+// kSumError, and of two ranks, by less than 2^-49 |s w| and for those 2^-49 c w
+// together. That shows with scores from 1e9 on.
 constexpr double kRounding = 0x1p-48;
 
 // exp(x - ref) in 64 bits, for finite ref and x below ref + 700 or -inf.
@@ -864,14 +865,14 @@ __global__ __launch_bounds__(kMergeThreads) void beam_merge_kernel(BeamSelectArg
   }
 
   // Ranks of two beams may be off against each other by this and kRounding of the rank.
-  uint32_t most_w = 0, most_c = 0;  // the largest weight, and the upper half of the largest |c w|
+  uint32_t most_w = 0, most_c = 0;  // the largest weight, and the upper half of the largest c w > 0
   for (int b = lane; b < K; b += kWave) {
     const float c = a.scores[item * K + b], w = a.weights != nullptr ? a.weights[item * K + b] : 1.0f;
     if (!beam_alive(c, w)) continue;
-    const double cw = fabs(static_cast<double>(c) * static_cast<double>(w));
+    const double cw = static_cast<double>(c) * static_cast<double>(w);
     const uint32_t upper = static_cast<uint32_t>(__builtin_bit_cast(uint64_t, cw) >> 32);
     most_w = most_w > __float_as_uint(w) ? most_w : __float_as_uint(w);
-    most_c = most_c > upper ? most_c : upper;
+    if (c > 0.0f) most_c = most_c > upper ? most_c : upper;
   }
   const double margin = 2.0 * kSumError * __uint_as_float(wave_max_u32(most_w)) +
                         kRounding * __builtin_bit_cast(double, static_cast<uint64_t>(wave_max_u32(most_c) + 1u) << 32);
