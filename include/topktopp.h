@@ -407,6 +407,154 @@ topktopp_status beam_backtrace(const int32_t* tokens, const int32_t* parents, in
                                const int32_t* beams, const int32_t* lengths, int64_t M, int32_t pad, int32_t* out,
                                void* stream);
 
+/* ------------------------------------------------- speculative decoding --- */
+
+#define TOPKTOPP_MAX_DRAFTS 255
+
+/*
+ * speculative_verify — how many drafted tokens stand, and the token behind them.
+ *
+ *   logits     [N * (D + 1), V], rows ld_logits elements apart, of any dtype:
+ *              row i * (D + 1) follows the last token of sequence i, row
+ *              i * (D + 1) + 1 + j its draft j. As they are to be sampled from:
+ *              divided by the temperature, filtered tokens at -inf.
+ *   D          drafts of a sequence, 0 <= D <= TOPKTOPP_MAX_DRAFTS.
+ *   drafts     [N, D] int32 tokens.
+ *   uniforms   [N, D + 1] fp32 in [0, 1), or NULL: greedy.
+ *   draft_logits  [N * D, V] in the dtype of logits, rows ld_draft elements
+ *              apart: row i * D + j is what draft j was drawn from; or NULL for
+ *              drafts that were not drawn. Needs uniforms, and no parents.
+ *   parents    [N, D] int32: draft j follows draft parents[i][j] < j, or -1 for
+ *              the last token, so that the drafts form a tree; or NULL for a
+ *              chain, each behind the one before it.
+ *   lengths    [N] int32, drafts of a sequence that count (values are clamped
+ *              to [0, D]), or NULL for D.
+ *   out_tokens [N, D + 1] int32, written completely: the accepted drafts, the
+ *              token behind them, and -1.
+ *   out_accepted  [N] int32, the number of accepted drafts.
+ *   out_path   [N, D] int32, the accepted drafts' numbers and -1, or NULL.
+ *   workspace  speculative_verify_workspace() bytes of device memory, 16-byte
+ *              aligned. It holds nothing between calls; calls that may run at
+ *              the same time need one each.
+ *
+ * With p_w the softmax of target row w, q_j that of draft row j and u the
+ * sequence's uniforms, at the last token (w = 0) or behind accepted draft w - 1:
+ *   - with draft logits, draft w is accepted if u[w] q_w(d) < p_w(d), d its
+ *     token. If it is not, the token behind is drawn from max(p_w - q_w, 0), or
+ *     from p_w if that adds up to no more than 2^-40.
+ *   - without, the drafts behind w in the order of their numbers cut [0, 1) into
+ *     pieces of p_w(token), and the one whose piece holds u[w] is accepted; a
+ *     token that an earlier one of them has counts once. If there is none, the
+ *     token is drawn from p_w without these tokens, or from p_w if that adds up
+ *     to no more than 2^-40.
+ *   - where no draft follows, the token is drawn from p_w.
+ *   - greedy, the largest logit (the lowest token of equal ones) accepts the
+ *     draft behind w that has it, or else is the token behind.
+ * Drawn from weights r: the lowest token v with sum_{t <= v} r(t) > u[D] sum r
+ * (for a uniform of 1 or more, the last one of any weight).
+ * Drafts whose token lies outside [0, V), or whose parent lies outside
+ * [-1, j), count as not there. A target row with a NaN or +inf, or with nothing
+ * above -inf, accepts nothing and gives the token -1; in such a draft row q is 0.
+ *
+ * Numerics. The sums of exp behind an acceptance have a relative error below
+ * 1e-6; a decision that this could turn is made again with sums in 64 bits, as
+ * are all sums behind a drawn token. Of two outcomes that only the roundings of
+ * 64 bits tell apart, either may come. Results are deterministic.
+ *
+ * Errors: ERR_NULLPTR for logits (unless V is 0), drafts (unless D is 0),
+ * out_tokens, out_accepted or the workspace NULL; ERR_INVALID for a dtype, N < 0,
+ * D or V out of range, N * (2 D + 1) above TOPKTOPP_MAX_B, a stride below V,
+ * draft_logits without uniforms or with parents, a workspace that is too small or
+ * not aligned, logits not aligned to their element, or an output or the workspace
+ * overlapping anything else. N == 0 is a successful no-op.
+ */
+topktopp_status speculative_verify(const void* logits, int64_t ld_logits, topktopp_dtype dtype, int64_t N, int64_t D,
+                                   int64_t V, const int32_t* drafts, const float* uniforms, const void* draft_logits,
+                                   int64_t ld_draft, const int32_t* parents, const int32_t* lengths,
+                                   int32_t* out_tokens, int32_t* out_accepted, int32_t* out_path, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace that speculative_verify needs for these sizes (at least
+ * 16), with or without draft logits, or -1 if it would refuse them. */
+int64_t speculative_verify_workspace(topktopp_dtype dtype, int64_t N, int64_t D, int64_t V, int draft_logits);
+
+/* -------------------------------------------------------- caches in pages --- */
+
+/*
+ * A page table. Position t of row r lies in page tables[r * ld_tables +
+ * t / page_size] at slot t % page_size; a row holds the pages of its first
+ * lengths[r] positions, C at most, and its entries behind them are not used.
+ *   tables     [R, C] int32 device buffer, rows ld_tables >= C entries apart.
+ *   lengths    [R] int32.
+ *   uses       [P] int32, how many held entries name each page. A page with 0
+ *              is free.
+ *   page_size  slots of a page, >= 1; C * page_size <= 2^31 - 1.
+ * The three belong together and are kept so by the calls below: begin with
+ * lengths and uses of 0. Entries outside [0, P) name no page.
+ *
+ * cache_pages_fork — rows follow their beams, in place: row i * K + b becomes
+ * what row i * K + parents[i][b] was (its length, its pages), for R = N * K. The
+ * pages themselves are not touched: rows that come from one share them.
+ *   parents  [N, K] int32; a row whose parent lies outside [0, K) stays as it is.
+ * ERR_NULLPTR for tables (unless C is 0), lengths, parents or uses (unless P is
+ * 0) NULL; ERR_INVALID for K outside [1, TOPKTOPP_MAX_BEAMS], negative sizes,
+ * N * K or P above TOPKTOPP_MAX_B, a page_size or C out of range, ld_tables below
+ * C, or buffers that overlap.
+ */
+topktopp_status cache_pages_fork(int32_t* tables, int64_t ld_tables, int64_t C, int32_t* lengths,
+                                 const int32_t* parents, int64_t N, int64_t K, int32_t* uses, int64_t P,
+                                 int64_t page_size, void* stream);
+
+/*
+ * cache_pages_resize — row r is to hold new_lengths[r] positions. First, rows
+ * that become shorter give back the pages behind their new end (their entries
+ * become -1). Then rows that grow are served in order of their numbers: each gets
+ * the pages that it lacks, free ones from the lowest number on, and where it is
+ * going to write into its last page (not full) and other rows use that as well,
+ * a page in its place into which its slots are copied. Rows that write into the
+ * same page in one call and are all that use it copy it but for the last of them.
+ * From the first row on that the free pages do not suffice for, growing rows
+ * stay as they are; so do rows whose old or new length is below 0 or above
+ * C * page_size. lengths[r] becomes new_lengths[r] for all others.
+ *   caches     host array of `count` descriptions as for beam_reorder_states,
+ *              read during the call, with P rows (the pages) and page_size
+ *              positions (the slots); disjoint. With count 0 nothing can be
+ *              copied: the first row that would have to and the growing rows
+ *              behind it stay as they are.
+ *   workspace  cache_pages_resize_workspace(R, P) bytes, 16-byte aligned; calls
+ *              that may run at the same time need one each.
+ * ERR_NULLPTR for tables (unless C is 0), lengths, new_lengths, uses (unless P
+ * is 0), the workspace, caches or a cache's data NULL; ERR_INVALID for sizes out
+ * of range as above, a cache with other positions than page_size, one whose
+ * elements share memory or of more than 2^31 - 1 columns of a page, a workspace
+ * too small or not aligned, or buffers that overlap. Nothing is changed if any
+ * argument is refused. R == 0 is a successful no-op.
+ */
+topktopp_status cache_pages_resize(int32_t* tables, int64_t ld_tables, int64_t R, int64_t C, int32_t* lengths,
+                                   const int32_t* new_lengths, int32_t* uses, int64_t P, int64_t page_size,
+                                   const topktopp_beam_state* caches, int64_t count, void* workspace,
+                                   int64_t workspace_bytes, void* stream);
+int64_t cache_pages_resize_workspace(int64_t R, int64_t P);
+
+/*
+ * cache_pages_compact — the entries of an accepted path move behind one
+ * another: in every cache, position starts[i] + j of sequence i becomes what
+ * position starts[i] + path[i][j] was, for j < counts[i].
+ *   path     [N, D] int32, D <= TOPKTOPP_MAX_DRAFTS: ascending numbers >= 0 (as
+ *            out_path of speculative_verify). A path ends before the first one
+ *            that is not larger than the one before it, or whose position lies
+ *            outside the table.
+ *   counts   [N] int32 (values are clamped to [0, D]); starts [N] int32.
+ * Entries whose page, or whose place's page, lies outside [0, P) stay. The pages
+ * written to must be used by one sequence only, as cache_pages_resize leaves
+ * those behind the length that it started from.
+ * Errors as for cache_pages_resize. N, D or count of 0 is a successful no-op.
+ */
+topktopp_status cache_pages_compact(const topktopp_beam_state* caches, int64_t count, int64_t P, int64_t page_size,
+                                    const int32_t* tables, int64_t ld_tables, int64_t N, int64_t C,
+                                    const int32_t* starts, const int32_t* path, int64_t D, const int32_t* counts,
+                                    void* stream);
+
 /* Text of the most recent error on the calling thread ("" if none); the
  * counterpart of aclGetRecentErrMsg (AKP §8). Valid until the next call on
  * the same thread. */

@@ -32,7 +32,13 @@ EXPORTED_SYMBOLS = (
     "beam_reorder_states",
     "beam_search_select",
     "beam_search_select_workspace",
+    "cache_pages_compact",
+    "cache_pages_fork",
+    "cache_pages_resize",
+    "cache_pages_resize_workspace",
     "sample_top_k_top_p",
+    "speculative_verify",
+    "speculative_verify_workspace",
     "top_k_top_p_sorted_survivors",
     "topktopp_last_error",
     "topktopp_set_plan_policy",
@@ -41,7 +47,7 @@ EXPORTED_SYMBOLS = (
 _lib = None
 
 
-TOPKTOPP_MAX_BEAMS, TOPKTOPP_MAX_CANDIDATES = 128, 256
+TOPKTOPP_MAX_BEAMS, TOPKTOPP_MAX_CANDIDATES, TOPKTOPP_MAX_DRAFTS = 128, 256, 255
 
 
 class BeamState(ctypes.Structure):
@@ -105,6 +111,18 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.beam_reorder_states.restype = i32
     lib.beam_backtrace.argtypes = [vp, vp, i64, i64, i64, vp, vp, i64, ctypes.c_int32, vp, vp]
     lib.beam_backtrace.restype = i32
+    lib.speculative_verify.argtypes = [vp, i64, i32, i64, i64, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.speculative_verify.restype = i32
+    lib.speculative_verify_workspace.argtypes = [i32, i64, i64, i64, i32]
+    lib.speculative_verify_workspace.restype = i64
+    lib.cache_pages_fork.argtypes = [vp, i64, i64, vp, vp, i64, i64, vp, i64, i64, vp]
+    lib.cache_pages_fork.restype = i32
+    lib.cache_pages_resize.argtypes = [vp, i64, i64, i64, vp, vp, vp, i64, i64, vp, i64, vp, i64, vp]
+    lib.cache_pages_resize.restype = i32
+    lib.cache_pages_resize_workspace.argtypes = [i64, i64]
+    lib.cache_pages_resize_workspace.restype = i64
+    lib.cache_pages_compact.argtypes = [vp, i64, i64, i64, vp, i64, i64, i64, vp, vp, i64, vp, vp]
+    lib.cache_pages_compact.restype = i32
     lib.topktopp_last_error.argtypes = []
     lib.topktopp_last_error.restype = ctypes.c_char_p
     lib.topktopp_set_plan_policy.argtypes = [i32]
@@ -638,3 +656,278 @@ def beam_backtrace(tokens, parents, beams=None, lengths=None, pad=-1, out=None, 
     if given:
         torch.autograd.graph.increment_version(out)
     return out
+
+
+def _row_strided(t, name, shape, dtype, device):
+    """The row stride of a 2-D tensor with contiguous rows; checks it like _check_dense."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got shape {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"tensors must share one device: {name} is on {t.device}")
+    ld, step = t.stride()
+    if step != 1 and shape[1] > 1:
+        raise ValueError(f"{name}: rows must be contiguous (stride 1 along the last dimension)")
+    return shape[1] if shape[0] <= 1 else ld
+
+
+def speculative_verify_workspace(dtype, N, D, V, draft_logits=False):
+    """Bytes of the workspace that speculative_verify takes for N sequences of
+    D drafts, V tokens and torch dtype `dtype`, with draft logits or without."""
+    import torch
+
+    size = load_library().speculative_verify_workspace(
+        _dtype_code(torch.empty(0, dtype=dtype)), int(N), int(D), int(V), int(bool(draft_logits)))
+    if size < 0:
+        raise TopKTopPError(2, last_error())
+    return size
+
+
+def speculative_verify(logits, drafts, uniforms=None, draft_logits=None, parents=None, lengths=None, out=None,
+                       workspace=None, stream=None):
+    """How many drafted tokens stand, and the token behind them: (tokens
+    [N, D + 1] int32, accepted [N] int32, path [N, D] int32 or None).
+
+    logits [N * (D + 1), V], rows contiguous, any row stride from V on: of each
+    sequence, what follows its last token and each of its drafts, ready to be
+    sampled from (divided by the temperature, filtered tokens at -inf). drafts
+    [N, D] int32; uniforms [N, D + 1] float32 in [0, 1): one for each row's
+    acceptance, and the last one for the token behind. draft_logits [N * D, V]
+    (as logits): what each draft was drawn from; without, drafts count as
+    proposals that were not drawn. parents [N, D] int32: the drafts form a tree,
+    draft j behind draft parents[i, j] < j or, for -1, behind the last token;
+    default: a chain. lengths [N] int32: drafts that count (default D). Without
+    uniforms the verification is greedy.
+
+    tokens holds the accepted drafts, the token behind them and -1; path (with
+    parents) the accepted drafts' numbers and -1. Draft w behind an accepted one
+    stands if u[w] q(d) < p(d); where it does not, the token is drawn from
+    max(p - q, 0). A row with a NaN or +inf or nothing above -inf accepts
+    nothing and gives -1. out: the three tensors to fill (path None without
+    parents, or wherever it is not needed); workspace: a uint8 tensor of
+    speculative_verify_workspace() bytes, not used by any other call that may
+    run at the same time (each call allocates one else). No gradients."""
+    import torch
+
+    lib = _lib or load_library()
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [N * (D + 1), V]")
+    if drafts.dim() != 2:
+        raise ValueError("drafts must be 2-D [N, D]")
+    (R, V), (N, D) = logits.shape, drafts.shape
+    if N * (D + 1) != R:
+        raise ValueError(f"logits must have N * (D + 1) = {N * (D + 1)} rows, got {R}")
+    dtype, dev = _dtype_code(logits), logits.get_device()
+    ldx = _row_strided(logits, "logits", (R, V), logits.dtype, dev)
+    _check_dense(drafts, (N, D), torch.int32, "drafts", dev)
+    ldq, p_draft, p_uniforms, p_parents, p_lengths = V, None, None, None, None
+    if uniforms is not None:
+        _check_dense(uniforms, (N, D + 1), torch.float32, "uniforms", dev)
+        p_uniforms = uniforms.data_ptr()
+    if draft_logits is not None:
+        if uniforms is None:
+            raise ValueError("draft_logits needs uniforms")
+        if parents is not None:
+            raise ValueError("draft_logits cannot go with parents")
+        ldq = _row_strided(draft_logits, "draft_logits", (N * D, V), logits.dtype, dev)
+        p_draft = draft_logits.data_ptr() or None
+    if parents is not None:
+        _check_dense(parents, (N, D), torch.int32, "parents", dev)
+        p_parents = parents.data_ptr() or None
+    if lengths is not None:
+        _check_dense(lengths, (N,), torch.int32, "lengths", dev)
+        p_lengths = lengths.data_ptr()
+    handle, scope = _scope(stream, logits.device)
+    given = out is not None
+    with scope:
+        if not given:
+            out = (torch.empty((N, D + 1), dtype=torch.int32, device=logits.device),
+                   torch.empty((N,), dtype=torch.int32, device=logits.device),
+                   None if parents is None else torch.empty((N, D), dtype=torch.int32, device=logits.device))
+        tokens, accepted, path = out
+        _check_dense(tokens, (N, D + 1), torch.int32, "out tokens", dev)
+        _check_dense(accepted, (N,), torch.int32, "out accepted", dev)
+        if path is not None:
+            _check_dense(path, (N, D), torch.int32, "out path", dev)
+        if workspace is None:
+            size = lib.speculative_verify_workspace(dtype, N, D, V, int(p_draft is not None))
+            if size < 0:
+                raise TopKTopPError(2, last_error())
+            workspace = torch.empty(size, dtype=torch.uint8, device=logits.device)
+        else:
+            size = workspace.numel()
+            _check_dense(workspace, workspace.shape, torch.uint8, "workspace", dev)
+        status = lib.speculative_verify(
+            logits.data_ptr(), ldx, dtype, N, D, V, drafts.data_ptr(), p_uniforms, p_draft, ldq, p_parents, p_lengths,
+            tokens.data_ptr(), accepted.data_ptr(), None if path is None else path.data_ptr(), workspace.data_ptr(),
+            size, handle)
+    _check(status)
+    if given:
+        torch.autograd.graph.increment_version([t for t in out if t is not None])
+    return out
+
+
+def _page_table(tables, lengths, uses, R):
+    """(row stride, C, P) of a page table of R rows, checked."""
+    import torch
+
+    if tables.dim() != 2:
+        raise ValueError("tables must be 2-D [rows, pages of a row]")
+    dev, C = tables.get_device(), tables.shape[1]
+    ld = _row_strided(tables, "tables", (R, C), torch.int32, dev)
+    if lengths is not None:
+        _check_dense(lengths, (R,), torch.int32, "lengths", dev)
+    if uses is None:
+        return ld, C, 0
+    if uses.dim() != 1:
+        raise ValueError("uses must be 1-D [pages]")
+    _check_dense(uses, uses.shape, torch.int32, "uses", dev)
+    return ld, C, uses.shape[0]
+
+
+def _page_caches(caches, P, page_size, page_dim, slot_dim, dev):
+    """(tensors, their descriptions) of caches of P pages."""
+    import torch
+
+    tensors = [caches] if isinstance(caches, torch.Tensor) else list(caches)
+    descs = []
+    for t in tensors:
+        if t.get_device() != dev:
+            raise ValueError(f"tensors must share one device: a cache is on {t.device}")
+        if t.is_neg() or (t.is_complex() and t.is_conj()):
+            raise ValueError("a cache must not be a lazily conjugated or negated view")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError("a cache that requires grad can only be changed under no_grad")
+        dims = t.dim()
+        if not (-dims <= page_dim < dims and -dims <= slot_dim < dims) or (page_dim - slot_dim) % dims == 0:
+            raise ValueError(f"a cache of {dims} axes has no page_dim {page_dim} and slot_dim {slot_dim}")
+        if t.shape[page_dim] != P or t.shape[slot_dim] != page_size:
+            raise ValueError(f"a cache must have {P} pages of {page_size} slots, got shape {tuple(t.shape)}")
+        descs.append(_pack_pointer(t.data_ptr()))
+        descs.append(_state_bytes(t.shape, t.stride(), t.element_size(), page_dim, slot_dim, P))
+    return tensors, b"".join(descs)
+
+
+def cache_pages_fork(tables, lengths, parents, uses, page_size, stream=None):
+    """The rows of a page table follow their beams, in place: row i * K + b
+    becomes what row i * K + parents[i, b] was. The pages are not touched; rows
+    that come from one share them until one grows (cache_pages_resize).
+
+    tables [N * K, C] int32, rows contiguous: position t of a row lies in page
+    tables[row, t // page_size]; lengths [N * K] int32, the positions that a row
+    holds; uses [P] int32, how many held entries name each page (0: free). All
+    three are changed; begin with lengths and uses of 0. parents [N, K] int32, a
+    row whose parent lies outside [0, K) stays as it is. Returns tables."""
+    import torch
+
+    lib = _lib or load_library()
+    if parents.dim() != 2:
+        raise ValueError("parents must be 2-D [N, K]")
+    N, K = parents.shape
+    ld, C, P = _page_table(tables, lengths, uses, N * K)
+    _check_dense(parents, (N, K), torch.int32, "parents", tables.get_device())
+    handle, scope = _scope(stream, tables.device)
+    with scope:
+        status = lib.cache_pages_fork(tables.data_ptr(), ld, C, lengths.data_ptr(), parents.data_ptr(), N, K,
+                                      uses.data_ptr(), P, int(page_size), handle)
+    _check(status)
+    torch.autograd.graph.increment_version((tables, lengths, uses))
+    return tables
+
+
+def cache_pages_resize_workspace(R, P):
+    """Bytes of the workspace that cache_pages_resize takes for R rows and P pages."""
+    size = load_library().cache_pages_resize_workspace(int(R), int(P))
+    if size < 0:
+        raise TopKTopPError(2, last_error())
+    return size
+
+
+def cache_pages_resize(tables, lengths, new_lengths, uses, page_size, caches=None, page_dim=0, slot_dim=1,
+                       workspace=None, stream=None):
+    """Row r of a page table is to hold new_lengths[r] positions, in place.
+
+    Rows that become shorter give back the pages behind their new end (entries
+    become -1); then those that grow get theirs, in order of the rows, the free
+    pages of the lowest numbers first. A row that is going to write into its last
+    page, which is not full and used by other rows as well, gets a page of its own
+    in its place, with the slots that it holds copied in all caches; the last of
+    several such rows keeps the page if no other uses it. From the first row that
+    cannot be served on, rows that would grow stay as they are: `lengths` becomes
+    new_lengths for all others, so comparing the two tells. Lengths outside
+    [0, C * page_size] leave their row as it is.
+
+    tables, lengths, uses: as for cache_pages_fork; new_lengths [R] int32. caches:
+    a tensor or a sequence of them, any dtype and strides, with the pages along
+    page_dim and their slots along slot_dim; without, nothing can be copied, and
+    the first row that would have to be counts as not served. workspace: a uint8
+    tensor of cache_pages_resize_workspace() bytes, not used by any other call that
+    may run at the same time. Returns lengths."""
+    import torch
+
+    lib = _lib or load_library()
+    if lengths.dim() != 1:
+        raise ValueError("lengths must be 1-D [rows]")
+    R = lengths.shape[0]
+    ld, C, P = _page_table(tables, lengths, uses, R)
+    dev = tables.get_device()
+    _check_dense(new_lengths, (R,), torch.int32, "new_lengths", dev)
+    tensors, descs = [], None
+    if caches is not None:
+        tensors, descs = _page_caches(caches, P, int(page_size), page_dim, slot_dim, dev)
+    handle, scope = _scope(stream, tables.device)
+    with scope:
+        if workspace is None:
+            size = cache_pages_resize_workspace(R, P)
+            workspace = torch.empty(size, dtype=torch.uint8, device=tables.device)
+        else:
+            size = workspace.numel()
+            _check_dense(workspace, workspace.shape, torch.uint8, "workspace", dev)
+        status = lib.cache_pages_resize(tables.data_ptr(), ld, R, C, lengths.data_ptr(), new_lengths.data_ptr(),
+                                        uses.data_ptr(), P, int(page_size), descs, len(tensors),
+                                        workspace.data_ptr(), size, handle)
+    _check(status)
+    torch.autograd.graph.increment_version([tables, lengths, uses, *tensors])
+    return lengths
+
+
+def cache_pages_compact(caches, tables, starts, path, counts, page_dim=0, slot_dim=1, stream=None):
+    """The entries of accepted paths move behind one another, in place: in every
+    cache, position starts[i] + j of sequence i becomes what position
+    starts[i] + path[i, j] was, for j < counts[i].
+
+    caches: a tensor or a sequence of them, any dtype and strides, with the pages
+    along page_dim and their slots along slot_dim; tables [N, C] int32, rows
+    contiguous: position t lies in page tables[i, t // slots]; starts and counts
+    [N] int32; path [N, D] int32, ascending, as speculative_verify gives it (a
+    path ends before a number that is not larger than the one before). The pages
+    written to must be those of one sequence only. Returns caches."""
+    import torch
+
+    lib = _lib or load_library()
+    if path.dim() != 2:
+        raise ValueError("path must be 2-D [N, D]")
+    N, D = path.shape
+    ld, C, _ = _page_table(tables, None, None, N)
+    dev = tables.get_device()
+    _check_dense(path, (N, D), torch.int32, "path", dev)
+    _check_dense(starts, (N,), torch.int32, "starts", dev)
+    _check_dense(counts, (N,), torch.int32, "counts", dev)
+    if not isinstance(caches, torch.Tensor):
+        caches = list(caches)
+        if not caches:
+            return caches
+    first = caches if isinstance(caches, torch.Tensor) else caches[0]
+    dims = first.dim()
+    if not (-dims <= page_dim < dims and -dims <= slot_dim < dims):
+        raise ValueError(f"a cache of {dims} axes has no page_dim {page_dim} and slot_dim {slot_dim}")
+    P, page_size = first.shape[page_dim], first.shape[slot_dim]
+    tensors, descs = _page_caches(caches, P, page_size, page_dim, slot_dim, dev)
+    handle, scope = _scope(stream, tables.device)
+    with scope:
+        status = lib.cache_pages_compact(descs, len(tensors), P, page_size, tables.data_ptr(), ld, N, C,
+                                         starts.data_ptr(), path.data_ptr(), D, counts.data_ptr(), handle)
+    _check(status)
+    torch.autograd.graph.increment_version(tensors)
+    return caches

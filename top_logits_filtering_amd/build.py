@@ -22,7 +22,8 @@ LIB_NAME = "libtopktopp.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 
 SOURCES = ["api.cpp", "apply_f32.hip", "apply_f16.hip", "apply_bf16.hip", "sorted_kernels.hip", "util_kernels.hip",
-           "beam_select.hip", "beam_states.hip", "beam_backtrace.hip"]
+           "beam_select.hip", "beam_states.hip", "beam_backtrace.hip", "speculative.hip",
+           "cache_pages.hip"]
 
 ARCH = "gfx950"
 COMMON_FLAGS = [
@@ -39,8 +40,9 @@ COMMON_FLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 
-# Flags of single sources. The beam selection honours NaN: a row that holds one proposes nothing.
-SOURCE_FLAGS = {"beam_select.hip": ["-fhonor-nans"]}
+# Flags of single sources. The beam selection and the verification of drafts honour NaN: a row that holds one proposes
+# nothing.
+SOURCE_FLAGS = {"beam_select.hip": ["-fhonor-nans"], "speculative.hip": ["-fhonor-nans"]}
 
 
 def _hipcc() -> str:

@@ -4,15 +4,21 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
 #include <cstdint>
+#include <exception>
 #include <string>
+#include <utility>
+#include <vector>
 
 #include "../../include/topktopp.h"
 #include "beam.h"
+#include "cache_pages.h"
 #include "launch.h"
+#include "speculative.h"
 
 namespace {
 
@@ -586,6 +592,248 @@ topktopp_status beam_backtrace(const int32_t* tokens, const int32_t* parents, in
   const tkp::BeamBacktraceArgs a{tokens, parents, beams, lengths, out, T, N, static_cast<int>(K), static_cast<int>(M),
                                  pad};
   return check_launch(tkp::launch_beam_backtrace(a, static_cast<hipStream_t>(stream)), "backtrace launch");
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------- speculative decoding ---
+
+namespace {
+
+topktopp_status check_verify(int dtype, int64_t N, int64_t D, int64_t V) {
+  if (!valid_dtype(dtype)) return fail(TOPKTOPP_ERR_INVALID, "dtype %d is not one of F32, F16, BF16", dtype);
+  if (N < 0) return fail(TOPKTOPP_ERR_INVALID, "N=%lld is negative", (long long)N);
+  if (D < 0 || D > TOPKTOPP_MAX_DRAFTS)
+    return fail(TOPKTOPP_ERR_INVALID, "D=%lld drafts are outside [0, %d]", (long long)D, TOPKTOPP_MAX_DRAFTS);
+  if (N > TOPKTOPP_MAX_B / (2 * D + 1))
+    return fail(TOPKTOPP_ERR_INVALID, "N * (2 D + 1) for N=%lld, D=%lld exceeds the supported maximum 2^31-1",
+                (long long)N, (long long)D);
+  return check_shape(N * (2 * D + 1), V);
+}
+
+int64_t verify_bytes(int dtype, int64_t N, int64_t D, int64_t V, bool draft) {
+  const int64_t bytes = tkp::verify_workspace(dtype, N, static_cast<int>(D), static_cast<int>(V), draft);
+  return bytes > 16 ? bytes : 16;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t speculative_verify_workspace(topktopp_dtype dtype, int64_t N, int64_t D, int64_t V, int draft_logits) {
+  g_last_error.clear();
+  if (check_verify(dtype, N, D, V) != TOPKTOPP_OK) return -1;
+  return verify_bytes(dtype, N, D, V, draft_logits != 0);
+}
+
+topktopp_status speculative_verify(const void* logits, int64_t ld_logits, topktopp_dtype dtype, int64_t N, int64_t D,
+                                   int64_t V, const int32_t* drafts, const float* uniforms, const void* draft_logits,
+                                   int64_t ld_draft, const int32_t* parents, const int32_t* lengths,
+                                   int32_t* out_tokens, int32_t* out_accepted, int32_t* out_path, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (N != 0) {
+    if (logits == nullptr && V != 0) return fail(TOPKTOPP_ERR_NULLPTR, "logits is NULL");
+    if (drafts == nullptr && D != 0) return fail(TOPKTOPP_ERR_NULLPTR, "drafts is NULL");
+    if (out_tokens == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "out_tokens is NULL");
+    if (out_accepted == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "out_accepted is NULL");
+    if (workspace == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "workspace is NULL");
+  }
+  if (topktopp_status s = check_verify(dtype, N, D, V)) return s;
+  if (draft_logits != nullptr && uniforms == nullptr)
+    return fail(TOPKTOPP_ERR_INVALID, "draft_logits without uniforms: a greedy verification does not use them");
+  if (draft_logits != nullptr && parents != nullptr)
+    return fail(TOPKTOPP_ERR_INVALID, "draft_logits with parents: drafts that were drawn form a chain");
+  if (N == 0) return TOPKTOPP_OK;
+  if (topktopp_status s = check_ld(ld_logits, V, "logits")) return s;
+  if (draft_logits != nullptr)
+    if (topktopp_status s = check_ld(ld_draft, V, "draft_logits")) return s;
+  const size_t es = elem_size(dtype);
+  if (reinterpret_cast<uintptr_t>(logits) % es != 0 || reinterpret_cast<uintptr_t>(draft_logits) % es != 0)
+    return fail(TOPKTOPP_ERR_INVALID, "logits or draft_logits are not aligned to their elements");
+  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
+    return fail(TOPKTOPP_ERR_INVALID, "workspace is not 16-byte aligned");
+  const int64_t need = verify_bytes(dtype, N, D, V, draft_logits != nullptr);
+  if (workspace_bytes < need)
+    return fail(TOPKTOPP_ERR_INVALID, "workspace has %lld bytes, %lld are needed", (long long)workspace_bytes,
+                (long long)need);
+  const size_t seqs = static_cast<size_t>(N), nd = seqs * static_cast<size_t>(D) * 4,
+               nr = seqs * static_cast<size_t>(D + 1) * 4;
+  const Span spans[] = {{out_tokens, nr, "out_tokens"},
+                        {out_accepted, seqs * 4, "out_accepted"},
+                        {out_path, nd, "out_path"},
+                        {workspace, static_cast<size_t>(need), "workspace"},
+                        {logits, V == 0 ? 0 : extent(N * (D + 1), V, ld_logits, es), "logits"},
+                        {draft_logits, V == 0 || D == 0 ? 0 : extent(N * D, V, ld_draft, es), "draft_logits"},
+                        {drafts, nd, "drafts"},
+                        {uniforms, nr, "uniforms"},
+                        {parents, nd, "parents"},
+                        {lengths, seqs * 4, "lengths"}};
+  if (topktopp_status s = check_disjoint(spans, 10, 4)) return s;
+  // without drafts there are no draft rows
+  const tkp::VerifyArgs a{logits, ld_logits, D == 0 ? nullptr : draft_logits, ld_draft, N, static_cast<int>(D),
+                          static_cast<int>(V), drafts, uniforms, parents, lengths, out_tokens, out_accepted, out_path,
+                          workspace};
+  return check_launch(tkp::launch_verify(dtype, a, static_cast<hipStream_t>(stream)), "verification launch");
+}
+
+}  // extern "C"
+
+// --------------------------------------------------------- caches in pages ---
+
+namespace {
+
+topktopp_status check_table(const int32_t* tables, int64_t ld, int64_t R, int64_t C, int64_t P, int64_t page_size) {
+  if (R < 0 || C < 0 || P < 0) return fail(TOPKTOPP_ERR_INVALID, "a size of the page table is negative");
+  if (R > TOPKTOPP_MAX_B || P > TOPKTOPP_MAX_B - 1)
+    return fail(TOPKTOPP_ERR_INVALID, "R=%lld rows or P=%lld pages exceed the supported maximum", (long long)R, (long long)P);
+  if (page_size < 1 || page_size > 0x7FFFFFFFLL)
+    return fail(TOPKTOPP_ERR_INVALID, "page_size=%lld is outside [1, 2^31-1]", (long long)page_size);
+  if (C > 0x7FFFFFFFLL / page_size)
+    return fail(TOPKTOPP_ERR_INVALID, "C * page_size for C=%lld, page_size=%lld exceeds 2^31-1", (long long)C,
+                (long long)page_size);
+  if (topktopp_status s = check_ld(ld, C, "tables")) return s;
+  if (tables == nullptr && C != 0 && R != 0) return fail(TOPKTOPP_ERR_NULLPTR, "tables is NULL");
+  return TOPKTOPP_OK;
+}
+
+size_t table_bytes(int64_t R, int64_t C, int64_t ld) { return R == 0 || C == 0 ? 0 : extent(R, C, ld, 4); }
+
+// Caches of P pages: each one's memory its own, apart from `others`. Those without elements are left out of `kept`.
+topktopp_status check_caches(const topktopp_beam_state* caches, int64_t count, int64_t P, int64_t page_size,
+                             const Span* others, int n, std::vector<tkp::BeamState>* kept) {
+  if (count < 0) return fail(TOPKTOPP_ERR_INVALID, "count=%lld is negative", (long long)count);
+  if (count == 0) return TOPKTOPP_OK;
+  if (caches == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "caches is NULL");
+  std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+  for (int64_t i = 0; i < count; ++i) {
+    const tkp::BeamState s = state_of(caches[i]);
+    size_t bytes;
+    if (topktopp_status e = state_span(s, P, &bytes)) return e;
+    if (bytes == 0) continue;
+    if (s.data == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "data of cache %lld is NULL", (long long)i);
+    if (s.positions != page_size)
+      return fail(TOPKTOPP_ERR_INVALID, "cache %lld has %lld slots a page, not page_size=%lld", (long long)i,
+                  (long long)s.positions, (long long)page_size);
+    if (!tkp::page_state_fits(s))
+      return fail(TOPKTOPP_ERR_INVALID, "a page of cache %lld has more than 2^31-1 columns", (long long)i);
+    for (int j = 0; j < n; ++j)
+      if (overlaps(s.data, bytes, others[j].p, others[j].bytes))
+        return fail(TOPKTOPP_ERR_INVALID, "cache %lld overlaps %s", (long long)i, others[j].name);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(s.data);
+    spans.emplace_back(at, at + bytes);
+    kept->push_back(s);
+  }
+  std::sort(spans.begin(), spans.end());
+  for (size_t i = 1; i < spans.size(); ++i)
+    if (spans[i].first < spans[i - 1].second) return fail(TOPKTOPP_ERR_INVALID, "two caches overlap");
+  return TOPKTOPP_OK;
+}
+
+int64_t resize_bytes(int64_t R, int64_t P) { return tkp::pages_resize_workspace(R, P); }
+
+// f(), with what C++ may throw (no memory on the host) as a status.
+template <class F>
+topktopp_status guarded(F f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return fail(TOPKTOPP_ERR_RUNTIME, "%s", e.what());
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+topktopp_status cache_pages_fork(int32_t* tables, int64_t ld_tables, int64_t C, int32_t* lengths,
+                                 const int32_t* parents, int64_t N, int64_t K, int32_t* uses, int64_t P,
+                                 int64_t page_size, void* stream) {
+  g_last_error.clear();
+  if (topktopp_status s = check_beams(N, K)) return s;
+  if (topktopp_status s = check_table(tables, ld_tables, N * K, C, P, page_size)) return s;
+  if (N == 0) return TOPKTOPP_OK;
+  if (lengths == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "lengths is NULL");
+  if (parents == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "parents is NULL");
+  if (uses == nullptr && P != 0) return fail(TOPKTOPP_ERR_NULLPTR, "uses is NULL");
+  const size_t rows = static_cast<size_t>(N * K) * 4;
+  const Span spans[] = {{tables, table_bytes(N * K, C, ld_tables), "tables"},
+                        {lengths, rows, "lengths"},
+                        {uses, static_cast<size_t>(P) * 4, "uses"},
+                        {parents, rows, "parents"}};
+  if (topktopp_status s = check_disjoint(spans, 4, 3)) return s;
+  const tkp::PageTable t{tables, ld_tables, N * K, static_cast<int>(C), static_cast<int>(page_size), lengths, uses, P};
+  return check_launch(tkp::launch_pages_fork(t, parents, N, static_cast<int>(K), static_cast<hipStream_t>(stream)),
+                      "fork launch");
+}
+
+int64_t cache_pages_resize_workspace(int64_t R, int64_t P) {
+  g_last_error.clear();
+  if (check_table(nullptr, 0, R, 0, P, 1) != TOPKTOPP_OK) return -1;
+  return resize_bytes(R, P);
+}
+
+topktopp_status cache_pages_resize(int32_t* tables, int64_t ld_tables, int64_t R, int64_t C, int32_t* lengths,
+                                   const int32_t* new_lengths, int32_t* uses, int64_t P, int64_t page_size,
+                                   const topktopp_beam_state* caches, int64_t count, void* workspace,
+                                   int64_t workspace_bytes, void* stream) {
+  g_last_error.clear();
+  if (topktopp_status s = check_table(tables, ld_tables, R, C, P, page_size)) return s;
+  if (R == 0) return TOPKTOPP_OK;
+  if (lengths == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "lengths is NULL");
+  if (new_lengths == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "new_lengths is NULL");
+  if (uses == nullptr && P != 0) return fail(TOPKTOPP_ERR_NULLPTR, "uses is NULL");
+  if (workspace == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(workspace) % 16 != 0)
+    return fail(TOPKTOPP_ERR_INVALID, "workspace is not 16-byte aligned");
+  const int64_t need = resize_bytes(R, P);
+  if (workspace_bytes < need)
+    return fail(TOPKTOPP_ERR_INVALID, "workspace has %lld bytes, %lld are needed", (long long)workspace_bytes,
+                (long long)need);
+  const size_t rows = static_cast<size_t>(R) * 4;
+  const Span spans[] = {{tables, table_bytes(R, C, ld_tables), "tables"},
+                        {lengths, rows, "lengths"},
+                        {uses, static_cast<size_t>(P) * 4, "uses"},
+                        {workspace, static_cast<size_t>(need), "workspace"},
+                        {new_lengths, rows, "new_lengths"}};
+  if (topktopp_status s = check_disjoint(spans, 5, 4)) return s;
+  return guarded([&]() -> topktopp_status {
+    std::vector<tkp::BeamState> kept;
+    if (topktopp_status s = check_caches(caches, count, P, page_size, spans, 5, &kept)) return s;
+    const tkp::PageTable t{tables, ld_tables, R, static_cast<int>(C), static_cast<int>(page_size), lengths, uses, P};
+    return check_launch(tkp::launch_pages_resize(t, new_lengths, kept.data(), static_cast<int64_t>(kept.size()), count > 0,
+                                                 workspace, static_cast<hipStream_t>(stream)),
+                        "resize launch");
+  });
+}
+
+topktopp_status cache_pages_compact(const topktopp_beam_state* caches, int64_t count, int64_t P, int64_t page_size,
+                                    const int32_t* tables, int64_t ld_tables, int64_t N, int64_t C,
+                                    const int32_t* starts, const int32_t* path, int64_t D, const int32_t* counts,
+                                    void* stream) {
+  g_last_error.clear();
+  if (topktopp_status s = check_table(tables, ld_tables, N, C, P, page_size)) return s;
+  if (D < 0 || D > TOPKTOPP_MAX_DRAFTS)
+    return fail(TOPKTOPP_ERR_INVALID, "D=%lld drafts are outside [0, %d]", (long long)D, TOPKTOPP_MAX_DRAFTS);
+  if (count < 0) return fail(TOPKTOPP_ERR_INVALID, "count=%lld is negative", (long long)count);
+  if (N == 0 || D == 0 || count == 0) return TOPKTOPP_OK;
+  if (starts == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "starts is NULL");
+  if (path == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "path is NULL");
+  if (counts == nullptr) return fail(TOPKTOPP_ERR_NULLPTR, "counts is NULL");
+  const size_t rows = static_cast<size_t>(N) * 4;
+  const Span spans[] = {{tables, table_bytes(N, C, ld_tables), "tables"},
+                        {starts, rows, "starts"},
+                        {path, rows * static_cast<size_t>(D), "path"},
+                        {counts, rows, "counts"}};
+  return guarded([&]() -> topktopp_status {
+    std::vector<tkp::BeamState> kept;
+    if (topktopp_status s = check_caches(caches, count, P, page_size, spans, 4, &kept)) return s;
+    const tkp::CompactArgs a{tables, ld_tables, N, static_cast<int>(C), static_cast<int>(page_size), static_cast<int>(D),
+                             P, starts, path, counts};
+    return check_launch(tkp::launch_pages_compact(kept.data(), static_cast<int64_t>(kept.size()), a,
+                                                  static_cast<hipStream_t>(stream)),
+                        "compaction launch");
+  });
 }
 
 }  // extern "C"
