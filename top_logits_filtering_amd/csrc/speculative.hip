@@ -7,17 +7,22 @@
 // the last uniform, by its place in the cumulative sum, from max(p - q, 0) where
 // a draft was rejected (from p without the rejected tokens if there is no q) and
 // from p where none was. Several drafts behind one token share its uniform: they
-// cut [0, 1) into pieces of p(token). Tokens are whole numbers, so decisions are
-// those of 64-bit sums.
+// cut [0, 1) into pieces of p(token).
 //
 //   1. verify_rows_kernel: sums of exp of chunks of the rows.
 //   2. verify_final_kernel: every workgroup goes down the path by those sums, then
-//      sums its chunk of the row where the path ends; the last workgroup of a
+//      sums its range of the row where the path ends; the last workgroup of a
 //      sequence finds the token.
+//
+// Tokens are whole numbers, so decisions are those of 64-bit sums. An acceptance
+// has one border, which sums in 32 bits with a known error (exp_sum.h) miss about
+// once in a million; then both rows are summed again in 64 bits. A token that is
+// drawn has a border beside every other one: that row's terms are in 64 bits.
 
 #include <float.h>
 
 #include "device_common.h"
+#include "exp_sum.h"
 #include "reg_tile.h"
 #include "speculative.h"
 
@@ -28,7 +33,11 @@ constexpr int kT = 256;  // threads of a workgroup
 constexpr int kW = kT / kWave;
 constexpr int kMaxRows = 256;  // D + 1 at most
 constexpr int kBlock = 8;      // neighbouring elements of a thread
-constexpr int kMaxParts = (1 << 20) / (kT * kBlock);
+constexpr int kPiece = kWave * kBlock;  // of a wave
+// A wave's part of the row where the path ends is up to kMaxPieces pieces, so that
+// a row has no more parts than the workgroup that looks through them holds.
+constexpr int kMaxPieces = 4;
+constexpr int kMaxParts = (1 << 20) / (kPiece * kMaxPieces);
 static_assert(kMaxParts <= 2 * kT);
 // A residual of no more mass than this is what roundings of the logits leave; the
 // token then comes from p itself.
@@ -48,15 +57,31 @@ struct RowChunk {
 // Sums over a chunk of the row where the path ends.
 struct FinalPart {
   double all;    // of p's terms
-  double kept;   // of those that are left: all but the rejected tokens', or where p > q
-  double other;  // of q's terms where p > q
+  double left;   // of what is left: p's terms without the rejected tokens', or ratio * p's less q's where that is above 0
+  double kept;   // of p's terms where it is
   double draft;  // of q's terms
   double close;  // of p's terms where p and q are too close to tell which is larger
 };
 
-// exp(x - ref) in 64 bits, for x <= ref or not far above it, or -inf.
+// exp(x - ref) in 64 bits, 0 for -inf and NaN: 2^t with t cut into a whole number
+// and r in [-1/2, 1/2], 2^r by the polynomial of degree 9 that meets it at the
+// Chebyshev points, within 1.9e-14 of it. 17 instructions; the library's exp takes
+// about 30.
 __device__ __forceinline__ double exp_from(float x, float ref) {
-  return exp(static_cast<double>(x) - static_cast<double>(ref));
+  double t = (static_cast<double>(x) - static_cast<double>(ref)) * 1.4426950408889634;
+  t = __builtin_fmax(t, -1100.0);
+  const double n = __builtin_rint(t), r = t - n;
+  double e = 1.0205905413765595e-07;
+  e = __builtin_fma(e, r, 1.325964524488711e-06);
+  e = __builtin_fma(e, r, 1.5252672924850737e-05);
+  e = __builtin_fma(e, r, 0.0001540343375125101);
+  e = __builtin_fma(e, r, 0.0013333558200794592);
+  e = __builtin_fma(e, r, 0.009618129193934313);
+  e = __builtin_fma(e, r, 0.05550410866465167);
+  e = __builtin_fma(e, r, 0.2402265069564034);
+  e = __builtin_fma(e, r, 0.6931471805599462);
+  e = __builtin_fma(e, r, 1.0000000000000135);
+  return __builtin_ldexp(e, static_cast<int>(n));
 }
 
 __device__ __forceinline__ double wave_incl_scan_f64(double v) {
@@ -86,51 +111,107 @@ __device__ __forceinline__ void load_block(const typename DT::raw_t* row, int v,
   }
 }
 
+// What workgroups of one kernel tell each other goes past the caches of their dies:
+// stores and loads of device scope, in order by waiting for the stores. (A fence
+// of device scope writes back a die's whole cache: with one in every wave the
+// second kernel took 488 us instead of 35 for 128 rows of 128256 fp32.)
+__device__ __forceinline__ void put_far(double* to, double v) {
+  __hip_atomic_store(to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ double get_far(const double* from) {
+  return __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Whether this workgroup is the last of `count` that come here, which then sees
+// what all of them have put. `told`: in shared memory.
+__device__ __forceinline__ bool last_of(uint32_t* arrived, int count, int& told) {
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  if (threadIdx.x == 0)
+    told = __hip_atomic_fetch_add(arrived, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+                   static_cast<uint32_t>(count) - 1u
+               ? 1
+               : 0;
+  asm volatile("" ::: "memory");
+  __syncthreads();
+  return told != 0;
+}
+
 struct WalkSmem {
   int32_t token[kMaxRows];   // -1: the draft counts as not there
   int32_t node[kMaxRows];    // the row that it follows
   float u[kMaxRows];
-  float x[kMaxRows];         // its logit in that row
-  float y[kMaxRows];         // and in the draft's row
-  double sum[2][kMaxRows];   // of the rows (a chain's): target, draft
+  double term[kMaxRows];     // its term in that row
+  union {
+    double sum[2][kMaxRows];  // of the rows: target, draft
+    uint64_t best[kMaxRows];
+  };
   float ref[2][kMaxRows];
   int32_t path[kMaxRows];
+  uint64_t ends[kMaxRows / kWave];   // drafts of a chain that are not accepted
+  uint64_t close[kMaxRows / kWave];  // or too close to tell
   double part[kW];
 };
 
-// A row's sum out of its chunks, in every lane of the wave. sum = 0: no
-// distribution. In the same way the largest (logit, token): 0 for none.
+// A row's sum out of its chunks, held by LANES neighbouring lanes (16 or a wave),
+// which all get it. sum = 0: no distribution.
 struct RowSum {
   double sum;
   float ref;
 };
-__device__ __forceinline__ RowSum row_sum(const RowChunk* __restrict__ s, int chunks) {
-  const int lane = threadIdx.x % kWave;
-  uint32_t bad = 0;
-  float top = -INFINITY;
-  for (int c = lane; c < chunks; c += kWave) {
-    bad |= static_cast<uint32_t>(s[c].bad);
-    if (s[c].sum > 0.0) top = fmaxf(top, s[c].ref);
+template <int LANES, class T, class Op>
+__device__ __forceinline__ T over_lanes(T v, Op op) {
+  auto step = [&](uint64_t moved) { v = op(v, __builtin_bit_cast(T, moved)); };
+  auto bits = [&]() { return __builtin_bit_cast(uint64_t, v); };
+  step(dpp_u64<dpp::kQuad1032>(bits(), 0ull));
+  step(dpp_u64<dpp::kQuad2301>(bits(), 0ull));
+  step(dpp_u64<dpp::kRowHalfMirror>(bits(), 0ull));
+  step(dpp_u64<dpp::kRowMirror>(bits(), 0ull));
+  if constexpr (LANES == kWave) {
+    T all = __builtin_bit_cast(T, readlane_u64(bits(), 0));
+#pragma unroll
+    for (int i = 16; i < kWave; i += 16) all = op(all, __builtin_bit_cast(T, readlane_u64(bits(), i)));
+    v = all;
   }
-  bad = wave_max_u32(bad);
-  top = wave_max_f32(top);
-  double sum = 0.0;
-  for (int c = lane; c < chunks; c += kWave) {
-    const double t = s[c].sum, d = static_cast<double>(s[c].ref) - top;
-    if (t > 0.0) sum += d == 0.0 ? t : t * exp(d);
-  }
-  sum = wave_sum_f64(sum);
-  return bad != 0 ? RowSum{0.0, 0.0f} : RowSum{sum, top};
+  return v;
 }
-__device__ __forceinline__ uint64_t row_best(const RowChunk* __restrict__ s, int chunks) {
-  uint32_t bad = 0;
-  uint64_t best = 0;
-  for (int c = threadIdx.x % kWave; c < chunks; c += kWave) {
-    bad |= static_cast<uint32_t>(s[c].bad);
-    best = best > s[c].best ? best : s[c].best;
+template <int LANES>
+__device__ __forceinline__ RowSum row_sum(const RowChunk* __restrict__ s, int chunks) {
+  const int lane = threadIdx.x % LANES;
+  // references and bad chunks as one number: those of 0 need no exp
+  double sum = 0.0;
+  float top = -INFINITY;
+  bool bad = false, moved = false;
+  for (int c = lane; c < chunks; c += LANES) {
+    const RowChunk t = s[c];
+    bad |= t.bad != 0;
+    if (t.sum > 0.0) {
+      top = fmaxf(top, t.ref);
+      moved |= t.ref != 0.0f;
+      sum += t.sum;
+    }
   }
-  best = wave_reduce_u64(best, 0ull, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-  return wave_max_u32(bad) != 0 ? 0ull : best;
+  if (__ballot(moved) != 0) {  // some chunk of the wave's rows has a reference of its own
+    top = static_cast<float>(over_lanes<LANES>(static_cast<double>(top), [](double a, double b) { return fmax(a, b); }));
+    sum = 0.0;
+    for (int c = lane; c < chunks; c += LANES)
+      if (s[c].sum > 0.0) sum += s[c].sum * exp_from(s[c].ref, top);
+  } else {
+    top = 0.0f;
+  }
+  sum = over_lanes<LANES>(sum, [](double a, double b) { return a + b; });
+  const uint64_t any = over_lanes<LANES>(static_cast<uint64_t>(bad ? 1 : 0), [](uint64_t a, uint64_t b) { return a | b; });
+  return any != 0 ? RowSum{0.0, 0.0f} : RowSum{sum, top};
+}
+// In the same way the largest (logit, token) as one number: 0 for none.
+template <int LANES>
+__device__ __forceinline__ uint64_t row_best(const RowChunk* __restrict__ s, int chunks) {
+  uint64_t best = 0;
+  for (int c = threadIdx.x % LANES; c < chunks; c += LANES) {
+    const uint64_t one = s[c].bad != 0 ? ~0ull : s[c].best;
+    best = best > one ? best : one;
+  }
+  best = over_lanes<LANES>(best, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+  return best == ~0ull ? 0ull : best;
 }
 __device__ __forceinline__ int best_token(uint64_t best) {
   return best == 0 ? -1 : static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(best));
@@ -190,110 +271,180 @@ struct Walk {
 // Relative error of a row's sum out of its chunks, and what decisions closer than
 // that take: both sums again in 64 bits.
 constexpr double kClose = 1e-6;
+// Elements whose terms of p and q, by the ratio of such sums, differ by no more.
+constexpr double kBand = 4e-7;
 
 // Goes down a sequence's path. All threads of the workgroup take part and get the
 // same result.
 template <class DT>
 __device__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int64_t seq, WalkSmem& sm) {
+  constexpr int kSets = kMaxRows / kWave;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int D = a.D, n = draft_count(a, seq);
-  const bool greedy = a.uniforms == nullptr, chain = a.parents == nullptr;
-  if (tid < D) {
-    int token = a.drafts[seq * D + tid];
+  const bool greedy = a.uniforms == nullptr, chain = a.parents == nullptr, drawn = a.draft_logits != nullptr;
+  int token = -1, node = 0;
+  float x = -INFINITY, y = -INFINITY;
+  if (tid < n) {
+    token = a.drafts[seq * D + tid];
     const int parent = chain ? tid - 1 : a.parents[seq * D + tid];
-    if (tid >= n || token < 0 || token >= a.V || parent < -1 || parent >= tid) token = -1;
-    sm.token[tid] = token;
-    sm.node[tid] = parent + 1;
-    sm.x[tid] = token < 0 || greedy ? -INFINITY : DT::value(target_row<DT>(a, seq, parent + 1)[token]);
-    sm.y[tid] = token < 0 || a.draft_logits == nullptr ? -INFINITY : DT::value(draft_row<DT>(a, seq, tid)[token]);
+    if (token < 0 || token >= a.V || parent < -1 || parent >= tid) token = -1;
+    node = parent + 1;
+    if (token >= 0 && !greedy) x = DT::value(target_row<DT>(a, seq, node)[token]);
+    if (token >= 0 && drawn) y = DT::value(draft_row<DT>(a, seq, tid)[token]);
   }
-  if (!greedy && tid <= D) sm.u[tid] = a.uniforms[seq * (D + 1) + tid];
-  if (chain && !greedy) {
-    for (int r = wave; r < n + 1; r += kW) {
-      const RowSum t = row_sum(target_stats(a, stats, chunks, seq, r), chunks);
-      RowSum q{0.0, 0.0f};
-      if (a.draft_logits != nullptr && r < n) q = row_sum(draft_stats(a, stats, chunks, seq, r), chunks);
-      if (lane == 0) {
-        sm.sum[0][r] = t.sum;
-        sm.ref[0][r] = t.ref;
-        sm.sum[1][r] = q.sum;
-        sm.ref[1][r] = q.ref;
+  sm.token[tid] = token;
+  sm.node[tid] = node;
+  sm.u[tid] = !greedy && tid <= D ? a.uniforms[seq * (D + 1) + tid] : 0.0f;
+  // 16 lanes a row: target rows, then draft rows
+  const int rows = n + 1 + (drawn ? n : 0);
+  for (int i = tid / 16; i < (rows + 3) / 4 * 4; i += kT / 16) {
+    const int r = i < rows ? i : 0;
+    const bool target = r <= n;
+    const RowChunk* s = target ? target_stats(a, stats, chunks, seq, r) : draft_stats(a, stats, chunks, seq, r - n - 1);
+    if (greedy) {
+      const uint64_t best = row_best<16>(s, chunks);
+      if (tid % 16 == 0) sm.best[r] = best;
+    } else {
+      const RowSum t = row_sum<16>(s, chunks);
+      if (tid % 16 == 0) {
+        sm.sum[target ? 0 : 1][target ? r : r - n - 1] = t.sum;
+        sm.ref[target ? 0 : 1][target ? r : r - n - 1] = t.ref;
       }
     }
   }
   __syncthreads();
-  // a token that an earlier draft behind the same one has already counts once
-  if (!chain) {
-    bool twice = false;
-    if (tid < D)
-      for (int j = 0; j < tid; ++j) twice |= sm.node[j] == sm.node[tid] && sm.token[j] == sm.token[tid];
+
+  // Acceptance of a chain's draft, behind accepted ones: u q < p, with both sums on
+  // the other side.
+  Walk w{0, 0, kNone, {0.0, 0.0f}, {0.0, 0.0f}, 0ull};
+  auto stands = [&](double u, double pe, double qe, double psum, double qsum, bool& close) -> bool {
+    const double left = u * qe * psum, right = pe * qsum;
+    close = right > 0.0 && left > right * (1.0 - kClose) && left < right * (1.0 + kClose);
+    return left < right;
+  };
+  double pe = 0.0, qe = 1.0;
+  if (!greedy && token >= 0) pe = exp_from(x, sm.ref[0][node]);
+  if (drawn) qe = token >= 0 && sm.sum[1][tid] > 0.0 ? exp_from(y, sm.ref[1][tid]) : 0.0;
+  if (chain) {
+    bool close = false, stays = false;
+    if (token >= 0) {
+      if (greedy) {
+        stays = token == best_token(sm.best[tid]);
+      } else if (sm.sum[0][tid] > 0.0) {
+        const double q = drawn && sm.sum[1][tid] > 0.0 ? sm.sum[1][tid] : 1.0;
+        stays = stands(sm.u[tid], pe, qe, sm.sum[0][tid], q, close);
+      }
+    }
+    const uint64_t ends = __ballot(!stays), closes = __ballot(close);
+    if (lane == 0) {
+      sm.ends[wave] = ends;
+      sm.close[wave] = closes;
+    }
     __syncthreads();
-    if (twice) sm.token[tid] = -1;
+    for (;;) {
+      // the first draft that is rejected, is not there or cannot be told
+      uint64_t end[kSets], open[kSets];
+#pragma unroll
+      for (int i = 0; i < kSets; ++i) {
+        open[i] = sm.close[i];
+        end[i] = sm.ends[i] | open[i];
+      }
+      w.node = D;
+      bool again = false;
+#pragma unroll
+      for (int i = kSets - 1; i >= 0; --i)
+        if (end[i] != 0) {
+          const int j = __builtin_ctzll(end[i]);
+          w.node = i * kWave + j;
+          again = (open[i] >> j & 1u) != 0;
+        }
+      w.node = w.node < D ? w.node : D;
+      if (!again) break;
+      const int j = w.node;
+      const double psum = sum_again<DT>(target_row<DT>(a, seq, j), a.V, sm.ref[0][j], sm);
+      const bool q = drawn && sm.sum[1][j] > 0.0;
+      const double qsum = q ? sum_again<DT>(draft_row<DT>(a, seq, j), a.V, sm.ref[1][j], sm) : 1.0;
+      __syncthreads();
+      if (tid == j) {
+        bool same;
+        if (stands(sm.u[j], pe, qe, psum, qsum, same)) sm.ends[wave] &= ~(1ull << lane);
+        else sm.ends[wave] |= 1ull << lane;
+        sm.close[wave] &= ~(1ull << lane);
+      }
+      __syncthreads();
+    }
+    w.count = w.node;
+    sm.path[tid] = tid;
+    if (greedy) {
+      w.best = sm.best[w.node];
+    } else {
+      w.p = RowSum{sm.sum[0][w.node], sm.ref[0][w.node]};
+      w.kind = w.p.sum > 0.0 ? kPlain : kNone;
+      if (w.kind == kPlain && w.node < n && sm.token[w.node] >= 0) {  // a draft was rejected
+        if (drawn) {
+          w.q = RowSum{sm.sum[1][w.node], sm.ref[1][w.node]};
+          if (w.q.sum > 0.0) w.kind = kResidual;
+        } else {
+          w.kind = kWithout;
+        }
+      }
+    }
     __syncthreads();
+    return w;
   }
 
-  Walk w{0, 0, kNone, {0.0, 0.0f}, {0.0, 0.0f}, 0ull};
+  sm.term[tid] = pe;
+  __syncthreads();
+  // every wave holds all drafts, kSets a lane
+  int tokens[kSets], nodes[kSets];
+#pragma unroll
+  for (int i = 0; i < kSets; ++i) {
+    tokens[i] = sm.token[i * kWave + lane];
+    nodes[i] = sm.node[i * kWave + lane];
+  }
   for (;;) {
     // the drafts behind this node: bits of the draft numbers
-    uint64_t kids[kMaxRows / kWave];
-    bool any = false;
+    uint64_t kids[kSets];
 #pragma unroll
-    for (int i = 0; i < kMaxRows / kWave; ++i) {
-      const int j = i * kWave + lane;
-      kids[i] = __ballot(j < D && sm.token[j] >= 0 && sm.node[j] == w.node);
-      any |= kids[i] != 0;
-    }
+    for (int i = 0; i < kSets; ++i) kids[i] = __ballot(tokens[i] >= 0 && nodes[i] == w.node);
     int taken = -1;
     if (greedy) {
-      w.best = row_best(target_stats(a, stats, chunks, seq, w.node), chunks);
-      const int token = best_token(w.best);
+      w.best = sm.best[w.node];
+      const int top = best_token(w.best);
 #pragma unroll
-      for (int i = 0; i < kMaxRows / kWave; ++i)
-        for (uint64_t m = kids[i]; m != 0 && taken < 0; m &= m - 1) {
-          const int j = i * kWave + __builtin_ctzll(m);
-          if (sm.token[j] == token) taken = j;
-        }
+      for (int i = kSets - 1; i >= 0; --i) {
+        const uint64_t hit = __ballot(tokens[i] == top) & kids[i];
+        if (hit != 0 && top >= 0) taken = i * kWave + __builtin_ctzll(hit);
+      }
     } else {
-      w.p = chain ? RowSum{sm.sum[0][w.node], sm.ref[0][w.node]}
-                  : row_sum(target_stats(a, stats, chunks, seq, w.node), chunks);
-      w.q = RowSum{0.0, 0.0f};
-      w.kind = !(w.p.sum > 0.0) ? kNone : kPlain;
-      if (any && w.kind != kNone) {
-        const double u = sm.u[w.node];
-        if (a.draft_logits != nullptr) {
-          const int j = w.node;
-          w.q = RowSum{sm.sum[1][j], sm.ref[1][j]};
-          const double pe = exp_from(sm.x[j], w.p.ref);
-          const double qe = w.q.sum > 0.0 ? exp_from(sm.y[j], w.q.ref) : 0.0;
-          // u q < p with both sums on the other side
-          double left = u * qe * w.p.sum, right = pe * (w.q.sum > 0.0 ? w.q.sum : 1.0);
-          if (right > 0.0 && left > right * (1.0 - kClose) && left < right * (1.0 + kClose)) {
-            w.p.sum = sum_again<DT>(target_row<DT>(a, seq, j), a.V, w.p.ref, sm);
-            w.q.sum = sum_again<DT>(draft_row<DT>(a, seq, j), a.V, w.q.ref, sm);
-            left = u * qe * w.p.sum;
-            right = pe * w.q.sum;
-          }
-          if (left < right) taken = j;
-          else if (w.q.sum > 0.0) w.kind = kResidual;
-        } else {
-          for (int turn = 0; turn < 2; ++turn) {
-            const double at = u * w.p.sum;
-            double upto = 0.0;
-            bool close = false;
-            taken = -1;
+      w.p = RowSum{sm.sum[0][w.node], sm.ref[0][w.node]};
+      w.kind = w.p.sum > 0.0 ? kPlain : kNone;
+      if (w.kind == kNone) break;
+      const double u = sm.u[w.node];
+      for (int turn = 0; turn < 2; ++turn) {
+        const double at = u * w.p.sum;
+        double upto = 0.0;
+        bool close = false, any = false;
+        taken = -1;
 #pragma unroll
-            for (int i = 0; i < kMaxRows / kWave; ++i)
-              for (uint64_t m = kids[i]; m != 0; m &= m - 1) {
-                const int j = i * kWave + __builtin_ctzll(m);
-                upto += exp_from(sm.x[j], w.p.ref);
-                close |= upto > at * (1.0 - kClose) && upto < at * (1.0 + kClose);
-                if (at < upto && taken < 0) taken = j;
-              }
-            if (!close || turn == 1) break;
-            w.p.sum = sum_again<DT>(target_row<DT>(a, seq, w.node), a.V, w.p.ref, sm);
+        for (int i = 0; i < kSets; ++i)
+          for (uint64_t m = kids[i]; m != 0; m &= m - 1) {
+            const int bit = __builtin_ctzll(m), j = i * kWave + bit;
+            // a token that an earlier one of them has counts once
+            const int same = __builtin_amdgcn_readlane(tokens[i], bit);
+            uint64_t before = __ballot(tokens[i] == same) & kids[i] & ((1ull << bit) - 1);
+#pragma unroll
+            for (int k = 0; k < i; ++k) before |= __ballot(tokens[k] == same) & kids[k];
+            if (before != 0) continue;
+            any = true;
+            upto += sm.term[j];
+            close |= upto > at * (1.0 - kClose) && upto < at * (1.0 + kClose);
+            if (at < upto && taken < 0) taken = j;
           }
-          if (taken < 0) w.kind = kWithout;
-        }
+        if (taken < 0 && any) w.kind = kWithout;
+        if (!close || turn == 1) break;
+        w.kind = kPlain;
+        w.p.sum = sum_again<DT>(target_row<DT>(a, seq, w.node), a.V, w.p.ref, sm);
       }
     }
     if (taken < 0) break;
@@ -305,136 +456,246 @@ __device__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int
   return w;
 }
 
-// One chunk of one row: its sum of exp, or its largest element. Blocks of a
-// sequence: its target rows, then its draft rows.
+struct ChunkSmem {
+  double sum[kW];
+  uint32_t top[kW];
+  uint64_t best[kW];
+};
+
+// One chunk of a row, of split.vecs vectors of 16 bytes: its sum of exp, or its
+// largest element. The vectors of one group are on their way while the ones before
+// are summed; the few elements before the row's first 16-byte boundary and behind
+// its last one belong to the first and the last chunk. Returned to all threads.
+struct Split {
+  int chunks, vecs;
+};
 template <class DT, bool GREEDY>
-__global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, int chunks, int blocks, int64_t seq0,
-                                                         RowChunk* __restrict__ stats, uint32_t* __restrict__ arrived) {
+__device__ RowChunk chunk_of(const typename DT::raw_t* row, int V, int ch, Split split, ChunkSmem& sm) {
   using raw_t = typename DT::raw_t;
-  __shared__ double sum_of[kW];
-  __shared__ uint32_t top_of[kW];
-  __shared__ uint64_t best_of[kW];
+  constexpr int P = DT::kPerVec, kGroup = 32 / P;
+  constexpr uint32_t kNeg = P == 4 ? static_cast<uint32_t>(DT::kNegInf)
+                                   : static_cast<uint32_t>(DT::kNegInf) * 0x00010001u;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  const int head = head_of(row, V);
+  const int nfull = (V - head) / P;
+  const int tail0 = head + nfull * P;
+  const int v0 = ch * split.vecs;
+  int cnt = nfull - v0;
+  cnt = cnt < 0 ? 0 : (cnt < split.vecs ? cnt : split.vecs);
+  const int first = head + v0 * P;
+  const __amdgpu_buffer_rsrc_t rs = row_rsrc(row + (cnt > 0 ? first : 0), cnt * P);
+  auto load = [&](int i) __attribute__((always_inline)) -> vec_t {
+    return __builtin_amdgcn_raw_buffer_load_b128(rs, (i * kT + tid) * 16, 0, kLoadPolicy);
+  };
+  vec_t next[kGroup];
+#pragma unroll
+  for (int g = 0; g < kGroup; ++g) next[g] = load(g);
+  int te = -1;
+  if (ch == 0 && tid < head) te = tid;
+  if (ch == split.chunks - 1 && tid >= 16 && tid - 16 < V - tail0) te = tail0 + tid - 16;
+  raw_t re = DT::kNegInf;
+  if (te >= 0) re = row[te];
+
+  double sum = 0.0, sum_rest = 0.0;
+  float top = -INFINITY;  // maximum() keeps a NaN
+  float most = -INFINITY;
+  int most_at = 0;        // the first element that is as large
+  const int layers = (cnt + kT - 1) / kT;
+#pragma unroll 1
+  for (int i0 = 0; i0 < layers; i0 += kGroup) {
+    vec_t now[kGroup];
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) now[g] = next[g];
+    if (i0 + kGroup < layers) {
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g) next[g] = load(i0 + kGroup + g);
+    }
+    if ((i0 + kGroup) * kT > cnt) {  // the last group
+#pragma unroll
+      for (int g = 0; g < kGroup; ++g)
+        if ((i0 + g) * kT + tid >= cnt) now[g] = vec_t{kNeg, kNeg, kNeg, kNeg};
+    }
+#pragma unroll
+    for (int g = 0; g < kGroup; ++g) {
+      float e[P], rest = 0.0f;
+#pragma unroll
+      for (int j = 0; j < P; ++j) {
+        const float x = DT::value(lane_of<raw_t>(now[g], j));
+        top = __builtin_elementwise_maximum(top, x);
+        if constexpr (GREEDY) {
+          const bool more = x > most;
+          most = more ? x : most;
+          most_at = more ? ((i0 + g) * kT + tid) * P + j : most_at;
+        } else {
+          e[j] = exp_parts<DT>(x, rest);
+        }
+      }
+      if constexpr (!GREEDY) {
+#pragma unroll
+        for (int d = 1; d < P; d *= 2) {
+#pragma unroll
+          for (int j = 0; j < P; j += 2 * d) e[j] += e[j + d];
+        }
+        if constexpr (P == 4) {
+          sum += static_cast<double>(__builtin_fmaf(rest, kLn2, e[0]));
+        } else {
+          sum += static_cast<double>(e[0]);
+          sum_rest += static_cast<double>(rest);
+        }
+      }
+    }
+  }
+  const float xe = DT::value(re);
+  top = __builtin_elementwise_maximum(top, xe);
+  auto key_or_nan = [](float x) -> uint32_t {
+    return __builtin_isnan(x) ? 0xFFFFFFFFu : F32T::key(__float_as_uint(x));
+  };
+  uint32_t top_key = wave_max_u32(key_or_nan(top));
+  uint64_t best = 0;
+  if constexpr (GREEDY) {
+    auto pack = [](float x, int at) -> uint64_t {
+      return x > -INFINITY ? (static_cast<uint64_t>(F32T::key(__float_as_uint(x))) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(at))
+                           : 0ull;
+    };
+    best = pack(most, first + most_at);
+    const uint64_t one = pack(xe, te);
+    best = best > one ? best : one;
+    best = over_lanes<kWave>(best, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
+  } else {
+    float rest = 0.0f;
+    sum += static_cast<double>(exp_parts<DT>(xe, rest));
+    sum_rest += static_cast<double>(rest);
+    sum = wave_sum_f64(sum_of<DT>(sum, sum_rest));  // (fp32: rest is that of this element alone)
+  }
+  __syncthreads();
+  if (lane == 0) {
+    sm.sum[wave] = sum;
+    sm.top[wave] = top_key;
+    sm.best[wave] = best;
+  }
+  __syncthreads();
+  sum = 0.0;
+#pragma unroll
+  for (int i = 0; i < kW; ++i) {
+    sum += sm.sum[i];
+    top_key = top_key > sm.top[i] ? top_key : sm.top[i];
+    best = best > sm.best[i] ? best : sm.best[i];
+  }
+  RowChunk out;
+  out.ref = 0.0f;
+  out.bad = top_key >= F32T::key(0x7F800000u) ? 1 : 0;
+  if constexpr (GREEDY) {
+    out.best = best;
+    return out;
+  }
+  if (out.bad || top_key <= F32T::key(0xFF800000u)) {
+    sum = 0.0;  // nothing but -inf, or a row that does not count
+  } else {
+    const float all = __uint_as_float(F32T::raw_of_key(top_key));
+    if (all > kHighMax || all < kLowMax) {  // read again, in 64 bits and less the maximum
+      out.ref = all;
+      double part = te >= 0 ? exp_from(xe, all) : 0.0;
+#pragma unroll 1
+      for (int i = tid; i < cnt; i += kT) {
+        const vec_t q = __builtin_amdgcn_raw_buffer_load_b128(rs, i * 16, 0, 0);
+#pragma unroll
+        for (int j = 0; j < P; ++j) part += exp_from(DT::value(lane_of<raw_t>(q, j)), all);
+      }
+      part = wave_sum_f64(part);
+      __syncthreads();
+      if (lane == 0) sm.sum[wave] = part;
+      __syncthreads();
+      sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < kW; ++i) sum += sm.sum[i];
+    }
+  }
+  out.sum = sum;
+  return out;
+}
+
+// Chunks of all rows. Workgroups of a sequence: its target rows, then its draft rows.
+template <class DT, bool GREEDY>
+__global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, Split split, int64_t seq0,
+                                                         RowChunk* __restrict__ stats, uint32_t* __restrict__ arrived) {
+  __shared__ ChunkSmem sm;
   const int rows = a.D + 1 + (a.draft_logits != nullptr ? a.D : 0);
   const unsigned b = blockIdx.x;
-  const int ch = static_cast<int>(b % static_cast<unsigned>(chunks));
-  const unsigned item = b / static_cast<unsigned>(chunks);
+  const int ch = static_cast<int>(b % static_cast<unsigned>(split.chunks));
+  const unsigned item = b / static_cast<unsigned>(split.chunks);
   const int r = static_cast<int>(item % static_cast<unsigned>(rows));
   const int64_t seq = seq0 + item / static_cast<unsigned>(rows);
-  if (r == 0 && ch == 0 && tid == 0) arrived[seq] = 0;
+  if (r == 0 && ch == 0 && threadIdx.x == 0) arrived[seq] = 0;
   const bool target = r <= a.D;
   const int w = target ? r : r - a.D - 1;
   const int n = draft_count(a, seq);
   if (target ? w > n : w >= n) return;
-  const raw_t* row = target ? target_row<DT>(a, seq, w) : draft_row<DT>(a, seq, w);
-  RowChunk* out = const_cast<RowChunk*>(target ? target_stats(a, stats, chunks, seq, w)
-                                               : draft_stats(a, stats, chunks, seq, w)) + ch;
-  const int first = ch * blocks * kT * kBlock;
-
-  auto key_or_nan = [](float x) -> uint32_t {
-    if (__builtin_isnan(x)) return 0xFFFFFFFFu;
-    return F32T::key(__float_as_uint(x));
-  };
-  uint32_t top = 0;
-  uint64_t best = 0;
-  for (int i = 0; i < blocks; ++i) {
-    const int v = first + (i * kT + tid) * kBlock;
-    if (v >= a.V) break;
-    float x[kBlock];
-    load_block<DT>(row, v, a.V, x);
-#pragma unroll
-    for (int j = 0; j < kBlock; ++j) {
-      const uint32_t k = key_or_nan(x[j]);
-      top = top > k ? top : k;
-      if constexpr (GREEDY) {
-        const uint64_t one = (static_cast<uint64_t>(k) << 32) | (0xFFFFFFFFu - static_cast<uint32_t>(v + j));
-        if (x[j] > -INFINITY && one > best) best = one;
-      }
-    }
-  }
-  top = wave_max_u32(top);
-  if constexpr (GREEDY)
-    best = wave_reduce_u64(best, 0ull, [](uint64_t p, uint64_t q) { return p > q ? p : q; });
-  if (lane == 0) {
-    top_of[wave] = top;
-    best_of[wave] = best;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kW; ++i) {
-    top = top > top_of[i] ? top : top_of[i];
-    best = best > best_of[i] ? best : best_of[i];
-  }
-  const int bad = top >= F32T::key(0x7F800000u) ? 1 : 0;
-  if constexpr (GREEDY) {
-    if (tid == 0) {
-      out->best = best;
-      out->ref = 0.0f;
-      out->bad = bad;
-    }
-    return;
-  }
-  const float ref = __uint_as_float(F32T::raw_of_key(top));
-  double sum = 0.0;
-  if (!bad && top > F32T::key(0xFF800000u)) {
-    for (int i = 0; i < blocks; ++i) {
-      const int v = first + (i * kT + tid) * kBlock;
-      if (v >= a.V) break;
-      float x[kBlock];
-      load_block<DT>(row, v, a.V, x);
-#pragma unroll
-      for (int j = 0; j < kBlock; ++j) sum += exp_from(x[j], ref);
-    }
-  }
-  sum = wave_sum_f64(sum);
-  if (lane == 0) sum_of[wave] = sum;
-  __syncthreads();
-  if (tid == 0) {
-    sum = 0.0;
-    for (int i = 0; i < kW; ++i) sum += sum_of[i];
-    out->sum = sum;
-    out->ref = ref;
-    out->bad = bad;
-  }
+  const RowChunk c = chunk_of<DT, GREEDY>(target ? target_row<DT>(a, seq, w) : draft_row<DT>(a, seq, w), a.V, ch, split, sm);
+  RowChunk* out = const_cast<RowChunk*>(target ? target_stats(a, stats, split.chunks, seq, w)
+                                               : draft_stats(a, stats, split.chunks, seq, w)) + ch;
+  if (threadIdx.x == 0) *out = c;
 }
 
 struct FinalSmem {
   WalkSmem walk;
-  int32_t out[kMaxRows];  // rejected tokens within the chunk
+  int32_t out[kMaxRows];  // rejected tokens within the range
   int outs;
-  double sum[5][kW];
-  double parts[kMaxParts];  // of chunks, where summed again
+  double sum[4][kW];
+  double parts[kMaxParts];  // where summed again
+  uint64_t is[kW], may[kW];
+  double below;
   int last;
   int found;
-  double below;
 };
 
 // The terms of eight neighbouring elements: p's, and q's.
-template <class DT>
 struct Terms {
   double p[kBlock], q[kBlock];
 };
+// Elements of no more than exp(-50) of the row, so a 2^-52nd of it all together,
+// count as 0 where a whole wave has none but them: rows that were filtered.
+constexpr float kFar = 50.0f;
+struct Rows {
+  float p_least, q_least;
+};
+__device__ __forceinline__ Rows least_of(const Walk& w) {
+  Rows r;
+  r.p_least = w.p.ref + static_cast<float>(log(w.p.sum)) - kFar;
+  r.q_least = w.kind == kResidual ? w.q.ref + static_cast<float>(log(w.q.sum)) - kFar : INFINITY;
+  return r;
+}
+__device__ __forceinline__ float largest(const float (&x)[kBlock]) {
+  return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+}
+// False if they are all 0, for the whole wave.
 template <class DT>
-__device__ __forceinline__ void terms_at(const typename DT::raw_t* prow, const typename DT::raw_t* qrow, int v, int V,
-                                         const Walk& w, bool two, Terms<DT>& t) {
-  float x[kBlock];
+__device__ __forceinline__ bool terms_at(const typename DT::raw_t* prow, const typename DT::raw_t* qrow, int v, int V,
+                                         const Walk& w, const Rows& least, bool two, Terms& t) {
+  float x[kBlock], y[kBlock];
   load_block<DT>(prow, v, V, x);
-#pragma unroll
-  for (int j = 0; j < kBlock; ++j) t.p[j] = x[j] == -INFINITY ? 0.0 : exp_from(x[j], w.p.ref);
+  bool some = largest(x) > least.p_least;
   if (two) {
-    load_block<DT>(qrow, v, V, x);
-#pragma unroll
-    for (int j = 0; j < kBlock; ++j) t.q[j] = x[j] == -INFINITY ? 0.0 : exp_from(x[j], w.q.ref);
+    load_block<DT>(qrow, v, V, y);
+    some |= largest(y) > least.q_least;
   }
+  if (__ballot(some) == 0) return false;
+#pragma unroll
+  for (int j = 0; j < kBlock; ++j) t.p[j] = exp_from(x[j], w.p.ref);
+  if (two) {
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) t.q[j] = exp_from(y[j], w.q.ref);
+  }
+  return true;
 }
 
 // The rejected tokens within [first, end).
 __device__ __forceinline__ void list_out(const VerifyArgs& a, const Walk& w, int first, int end, FinalSmem& sm) {
+  if (w.kind != kWithout) return;
   const int tid = threadIdx.x;
   __syncthreads();
   if (tid == 0) sm.outs = 0;
   __syncthreads();
-  if (w.kind == kWithout && tid < a.D && sm.walk.node[tid] == w.node) {
+  if (tid < a.D && sm.walk.node[tid] == w.node) {
     const int t = sm.walk.token[tid];
     if (t >= first && t < end) sm.out[atomicAdd(&sm.outs, 1)] = t;
   }
@@ -446,51 +707,257 @@ __device__ __forceinline__ bool is_out(int v, const FinalSmem& sm) {
   return out;
 }
 
-// The workgroup's sum of v, in all threads.
-__device__ __forceinline__ double block_sum(double v, double (&at)[kW]) {
-  v = wave_sum_f64(v);
-  __syncthreads();
-  if (threadIdx.x % kWave == 0) at[threadIdx.x / kWave] = v;
-  __syncthreads();
-  v = 0.0;
+// The workgroup's sums of v[0 .. COUNT), in all threads.
+template <int COUNT>
+__device__ __forceinline__ void block_sums(double (&v)[COUNT], double (&at)[4][kW]) {
 #pragma unroll
-  for (int i = 0; i < kW; ++i) v += at[i];
-  return v;
+  for (int i = 0; i < COUNT; ++i) v[i] = wave_sum_f64(v[i]);
+  __syncthreads();
+  if (threadIdx.x % kWave == 0) {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) at[i][threadIdx.x / kWave] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < COUNT; ++i) {
+    v[i] = 0.0;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) v[i] += at[i][w];
+  }
 }
-// The sum of v over the threads below, and of all.
-__device__ __forceinline__ double block_below(double v, double& all, double (&at)[kW]) {
-  const int wave = threadIdx.x / kWave;
-  const double upto = wave_incl_scan_f64(v);
+// The sums of v over the threads below, up to this one, and over all. What one
+// thread gets as its end is what the next one gets as its beginning.
+__device__ __forceinline__ void block_scan(double v, double& below, double& upto, double& all, double (&at)[4][kW]) {
+  const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+  const double end = wave_incl_scan_f64(v);
+  const double begin = __shfl_up(end, 1);
   __syncthreads();
-  if (threadIdx.x % kWave == kWave - 1) at[wave] = upto;
+  if (lane == kWave - 1) at[0][wave] = end;
   __syncthreads();
-  double below = 0.0;
+  double base = 0.0;
   all = 0.0;
 #pragma unroll
-  for (int i = 0; i < kW; ++i) {
-    if (i < wave) below += at[i];
-    all += at[i];
+  for (int w = 0; w < kW; ++w) {
+    if (w == wave) base = all;
+    all += at[0][w];
   }
-  return below + (upto - v);
+  below = lane == 0 ? base : base + begin;
+  upto = base + end;
+}
+
+// v, or next to 0 (below 2^-1022): one instruction, where a choice of both halves takes two.
+__device__ __forceinline__ double if_or_none(bool is, double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t high = is ? static_cast<uint32_t>(u >> 32) : 0u;
+  return __builtin_bit_cast(double, (static_cast<uint64_t>(high) << 32) | static_cast<uint32_t>(u));
+}
+
+// Sums over a wave's part of the row, of every lane's elements.
+template <class DT>
+__device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, const typename DT::raw_t* qrow, int first,
+                                             int pieces, int V, const Walk& w, const FinalSmem& sm) {
+  FinalPart mine{0.0, 0.0, 0.0, 0.0, 0.0};
+  const Rows least = least_of(w);
+  const int lane = threadIdx.x % kWave;
+  if (w.kind == kResidual) {
+    // p > q where near * p's term > q's
+    const double near = w.q.sum / w.p.sum;
+#pragma unroll 1
+    for (int i = 0; i < pieces; ++i) {
+      const int v = first + i * kPiece + lane * kBlock;
+      Terms t;
+      if (!terms_at<DT>(prow, qrow, v, V, w, least, true, t)) continue;
+#pragma unroll
+      for (int j = 0; j < kBlock; ++j) {
+        const double more = __builtin_fma(near, t.p[j], -t.q[j]);
+        mine.all += t.p[j];
+        mine.draft += t.q[j];
+        mine.left += __builtin_fmax(more, 0.0);
+        mine.kept += if_or_none(more > 0.0, t.p[j]);
+        const bool close = __builtin_fabs(more) < kBand * t.q[j];
+        if (__ballot(close) != 0) mine.close += close ? t.p[j] : 0.0;
+      }
+    }
+  } else {
+    const bool outs = w.kind == kWithout && sm.outs != 0;
+#pragma unroll 1
+    for (int i = 0; i < pieces; ++i) {
+      const int v = first + i * kPiece + lane * kBlock;
+      Terms t;
+      if (!terms_at<DT>(prow, qrow, v, V, w, least, false, t)) continue;
+      double sum = 0.0;
+#pragma unroll
+      for (int j = 0; j < kBlock; ++j) sum += t.p[j];
+      mine.all += sum;
+      if (outs) {
+        sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j) sum += is_out(v + j, sm) ? 0.0 : t.p[j];
+      }
+      mine.left += sum;
+    }
+  }
+  return mine;
+}
+
+// What the row's elements weigh: scale * p's term less q's, or p's term, or nothing.
+struct Weights {
+  double scale;
+  bool residual, without;
+  __device__ __forceinline__ double of(const Terms& t, int j, int v, const FinalSmem& sm) const {
+    if (residual) {
+      const double more = __builtin_fma(scale, t.p[j], -t.q[j]);
+      return more > 0.0 ? more : 0.0;
+    }
+    return without && is_out(v, sm) ? 0.0 : t.p[j];
+  }
+};
+
+// The first thread for which `is` holds, and the last one for which `may` does: -1 for none.
+__device__ __forceinline__ int first_or_last(bool is, bool may, FinalSmem& sm) {
+  const int wave = threadIdx.x / kWave;
+  const uint64_t a = __ballot(is), b = __ballot(may);
+  if (threadIdx.x % kWave == 0) {
+    sm.is[wave] = a;
+    sm.may[wave] = b;
+  }
+  __syncthreads();
+  int first = -1, last = -1;
+#pragma unroll
+  for (int i = kW - 1; i >= 0; --i)
+    if (sm.is[i] != 0) first = i * kWave + __builtin_ctzll(sm.is[i]);
+#pragma unroll
+  for (int i = 0; i < kW; ++i)
+    if (sm.may[i] != 0) last = i * kWave + 63 - __builtin_clzll(sm.may[i]);
+  __syncthreads();
+  return first >= 0 ? first : last;
+}
+
+// Finds the token out of the parts' sums, by the whole workgroup.
+template <class DT>
+__device__ int token_of(const VerifyArgs& a, const Walk& w, const FinalPart* slots, int parts, int pieces,
+                        const typename DT::raw_t* prow, const typename DT::raw_t* qrow, FinalSmem& sm) {
+  const int tid = threadIdx.x, span = pieces * kPiece;
+  const bool two = w.kind == kResidual;
+  const Rows least = least_of(w);
+  FinalPart p[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // parts that are not there: those of the last one, taken out below
+    const FinalPart* from = slots + (2 * tid + i < parts ? 2 * tid + i : parts - 1);
+    p[i] = FinalPart{get_far(&from->all), get_far(&from->left), 0.0, 0.0, 0.0};
+    if (two) {
+      p[i].kept = get_far(&from->kept);
+      p[i].draft = get_far(&from->draft);
+      p[i].close = get_far(&from->close);
+    }
+  }
+  double total[3] = {0.0, 0.0, 0.0};  // all, draft, close
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (2 * tid + i >= parts) p[i] = FinalPart{0.0, 0.0, 0.0, 0.0, 0.0};
+    total[0] += p[i].all;
+    total[1] += p[i].draft;
+    total[2] += p[i].close;
+  }
+  block_sums(total, sm.sum);
+  Weights weights{two ? total[1] / total[0] : 1.0, two, w.kind == kWithout};
+  const double near = two ? w.q.sum / w.p.sum : 1.0, off = weights.scale - near;
+  double part[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) part[i] = __builtin_fmax(two ? __builtin_fma(off, p[i].kept, p[i].left) : p[i].left, 0.0);
+  double below, upto, all;
+  block_scan(part[0] + part[1], below, upto, all, sm.sum);
+  // Elements between the parts' ratio of the sums and the one in 64 bits are taken
+  // in or left out by mistake, each with no more than their difference. That is
+  // next to nothing (some 1e-8 of some 1e-7 of the mass) unless the rows are alike;
+  // then the parts are summed again.
+  if (two && (__builtin_fabs(off) * total[2] > 0x1p-43 * all || __builtin_fabs(off) > 0.5 * kBand * near)) {
+    for (int c0 = 0; c0 < parts; c0 += kW) {
+      const int c = c0 + tid / kWave;
+      double sum = 0.0;
+      for (int i = 0; i < pieces; ++i) {
+        const int v = c * span + i * kPiece + tid % kWave * kBlock;
+        Terms t;
+        if (!terms_at<DT>(prow, qrow, v, a.V, w, least, true, t)) continue;
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j) sum += weights.of(t, j, v + j, sm);
+      }
+      sum = wave_sum_f64(sum);
+      if (c < parts && tid % kWave == 0) sm.parts[c] = sum;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) part[i] = 2 * tid + i < parts ? sm.parts[2 * tid + i] : 0.0;
+    block_scan(part[0] + part[1], below, upto, all, sm.sum);
+  }
+  if (w.kind != kPlain && !(all > kLeast * (two ? total[1] : total[0]))) {
+    weights.residual = weights.without = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) part[i] = p[i].all;
+    block_scan(part[0] + part[1], below, upto, all, sm.sum);
+  }
+  const double at = static_cast<double>(sm.walk.u[a.D]) * all;
+  // the part that `at` lies in; for a uniform out of range the first or the last one of any weight
+  const int owner = first_or_last(upto > at && upto > below, upto > below, sm);
+  if (owner < 0) return -1;
+  if (tid == owner) {
+    const double middle = below + part[0];
+    const bool second = !(part[0] > 0.0 && (middle > at || !(part[1] > 0.0)));
+    sm.below = second ? middle : below;
+    sm.found = 2 * tid + (second ? 1 : 0);
+  }
+  __syncthreads();
+  const int c = sm.found;
+  const double base = sm.below;
+  list_out(a, w, c * span, (c + 1) * span, sm);
+  // at most kMaxPieces * 512 elements: eight for each thread
+  static_assert(kMaxPieces * kPiece <= kT * kBlock);
+  const int v = tid * kBlock < span ? c * span + tid * kBlock : a.V;
+  double wt[kBlock], sum = 0.0;
+  int last = -1;  // the last element of any weight
+  Terms t;
+  if (terms_at<DT>(prow, qrow, v, a.V, w, least, two, t)) {
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) {
+      wt[j] = weights.of(t, j, v + j, sm);
+      sum += wt[j];
+      if (wt[j] > 0.0) last = v + j;
+    }
+  }
+  block_scan(sum, below, upto, all, sm.sum);
+  const int finder = first_or_last(last >= 0 && base + upto > at, last >= 0, sm);
+  if (finder < 0) return -1;
+  if (tid == finder) {
+    int token = last;
+    double reach = base + below;
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) {
+      reach += wt[j];
+      if (wt[j] > 0.0 && reach > at) token = token < v + j ? token : v + j;
+    }
+    sm.found = token;
+  }
+  __syncthreads();
+  return sm.found;
 }
 
 template <class DT>
-__global__ __launch_bounds__(kT) void verify_final_kernel(VerifyArgs a, int chunks, int parts, int blocks, int64_t seq0,
+__global__ __launch_bounds__(kT) void verify_final_kernel(VerifyArgs a, int chunks, int groups, int pieces, int64_t seq0,
                                                           const RowChunk* __restrict__ stats,
                                                           FinalPart* __restrict__ finals,
                                                           uint32_t* __restrict__ arrived) {
   using raw_t = typename DT::raw_t;
   __shared__ FinalSmem sm;
   const int tid = threadIdx.x;
-  const int ch = static_cast<int>(blockIdx.x % static_cast<unsigned>(parts));
-  const int64_t seq = seq0 + blockIdx.x / static_cast<unsigned>(parts);
+  const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(groups));
+  const int64_t seq = seq0 + blockIdx.x / static_cast<unsigned>(groups);
   const Walk w = walk<DT>(a, stats, chunks, seq, sm.walk);
   int32_t* tokens = a.out_tokens + seq * (a.D + 1);
   const bool greedy = a.uniforms == nullptr;
   const bool draws = !greedy && w.kind != kNone;
-  if (ch == 0) {
+  if (group == 0) {
     if (tid <= a.D && !(tid == w.count && draws))
-      tokens[tid] = tid < w.count ? a.drafts[seq * a.D + sm.walk.path[tid]]
+      tokens[tid] = tid < w.count ? sm.walk.token[sm.walk.path[tid]]
                                   : (tid == w.count && greedy ? best_token(w.best) : -1);
     if (a.out_path != nullptr && tid < a.D) a.out_path[seq * a.D + tid] = tid < w.count ? sm.walk.path[tid] : -1;
     if (tid == 0) a.out_accepted[seq] = w.count;
@@ -498,242 +965,100 @@ __global__ __launch_bounds__(kT) void verify_final_kernel(VerifyArgs a, int chun
   if (!draws) return;
 
   const raw_t* prow = target_row<DT>(a, seq, w.node);
-  const bool two = w.kind == kResidual;
-  const raw_t* qrow = two ? draft_row<DT>(a, seq, w.node) : prow;
-  const int span = blocks * kT * kBlock;
-  // p > q where scale * p's term > q's
-  const double near = two ? w.q.sum / w.p.sum : 0.0;
-  FinalPart mine{0.0, 0.0, 0.0, 0.0, 0.0};
-  {
-    const int first = ch * span;
-    list_out(a, w, first, first + span, sm);
-    for (int i = 0; i < blocks; ++i) {
-      const int v = first + (i * kT + tid) * kBlock;
-      if (v >= a.V) break;
-      Terms<DT> t;
-      terms_at<DT>(prow, qrow, v, a.V, w, two, t);
-#pragma unroll
-      for (int j = 0; j < kBlock; ++j) {
-        mine.all += t.p[j];
-        if (two) {
-          const double more = near * t.p[j] - t.q[j];
-          mine.draft += t.q[j];
-          if (more > 0.0) {
-            mine.kept += t.p[j];
-            mine.other += t.q[j];
-          }
-          if (__builtin_fabs(more) <= 2.0 * kClose * t.q[j]) mine.close += t.p[j];
-        } else if (!is_out(v + j, sm)) {
-          mine.kept += t.p[j];
-        }
-      }
-    }
-  }
-  mine.all = block_sum(mine.all, sm.sum[0]);
-  mine.kept = block_sum(mine.kept, sm.sum[1]);
-  mine.other = block_sum(mine.other, sm.sum[2]);
-  mine.draft = block_sum(mine.draft, sm.sum[3]);
-  mine.close = block_sum(mine.close, sm.sum[4]);
+  const raw_t* qrow = w.kind == kResidual ? draft_row<DT>(a, seq, w.node) : prow;
+  const int span = pieces * kPiece, parts = groups * kW;
+  list_out(a, w, group * kW * span, (group + 1) * kW * span, sm);
+  const int c = group * kW + tid / kWave;
+  FinalPart mine = part_of<DT>(prow, qrow, c * span, pieces, a.V, w, sm);
+  mine.all = wave_sum_f64(mine.all);
+  mine.left = wave_sum_f64(mine.left);
   FinalPart* slots = finals + seq * parts;
-  if (tid == 0) {
-    auto put = [](double* to, double v) { __hip_atomic_store(to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-    put(&slots[ch].all, mine.all);
-    put(&slots[ch].kept, mine.kept);
-    put(&slots[ch].other, mine.other);
-    put(&slots[ch].draft, mine.draft);
-    put(&slots[ch].close, mine.close);
-    const uint32_t before =
-        __hip_atomic_fetch_add(&arrived[seq], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-    sm.last = before == static_cast<uint32_t>(parts) - 1u ? 1 : 0;
-    sm.found = 0x7FFFFFFF;
+  if (w.kind == kResidual) {
+    mine.kept = wave_sum_f64(mine.kept);
+    mine.draft = wave_sum_f64(mine.draft);
+    if (__ballot(mine.close != 0.0) != 0) mine.close = wave_sum_f64(mine.close);
   }
-  __syncthreads();
-  if (!sm.last) return;
-
-  // The sequence's last workgroup: all sums are there.
-  __threadfence();
-  auto get = [](const double* from) { return __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT); };
-  FinalPart p[2];
-  FinalPart total{0.0, 0.0, 0.0, 0.0, 0.0};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int c = 2 * tid + i;
-    p[i] = FinalPart{0.0, 0.0, 0.0, 0.0, 0.0};
-    if (c < parts) p[i] = FinalPart{get(&slots[c].all), get(&slots[c].kept), get(&slots[c].other), get(&slots[c].draft),
-                                    get(&slots[c].close)};
-    total.all += p[i].all;
-    total.draft += p[i].draft;
-    total.close += p[i].close;
-  }
-  total.all = block_sum(total.all, sm.sum[0]);
-  total.draft = block_sum(total.draft, sm.sum[1]);
-  total.close = block_sum(total.close, sm.sum[2]);
-  // what an element weighs: scale * p's term, less q's term or nothing if left out
-  double scale = two ? total.draft / total.all : 1.0;
-  bool residual = two, without = w.kind == kWithout;
-  auto weight = [&](const Terms<DT>& t, int j, int v) -> double {
-    if (residual) {
-      const double more = scale * t.p[j] - t.q[j];
-      return more > 0.0 ? more : 0.0;
-    }
-    return without && is_out(v, sm) ? 0.0 : t.p[j];
-  };
-  double part[2];
-  if (two && total.close > 0x1p-20 * total.all) {
-    // too much lies where the first ratio of the sums does not tell which is larger
-    for (int c = 0; c < parts; ++c) {
-      double sum = 0.0;
-      for (int i = 0; i < blocks; ++i) {
-        const int v = c * span + (i * kT + tid) * kBlock;
-        if (v >= a.V) break;
-        Terms<DT> t;
-        terms_at<DT>(prow, qrow, v, a.V, w, true, t);
-#pragma unroll
-        for (int j = 0; j < kBlock; ++j) sum += weight(t, j, v + j);
-      }
-      sum = block_sum(sum, sm.sum[0]);
-      if (tid == 0) sm.parts[c] = sum;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) part[i] = 2 * tid + i < parts ? sm.parts[2 * tid + i] : 0.0;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const double left = two ? scale * p[i].kept - p[i].other : p[i].kept;
-      part[i] = left > 0.0 ? left : 0.0;
+  if (tid % kWave == 0) {
+    put_far(&slots[c].all, mine.all);
+    put_far(&slots[c].left, mine.left);
+    if (w.kind == kResidual) {
+      put_far(&slots[c].kept, mine.kept);
+      put_far(&slots[c].draft, mine.draft);
+      put_far(&slots[c].close, mine.close);
     }
   }
-  const double rest = block_sum(part[0] + part[1], sm.sum[0]);
-  if (w.kind != kPlain && !(rest > kLeast * (two ? total.draft : total.all))) {
-    residual = without = false;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) part[i] = p[i].all;
-  }
-  double all;
-  const double below = block_below(part[0] + part[1], all, sm.sum[1]);
-  const double at = static_cast<double>(sm.walk.u[a.D]) * all;
-  // the first chunk that reaches past `at`; if none does, the last one with any weight
-  int mine_c = -1;
-  if (part[0] > 0.0 && below + part[0] > at) mine_c = 2 * tid;
-  else if (part[1] > 0.0 && below + part[0] + part[1] > at) mine_c = 2 * tid + 1;
-  if (mine_c >= 0) atomicMin(&sm.found, mine_c);
-  __syncthreads();
-  const bool past = sm.found == 0x7FFFFFFF;
-  __syncthreads();
-  if (past) {
-    if (tid == 0) sm.found = -1;
-    __syncthreads();
-    if (part[1] > 0.0) atomicMax(&sm.found, 2 * tid + 1);
-    else if (part[0] > 0.0) atomicMax(&sm.found, 2 * tid);
-    __syncthreads();
-  }
-  const int c = sm.found;
-  if (c >= 0 && c / 2 == tid) sm.below = below + (c % 2 != 0 ? part[0] : 0.0);
-  list_out(a, w, c * span, (c + 1) * span, sm);
-  if (tid == 0) {
-    sm.found = 0x7FFFFFFF;
-    sm.last = -1;
-  }
-  double base = sm.below;
-  __syncthreads();
-  if (c < 0) {  // nothing weighs anything
-    if (tid == 0) tokens[w.count] = -1;
-    return;
-  }
-  for (int i = 0; i < blocks; ++i) {
-    const int v = c * span + (i * kT + tid) * kBlock;
-    double wt[kBlock], sum = 0.0;
-    int some = -1;  // the last element with any weight
-    if (v < a.V) {
-      Terms<DT> t;
-      terms_at<DT>(prow, qrow, v, a.V, w, two, t);
-#pragma unroll
-      for (int j = 0; j < kBlock; ++j) {
-        wt[j] = weight(t, j, v + j);
-        sum += wt[j];
-        if (wt[j] > 0.0) some = v + j;
-      }
-    }
-    double here;
-    double upto = base + block_below(sum, here, sm.sum[2]);
-    if (some >= 0) {
-      atomicMax(&sm.last, some);
-      int token = 0x7FFFFFFF;
-      if (upto + sum > at) {
-        token = some;
-#pragma unroll
-        for (int j = 0; j < kBlock; ++j) {
-          upto += wt[j];
-          if (wt[j] > 0.0 && upto > at) {
-            token = token < v + j ? token : v + j;
-          }
-        }
-        atomicMin(&sm.found, token);
-      }
-    }
-    base += here;
-    __syncthreads();
-    if (sm.found != 0x7FFFFFFF) break;
-  }
-  if (tid == 0) tokens[w.count] = sm.found != 0x7FFFFFFF ? sm.found : sm.last;
+  if (!last_of(&arrived[seq], groups, sm.last)) return;
+  const int token = token_of<DT>(a, w, slots, parts, pieces, prow, qrow, sm);
+  if (tid == 0) tokens[w.count] = token;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Chunks that a row is cut into, of whole layers of a workgroup.
-struct Cut {
-  int chunks, blocks;
-};
-Cut cut_of(int64_t rows, int V, int most) {
-  const int64_t layers = V > 0 ? ceil_div(V, kT * kBlock) : 1;
-  int64_t blocks = rows * layers / 1024;
-  blocks = blocks < 1 ? 1 : (blocks > most ? most : blocks);
-  return Cut{static_cast<int>(ceil_div(layers, blocks)), static_cast<int>(blocks)};
+constexpr int kTargetBlocks = 512;  // chunks wanted where rows are few
+constexpr int kMaxLayers = 32;      // vectors of a thread at most, 16-bit types (fp32: twice)
+
+Split split_of(int dtype, int64_t rows, int V) {
+  const int64_t per = dtype == 0 ? 4 : 8;
+  const int64_t nv = V / per;
+  const int64_t largest = kT * kMaxLayers * 8 / per, smallest = kT * 32 / per;
+  const int64_t least = ceil_div(nv, largest), most = ceil_div(nv, smallest);
+  int64_t c = rows > 0 ? ceil_div(kTargetBlocks, rows) : 1;
+  c = c < most ? c : most;
+  c = c > least ? c : least;
+  c = c > 1 ? c : 1;
+  return Split{static_cast<int>(c), static_cast<int>(ceil_div(nv, c))};
 }
-Cut rows_cut(int64_t N, int D, int V, bool draft) { return cut_of(N * (D + 1 + (draft ? D : 0)), V, 8); }
-Cut final_cut(int64_t N, int V) { return cut_of(N, V, 4); }
+
+// Workgroups for the row where a sequence's path ends, and pieces of their waves.
+struct Cut {
+  int groups, pieces;
+};
+Cut cut_of(int64_t N, int V) {
+  const int64_t all = V > 0 ? ceil_div(V, kPiece * kW) : 1;
+  int64_t pieces = N * all / 1024;
+  pieces = pieces < 1 ? 1 : (pieces > kMaxPieces ? kMaxPieces : pieces);
+  if (all > kMaxParts / kW) pieces = kMaxPieces;
+  return Cut{static_cast<int>(ceil_div(all, pieces)), static_cast<int>(pieces)};
+}
 
 struct Layout {
   int64_t stats, finals, arrived, bytes;
 };
-Layout layout_of(int64_t N, int D, int V, bool draft) {
+Layout layout_of(int dtype, int64_t N, int D, int V, bool draft) {
   const int64_t rows = N * (D + 1 + (draft ? D : 0));
   Layout l;
   l.stats = 0;
-  l.finals = l.stats + rows * rows_cut(N, D, V, draft).chunks * static_cast<int64_t>(sizeof(RowChunk));
-  l.arrived = l.finals + N * final_cut(N, V).chunks * static_cast<int64_t>(sizeof(FinalPart));
+  l.finals = l.stats + rows * split_of(dtype, rows, V).chunks * static_cast<int64_t>(sizeof(RowChunk));
+  l.arrived = l.finals + N * cut_of(N, V).groups * kW * static_cast<int64_t>(sizeof(FinalPart));
   l.bytes = l.arrived + N * 4;
   return l;
 }
 
 template <class DT>
-hipError_t launch_typed(const VerifyArgs& a, hipStream_t stream) {
-  const bool draft = a.draft_logits != nullptr;
+hipError_t launch_typed(int dtype, const VerifyArgs& a, hipStream_t stream) {
+  const bool draft = a.draft_logits != nullptr, greedy = a.uniforms == nullptr;
   const int rows = a.D + 1 + (draft ? a.D : 0);
-  const Cut rc = rows_cut(a.N, a.D, a.V, draft), fc = final_cut(a.N, a.V);
-  const Layout l = layout_of(a.N, a.D, a.V, draft);
+  const Split split = split_of(dtype, a.N * rows, a.V);
+  const Cut cut = cut_of(a.N, a.V);
+  const Layout l = layout_of(dtype, a.N, a.D, a.V, draft);
   char* ws = static_cast<char*>(a.workspace);
   RowChunk* stats = reinterpret_cast<RowChunk*>(ws + l.stats);
   FinalPart* finals = reinterpret_cast<FinalPart*>(ws + l.finals);
   uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
-  const bool greedy = a.uniforms == nullptr;
+  const int groups = greedy ? 1 : cut.groups;
   // a launch holds at most 2^22 workgroups of 256 threads
-  const int64_t per = static_cast<int64_t>(rows) * rc.chunks > fc.chunks ? static_cast<int64_t>(rows) * rc.chunks
-                                                                           : fc.chunks;
+  const int64_t of_rows = static_cast<int64_t>(rows) * split.chunks, per = of_rows > groups ? of_rows : groups;
   const int64_t step = (int64_t{1} << 22) / per > 0 ? (int64_t{1} << 22) / per : 1;
   for (int64_t i = 0; i < a.N; i += step) {
     const int64_t n = a.N - i < step ? a.N - i : step;
-    const dim3 g1(static_cast<unsigned>(n * rows * rc.chunks)), g2(static_cast<unsigned>(n * (greedy ? 1 : fc.chunks)));
+    const dim3 g1(static_cast<unsigned>(n * of_rows)), g2(static_cast<unsigned>(n * groups));
     if (greedy)
-      hipLaunchKernelGGL((verify_rows_kernel<DT, true>), g1, dim3(kT), 0, stream, a, rc.chunks, rc.blocks, i, stats,
-                         arrived);
+      hipLaunchKernelGGL((verify_rows_kernel<DT, true>), g1, dim3(kT), 0, stream, a, split, i, stats, arrived);
     else
-      hipLaunchKernelGGL((verify_rows_kernel<DT, false>), g1, dim3(kT), 0, stream, a, rc.chunks, rc.blocks, i, stats,
-                         arrived);
+      hipLaunchKernelGGL((verify_rows_kernel<DT, false>), g1, dim3(kT), 0, stream, a, split, i, stats, arrived);
     if (const hipError_t e = hipGetLastError()) return e;
-    hipLaunchKernelGGL((verify_final_kernel<DT>), g2, dim3(kT), 0, stream, a, rc.chunks, greedy ? 1 : fc.chunks,
-                       fc.blocks, i, stats, finals, arrived);
+    hipLaunchKernelGGL((verify_final_kernel<DT>), g2, dim3(kT), 0, stream, a, split.chunks, groups, cut.pieces, i, stats,
+                       finals, arrived);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
@@ -742,14 +1067,13 @@ hipError_t launch_typed(const VerifyArgs& a, hipStream_t stream) {
 }  // namespace
 
 int64_t verify_workspace(int dtype, int64_t N, int D, int V, bool draft_logits) {
-  (void)dtype;
-  return layout_of(N, D, V, draft_logits).bytes;
+  return layout_of(dtype, N, D, V, draft_logits).bytes;
 }
 
 hipError_t launch_verify(int dtype, const VerifyArgs& a, hipStream_t stream) {
-  if (dtype == 0) return launch_typed<F32T>(a, stream);
-  if (dtype == 1) return launch_typed<F16T>(a, stream);
-  return launch_typed<BF16T>(a, stream);
+  if (dtype == 0) return launch_typed<F32T>(dtype, a, stream);
+  if (dtype == 1) return launch_typed<F16T>(dtype, a, stream);
+  return launch_typed<BF16T>(dtype, a, stream);
 }
 
 }  // namespace tkp
