@@ -171,6 +171,79 @@ def test_chain_is_a_tree_of_single_branches(dtype):
         assert torch.equal(b[2].long(), want)
 
 
+# More logits than are worth reading whole: the path is followed row by row.
+LARGE = [
+    # N, D, V, mode, branch, pad
+    (1200, 3, 4001, "draft", 0, 0), (150, 10, 20003, "draft", 0, 5), (3, 8, 1000003, "draft", 0, 0),
+    (2500, 2, 5000, "lookup", 0, 3), (40, 30, 30000, "lookup", 0, 0), (500, 39, 3001, "lookup", 3, 0),
+    (90, 255, 1500, "lookup", 4, 1), (2, 60, 400000, "lookup", 5, 0), (2000, 5, 3000, "greedy", 0, 0),
+    (600, 39, 1501, "greedy", 3, 2), (1, 255, 260000, "lookup", 255, 0), (20000, 1, 800, "draft", 0, 0),
+]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("case", LARGE, ids=[str(c) for c in LARGE])
+def test_large(case, dtype):
+    torch = need_gpu()
+    N, D, V, mode, branch, pad = case
+    say("large", case, dtype)
+    t = getattr(torch, dtype)
+    assert N * (D + 1) * V * t.itemsize >= 2 ** 25
+    g = torch.Generator(device="cuda").manual_seed(N + D)
+    rng = np.random.default_rng(N + D)
+    x = torch.empty(N * (D + 1), V + pad, dtype=t, device="cuda")
+    x.normal_(generator=g).mul_(3)
+    x = x[:, :V]
+    y = None
+    if mode == "draft":
+        y = (x.view(N, D + 1, V)[:, :D].float() + 0.4 * torch.randn(N, D, V, device="cuda", generator=g)).to(t)
+        y = y.view(N * D, V)
+    # drafts that stand more often than not
+    width = max(1, branch)
+    best = torch.topk(x.float(), min(width, V), dim=1).indices.view(N, D + 1, -1)
+    node = torch.arange(D, device="cuda") // width if branch else torch.arange(D, device="cuda")
+    drafts = best[:, node, torch.arange(D, device="cuda") % best.shape[2]]
+    drafts = torch.where(torch.rand(N, D, device="cuda", generator=g) < 0.2, 7 % V, drafts).to(torch.int32).cpu().numpy()
+    parents = np.broadcast_to(node.cpu().numpy() - 1, (N, D)).copy() if branch else None
+    lengths = rng.integers(-1, D + 2, N) if N > 3 else None
+    u = None if mode == "greedy" else rng.random((N, D + 1)) * rng.choice([1.0, 0.05, 0.01], (N, D + 1))
+    at = np.unique(np.concatenate([np.arange(min(N, 40)), rng.integers(0, N, 60), np.arange(max(0, N - 20), N)]))
+    import top_logits_filtering_amd as tk
+
+    i32 = lambda a: None if a is None else torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()
+    gu = None if u is None else torch.from_numpy(np.float32(u)).cuda()
+    for turn in range(2):
+        if turn == 1 and N > 1:  # rows that hold nothing, or too much
+            x.view(N, D + 1, V)[0, 0] = -float("inf")
+            x.view(N, D + 1, V)[N - 1, min(1, D), V // 2] = float("nan")
+            if y is not None:
+                y.view(N, D, V)[N // 2, 0, V - 1] = float("inf")
+        tokens, accepted, path = tk.speculative_verify(x, i32(drafts), gu, draft_logits=y, parents=i32(parents),
+                                                       lengths=i32(lengths))
+        torch.cuda.synchronize()
+        assert int(accepted.min()) >= 0 and int(accepted.max()) <= D
+        sel = torch.from_numpy(at).cuda()
+        pick = lambda m: None if m is None else m[at]
+        rt, ra, rp, margin = spec_ref.verify(
+            Rows(x.view(N, D + 1, V), sel), drafts[at], None if u is None else np.float32(u)[at],
+            None if y is None else Rows(y.view(N, D, V), sel), pick(parents), pick(lengths))
+        sure = margin > BORDER
+        assert (accepted.cpu().numpy()[at][sure] == ra[sure]).all(), turn
+        assert (tokens.cpu().numpy()[at][sure] == rt[sure]).all(), turn
+        if parents is not None:
+            assert (path.cpu().numpy()[at][sure] == rp[sure]).all(), turn
+
+
+class Rows:
+    """Some sequences' rows, fetched one at a time."""
+
+    def __init__(self, t, at):
+        self.t, self.at, self.shape = t, at, (len(at),) + tuple(t.shape[1:])
+
+    def __getitem__(self, key):
+        return self.t[self.at[key[0]], key[1]].double().cpu().numpy()
+
+
 def odd_rows(kind, V, rng):
     x = head(rng, (V,), spikes=4)
     if kind == "filtered":

@@ -53,6 +53,7 @@ struct RowChunk {
   float ref;
   int bad;
 };
+static_assert(sizeof(RowChunk) == 16);
 
 // Sums over a chunk of the row where the path ends.
 struct FinalPart {
@@ -193,8 +194,10 @@ __device__ __forceinline__ RowSum row_sum(const RowChunk* __restrict__ s, int ch
   if (__ballot(moved) != 0) {  // some chunk of the wave's rows has a reference of its own
     top = static_cast<float>(over_lanes<LANES>(static_cast<double>(top), [](double a, double b) { return fmax(a, b); }));
     sum = 0.0;
-    for (int c = lane; c < chunks; c += LANES)
-      if (s[c].sum > 0.0) sum += s[c].sum * exp_from(s[c].ref, top);
+    for (int c = lane; c < chunks; c += LANES) {
+      const RowChunk t = s[c];
+      if (t.sum > 0.0) sum += t.sum * exp_from(t.ref, top);
+    }
   } else {
     top = 0.0f;
   }
@@ -207,7 +210,8 @@ template <int LANES>
 __device__ __forceinline__ uint64_t row_best(const RowChunk* __restrict__ s, int chunks) {
   uint64_t best = 0;
   for (int c = threadIdx.x % LANES; c < chunks; c += LANES) {
-    const uint64_t one = s[c].bad != 0 ? ~0ull : s[c].best;
+    const RowChunk t = s[c];
+    const uint64_t one = t.bad != 0 ? ~0ull : t.best;
     best = best > one ? best : one;
   }
   best = over_lanes<LANES>(best, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
@@ -238,25 +242,35 @@ __device__ __forceinline__ int draft_count(const VerifyArgs& a, int64_t seq) {
   return n < 0 ? 0 : (n < a.D ? n : a.D);
 }
 
-// sum exp(x - ref) of a whole row in 64 bits, by the workgroup.
+// sum exp(x - ref) of a whole row in 64 bits, by the workgroup. Rarely taken, so
+// the elements of a block go through one exp in turn.
 template <class DT>
-__device__ double sum_again(const typename DT::raw_t* row, int V, float ref, WalkSmem& sm) {
+__device__ __forceinline__ double sum_again(const typename DT::raw_t* row, int V, float ref, double (&at)[kW]) {
   double sum = 0.0;
+#pragma unroll 1
   for (int v = threadIdx.x * kBlock; v < V; v += kT * kBlock) {
     float x[kBlock];
     load_block<DT>(row, v, V, x);
+#pragma unroll 1
+    for (int j = 0; j < kBlock; ++j) {
+      sum += exp_from(x[0], ref);
 #pragma unroll
-    for (int j = 0; j < kBlock; ++j) sum += exp_from(x[j], ref);
+      for (int k = 0; k + 1 < kBlock; ++k) x[k] = x[k + 1];
+    }
   }
   sum = wave_sum_f64(sum);
   __syncthreads();
-  if (threadIdx.x % kWave == 0) sm.part[threadIdx.x / kWave] = sum;
+  if (threadIdx.x % kWave == 0) at[threadIdx.x / kWave] = sum;
   __syncthreads();
   sum = 0.0;
 #pragma unroll
-  for (int w = 0; w < kW; ++w) sum += sm.part[w];
+  for (int w = 0; w < kW; ++w) sum += at[w];
   return sum;
 }
+
+// What the drafts are, as kernels of their own: the code of one that does
+// everything is 43 KB, which every compute unit has to fetch.
+enum Mode : int { kGreedy = 0, kProposed = 1, kDrawn = 2 };
 
 // Where the path of a sequence ends.
 enum Kind : int { kNone = 0, kPlain = 1, kWithout = 2, kResidual = 3 };
@@ -274,24 +288,87 @@ constexpr double kClose = 1e-6;
 // Elements whose terms of p and q, by the ratio of such sums, differ by no more.
 constexpr double kBand = 4e-7;
 
+// Draft j's token and the row that it follows; -1: it counts as not there.
+__device__ __forceinline__ void draft_of(const VerifyArgs& a, int64_t seq, int j, int n, int& token, int& node) {
+  token = -1;
+  node = 0;
+  if (j >= n) return;
+  token = a.drafts[seq * a.D + j];
+  const int parent = a.parents == nullptr ? j - 1 : a.parents[seq * a.D + j];
+  if (token < 0 || token >= a.V || parent < -1 || parent >= j) token = -1;
+  node = parent + 1;
+}
+
+// Acceptance of a draft that was drawn, or of a chain's proposal (then with 1 for
+// q and its sum): u q < p, with both sums on the other side.
+__device__ __forceinline__ bool stands(double u, double pe, double qe, double psum, double qsum, bool& close) {
+  const double left = u * qe * psum, right = pe * qsum;
+  close = right > 0.0 && left > right * (1.0 - kClose) && left < right * (1.0 + kClose);
+  return left < right;
+}
+
+// The draft that follows w.node, -1 for none, out of w.p or w.best; sets w.kind.
+// Every wave holds all drafts, kSets a lane; their terms are in sm.term.
+constexpr int kSets = kMaxRows / kWave;
+template <class DT, Mode MODE>
+__device__ __forceinline__ int next_of(const VerifyArgs& a, int64_t seq, const int (&tokens)[kSets],
+                                       const int (&nodes)[kSets], Walk& w, WalkSmem& sm) {
+  uint64_t kids[kSets];  // bits of the draft numbers
+#pragma unroll
+  for (int i = 0; i < kSets; ++i) kids[i] = __ballot(tokens[i] >= 0 && nodes[i] == w.node);
+  int taken = -1;
+  if constexpr (MODE == kGreedy) {
+    const int top = best_token(w.best);
+#pragma unroll
+    for (int i = kSets - 1; i >= 0; --i) {
+      const uint64_t hit = __ballot(tokens[i] == top) & kids[i];
+      if (hit != 0 && top >= 0) taken = i * kWave + __builtin_ctzll(hit);
+    }
+    return taken;
+  }
+  w.kind = w.p.sum > 0.0 ? kPlain : kNone;
+  if (w.kind == kNone) return -1;
+  const double u = sm.u[w.node];
+  for (int turn = 0; turn < 2; ++turn) {
+    const double at = u * w.p.sum;
+    double upto = 0.0;
+    bool close = false, any = false;
+    taken = -1;
+#pragma unroll
+    for (int i = 0; i < kSets; ++i)
+      for (uint64_t m = kids[i]; m != 0; m &= m - 1) {
+        const int bit = __builtin_ctzll(m), j = i * kWave + bit;
+        // a token that an earlier one of them has counts once
+        const int same = __builtin_amdgcn_readlane(tokens[i], bit);
+        uint64_t before = __ballot(tokens[i] == same) & kids[i] & ((1ull << bit) - 1);
+#pragma unroll
+        for (int k = 0; k < i; ++k) before |= __ballot(tokens[k] == same) & kids[k];
+        if (before != 0) continue;
+        any = true;
+        upto += sm.term[j];
+        close |= upto > at * (1.0 - kClose) && upto < at * (1.0 + kClose);
+        if (at < upto && taken < 0) taken = j;
+      }
+    w.kind = taken < 0 && any ? kWithout : kPlain;
+    if (!close || turn == 1) break;
+    w.p.sum = sum_again<DT>(target_row<DT>(a, seq, w.node), a.V, w.p.ref, sm.part);
+  }
+  return taken;
+}
+
 // Goes down a sequence's path. All threads of the workgroup take part and get the
 // same result.
-template <class DT>
-__device__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int64_t seq, WalkSmem& sm) {
-  constexpr int kSets = kMaxRows / kWave;
+template <class DT, Mode MODE>
+__device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int64_t seq, WalkSmem& sm) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int D = a.D, n = draft_count(a, seq);
-  const bool greedy = a.uniforms == nullptr, chain = a.parents == nullptr, drawn = a.draft_logits != nullptr;
-  int token = -1, node = 0;
+  constexpr bool greedy = MODE == kGreedy, drawn = MODE == kDrawn;
+  const bool chain = drawn || a.parents == nullptr;
+  int token, node;
+  draft_of(a, seq, tid, n, token, node);
   float x = -INFINITY, y = -INFINITY;
-  if (tid < n) {
-    token = a.drafts[seq * D + tid];
-    const int parent = chain ? tid - 1 : a.parents[seq * D + tid];
-    if (token < 0 || token >= a.V || parent < -1 || parent >= tid) token = -1;
-    node = parent + 1;
-    if (token >= 0 && !greedy) x = DT::value(target_row<DT>(a, seq, node)[token]);
-    if (token >= 0 && drawn) y = DT::value(draft_row<DT>(a, seq, tid)[token]);
-  }
+  if (token >= 0 && !greedy) x = DT::value(target_row<DT>(a, seq, node)[token]);
+  if (token >= 0 && drawn) y = DT::value(draft_row<DT>(a, seq, tid)[token]);
   sm.token[tid] = token;
   sm.node[tid] = node;
   sm.u[tid] = !greedy && tid <= D ? a.uniforms[seq * (D + 1) + tid] : 0.0f;
@@ -301,7 +378,7 @@ __device__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int
     const int r = i < rows ? i : 0;
     const bool target = r <= n;
     const RowChunk* s = target ? target_stats(a, stats, chunks, seq, r) : draft_stats(a, stats, chunks, seq, r - n - 1);
-    if (greedy) {
+    if constexpr (greedy) {
       const uint64_t best = row_best<16>(s, chunks);
       if (tid % 16 == 0) sm.best[r] = best;
     } else {
@@ -314,14 +391,7 @@ __device__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int
   }
   __syncthreads();
 
-  // Acceptance of a chain's draft, behind accepted ones: u q < p, with both sums on
-  // the other side.
   Walk w{0, 0, kNone, {0.0, 0.0f}, {0.0, 0.0f}, 0ull};
-  auto stands = [&](double u, double pe, double qe, double psum, double qsum, bool& close) -> bool {
-    const double left = u * qe * psum, right = pe * qsum;
-    close = right > 0.0 && left > right * (1.0 - kClose) && left < right * (1.0 + kClose);
-    return left < right;
-  };
   double pe = 0.0, qe = 1.0;
   if (!greedy && token >= 0) pe = exp_from(x, sm.ref[0][node]);
   if (drawn) qe = token >= 0 && sm.sum[1][tid] > 0.0 ? exp_from(y, sm.ref[1][tid]) : 0.0;
@@ -361,9 +431,15 @@ __device__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int
       w.node = w.node < D ? w.node : D;
       if (!again) break;
       const int j = w.node;
-      const double psum = sum_again<DT>(target_row<DT>(a, seq, j), a.V, sm.ref[0][j], sm);
       const bool q = drawn && sm.sum[1][j] > 0.0;
-      const double qsum = q ? sum_again<DT>(draft_row<DT>(a, seq, j), a.V, sm.ref[1][j], sm) : 1.0;
+      double psum = 0.0, qsum = 1.0;
+#pragma unroll 1
+      for (int i = 0; i < (q ? 2 : 1); ++i) {
+        const double sum = sum_again<DT>(i == 0 ? target_row<DT>(a, seq, j) : draft_row<DT>(a, seq, j), a.V, sm.ref[i][j],
+                                         sm.part);
+        psum = i == 0 ? sum : psum;
+        qsum = i == 1 ? sum : qsum;
+      }
       __syncthreads();
       if (tid == j) {
         bool same;
@@ -375,7 +451,7 @@ __device__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int
     }
     w.count = w.node;
     sm.path[tid] = tid;
-    if (greedy) {
+    if constexpr (greedy) {
       w.best = sm.best[w.node];
     } else {
       w.p = RowSum{sm.sum[0][w.node], sm.ref[0][w.node]};
@@ -395,7 +471,6 @@ __device__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int
 
   sm.term[tid] = pe;
   __syncthreads();
-  // every wave holds all drafts, kSets a lane
   int tokens[kSets], nodes[kSets];
 #pragma unroll
   for (int i = 0; i < kSets; ++i) {
@@ -403,50 +478,9 @@ __device__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int
     nodes[i] = sm.node[i * kWave + lane];
   }
   for (;;) {
-    // the drafts behind this node: bits of the draft numbers
-    uint64_t kids[kSets];
-#pragma unroll
-    for (int i = 0; i < kSets; ++i) kids[i] = __ballot(tokens[i] >= 0 && nodes[i] == w.node);
-    int taken = -1;
-    if (greedy) {
-      w.best = sm.best[w.node];
-      const int top = best_token(w.best);
-#pragma unroll
-      for (int i = kSets - 1; i >= 0; --i) {
-        const uint64_t hit = __ballot(tokens[i] == top) & kids[i];
-        if (hit != 0 && top >= 0) taken = i * kWave + __builtin_ctzll(hit);
-      }
-    } else {
-      w.p = RowSum{sm.sum[0][w.node], sm.ref[0][w.node]};
-      w.kind = w.p.sum > 0.0 ? kPlain : kNone;
-      if (w.kind == kNone) break;
-      const double u = sm.u[w.node];
-      for (int turn = 0; turn < 2; ++turn) {
-        const double at = u * w.p.sum;
-        double upto = 0.0;
-        bool close = false, any = false;
-        taken = -1;
-#pragma unroll
-        for (int i = 0; i < kSets; ++i)
-          for (uint64_t m = kids[i]; m != 0; m &= m - 1) {
-            const int bit = __builtin_ctzll(m), j = i * kWave + bit;
-            // a token that an earlier one of them has counts once
-            const int same = __builtin_amdgcn_readlane(tokens[i], bit);
-            uint64_t before = __ballot(tokens[i] == same) & kids[i] & ((1ull << bit) - 1);
-#pragma unroll
-            for (int k = 0; k < i; ++k) before |= __ballot(tokens[k] == same) & kids[k];
-            if (before != 0) continue;
-            any = true;
-            upto += sm.term[j];
-            close |= upto > at * (1.0 - kClose) && upto < at * (1.0 + kClose);
-            if (at < upto && taken < 0) taken = j;
-          }
-        if (taken < 0 && any) w.kind = kWithout;
-        if (!close || turn == 1) break;
-        w.kind = kPlain;
-        w.p.sum = sum_again<DT>(target_row<DT>(a, seq, w.node), a.V, w.p.ref, sm);
-      }
-    }
+    if constexpr (greedy) w.best = sm.best[w.node];
+    else w.p = RowSum{sm.sum[0][w.node], sm.ref[0][w.node]};
+    const int taken = next_of<DT, MODE>(a, seq, tokens, nodes, w, sm);
     if (taken < 0) break;
     if (tid == 0) sm.path[w.count] = taken;
     ++w.count;
@@ -470,7 +504,7 @@ struct Split {
   int chunks, vecs;
 };
 template <class DT, bool GREEDY>
-__device__ RowChunk chunk_of(const typename DT::raw_t* row, int V, int ch, Split split, ChunkSmem& sm) {
+__device__ __forceinline__ RowChunk chunk_of(const typename DT::raw_t* row, int V, int ch, Split split, ChunkSmem& sm) {
   using raw_t = typename DT::raw_t;
   constexpr int P = DT::kPerVec, kGroup = 32 / P;
   constexpr uint32_t kNeg = P == 4 ? static_cast<uint32_t>(DT::kNegInf)
@@ -658,10 +692,13 @@ constexpr float kFar = 50.0f;
 struct Rows {
   float p_least, q_least;
 };
+__device__ __forceinline__ float log_below(double sum) {  // no more than ln 2 below the logarithm
+  return static_cast<float>(static_cast<int>(__builtin_bit_cast(uint64_t, sum) >> 52) - 1023) * kLn2;
+}
 __device__ __forceinline__ Rows least_of(const Walk& w) {
   Rows r;
-  r.p_least = w.p.ref + static_cast<float>(log(w.p.sum)) - kFar;
-  r.q_least = w.kind == kResidual ? w.q.ref + static_cast<float>(log(w.q.sum)) - kFar : INFINITY;
+  r.p_least = w.p.ref + log_below(w.p.sum) - kFar;
+  r.q_least = w.kind == kResidual ? w.q.ref + log_below(w.q.sum) - kFar : INFINITY;
   return r;
 }
 __device__ __forceinline__ float largest(const float (&x)[kBlock]) {
@@ -753,13 +790,13 @@ __device__ __forceinline__ double if_or_none(bool is, double v) {
 }
 
 // Sums over a wave's part of the row, of every lane's elements.
-template <class DT>
+template <class DT, Mode MODE>
 __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, const typename DT::raw_t* qrow, int first,
                                              int pieces, int V, const Walk& w, const FinalSmem& sm) {
   FinalPart mine{0.0, 0.0, 0.0, 0.0, 0.0};
   const Rows least = least_of(w);
   const int lane = threadIdx.x % kWave;
-  if (w.kind == kResidual) {
+  if (MODE == kDrawn && w.kind == kResidual) {
     // p > q where near * p's term > q's
     const double near = w.q.sum / w.p.sum;
 #pragma unroll 1
@@ -779,7 +816,7 @@ __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, con
       }
     }
   } else {
-    const bool outs = w.kind == kWithout && sm.outs != 0;
+    const bool outs = MODE != kDrawn && w.kind == kWithout && sm.outs != 0;
 #pragma unroll 1
     for (int i = 0; i < pieces; ++i) {
       const int v = first + i * kPiece + lane * kBlock;
@@ -834,11 +871,11 @@ __device__ __forceinline__ int first_or_last(bool is, bool may, FinalSmem& sm) {
 }
 
 // Finds the token out of the parts' sums, by the whole workgroup.
-template <class DT>
-__device__ int token_of(const VerifyArgs& a, const Walk& w, const FinalPart* slots, int parts, int pieces,
+template <class DT, Mode MODE>
+__device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, const FinalPart* slots, int parts, int pieces,
                         const typename DT::raw_t* prow, const typename DT::raw_t* qrow, FinalSmem& sm) {
   const int tid = threadIdx.x, span = pieces * kPiece;
-  const bool two = w.kind == kResidual;
+  const bool two = MODE == kDrawn && w.kind == kResidual;
   const Rows least = least_of(w);
   FinalPart p[2];
 #pragma unroll
@@ -860,7 +897,7 @@ __device__ int token_of(const VerifyArgs& a, const Walk& w, const FinalPart* slo
     total[2] += p[i].close;
   }
   block_sums(total, sm.sum);
-  Weights weights{two ? total[1] / total[0] : 1.0, two, w.kind == kWithout};
+  Weights weights{two ? total[1] / total[0] : 1.0, two, MODE != kDrawn && w.kind == kWithout};
   const double near = two ? w.q.sum / w.p.sum : 1.0, off = weights.scale - near;
   double part[2];
 #pragma unroll
@@ -875,12 +912,21 @@ __device__ int token_of(const VerifyArgs& a, const Walk& w, const FinalPart* slo
     for (int c0 = 0; c0 < parts; c0 += kW) {
       const int c = c0 + tid / kWave;
       double sum = 0.0;
+#pragma unroll 1
       for (int i = 0; i < pieces; ++i) {
         const int v = c * span + i * kPiece + tid % kWave * kBlock;
-        Terms t;
-        if (!terms_at<DT>(prow, qrow, v, a.V, w, least, true, t)) continue;
+        float x[kBlock], y[kBlock];
+        load_block<DT>(prow, v, a.V, x);
+        load_block<DT>(qrow, v, a.V, y);
+#pragma unroll 1
+        for (int j = 0; j < kBlock; ++j) {  // one after the other: rarely taken
+          sum += __builtin_fmax(__builtin_fma(weights.scale, exp_from(x[0], w.p.ref), -exp_from(y[0], w.q.ref)), 0.0);
 #pragma unroll
-        for (int j = 0; j < kBlock; ++j) sum += weights.of(t, j, v + j, sm);
+          for (int k = 0; k + 1 < kBlock; ++k) {
+            x[k] = x[k + 1];
+            y[k] = y[k + 1];
+          }
+        }
       }
       sum = wave_sum_f64(sum);
       if (c < parts && tid % kWave == 0) sm.parts[c] = sum;
@@ -909,7 +955,7 @@ __device__ int token_of(const VerifyArgs& a, const Walk& w, const FinalPart* slo
   __syncthreads();
   const int c = sm.found;
   const double base = sm.below;
-  list_out(a, w, c * span, (c + 1) * span, sm);
+  if constexpr (MODE == kProposed) list_out(a, w, c * span, (c + 1) * span, sm);
   // at most kMaxPieces * 512 elements: eight for each thread
   static_assert(kMaxPieces * kPiece <= kT * kBlock);
   const int v = tid * kBlock < span ? c * span + tid * kBlock : a.V;
@@ -941,19 +987,52 @@ __device__ int token_of(const VerifyArgs& a, const Walk& w, const FinalPart* slo
   return sm.found;
 }
 
-template <class DT>
+// A group's parts of the row where the path ends, one of each wave. Then the last
+// of a sequence's `groups` workgroups finds the token; -2 for the others.
+template <class DT, Mode MODE>
+__device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w, int64_t seq, int group, int groups, int pieces,
+                              FinalPart* slots, uint32_t* arrived, FinalSmem& sm) {
+  using raw_t = typename DT::raw_t;
+  const int tid = threadIdx.x;
+  const raw_t* prow = target_row<DT>(a, seq, w.node);
+  const bool two = MODE == kDrawn && w.kind == kResidual;
+  const raw_t* qrow = two ? draft_row<DT>(a, seq, w.node) : prow;
+  const int span = pieces * kPiece, parts = groups * kW;
+  if constexpr (MODE == kProposed) list_out(a, w, group * kW * span, (group + 1) * kW * span, sm);
+  const int c = group * kW + tid / kWave;
+  FinalPart mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm);
+  mine.all = wave_sum_f64(mine.all);
+  mine.left = wave_sum_f64(mine.left);
+  if (two) {
+    mine.kept = wave_sum_f64(mine.kept);
+    mine.draft = wave_sum_f64(mine.draft);
+    if (__ballot(mine.close != 0.0) != 0) mine.close = wave_sum_f64(mine.close);
+  }
+  if (tid % kWave == 0) {
+    put_far(&slots[c].all, mine.all);
+    put_far(&slots[c].left, mine.left);
+    if (two) {
+      put_far(&slots[c].kept, mine.kept);
+      put_far(&slots[c].draft, mine.draft);
+      put_far(&slots[c].close, mine.close);
+    }
+  }
+  if (!last_of(arrived, groups, sm.last)) return -2;
+  return token_of<DT, MODE>(a, w, slots, parts, pieces, prow, qrow, sm);
+}
+
+template <class DT, Mode MODE>
 __global__ __launch_bounds__(kT) void verify_final_kernel(VerifyArgs a, int chunks, int groups, int pieces, int64_t seq0,
                                                           const RowChunk* __restrict__ stats,
                                                           FinalPart* __restrict__ finals,
                                                           uint32_t* __restrict__ arrived) {
-  using raw_t = typename DT::raw_t;
   __shared__ FinalSmem sm;
   const int tid = threadIdx.x;
   const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(groups));
   const int64_t seq = seq0 + blockIdx.x / static_cast<unsigned>(groups);
-  const Walk w = walk<DT>(a, stats, chunks, seq, sm.walk);
+  const Walk w = walk<DT, MODE>(a, stats, chunks, seq, sm.walk);
   int32_t* tokens = a.out_tokens + seq * (a.D + 1);
-  const bool greedy = a.uniforms == nullptr;
+  constexpr bool greedy = MODE == kGreedy;
   const bool draws = !greedy && w.kind != kNone;
   if (group == 0) {
     if (tid <= a.D && !(tid == w.count && draws))
@@ -962,34 +1041,12 @@ __global__ __launch_bounds__(kT) void verify_final_kernel(VerifyArgs a, int chun
     if (a.out_path != nullptr && tid < a.D) a.out_path[seq * a.D + tid] = tid < w.count ? sm.walk.path[tid] : -1;
     if (tid == 0) a.out_accepted[seq] = w.count;
   }
-  if (!draws) return;
-
-  const raw_t* prow = target_row<DT>(a, seq, w.node);
-  const raw_t* qrow = w.kind == kResidual ? draft_row<DT>(a, seq, w.node) : prow;
-  const int span = pieces * kPiece, parts = groups * kW;
-  list_out(a, w, group * kW * span, (group + 1) * kW * span, sm);
-  const int c = group * kW + tid / kWave;
-  FinalPart mine = part_of<DT>(prow, qrow, c * span, pieces, a.V, w, sm);
-  mine.all = wave_sum_f64(mine.all);
-  mine.left = wave_sum_f64(mine.left);
-  FinalPart* slots = finals + seq * parts;
-  if (w.kind == kResidual) {
-    mine.kept = wave_sum_f64(mine.kept);
-    mine.draft = wave_sum_f64(mine.draft);
-    if (__ballot(mine.close != 0.0) != 0) mine.close = wave_sum_f64(mine.close);
+  if constexpr (!greedy) {
+    if (!draws) return;
+    const int token = token_by_parts<DT, MODE>(a, w, seq, group, groups, pieces, finals + seq * groups * kW, &arrived[seq],
+                                               sm);
+    if (tid == 0 && token >= -1) tokens[w.count] = token;
   }
-  if (tid % kWave == 0) {
-    put_far(&slots[c].all, mine.all);
-    put_far(&slots[c].left, mine.left);
-    if (w.kind == kResidual) {
-      put_far(&slots[c].kept, mine.kept);
-      put_far(&slots[c].draft, mine.draft);
-      put_far(&slots[c].close, mine.close);
-    }
-  }
-  if (!last_of(&arrived[seq], groups, sm.last)) return;
-  const int token = token_of<DT>(a, w, slots, parts, pieces, prow, qrow, sm);
-  if (tid == 0) tokens[w.count] = token;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -1052,13 +1109,21 @@ hipError_t launch_typed(int dtype, const VerifyArgs& a, hipStream_t stream) {
   for (int64_t i = 0; i < a.N; i += step) {
     const int64_t n = a.N - i < step ? a.N - i : step;
     const dim3 g1(static_cast<unsigned>(n * of_rows)), g2(static_cast<unsigned>(n * groups));
-    if (greedy)
+    if (greedy) {
       hipLaunchKernelGGL((verify_rows_kernel<DT, true>), g1, dim3(kT), 0, stream, a, split, i, stats, arrived);
-    else
+      if (const hipError_t e = hipGetLastError()) return e;
+      hipLaunchKernelGGL((verify_final_kernel<DT, kGreedy>), g2, dim3(kT), 0, stream, a, split.chunks, groups, cut.pieces,
+                         i, stats, finals, arrived);
+    } else {
       hipLaunchKernelGGL((verify_rows_kernel<DT, false>), g1, dim3(kT), 0, stream, a, split, i, stats, arrived);
-    if (const hipError_t e = hipGetLastError()) return e;
-    hipLaunchKernelGGL((verify_final_kernel<DT>), g2, dim3(kT), 0, stream, a, split.chunks, groups, cut.pieces, i, stats,
-                       finals, arrived);
+      if (const hipError_t e = hipGetLastError()) return e;
+      if (draft)
+        hipLaunchKernelGGL((verify_final_kernel<DT, kDrawn>), g2, dim3(kT), 0, stream, a, split.chunks, groups, cut.pieces,
+                           i, stats, finals, arrived);
+      else
+        hipLaunchKernelGGL((verify_final_kernel<DT, kProposed>), g2, dim3(kT), 0, stream, a, split.chunks, groups,
+                           cut.pieces, i, stats, finals, arrived);
+    }
     if (const hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
