@@ -137,22 +137,6 @@ __device__ __forceinline__ bool last_of(uint32_t* arrived, int count, int& told)
   return told != 0;
 }
 
-struct WalkSmem {
-  int32_t token[kMaxRows];   // -1: the draft counts as not there
-  int32_t node[kMaxRows];    // the row that it follows
-  float u[kMaxRows];
-  double term[kMaxRows];     // its term in that row
-  union {
-    double sum[2][kMaxRows];  // of the rows: target, draft
-    uint64_t best[kMaxRows];
-  };
-  float ref[2][kMaxRows];
-  int32_t path[kMaxRows];
-  uint64_t ends[kMaxRows / kWave];   // drafts of a chain that are not accepted
-  uint64_t close[kMaxRows / kWave];  // or too close to tell
-  double part[kW];
-};
-
 // A row's sum out of its chunks, held by LANES neighbouring lanes (16 or a wave),
 // which all get it. sum = 0: no distribution.
 struct RowSum {
@@ -282,6 +266,25 @@ struct Walk {
   uint64_t best;
 };
 
+
+struct WalkSmem {
+  int32_t token[kMaxRows];   // -1: the draft counts as not there
+  int32_t node[kMaxRows];    // the row that it follows
+  float u[kMaxRows];
+  double term[kMaxRows];     // its term in that row
+  union {
+    double sum[2][kMaxRows];  // of the rows: target, draft
+    uint64_t best[kMaxRows];
+  };
+  float ref[2][kMaxRows];
+  int32_t path[kMaxRows];
+  uint64_t ends[kMaxRows / kWave];   // drafts of a chain that are rejected, are not there or cannot be told
+  uint64_t close[kMaxRows / kWave];  // those that cannot be told
+  double part[kW];
+  Walk state;
+  int again;
+  float last_u;  // the one that the token is drawn with
+};
 // Relative error of a row's sum out of its chunks, and what decisions closer than
 // that take: both sums again in 64 bits.
 constexpr double kClose = 1e-6;
@@ -299,79 +302,27 @@ __device__ __forceinline__ void draft_of(const VerifyArgs& a, int64_t seq, int j
   node = parent + 1;
 }
 
-// Acceptance of a draft that was drawn, or of a chain's proposal (then with 1 for
-// q and its sum): u q < p, with both sums on the other side.
-__device__ __forceinline__ bool stands(double u, double pe, double qe, double psum, double qsum, bool& close) {
-  const double left = u * qe * psum, right = pe * qsum;
-  close = right > 0.0 && left > right * (1.0 - kClose) && left < right * (1.0 + kClose);
-  return left < right;
-}
-
-// The draft that follows w.node, -1 for none, out of w.p or w.best; sets w.kind.
-// Every wave holds all drafts, kSets a lane; their terms are in sm.term.
-constexpr int kSets = kMaxRows / kWave;
-template <class DT, Mode MODE>
-__device__ __forceinline__ int next_of(const VerifyArgs& a, int64_t seq, const int (&tokens)[kSets],
-                                       const int (&nodes)[kSets], Walk& w, WalkSmem& sm) {
-  uint64_t kids[kSets];  // bits of the draft numbers
-#pragma unroll
-  for (int i = 0; i < kSets; ++i) kids[i] = __ballot(tokens[i] >= 0 && nodes[i] == w.node);
-  int taken = -1;
-  if constexpr (MODE == kGreedy) {
-    const int top = best_token(w.best);
-#pragma unroll
-    for (int i = kSets - 1; i >= 0; --i) {
-      const uint64_t hit = __ballot(tokens[i] == top) & kids[i];
-      if (hit != 0 && top >= 0) taken = i * kWave + __builtin_ctzll(hit);
-    }
-    return taken;
-  }
-  w.kind = w.p.sum > 0.0 ? kPlain : kNone;
-  if (w.kind == kNone) return -1;
-  const double u = sm.u[w.node];
-  for (int turn = 0; turn < 2; ++turn) {
-    const double at = u * w.p.sum;
-    double upto = 0.0;
-    bool close = false, any = false;
-    taken = -1;
-#pragma unroll
-    for (int i = 0; i < kSets; ++i)
-      for (uint64_t m = kids[i]; m != 0; m &= m - 1) {
-        const int bit = __builtin_ctzll(m), j = i * kWave + bit;
-        // a token that an earlier one of them has counts once
-        const int same = __builtin_amdgcn_readlane(tokens[i], bit);
-        uint64_t before = __ballot(tokens[i] == same) & kids[i] & ((1ull << bit) - 1);
-#pragma unroll
-        for (int k = 0; k < i; ++k) before |= __ballot(tokens[k] == same) & kids[k];
-        if (before != 0) continue;
-        any = true;
-        upto += sm.term[j];
-        close |= upto > at * (1.0 - kClose) && upto < at * (1.0 + kClose);
-        if (at < upto && taken < 0) taken = j;
-      }
-    w.kind = taken < 0 && any ? kWithout : kPlain;
-    if (!close || turn == 1) break;
-    w.p.sum = sum_again<DT>(target_row<DT>(a, seq, w.node), a.V, w.p.ref, sm.part);
-  }
-  return taken;
-}
-
 // Goes down a sequence's path. All threads of the workgroup take part and get the
-// same result.
+// same result; what is one thing after the other is left to the first wave.
+constexpr int kSets = kMaxRows / kWave;
 template <class DT, Mode MODE>
 __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int64_t seq, WalkSmem& sm) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int D = a.D, n = draft_count(a, seq);
   constexpr bool greedy = MODE == kGreedy, drawn = MODE == kDrawn;
   const bool chain = drawn || a.parents == nullptr;
-  int token, node;
-  draft_of(a, seq, tid, n, token, node);
+  const bool mine = wave * kWave <= n;  // waves that have drafts or rows to look at
+  int token = -1, node = 0;
   float x = -INFINITY, y = -INFINITY;
-  if (token >= 0 && !greedy) x = DT::value(target_row<DT>(a, seq, node)[token]);
-  if (token >= 0 && drawn) y = DT::value(draft_row<DT>(a, seq, tid)[token]);
+  if (mine) {
+    draft_of(a, seq, tid, n, token, node);
+    if (token >= 0 && !greedy) x = DT::value(target_row<DT>(a, seq, node)[token]);
+    if (token >= 0 && drawn) y = DT::value(draft_row<DT>(a, seq, tid)[token]);
+    sm.u[tid] = !greedy && tid <= n ? a.uniforms[seq * (D + 1) + tid] : 0.0f;
+  }
   sm.token[tid] = token;
   sm.node[tid] = node;
-  sm.u[tid] = !greedy && tid <= D ? a.uniforms[seq * (D + 1) + tid] : 0.0f;
+  if (tid == 0) sm.last_u = greedy ? 0.0f : a.uniforms[seq * (D + 1) + D];
   // 16 lanes a row: target rows, then draft rows
   const int rows = n + 1 + (drawn ? n : 0);
   for (int i = tid / 16; i < (rows + 3) / 4 * 4; i += kT / 16) {
@@ -392,101 +343,172 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
   __syncthreads();
 
   Walk w{0, 0, kNone, {0.0, 0.0f}, {0.0, 0.0f}, 0ull};
-  double pe = 0.0, qe = 1.0;
-  if (!greedy && token >= 0) pe = exp_from(x, sm.ref[0][node]);
-  if (drawn) qe = token >= 0 && sm.sum[1][tid] > 0.0 ? exp_from(y, sm.ref[1][tid]) : 0.0;
   if (chain) {
-    bool close = false, stays = false;
-    if (token >= 0) {
-      if (greedy) {
-        stays = token == best_token(sm.best[tid]);
-      } else if (sm.sum[0][tid] > 0.0) {
-        const double q = drawn && sm.sum[1][tid] > 0.0 ? sm.sum[1][tid] : 1.0;
-        stays = stands(sm.u[tid], pe, qe, sm.sum[0][tid], q, close);
+    // All drafts side by side. One that was drawn, or a proposal (then with 1 for q
+    // and its sum), stands behind accepted ones if u q < p, with both sums on the
+    // other side.
+    bool stays = false, close = false;
+    double pe = 0.0, qe = 1.0;
+    auto stands = [&](double psum, double qsum) -> bool {
+      const double left = sm.u[tid] * qe * psum, right = pe * qsum;
+      close = right > 0.0 && left > right * (1.0 - kClose) && left < right * (1.0 + kClose);
+      return left < right;
+    };
+    if (mine) {
+      if (token >= 0) {
+        if constexpr (greedy) {
+          stays = token == best_token(sm.best[tid]);
+        } else {
+          const double psum = sm.sum[0][tid], qsum = drawn ? sm.sum[1][tid] : 1.0;
+          pe = exp_from(x, sm.ref[0][tid]);
+          if (drawn) qe = qsum > 0.0 ? exp_from(y, sm.ref[1][tid]) : 0.0;
+          if (psum > 0.0) stays = stands(psum, qsum > 0.0 ? qsum : 1.0);
+        }
       }
+      const uint64_t ends = __ballot(!stays || close), closes = __ballot(close);
+      if (lane == 0) {
+        sm.ends[wave] = ends;
+        sm.close[wave] = closes;
+      }
+    } else if (lane == 0) {
+      sm.ends[wave] = ~0ull;
+      sm.close[wave] = 0ull;
     }
-    const uint64_t ends = __ballot(!stays), closes = __ballot(close);
-    if (lane == 0) {
-      sm.ends[wave] = ends;
-      sm.close[wave] = closes;
-    }
+    sm.path[tid] = tid;
     __syncthreads();
+    int at;
     for (;;) {
       // the first draft that is rejected, is not there or cannot be told
-      uint64_t end[kSets], open[kSets];
-#pragma unroll
-      for (int i = 0; i < kSets; ++i) {
-        open[i] = sm.close[i];
-        end[i] = sm.ends[i] | open[i];
-      }
-      w.node = D;
+      at = D;
       bool again = false;
 #pragma unroll
-      for (int i = kSets - 1; i >= 0; --i)
-        if (end[i] != 0) {
-          const int j = __builtin_ctzll(end[i]);
-          w.node = i * kWave + j;
-          again = (open[i] >> j & 1u) != 0;
+      for (int i = kSets - 1; i >= 0; --i) {
+        const uint64_t end = sm.ends[i];
+        if (end != 0) {
+          const int bit = __builtin_ctzll(end);
+          at = i * kWave + bit;
+          again = (sm.close[i] >> bit & 1u) != 0;
         }
-      w.node = w.node < D ? w.node : D;
+      }
+      at = at < D ? at : D;
       if (!again) break;
-      const int j = w.node;
-      const bool q = drawn && sm.sum[1][j] > 0.0;
       double psum = 0.0, qsum = 1.0;
+      const bool q = drawn && sm.sum[1][at] > 0.0;
 #pragma unroll 1
       for (int i = 0; i < (q ? 2 : 1); ++i) {
-        const double sum = sum_again<DT>(i == 0 ? target_row<DT>(a, seq, j) : draft_row<DT>(a, seq, j), a.V, sm.ref[i][j],
-                                         sm.part);
+        const double sum = sum_again<DT>(i == 0 ? target_row<DT>(a, seq, at) : draft_row<DT>(a, seq, at), a.V,
+                                         sm.ref[i][at], sm.part);
         psum = i == 0 ? sum : psum;
         qsum = i == 1 ? sum : qsum;
       }
       __syncthreads();
-      if (tid == j) {
-        bool same;
-        if (stands(sm.u[j], pe, qe, psum, qsum, same)) sm.ends[wave] &= ~(1ull << lane);
-        else sm.ends[wave] |= 1ull << lane;
+      if (tid == at) {
+        if (stands(psum, qsum)) sm.ends[wave] &= ~(1ull << lane);
         sm.close[wave] &= ~(1ull << lane);
       }
       __syncthreads();
     }
-    w.count = w.node;
-    sm.path[tid] = tid;
+    w.node = w.count = at;
     if constexpr (greedy) {
-      w.best = sm.best[w.node];
+      w.best = sm.best[at];
     } else {
-      w.p = RowSum{sm.sum[0][w.node], sm.ref[0][w.node]};
+      w.p = RowSum{sm.sum[0][at], sm.ref[0][at]};
       w.kind = w.p.sum > 0.0 ? kPlain : kNone;
-      if (w.kind == kPlain && w.node < n && sm.token[w.node] >= 0) {  // a draft was rejected
-        if (drawn) {
-          w.q = RowSum{sm.sum[1][w.node], sm.ref[1][w.node]};
+      if (w.kind == kPlain && at < n && sm.token[at] >= 0) {  // a draft was rejected
+        if constexpr (drawn) {
+          w.q = RowSum{sm.sum[1][at], sm.ref[1][at]};
           if (w.q.sum > 0.0) w.kind = kResidual;
         } else {
           w.kind = kWithout;
         }
       }
     }
+  } else if constexpr (!drawn) {
+    // A tree: from node to node, out of the drafts' terms in their rows.
+    if (mine && !greedy) sm.term[tid] = token >= 0 ? exp_from(x, sm.ref[0][node]) : 0.0;
     __syncthreads();
-    return w;
-  }
-
-  sm.term[tid] = pe;
-  __syncthreads();
-  int tokens[kSets], nodes[kSets];
+    bool exact = false;  // the sum of the node's row is in 64 bits
+    for (;;) {
+      if (wave == 0) {
+        if (exact) w.p.sum = sm.state.p.sum;
+        bool again = false;
+        int tokens[kSets], nodes[kSets];
 #pragma unroll
-  for (int i = 0; i < kSets; ++i) {
-    tokens[i] = sm.token[i * kWave + lane];
-    nodes[i] = sm.node[i * kWave + lane];
+        for (int i = 0; i < kSets; ++i) {
+          tokens[i] = sm.token[i * kWave + lane];
+          nodes[i] = sm.node[i * kWave + lane];
+        }
+        for (;;) {
+          uint64_t kids[kSets];  // the drafts behind this node: bits of the draft numbers
+#pragma unroll
+          for (int i = 0; i < kSets; ++i) kids[i] = __ballot(tokens[i] >= 0 && nodes[i] == w.node);
+          int taken = -1;
+          if constexpr (greedy) {
+            w.best = sm.best[w.node];
+            const int top = best_token(w.best);
+#pragma unroll
+            for (int i = kSets - 1; i >= 0; --i) {
+              const uint64_t hit = __ballot(tokens[i] == top) & kids[i];
+              if (hit != 0 && top >= 0) taken = i * kWave + __builtin_ctzll(hit);
+            }
+          } else {
+            if (!exact) w.p = RowSum{sm.sum[0][w.node], sm.ref[0][w.node]};
+            w.kind = w.p.sum > 0.0 ? kPlain : kNone;
+            if (w.kind == kNone) break;
+            const double at = sm.u[w.node] * w.p.sum;
+            double upto = 0.0;
+            bool close = false, any = false;
+#pragma unroll
+            for (int i = 0; i < kSets; ++i)
+              for (uint64_t m = kids[i]; m != 0; m &= m - 1) {
+                const int bit = __builtin_ctzll(m), j = i * kWave + bit;
+                // a token that an earlier one of them has counts once
+                const int same = __builtin_amdgcn_readlane(tokens[i], bit);
+                uint64_t before = __ballot(tokens[i] == same) & kids[i] & ((1ull << bit) - 1);
+#pragma unroll
+                for (int k = 0; k < i; ++k) before |= __ballot(tokens[k] == same) & kids[k];
+                if (before != 0) continue;
+                any = true;
+                upto += sm.term[j];
+                close |= upto > at * (1.0 - kClose) && upto < at * (1.0 + kClose);
+                if (at < upto && taken < 0) taken = j;
+              }
+            if (close && !exact) {
+              again = true;
+              break;
+            }
+            if (taken < 0 && any) w.kind = kWithout;
+          }
+          if (taken < 0) break;
+          if (lane == 0) sm.path[w.count] = taken;
+          ++w.count;
+          w.node = taken + 1;
+          exact = false;
+        }
+        if (lane == 0) {
+          sm.state.node = w.node;
+          sm.state.count = w.count;
+          sm.state.kind = w.kind;
+          sm.state.p.sum = w.p.sum;
+          sm.state.p.ref = w.p.ref;
+          sm.state.best = w.best;
+          sm.again = again ? 1 : 0;
+        }
+      }
+      __syncthreads();
+      if (sm.again == 0) break;
+      const double sum = sum_again<DT>(target_row<DT>(a, seq, sm.state.node), a.V, sm.state.p.ref, sm.part);
+      if (tid == 0) sm.state.p.sum = sum;
+      exact = true;
+      __syncthreads();
+    }
+    w.node = sm.state.node;
+    w.count = sm.state.count;
+    w.kind = sm.state.kind;
+    w.p.sum = sm.state.p.sum;
+    w.p.ref = sm.state.p.ref;
+    w.best = sm.state.best;
   }
-  for (;;) {
-    if constexpr (greedy) w.best = sm.best[w.node];
-    else w.p = RowSum{sm.sum[0][w.node], sm.ref[0][w.node]};
-    const int taken = next_of<DT, MODE>(a, seq, tokens, nodes, w, sm);
-    if (taken < 0) break;
-    if (tid == 0) sm.path[w.count] = taken;
-    ++w.count;
-    w.node = taken + 1;
-  }
-  __syncthreads();
   return w;
 }
 
@@ -942,7 +964,7 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
     for (int i = 0; i < 2; ++i) part[i] = p[i].all;
     block_scan(part[0] + part[1], below, upto, all, sm.sum);
   }
-  const double at = static_cast<double>(sm.walk.u[a.D]) * all;
+  const double at = static_cast<double>(sm.walk.last_u) * all;
   // the part that `at` lies in; for a uniform out of range the first or the last one of any weight
   const int owner = first_or_last(upto > at && upto > below, upto > below, sm);
   if (owner < 0) return -1;
