@@ -29,16 +29,14 @@
 namespace tkp {
 namespace {
 
-constexpr int kT = 256;  // threads of a workgroup
+constexpr int kT = 256;  // threads of a workgroup that sums chunks
 constexpr int kW = kT / kWave;
 constexpr int kMaxRows = 256;  // D + 1 at most
 constexpr int kBlock = 8;      // neighbouring elements of a thread
 constexpr int kPiece = kWave * kBlock;  // of a wave
-// A wave's part of the row where the path ends is up to kMaxPieces pieces, so that
-// a row has no more parts than the workgroup that looks through them holds.
-constexpr int kMaxPieces = 4;
-constexpr int kMaxParts = (1 << 20) / (kPiece * kMaxPieces);
-static_assert(kMaxParts <= 2 * kT);
+// Threads of a workgroup that works on the row where a path ends, which is cut into
+// parts of whole pieces, one for each wave, and no more parts than threads.
+constexpr int kFew = 256, kMany = 1024;
 // A residual of no more mass than this is what roundings of the logits leave; the
 // token then comes from p itself.
 constexpr double kLeast = 0x1p-40;
@@ -226,25 +224,28 @@ __device__ __forceinline__ int draft_count(const VerifyArgs& a, int64_t seq) {
   return n < 0 ? 0 : (n < a.D ? n : a.D);
 }
 
-// sum exp(x - ref) of a whole row in 64 bits, by the workgroup. Rarely taken, so
-// the elements of a block go through one exp in turn.
+// sum exp(x - ref) of a whole row in 64 bits, by the workgroup's first kT threads, so
+// that every kernel gets the same. Rarely taken, so the elements of a block go
+// through one exp in turn.
 template <class DT>
 __device__ __forceinline__ double sum_again(const typename DT::raw_t* row, int V, float ref, double (&at)[kW]) {
   double sum = 0.0;
+  if (threadIdx.x < kT) {
 #pragma unroll 1
-  for (int v = threadIdx.x * kBlock; v < V; v += kT * kBlock) {
-    float x[kBlock];
-    load_block<DT>(row, v, V, x);
+    for (int v = threadIdx.x * kBlock; v < V; v += kT * kBlock) {
+      float x[kBlock];
+      load_block<DT>(row, v, V, x);
 #pragma unroll 1
-    for (int j = 0; j < kBlock; ++j) {
-      sum += exp_from(x[0], ref);
+      for (int j = 0; j < kBlock; ++j) {
+        sum += exp_from(x[0], ref);
 #pragma unroll
-      for (int k = 0; k + 1 < kBlock; ++k) x[k] = x[k + 1];
+        for (int k = 0; k + 1 < kBlock; ++k) x[k] = x[k + 1];
+      }
     }
+    sum = wave_sum_f64(sum);
   }
-  sum = wave_sum_f64(sum);
   __syncthreads();
-  if (threadIdx.x % kWave == 0) at[threadIdx.x / kWave] = sum;
+  if (threadIdx.x < kT && threadIdx.x % kWave == 0) at[threadIdx.x / kWave] = sum;
   __syncthreads();
   sum = 0.0;
 #pragma unroll
@@ -262,6 +263,7 @@ struct Walk {
   int node;    // row
   int count;   // accepted drafts, in sm.path
   Kind kind;   // what the token is drawn from: nothing, p, p without rejected tokens, max(p - q, 0)
+  bool open;   // it goes on at rows that are not summed yet
   RowSum p, q;
   uint64_t best;
 };
@@ -302,16 +304,17 @@ __device__ __forceinline__ void draft_of(const VerifyArgs& a, int64_t seq, int j
   node = parent + 1;
 }
 
-// Goes down a sequence's path. All threads of the workgroup take part and get the
-// same result; what is one thing after the other is left to the first wave.
+// Goes down a sequence's path, as far as it is within the first `limit` rows (of a
+// tree all rows, or the first one). All threads of the workgroup take part and get
+// the same result; what is one thing after the other is left to the first wave.
 constexpr int kSets = kMaxRows / kWave;
-template <class DT, Mode MODE>
-__device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int64_t seq, WalkSmem& sm) {
+template <class DT, Mode MODE, int THREADS>
+__device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int limit, int64_t seq, WalkSmem& sm) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int D = a.D, n = draft_count(a, seq);
   constexpr bool greedy = MODE == kGreedy, drawn = MODE == kDrawn;
   const bool chain = drawn || a.parents == nullptr;
-  const bool mine = wave * kWave <= n;  // waves that have drafts or rows to look at
+  const bool mine = wave * kWave <= n;  // waves that have drafts to look at: the first kSets at most
   int token = -1, node = 0;
   float x = -INFINITY, y = -INFINITY;
   if (mine) {
@@ -320,29 +323,32 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
     if (token >= 0 && drawn) y = DT::value(draft_row<DT>(a, seq, tid)[token]);
     sm.u[tid] = !greedy && tid <= n ? a.uniforms[seq * (D + 1) + tid] : 0.0f;
   }
-  sm.token[tid] = token;
-  sm.node[tid] = node;
+  if (tid < kMaxRows) {
+    sm.token[tid] = token;
+    sm.node[tid] = node;
+    sm.path[tid] = tid;
+  }
   if (tid == 0) sm.last_u = greedy ? 0.0f : a.uniforms[seq * (D + 1) + D];
   // 16 lanes a row: target rows, then draft rows
-  const int rows = n + 1 + (drawn ? n : 0);
-  for (int i = tid / 16; i < (rows + 3) / 4 * 4; i += kT / 16) {
+  const int targets = n < limit ? n + 1 : limit, rows = targets + (drawn ? (n < limit ? n : limit) : 0);
+  for (int i = tid / 16; i < (rows + 3) / 4 * 4; i += THREADS / 16) {
     const int r = i < rows ? i : 0;
-    const bool target = r <= n;
-    const RowChunk* s = target ? target_stats(a, stats, chunks, seq, r) : draft_stats(a, stats, chunks, seq, r - n - 1);
+    const bool target = r < targets;
+    const RowChunk* s = target ? target_stats(a, stats, chunks, seq, r) : draft_stats(a, stats, chunks, seq, r - targets);
     if constexpr (greedy) {
       const uint64_t best = row_best<16>(s, chunks);
       if (tid % 16 == 0) sm.best[r] = best;
     } else {
       const RowSum t = row_sum<16>(s, chunks);
       if (tid % 16 == 0) {
-        sm.sum[target ? 0 : 1][target ? r : r - n - 1] = t.sum;
-        sm.ref[target ? 0 : 1][target ? r : r - n - 1] = t.ref;
+        sm.sum[target ? 0 : 1][target ? r : r - targets] = t.sum;
+        sm.ref[target ? 0 : 1][target ? r : r - targets] = t.ref;
       }
     }
   }
   __syncthreads();
 
-  Walk w{0, 0, kNone, {0.0, 0.0f}, {0.0, 0.0f}, 0ull};
+  Walk w{0, 0, kNone, false, {0.0, 0.0f}, {0.0, 0.0f}, 0ull};
   if (chain) {
     // All drafts side by side. One that was drawn, or a proposal (then with 1 for q
     // and its sum), stands behind accepted ones if u q < p, with both sums on the
@@ -355,7 +361,7 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
       return left < right;
     };
     if (mine) {
-      if (token >= 0) {
+      if (token >= 0 && tid < limit) {
         if constexpr (greedy) {
           stays = token == best_token(sm.best[tid]);
         } else {
@@ -370,11 +376,10 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
         sm.ends[wave] = ends;
         sm.close[wave] = closes;
       }
-    } else if (lane == 0) {
+    } else if (lane == 0 && wave < kSets) {
       sm.ends[wave] = ~0ull;
       sm.close[wave] = 0ull;
     }
-    sm.path[tid] = tid;
     __syncthreads();
     int at;
     for (;;) {
@@ -409,7 +414,9 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
       __syncthreads();
     }
     w.node = w.count = at;
-    if constexpr (greedy) {
+    w.open = at >= limit;
+    if (w.open) {
+    } else if constexpr (greedy) {
       w.best = sm.best[at];
     } else {
       w.p = RowSum{sm.sum[0][at], sm.ref[0][at]};
@@ -425,7 +432,7 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
     }
   } else if constexpr (!drawn) {
     // A tree: from node to node, out of the drafts' terms in their rows.
-    if (mine && !greedy) sm.term[tid] = token >= 0 ? exp_from(x, sm.ref[0][node]) : 0.0;
+    if (mine && !greedy) sm.term[tid] = token >= 0 && node < limit ? exp_from(x, sm.ref[0][node]) : 0.0;
     __syncthreads();
     bool exact = false;  // the sum of the node's row is in 64 bits
     for (;;) {
@@ -484,11 +491,14 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
           ++w.count;
           w.node = taken + 1;
           exact = false;
+          w.open = w.node >= limit;
+          if (w.open) break;
         }
         if (lane == 0) {
           sm.state.node = w.node;
           sm.state.count = w.count;
           sm.state.kind = w.kind;
+          sm.state.open = w.open;
           sm.state.p.sum = w.p.sum;
           sm.state.p.ref = w.p.ref;
           sm.state.best = w.best;
@@ -505,6 +515,7 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
     w.node = sm.state.node;
     w.count = sm.state.count;
     w.kind = sm.state.kind;
+    w.open = sm.state.open;
     w.p.sum = sm.state.p.sum;
     w.p.ref = sm.state.p.ref;
     w.best = sm.state.best;
@@ -670,35 +681,44 @@ __device__ __forceinline__ RowChunk chunk_of(const typename DT::raw_t* row, int 
   return out;
 }
 
-// Chunks of all rows. Workgroups of a sequence: its target rows, then its draft rows.
 template <class DT, bool GREEDY>
-__global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, Split split, int64_t seq0,
-                                                         RowChunk* __restrict__ stats, uint32_t* __restrict__ arrived) {
-  __shared__ ChunkSmem sm;
-  const int rows = a.D + 1 + (a.draft_logits != nullptr ? a.D : 0);
-  const unsigned b = blockIdx.x;
-  const int ch = static_cast<int>(b % static_cast<unsigned>(split.chunks));
-  const unsigned item = b / static_cast<unsigned>(split.chunks);
-  const int r = static_cast<int>(item % static_cast<unsigned>(rows));
-  const int64_t seq = seq0 + item / static_cast<unsigned>(rows);
-  if (r == 0 && ch == 0 && threadIdx.x == 0) arrived[seq] = 0;
-  const bool target = r <= a.D;
-  const int w = target ? r : r - a.D - 1;
-  const int n = draft_count(a, seq);
-  if (target ? w > n : w >= n) return;
+__device__ __forceinline__ void put_chunk(const VerifyArgs& a, int64_t seq, bool target, int w, int ch, Split split,
+                                          RowChunk* stats, ChunkSmem& sm) {
   const RowChunk c = chunk_of<DT, GREEDY>(target ? target_row<DT>(a, seq, w) : draft_row<DT>(a, seq, w), a.V, ch, split, sm);
   RowChunk* out = const_cast<RowChunk*>(target ? target_stats(a, stats, split.chunks, seq, w)
                                                : draft_stats(a, stats, split.chunks, seq, w)) + ch;
   if (threadIdx.x == 0) *out = c;
 }
 
+// Chunks of the first `limit` rows. Workgroups of a sequence: its target rows, then
+// its draft rows.
+template <class DT, bool GREEDY>
+__global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, Split split, int limit, int64_t seq0,
+                                                         RowChunk* __restrict__ stats, uint32_t* __restrict__ arrived) {
+  __shared__ ChunkSmem sm;
+  const int targets = limit, rows = targets + (a.draft_logits == nullptr ? 0 : (limit < a.D ? limit : a.D));
+  const unsigned b = blockIdx.x;
+  const int ch = static_cast<int>(b % static_cast<unsigned>(split.chunks));
+  const unsigned item = b / static_cast<unsigned>(split.chunks);
+  const int r = static_cast<int>(item % static_cast<unsigned>(rows));
+  const int64_t seq = seq0 + item / static_cast<unsigned>(rows);
+  if (r == 0 && ch == 0 && threadIdx.x == 0) arrived[seq] = 0;
+  const bool target = r < targets;
+  const int w = target ? r : r - targets;
+  const int n = draft_count(a, seq);
+  if (target ? w > n : w >= n) return;
+  put_chunk<DT, GREEDY>(a, seq, target, w, ch, split, stats, sm);
+}
+
+template <int THREADS>
 struct FinalSmem {
+  static constexpr int kWaves = THREADS / kWave;
   WalkSmem walk;
   int32_t out[kMaxRows];  // rejected tokens within the range
   int outs;
-  double sum[4][kW];
-  double parts[kMaxParts];  // where summed again
-  uint64_t is[kW], may[kW];
+  double sum[4][kWaves];
+  double parts[THREADS];  // where summed again
+  uint64_t is[kWaves], may[kWaves];
   double below;
   int last;
   int found;
@@ -748,7 +768,8 @@ __device__ __forceinline__ bool terms_at(const typename DT::raw_t* prow, const t
 }
 
 // The rejected tokens within [first, end).
-__device__ __forceinline__ void list_out(const VerifyArgs& a, const Walk& w, int first, int end, FinalSmem& sm) {
+template <class Smem>
+__device__ __forceinline__ void list_out(const VerifyArgs& a, const Walk& w, int first, int end, Smem& sm) {
   if (w.kind != kWithout) return;
   const int tid = threadIdx.x;
   __syncthreads();
@@ -760,15 +781,16 @@ __device__ __forceinline__ void list_out(const VerifyArgs& a, const Walk& w, int
   }
   __syncthreads();
 }
-__device__ __forceinline__ bool is_out(int v, const FinalSmem& sm) {
+template <class Smem>
+__device__ __forceinline__ bool is_out(int v, const Smem& sm) {
   bool out = false;
   for (int i = 0; i < sm.outs; ++i) out |= sm.out[i] == v;
   return out;
 }
 
 // The workgroup's sums of v[0 .. COUNT), in all threads.
-template <int COUNT>
-__device__ __forceinline__ void block_sums(double (&v)[COUNT], double (&at)[4][kW]) {
+template <int COUNT, int WAVES>
+__device__ __forceinline__ void block_sums(double (&v)[COUNT], double (&at)[4][WAVES]) {
 #pragma unroll
   for (int i = 0; i < COUNT; ++i) v[i] = wave_sum_f64(v[i]);
   __syncthreads();
@@ -781,12 +803,13 @@ __device__ __forceinline__ void block_sums(double (&v)[COUNT], double (&at)[4][k
   for (int i = 0; i < COUNT; ++i) {
     v[i] = 0.0;
 #pragma unroll
-    for (int w = 0; w < kW; ++w) v[i] += at[i][w];
+    for (int w = 0; w < WAVES; ++w) v[i] += at[i][w];
   }
 }
 // The sums of v over the threads below, up to this one, and over all. What one
 // thread gets as its end is what the next one gets as its beginning.
-__device__ __forceinline__ void block_scan(double v, double& below, double& upto, double& all, double (&at)[4][kW]) {
+template <int WAVES>
+__device__ __forceinline__ void block_scan(double v, double& below, double& upto, double& all, double (&at)[4][WAVES]) {
   const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
   const double end = wave_incl_scan_f64(v);
   const double begin = __shfl_up(end, 1);
@@ -796,7 +819,7 @@ __device__ __forceinline__ void block_scan(double v, double& below, double& upto
   double base = 0.0;
   all = 0.0;
 #pragma unroll
-  for (int w = 0; w < kW; ++w) {
+  for (int w = 0; w < WAVES; ++w) {
     if (w == wave) base = all;
     all += at[0][w];
   }
@@ -812,9 +835,9 @@ __device__ __forceinline__ double if_or_none(bool is, double v) {
 }
 
 // Sums over a wave's part of the row, of every lane's elements.
-template <class DT, Mode MODE>
+template <class DT, Mode MODE, class Smem>
 __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, const typename DT::raw_t* qrow, int first,
-                                             int pieces, int V, const Walk& w, const FinalSmem& sm) {
+                                             int pieces, int V, const Walk& w, const Smem& sm) {
   FinalPart mine{0.0, 0.0, 0.0, 0.0, 0.0};
   const Rows least = least_of(w);
   const int lane = threadIdx.x % kWave;
@@ -863,7 +886,8 @@ __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, con
 struct Weights {
   double scale;
   bool residual, without;
-  __device__ __forceinline__ double of(const Terms& t, int j, int v, const FinalSmem& sm) const {
+  template <class Smem>
+  __device__ __forceinline__ double of(const Terms& t, int j, int v, const Smem& sm) const {
     if (residual) {
       const double more = __builtin_fma(scale, t.p[j], -t.q[j]);
       return more > 0.0 ? more : 0.0;
@@ -872,8 +896,9 @@ struct Weights {
   }
 };
 
-// The first thread for which `is` holds, and the last one for which `may` does: -1 for none.
-__device__ __forceinline__ int first_or_last(bool is, bool may, FinalSmem& sm) {
+// The first thread for which `is` holds, or else the last one for which `may` does; -1 for none.
+template <int THREADS>
+__device__ __forceinline__ int first_or_last(bool is, bool may, FinalSmem<THREADS>& sm) {
   const int wave = threadIdx.x / kWave;
   const uint64_t a = __ballot(is), b = __ballot(may);
   if (threadIdx.x % kWave == 0) {
@@ -883,55 +908,48 @@ __device__ __forceinline__ int first_or_last(bool is, bool may, FinalSmem& sm) {
   __syncthreads();
   int first = -1, last = -1;
 #pragma unroll
-  for (int i = kW - 1; i >= 0; --i)
+  for (int i = THREADS / kWave - 1; i >= 0; --i)
     if (sm.is[i] != 0) first = i * kWave + __builtin_ctzll(sm.is[i]);
 #pragma unroll
-  for (int i = 0; i < kW; ++i)
+  for (int i = 0; i < THREADS / kWave; ++i)
     if (sm.may[i] != 0) last = i * kWave + 63 - __builtin_clzll(sm.may[i]);
   __syncthreads();
   return first >= 0 ? first : last;
 }
 
 // Finds the token out of the parts' sums, by the whole workgroup.
-template <class DT, Mode MODE>
+template <class DT, Mode MODE, int THREADS>
 __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, const FinalPart* slots, int parts, int pieces,
-                        const typename DT::raw_t* prow, const typename DT::raw_t* qrow, FinalSmem& sm) {
+                                        const typename DT::raw_t* prow, const typename DT::raw_t* qrow,
+                                        FinalSmem<THREADS>& sm) {
+  constexpr int kWaves = THREADS / kWave;
   const int tid = threadIdx.x, span = pieces * kPiece;
   const bool two = MODE == kDrawn && w.kind == kResidual;
   const Rows least = least_of(w);
-  FinalPart p[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {  // parts that are not there: those of the last one, taken out below
-    const FinalPart* from = slots + (2 * tid + i < parts ? 2 * tid + i : parts - 1);
-    p[i] = FinalPart{get_far(&from->all), get_far(&from->left), 0.0, 0.0, 0.0};
+  FinalPart p{0.0, 0.0, 0.0, 0.0, 0.0};
+  if (tid < parts) {
+    const FinalPart* from = slots + tid;
+    p.all = get_far(&from->all);
+    p.left = get_far(&from->left);
     if (two) {
-      p[i].kept = get_far(&from->kept);
-      p[i].draft = get_far(&from->draft);
-      p[i].close = get_far(&from->close);
+      p.kept = get_far(&from->kept);
+      p.draft = get_far(&from->draft);
+      p.close = get_far(&from->close);
     }
   }
-  double total[3] = {0.0, 0.0, 0.0};  // all, draft, close
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (2 * tid + i >= parts) p[i] = FinalPart{0.0, 0.0, 0.0, 0.0, 0.0};
-    total[0] += p[i].all;
-    total[1] += p[i].draft;
-    total[2] += p[i].close;
-  }
+  double total[3] = {p.all, p.draft, p.close};
   block_sums(total, sm.sum);
   Weights weights{two ? total[1] / total[0] : 1.0, two, MODE != kDrawn && w.kind == kWithout};
   const double near = two ? w.q.sum / w.p.sum : 1.0, off = weights.scale - near;
-  double part[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) part[i] = __builtin_fmax(two ? __builtin_fma(off, p[i].kept, p[i].left) : p[i].left, 0.0);
+  double part = __builtin_fmax(two ? __builtin_fma(off, p.kept, p.left) : p.left, 0.0);
   double below, upto, all;
-  block_scan(part[0] + part[1], below, upto, all, sm.sum);
+  block_scan(part, below, upto, all, sm.sum);
   // Elements between the parts' ratio of the sums and the one in 64 bits are taken
   // in or left out by mistake, each with no more than their difference. That is
   // next to nothing (some 1e-8 of some 1e-7 of the mass) unless the rows are alike;
   // then the parts are summed again.
   if (two && (__builtin_fabs(off) * total[2] > 0x1p-43 * all || __builtin_fabs(off) > 0.5 * kBand * near)) {
-    for (int c0 = 0; c0 < parts; c0 += kW) {
+    for (int c0 = 0; c0 < parts; c0 += kWaves) {
       const int c = c0 + tid / kWave;
       double sum = 0.0;
 #pragma unroll 1
@@ -954,74 +972,77 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
       if (c < parts && tid % kWave == 0) sm.parts[c] = sum;
     }
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) part[i] = 2 * tid + i < parts ? sm.parts[2 * tid + i] : 0.0;
-    block_scan(part[0] + part[1], below, upto, all, sm.sum);
+    part = tid < parts ? sm.parts[tid] : 0.0;
+    block_scan(part, below, upto, all, sm.sum);
   }
   if (w.kind != kPlain && !(all > kLeast * (two ? total[1] : total[0]))) {
     weights.residual = weights.without = false;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) part[i] = p[i].all;
-    block_scan(part[0] + part[1], below, upto, all, sm.sum);
+    part = p.all;
+    block_scan(part, below, upto, all, sm.sum);
   }
   const double at = static_cast<double>(sm.walk.last_u) * all;
   // the part that `at` lies in; for a uniform out of range the first or the last one of any weight
-  const int owner = first_or_last(upto > at && upto > below, upto > below, sm);
-  if (owner < 0) return -1;
-  if (tid == owner) {
-    const double middle = below + part[0];
-    const bool second = !(part[0] > 0.0 && (middle > at || !(part[1] > 0.0)));
-    sm.below = second ? middle : below;
-    sm.found = 2 * tid + (second ? 1 : 0);
-  }
+  const int c = first_or_last(upto > at && upto > below, upto > below, sm);
+  if (c < 0) return -1;
+  if (tid == c) sm.below = below;
   __syncthreads();
-  const int c = sm.found;
-  const double base = sm.below;
+  double base = sm.below;
   if constexpr (MODE == kProposed) list_out(a, w, c * span, (c + 1) * span, sm);
-  // at most kMaxPieces * 512 elements: eight for each thread
-  static_assert(kMaxPieces * kPiece <= kT * kBlock);
-  const int v = tid * kBlock < span ? c * span + tid * kBlock : a.V;
-  double wt[kBlock], sum = 0.0;
-  int last = -1;  // the last element of any weight
-  Terms t;
-  if (terms_at<DT>(prow, qrow, v, a.V, w, least, two, t)) {
+  int last_seen = -1;
+#pragma unroll 1
+  for (int i = 0; i < span; i += THREADS * kBlock) {
+    const int v = i + tid * kBlock < span ? c * span + i + tid * kBlock : a.V;
+    double wt[kBlock], sum = 0.0;
+    int last = -1;  // the last element of any weight
+    Terms t;
+    if (terms_at<DT>(prow, qrow, v, a.V, w, least, two, t)) {
 #pragma unroll
-    for (int j = 0; j < kBlock; ++j) {
-      wt[j] = weights.of(t, j, v + j, sm);
-      sum += wt[j];
-      if (wt[j] > 0.0) last = v + j;
+      for (int j = 0; j < kBlock; ++j) {
+        wt[j] = weights.of(t, j, v + j, sm);
+        sum += wt[j];
+        if (wt[j] > 0.0) last = v + j;
+      }
     }
-  }
-  block_scan(sum, below, upto, all, sm.sum);
-  const int finder = first_or_last(last >= 0 && base + upto > at, last >= 0, sm);
-  if (finder < 0) return -1;
-  if (tid == finder) {
-    int token = last;
-    double reach = base + below;
+    block_scan(sum, below, upto, all, sm.sum);
+    const bool here = last >= 0 && base + upto > at;
+    const int finder = first_or_last(here, last >= 0, sm);
+    if (finder >= 0) {
+      if (tid == finder) {
+        int token = last;
+        double reach = base + below;
 #pragma unroll
-    for (int j = 0; j < kBlock; ++j) {
-      reach += wt[j];
-      if (wt[j] > 0.0 && reach > at) token = token < v + j ? token : v + j;
+        for (int j = 0; j < kBlock; ++j) {
+          reach += wt[j];
+          if (wt[j] > 0.0 && reach > at) token = token < v + j ? token : v + j;
+        }
+        sm.found = token;
+        sm.last = here ? 1 : 0;
+      }
+      __syncthreads();
+      last_seen = sm.found;
+      const bool done = sm.last != 0;
+      __syncthreads();
+      if (done) break;
     }
-    sm.found = token;
+    base += all;
   }
-  __syncthreads();
-  return sm.found;
+  return last_seen;
 }
 
 // A group's parts of the row where the path ends, one of each wave. Then the last
 // of a sequence's `groups` workgroups finds the token; -2 for the others.
-template <class DT, Mode MODE>
-__device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w, int64_t seq, int group, int groups, int pieces,
-                              FinalPart* slots, uint32_t* arrived, FinalSmem& sm) {
+template <class DT, Mode MODE, int THREADS>
+__device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w, int64_t seq, int group, int groups,
+                                              int pieces, FinalPart* slots, uint32_t* arrived, FinalSmem<THREADS>& sm) {
   using raw_t = typename DT::raw_t;
+  constexpr int kWaves = THREADS / kWave;
   const int tid = threadIdx.x;
   const raw_t* prow = target_row<DT>(a, seq, w.node);
   const bool two = MODE == kDrawn && w.kind == kResidual;
   const raw_t* qrow = two ? draft_row<DT>(a, seq, w.node) : prow;
-  const int span = pieces * kPiece, parts = groups * kW;
-  if constexpr (MODE == kProposed) list_out(a, w, group * kW * span, (group + 1) * kW * span, sm);
-  const int c = group * kW + tid / kWave;
+  const int span = pieces * kPiece, parts = groups * kWaves;
+  if constexpr (MODE == kProposed) list_out(a, w, group * kWaves * span, (group + 1) * kWaves * span, sm);
+  const int c = group * kWaves + tid / kWave;
   FinalPart mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm);
   mine.all = wave_sum_f64(mine.all);
   mine.left = wave_sum_f64(mine.left);
@@ -1040,21 +1061,73 @@ __device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w
     }
   }
   if (!last_of(arrived, groups, sm.last)) return -2;
-  return token_of<DT, MODE>(a, w, slots, parts, pieces, prow, qrow, sm);
+  return token_of<DT, MODE, THREADS>(a, w, slots, parts, pieces, prow, qrow, sm);
 }
 
+struct BehindSmem {
+  WalkSmem walk;
+  ChunkSmem chunk;
+  int32_t rows[kMaxRows];
+  uint64_t is[kW];
+};
+// The rows of a tree at and behind row `node`, in sm.rows; how many.
+__device__ __forceinline__ int list_behind(int node, int n, BehindSmem& sm) {
+  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
+  int r = tid;  // row; draft tid - 1
+  bool in = tid <= n && (tid == 0 || sm.walk.token[tid - 1] >= 0);
+  if (in)
+    while (r > node) r = sm.walk.node[r - 1];
+  in = in && r == node;
+  const uint64_t mask = __ballot(in);
+  if (lane == 0) sm.is[wave] = mask;
+  __syncthreads();
+  int below = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kW; ++i) {
+    if (i < wave) below += __builtin_popcountll(sm.is[i]);
+    all += __builtin_popcountll(sm.is[i]);
+  }
+  if (in) sm.rows[below + lanes_below(mask)] = tid;
+  __syncthreads();
+  return all;
+}
+
+// Of a sequence that goes on behind the first `limit` rows, chunks of the others that
+// may be on its path: the target rows from where it stands on (of a tree, those that
+// are behind that), then their draft rows.
 template <class DT, Mode MODE>
-__global__ __launch_bounds__(kT) void verify_final_kernel(VerifyArgs a, int chunks, int groups, int pieces, int64_t seq0,
-                                                          const RowChunk* __restrict__ stats,
-                                                          FinalPart* __restrict__ finals,
-                                                          uint32_t* __restrict__ arrived) {
-  __shared__ FinalSmem sm;
+__global__ __launch_bounds__(kT) void verify_behind_kernel(VerifyArgs a, Split split, int limit, int groups, int64_t seq0,
+                                                           RowChunk* stats) {
+  __shared__ BehindSmem sm;
+  const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(groups));
+  const int64_t seq = seq0 + blockIdx.x / static_cast<unsigned>(groups);
+  const Walk w = walk<DT, MODE, kT>(a, stats, split.chunks, limit, seq, sm.walk);
+  if (!w.open) return;
+  const int n = draft_count(a, seq);
+  const bool chain = MODE == kDrawn || a.parents == nullptr;
+  const int rows = chain ? n + 1 - w.node : list_behind(w.node, n, sm);
+  const int items = (rows + (MODE == kDrawn ? rows - 1 : 0)) * split.chunks;
+  for (int i = group; i < items; i += groups) {
+    const int k = i / split.chunks, ch = i - k * split.chunks;
+    const bool target = k < rows;
+    const int r = chain ? w.node + (target ? k : k - rows) : sm.rows[k];
+    put_chunk<DT, MODE == kGreedy>(a, seq, target, r, ch, split, stats, sm.chunk);
+  }
+}
+
+// The end of every path, and the row where it lies.
+template <class DT, Mode MODE, int THREADS>
+__global__ __launch_bounds__(THREADS) void verify_final_kernel(VerifyArgs a, int chunks, int groups, int pieces,
+                                                               int64_t seq0, const RowChunk* __restrict__ stats,
+                                                               FinalPart* __restrict__ finals,
+                                                               uint32_t* __restrict__ arrived) {
+  __shared__ FinalSmem<THREADS> sm;
+  constexpr bool greedy = MODE == kGreedy;
   const int tid = threadIdx.x;
   const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(groups));
   const int64_t seq = seq0 + blockIdx.x / static_cast<unsigned>(groups);
-  const Walk w = walk<DT, MODE>(a, stats, chunks, seq, sm.walk);
+  const Walk w = walk<DT, MODE, THREADS>(a, stats, chunks, a.D + 1, seq, sm.walk);
   int32_t* tokens = a.out_tokens + seq * (a.D + 1);
-  constexpr bool greedy = MODE == kGreedy;
   const bool draws = !greedy && w.kind != kNone;
   if (group == 0) {
     if (tid <= a.D && !(tid == w.count && draws))
@@ -1065,8 +1138,8 @@ __global__ __launch_bounds__(kT) void verify_final_kernel(VerifyArgs a, int chun
   }
   if constexpr (!greedy) {
     if (!draws) return;
-    const int token = token_by_parts<DT, MODE>(a, w, seq, group, groups, pieces, finals + seq * groups * kW, &arrived[seq],
-                                               sm);
+    const int token = token_by_parts<DT, MODE, THREADS>(a, w, seq, group, groups, pieces,
+                                                        finals + seq * groups * (THREADS / kWave), &arrived[seq], sm);
     if (tid == 0 && token >= -1) tokens[w.count] = token;
   }
 }
@@ -1088,73 +1161,127 @@ Split split_of(int dtype, int64_t rows, int V) {
   return Split{static_cast<int>(c), static_cast<int>(ceil_div(nv, c))};
 }
 
-// Workgroups for the row where a sequence's path ends, and pieces of their waves.
+constexpr int kUnits = 256;      // compute units
+constexpr int kFewBlocks = 512;
+constexpr int kTurnPieces = 3;
+// Workgroups for the row where a sequence's path ends, their threads, and pieces of
+// their waves.
 struct Cut {
-  int groups, pieces;
+  int threads, groups, pieces;
 };
 Cut cut_of(int64_t N, int V) {
-  const int64_t all = V > 0 ? ceil_div(V, kPiece * kW) : 1;
-  int64_t pieces = N * all / 1024;
-  pieces = pieces < 1 ? 1 : (pieces > kMaxPieces ? kMaxPieces : pieces);
-  if (all > kMaxParts / kW) pieces = kMaxPieces;
-  return Cut{static_cast<int>(ceil_div(all, pieces)), static_cast<int>(pieces)};
+  const int64_t all = V > 0 ? ceil_div(V, kPiece) : 1;
+  if (N * ceil_div(all, kFew / kWave) <= kFewBlocks && all <= kFew)
+    return Cut{kFew, static_cast<int>(ceil_div(all, kFew / kWave)), 1};
+  // one workgroup fills a compute unit: as many for a sequence as take the fewest turns
+  constexpr int kWaves = kMany / kWave;
+  Cut best{kMany, 1, static_cast<int>(ceil_div(all, kWaves))};
+  int64_t least = INT64_MAX;
+  for (int g = 1; g <= kMany / kWaves && (g - 1) * kWaves < all; ++g) {
+    const int64_t pieces = ceil_div(all, g * kWaves), cost = ceil_div(N * g, kUnits) * (pieces + kTurnPieces);
+    if (cost < least) {
+      least = cost;
+      best.groups = g;
+      best.pieces = static_cast<int>(pieces);
+    }
+  }
+  return best;
+}
+
+
+constexpr int64_t kStagedTree = int64_t{32} << 20, kStagedChain = int64_t{256} << 20;
+constexpr int kFirstRows = 3;
+constexpr int kStagedLayers = 16;
+constexpr int kBehindGroups = 32;
+
+// How a call is cut. limit: rows of a sequence that are summed first; D + 1 for all.
+struct Plan {
+  int limit, behind;  // workgroups of a sequence that sum the rows behind them
+  Split split;
+  Cut cut;
+};
+Plan plan_of(int dtype, int64_t N, int D, int V, bool draft, bool tree) {
+  const int64_t rows = N * (D + 1 + (draft ? D : 0)), bytes = rows * V * (dtype == 0 ? 4 : 2);
+  Plan p;
+  p.limit = D + 1;
+  p.behind = 0;
+  p.cut = cut_of(N, V);
+  p.split = split_of(dtype, rows, V);
+  if (D > 0 && bytes > (tree ? kStagedTree : kStagedChain)) {
+    p.limit = tree ? 1 : (D + 1) / 2;
+    if (p.limit > kFirstRows) p.limit = kFirstRows;
+    const int64_t per = dtype == 0 ? 4 : 8, nv = V / per, c = ceil_div(nv, kT * kStagedLayers);
+    p.split.chunks = static_cast<int>(c > 1 ? c : 1);
+    p.split.vecs = static_cast<int>(ceil_div(nv, p.split.chunks));
+    const int64_t left = (D + 1 - p.limit) * (draft ? 2 : 1) * p.split.chunks;
+    p.behind = static_cast<int>(left < kBehindGroups ? left : kBehindGroups);
+  }
+  return p;
 }
 
 struct Layout {
   int64_t stats, finals, arrived, bytes;
 };
-Layout layout_of(int dtype, int64_t N, int D, int V, bool draft) {
+Layout layout_of(const Plan& p, int64_t N, int D, bool draft) {
   const int64_t rows = N * (D + 1 + (draft ? D : 0));
   Layout l;
   l.stats = 0;
-  l.finals = l.stats + rows * split_of(dtype, rows, V).chunks * static_cast<int64_t>(sizeof(RowChunk));
-  l.arrived = l.finals + N * cut_of(N, V).groups * kW * static_cast<int64_t>(sizeof(FinalPart));
+  l.finals = l.stats + rows * p.split.chunks * static_cast<int64_t>(sizeof(RowChunk));
+  l.arrived = l.finals + N * p.cut.groups * (p.cut.threads / kWave) * static_cast<int64_t>(sizeof(FinalPart));
   l.bytes = l.arrived + N * 4;
   return l;
 }
 
-template <class DT>
-hipError_t launch_typed(int dtype, const VerifyArgs& a, hipStream_t stream) {
-  const bool draft = a.draft_logits != nullptr, greedy = a.uniforms == nullptr;
-  const int rows = a.D + 1 + (draft ? a.D : 0);
-  const Split split = split_of(dtype, a.N * rows, a.V);
-  const Cut cut = cut_of(a.N, a.V);
-  const Layout l = layout_of(dtype, a.N, a.D, a.V, draft);
+template <class DT, Mode MODE>
+hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
+  const bool draft = MODE == kDrawn, greedy = MODE == kGreedy;
+  const Plan p = plan_of(dtype, a.N, a.D, a.V, draft, a.parents != nullptr);
+  const Layout l = layout_of(p, a.N, a.D, draft);
   char* ws = static_cast<char*>(a.workspace);
   RowChunk* stats = reinterpret_cast<RowChunk*>(ws + l.stats);
   FinalPart* finals = reinterpret_cast<FinalPart*>(ws + l.finals);
   uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
-  const int groups = greedy ? 1 : cut.groups;
-  // a launch holds at most 2^22 workgroups of 256 threads
-  const int64_t of_rows = static_cast<int64_t>(rows) * split.chunks, per = of_rows > groups ? of_rows : groups;
+  const int rows = p.limit + (draft ? (p.limit < a.D ? p.limit : a.D) : 0), groups = greedy ? 1 : p.cut.groups;
+  // a launch holds at most 2^22 workgroups
+  const int64_t of_rows = static_cast<int64_t>(rows) * p.split.chunks;
+  int64_t per = of_rows > groups ? of_rows : groups;
+  per = per > p.behind ? per : p.behind;
   const int64_t step = (int64_t{1} << 22) / per > 0 ? (int64_t{1} << 22) / per : 1;
   for (int64_t i = 0; i < a.N; i += step) {
     const int64_t n = a.N - i < step ? a.N - i : step;
-    const dim3 g1(static_cast<unsigned>(n * of_rows)), g2(static_cast<unsigned>(n * groups));
-    if (greedy) {
-      hipLaunchKernelGGL((verify_rows_kernel<DT, true>), g1, dim3(kT), 0, stream, a, split, i, stats, arrived);
+    auto grid = [&](int64_t of) { return dim3(static_cast<unsigned>(n * of)); };
+    hipLaunchKernelGGL((verify_rows_kernel<DT, greedy>), grid(of_rows), dim3(kT), 0, stream, a, p.split, p.limit, i, stats,
+                       arrived);
+    if (const hipError_t e = hipGetLastError()) return e;
+    if (p.behind > 0) {
+      hipLaunchKernelGGL((verify_behind_kernel<DT, MODE>), grid(p.behind), dim3(kT), 0, stream, a, p.split, p.limit,
+                         p.behind, i, stats);
       if (const hipError_t e = hipGetLastError()) return e;
-      hipLaunchKernelGGL((verify_final_kernel<DT, kGreedy>), g2, dim3(kT), 0, stream, a, split.chunks, groups, cut.pieces,
-                         i, stats, finals, arrived);
-    } else {
-      hipLaunchKernelGGL((verify_rows_kernel<DT, false>), g1, dim3(kT), 0, stream, a, split, i, stats, arrived);
-      if (const hipError_t e = hipGetLastError()) return e;
-      if (draft)
-        hipLaunchKernelGGL((verify_final_kernel<DT, kDrawn>), g2, dim3(kT), 0, stream, a, split.chunks, groups, cut.pieces,
-                           i, stats, finals, arrived);
-      else
-        hipLaunchKernelGGL((verify_final_kernel<DT, kProposed>), g2, dim3(kT), 0, stream, a, split.chunks, groups,
-                           cut.pieces, i, stats, finals, arrived);
     }
+    if (greedy || p.cut.threads == kFew)
+      hipLaunchKernelGGL((verify_final_kernel<DT, MODE, kFew>), grid(groups), dim3(kFew), 0, stream, a, p.split.chunks,
+                         groups, p.cut.pieces, i, stats, finals, arrived);
+    else if constexpr (!greedy)
+      hipLaunchKernelGGL((verify_final_kernel<DT, MODE, kMany>), grid(groups), dim3(kMany), 0, stream, a, p.split.chunks,
+                         groups, p.cut.pieces, i, stats, finals, arrived);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
 }
 
+template <class DT>
+hipError_t launch_typed(int dtype, const VerifyArgs& a, hipStream_t stream) {
+  if (a.uniforms == nullptr) return launch_mode<DT, kGreedy>(dtype, a, stream);
+  if (a.draft_logits != nullptr) return launch_mode<DT, kDrawn>(dtype, a, stream);
+  return launch_mode<DT, kProposed>(dtype, a, stream);
+}
+
 }  // namespace
 
 int64_t verify_workspace(int dtype, int64_t N, int D, int V, bool draft_logits) {
-  return layout_of(dtype, N, D, V, draft_logits).bytes;
+  const int64_t chain = layout_of(plan_of(dtype, N, D, V, draft_logits, false), N, D, draft_logits).bytes;
+  const int64_t tree = layout_of(plan_of(dtype, N, D, V, draft_logits, true), N, D, draft_logits).bytes;
+  return chain > tree ? chain : tree;
 }
 
 hipError_t launch_verify(int dtype, const VerifyArgs& a, hipStream_t stream) {
