@@ -21,6 +21,8 @@
 
 #include <float.h>
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "exp_sum.h"
 #include "reg_tile.h"
@@ -35,7 +37,7 @@ constexpr int kMaxRows = 256;  // D + 1 at most
 constexpr int kBlock = 8;      // neighbouring elements of a thread
 constexpr int kPiece = kWave * kBlock;  // of a wave
 // Threads of a workgroup that works on the row where a path ends, which is cut into
-// parts of whole pieces, one for each wave, and no more parts than threads.
+// parts of whole pieces, one for each wave, and no more parts than kFew.
 constexpr int kFew = 256, kMany = 1024;
 // A residual of no more mass than this is what roundings of the logits leave; the
 // token then comes from p itself.
@@ -81,6 +83,26 @@ __device__ __forceinline__ double exp_from(float x, float ref) {
   e = __builtin_fma(e, r, 0.6931471805599462);
   e = __builtin_fma(e, r, 1.0000000000000135);
   return __builtin_ldexp(e, static_cast<int>(n));
+}
+
+// exp(x): what is added in rounding t stays in its low bits as a whole number. 15
+// instructions.
+__device__ __forceinline__ double exp_of(float x) {
+  constexpr double kLog2e = 1.4426950408889634, kRound = 6755399441055744.0;  // 1.5 * 2^52
+  const double d = static_cast<double>(fmaxf(x, -760.0f));
+  const double t = __builtin_fma(d, kLog2e, kRound);
+  const double r = __builtin_fma(d, kLog2e, kRound - t);
+  double e = 1.0205905413765595e-07;
+  e = __builtin_fma(e, r, 1.325964524488711e-06);
+  e = __builtin_fma(e, r, 1.5252672924850737e-05);
+  e = __builtin_fma(e, r, 0.0001540343375125101);
+  e = __builtin_fma(e, r, 0.0013333558200794592);
+  e = __builtin_fma(e, r, 0.009618129193934313);
+  e = __builtin_fma(e, r, 0.05550410866465167);
+  e = __builtin_fma(e, r, 0.2402265069564034);
+  e = __builtin_fma(e, r, 0.6931471805599462);
+  e = __builtin_fma(e, r, 1.0000000000000135);
+  return __builtin_ldexp(e, static_cast<int>(static_cast<uint32_t>(__builtin_bit_cast(uint64_t, t))));
 }
 
 __device__ __forceinline__ double wave_incl_scan_f64(double v) {
@@ -308,7 +330,7 @@ __device__ __forceinline__ void draft_of(const VerifyArgs& a, int64_t seq, int j
 // tree all rows, or the first one). All threads of the workgroup take part and get
 // the same result; what is one thing after the other is left to the first wave.
 constexpr int kSets = kMaxRows / kWave;
-template <class DT, Mode MODE, int THREADS>
+template <class DT, Mode MODE>
 __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int limit, int64_t seq, WalkSmem& sm) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
   const int D = a.D, n = draft_count(a, seq);
@@ -331,7 +353,7 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
   if (tid == 0) sm.last_u = greedy ? 0.0f : a.uniforms[seq * (D + 1) + D];
   // 16 lanes a row: target rows, then draft rows
   const int targets = n < limit ? n + 1 : limit, rows = targets + (drawn ? (n < limit ? n : limit) : 0);
-  for (int i = tid / 16; i < (rows + 3) / 4 * 4; i += THREADS / 16) {
+  for (int i = tid < kT ? tid / 16 : rows + 3; i < (rows + 3) / 4 * 4; i += kT / 16) {
     const int r = i < rows ? i : 0;
     const bool target = r < targets;
     const RowChunk* s = target ? target_stats(a, stats, chunks, seq, r) : draft_stats(a, stats, chunks, seq, r - targets);
@@ -710,14 +732,21 @@ __global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, Split spl
   put_chunk<DT, GREEDY>(a, seq, target, w, ch, split, stats, sm);
 }
 
-template <int THREADS>
-struct FinalSmem {
-  static constexpr int kWaves = THREADS / kWave;
+template <class DT, int THREADS>
+constexpr bool kTabled = THREADS == kMany && DT::kPerVec == 8 && DT::kNegInf == 0xFF80u;
+constexpr int kTable = 8192 + ((134 - 83) << 7) + 1;
+struct NoTable {};
+struct Table {
+  double table[kTable];
+};
+template <class DT, int THREADS, Mode MODE>
+struct FinalSmem : std::conditional_t<kTabled<DT, THREADS> && MODE != kGreedy, Table, NoTable> {
+  static constexpr int kWaves = kFew / kWave;  // that find the token
   WalkSmem walk;
   int32_t out[kMaxRows];  // rejected tokens within the range
   int outs;
   double sum[4][kWaves];
-  double parts[THREADS];  // where summed again
+  double parts[kFew];  // where summed again
   uint64_t is[kWaves], may[kWaves];
   double below;
   int last;
@@ -834,6 +863,32 @@ __device__ __forceinline__ double if_or_none(bool is, double v) {
   return __builtin_bit_cast(double, (static_cast<uint64_t>(high) << 32) | static_cast<uint32_t>(u));
 }
 
+// Eight elements' share of a part's sums; p > q where near * p's term > q's.
+__device__ __forceinline__ void add_terms(FinalPart& mine, const Terms& t, double near) {
+  bool close = false;
+#pragma unroll
+  for (int j = 0; j < kBlock; ++j) {
+    const double more = __builtin_fma(near, t.p[j], -t.q[j]);
+    mine.all += t.p[j];
+    mine.draft += t.q[j];
+    mine.left += __builtin_fmax(more, 0.0);
+    mine.kept += if_or_none(more > 0.0, t.p[j]);
+    close |= __builtin_fabs(more) < kBand * t.q[j];
+  }
+  if (__ballot(close) != 0) {
+#pragma unroll 1
+    for (int j = 0; j < kBlock; ++j) {
+      double p = 0.0, q = 0.0;
+#pragma unroll
+      for (int k = 0; k < kBlock; ++k) {
+        p = j == k ? t.p[k] : p;
+        q = j == k ? t.q[k] : q;
+      }
+      if (__builtin_fabs(__builtin_fma(near, p, -q)) < kBand * q) mine.close += p;
+    }
+  }
+}
+
 // Sums over a wave's part of the row, of every lane's elements.
 template <class DT, Mode MODE, class Smem>
 __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, const typename DT::raw_t* qrow, int first,
@@ -842,23 +897,13 @@ __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, con
   const Rows least = least_of(w);
   const int lane = threadIdx.x % kWave;
   if (MODE == kDrawn && w.kind == kResidual) {
-    // p > q where near * p's term > q's
     const double near = w.q.sum / w.p.sum;
 #pragma unroll 1
     for (int i = 0; i < pieces; ++i) {
       const int v = first + i * kPiece + lane * kBlock;
       Terms t;
       if (!terms_at<DT>(prow, qrow, v, V, w, least, true, t)) continue;
-#pragma unroll
-      for (int j = 0; j < kBlock; ++j) {
-        const double more = __builtin_fma(near, t.p[j], -t.q[j]);
-        mine.all += t.p[j];
-        mine.draft += t.q[j];
-        mine.left += __builtin_fmax(more, 0.0);
-        mine.kept += if_or_none(more > 0.0, t.p[j]);
-        const bool close = __builtin_fabs(more) < kBand * t.q[j];
-        if (__ballot(close) != 0) mine.close += close ? t.p[j] : 0.0;
-      }
+      add_terms(mine, t, near);
     }
   } else {
     const bool outs = MODE != kDrawn && w.kind == kWithout && sm.outs != 0;
@@ -867,6 +912,102 @@ __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, con
       const int v = first + i * kPiece + lane * kBlock;
       Terms t;
       if (!terms_at<DT>(prow, qrow, v, V, w, least, false, t)) continue;
+      double sum = 0.0;
+#pragma unroll
+      for (int j = 0; j < kBlock; ++j) sum += t.p[j];
+      mine.all += sum;
+      if (outs) {
+        sum = 0.0;
+#pragma unroll
+        for (int j = 0; j < kBlock; ++j) sum += is_out(v + j, sm) ? 0.0 : t.p[j];
+      }
+      mine.left += sum;
+    }
+  }
+  return mine;
+}
+
+// bf16 rows whose references are 0, as a model's logits have: there are so few
+// values that exp of all of them fits shared memory, 1.0 below 2^-44 in size and 0
+// from -128 down. A look-up takes 5 instructions and 10 or so cycles of shared
+// memory, where the polynomial takes 17.
+constexpr int kTableLow = 83 << 7, kTableHigh = 134 << 7;  // bits of 2^-44 and 2^7
+constexpr int kTableSign = 8192;                           // entries of the negative ones come behind
+static_assert(kTable == kTableSign + kTableHigh - kTableLow + 1);
+constexpr int kTableNear = 118 << 7;                       // bits of 2^-9: below, four terms of the series are within 2^-52
+template <int FIRST, int THREADS>
+__device__ __forceinline__ void fill_table(double (&table)[kTable]) {  // by threads FIRST and up
+  for (int m = kTableLow + threadIdx.x - FIRST; m <= kTableHigh; m += THREADS - FIRST) {
+    const float x = __uint_as_float(static_cast<uint32_t>(m) << 16);
+    double up, down;
+    if (m < kTableNear) {
+      const double d = x;
+      const double even = __builtin_fma(d * d, __builtin_fma(d * d, 1.0 / 24, 0.5), 1.0);
+      const double odd = __builtin_fma(d * d, 1.0 / 6, 1.0) * d;
+      up = even + odd;
+      down = even - odd;
+    } else {
+      up = exp_from(x, 0.0f);
+      down = exp_from(-x, 0.0f);
+    }
+    table[m - kTableLow] = up;
+    table[kTableSign + m - kTableLow] = m == kTableHigh ? 0.0 : down;
+  }
+}
+using pair_t = uint16_t __attribute__((ext_vector_type(2)));
+// The terms of two elements of a row.
+__device__ __forceinline__ void look_up(const double (&table)[kTable], uint32_t word, double& first, double& second) {
+  const uint32_t size = word & 0x7FFF7FFFu;
+  pair_t m = __builtin_bit_cast(pair_t, size);
+  m = __builtin_elementwise_max(m, pair_t{kTableLow, kTableLow});
+  m = __builtin_elementwise_min(m, pair_t{kTableHigh, kTableHigh});
+  m = m - pair_t{kTableLow, kTableLow};
+  const uint32_t at = __builtin_bit_cast(uint32_t, m) | (word >> 2 & (kTableSign * 0x10001u));
+  first = table[at & 0xFFFFu];
+  second = table[at >> 16];
+}
+__device__ __forceinline__ vec_t load_words(const uint16_t* row, int v, int V) {
+  vec_t q;
+  if (v + kBlock <= V) {
+    __builtin_memcpy(&q, row + v, 16);
+  } else {
+    q = vec_t{0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u};
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j)
+      if (v + j < V) set_lane<uint16_t>(q, j, row[v + j]);
+  }
+  return q;
+}
+__device__ __forceinline__ bool all_masked(const vec_t& q) {
+  return (q.x & q.y & q.z & q.w) == 0xFF80FF80u && (q.x | q.y | q.z | q.w) == 0xFF80FF80u;
+}
+template <Mode MODE, class Smem>
+__device__ __forceinline__ FinalPart part_by_table(const uint16_t* prow, const uint16_t* qrow, int first, int pieces, int V,
+                                                   const Walk& w, const Smem& sm, const double (&table)[kTable]) {
+  FinalPart mine{0.0, 0.0, 0.0, 0.0, 0.0};
+  const int lane = threadIdx.x % kWave;
+  const bool two = MODE == kDrawn && w.kind == kResidual;
+  const bool outs = MODE != kDrawn && w.kind == kWithout && sm.outs != 0;
+  const double near = two ? w.q.sum / w.p.sum : 0.0;
+  vec_t x = load_words(prow, first + lane * kBlock, V), y = x;
+  if (two) y = load_words(qrow, first + lane * kBlock, V);
+#pragma unroll 1
+  for (int i = 0; i < pieces; ++i) {
+    const int v = first + i * kPiece + lane * kBlock;
+    const vec_t xn = x, yn = y;
+    if (i + 1 < pieces) {  // the next ones are on their way
+      x = load_words(prow, v + kPiece, V);
+      if (two) y = load_words(qrow, v + kPiece, V);
+    }
+    if (__ballot(!(all_masked(xn) && (!two || all_masked(yn)))) == 0) continue;
+    Terms t;
+#pragma unroll
+    for (int j = 0; j < kBlock; j += 2) look_up(table, vword(xn, j / 2), t.p[j], t.p[j + 1]);
+    if (two) {
+#pragma unroll
+      for (int j = 0; j < kBlock; j += 2) look_up(table, vword(yn, j / 2), t.q[j], t.q[j + 1]);
+      add_terms(mine, t, near);
+    } else {
       double sum = 0.0;
 #pragma unroll
       for (int j = 0; j < kBlock; ++j) sum += t.p[j];
@@ -897,8 +1038,9 @@ struct Weights {
 };
 
 // The first thread for which `is` holds, or else the last one for which `may` does; -1 for none.
-template <int THREADS>
-__device__ __forceinline__ int first_or_last(bool is, bool may, FinalSmem<THREADS>& sm) {
+template <class Smem>
+__device__ __forceinline__ int first_or_last(bool is, bool may, Smem& sm) {
+  constexpr int THREADS = kFew;
   const int wave = threadIdx.x / kWave;
   const uint64_t a = __ballot(is), b = __ballot(may);
   if (threadIdx.x % kWave == 0) {
@@ -917,12 +1059,13 @@ __device__ __forceinline__ int first_or_last(bool is, bool may, FinalSmem<THREAD
   return first >= 0 ? first : last;
 }
 
-// Finds the token out of the parts' sums, by the whole workgroup.
-template <class DT, Mode MODE, int THREADS>
+// Finds the token out of the parts' sums, by the first kFew threads (the other waves
+// have ended, and barriers wait for none of them).
+template <class DT, Mode MODE, class Smem>
 __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, const FinalPart* slots, int parts, int pieces,
                                         const typename DT::raw_t* prow, const typename DT::raw_t* qrow,
-                                        FinalSmem<THREADS>& sm) {
-  constexpr int kWaves = THREADS / kWave;
+                                        Smem& sm) {
+  constexpr int THREADS = kFew, kWaves = THREADS / kWave;
   const int tid = threadIdx.x, span = pieces * kPiece;
   const bool two = MODE == kDrawn && w.kind == kResidual;
   const Rows least = least_of(w);
@@ -1033,7 +1176,8 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
 // of a sequence's `groups` workgroups finds the token; -2 for the others.
 template <class DT, Mode MODE, int THREADS>
 __device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w, int64_t seq, int group, int groups,
-                                              int pieces, FinalPart* slots, uint32_t* arrived, FinalSmem<THREADS>& sm) {
+                                              int pieces, FinalPart* slots, uint32_t* arrived,
+                                              FinalSmem<DT, THREADS, MODE>& sm) {
   using raw_t = typename DT::raw_t;
   constexpr int kWaves = THREADS / kWave;
   const int tid = threadIdx.x;
@@ -1043,7 +1187,16 @@ __device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w
   const int span = pieces * kPiece, parts = groups * kWaves;
   if constexpr (MODE == kProposed) list_out(a, w, group * kWaves * span, (group + 1) * kWaves * span, sm);
   const int c = group * kWaves + tid / kWave;
-  FinalPart mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm);
+  FinalPart mine;
+  if constexpr (kTabled<DT, THREADS>) {
+    if (w.p.ref == 0.0f && (!two || w.q.ref == 0.0f)) {
+      mine = part_by_table<MODE>(prow, qrow, c * span, pieces, a.V, w, sm, sm.table);
+    } else {
+      mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm);
+    }
+  } else {
+    mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm);
+  }
   mine.all = wave_sum_f64(mine.all);
   mine.left = wave_sum_f64(mine.left);
   if (two) {
@@ -1060,8 +1213,8 @@ __device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w
       put_far(&slots[c].close, mine.close);
     }
   }
-  if (!last_of(arrived, groups, sm.last)) return -2;
-  return token_of<DT, MODE, THREADS>(a, w, slots, parts, pieces, prow, qrow, sm);
+  if (!last_of(arrived, groups, sm.last) || tid >= kFew) return -2;
+  return token_of<DT, MODE>(a, w, slots, parts, pieces, prow, qrow, sm);
 }
 
 struct BehindSmem {
@@ -1096,12 +1249,12 @@ __device__ __forceinline__ int list_behind(int node, int n, BehindSmem& sm) {
 // may be on its path: the target rows from where it stands on (of a tree, those that
 // are behind that), then their draft rows.
 template <class DT, Mode MODE>
-__global__ __launch_bounds__(kT) void verify_behind_kernel(VerifyArgs a, Split split, int limit, int groups, int64_t seq0,
+__global__ __launch_bounds__(kT, DT::kPerVec == 4 ? 4 : 5) void verify_behind_kernel(VerifyArgs a, Split split, int limit, int groups, int64_t seq0,
                                                            RowChunk* stats) {
   __shared__ BehindSmem sm;
   const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(groups));
   const int64_t seq = seq0 + blockIdx.x / static_cast<unsigned>(groups);
-  const Walk w = walk<DT, MODE, kT>(a, stats, split.chunks, limit, seq, sm.walk);
+  const Walk w = walk<DT, MODE>(a, stats, split.chunks, limit, seq, sm.walk);
   if (!w.open) return;
   const int n = draft_count(a, seq);
   const bool chain = MODE == kDrawn || a.parents == nullptr;
@@ -1121,12 +1274,15 @@ __global__ __launch_bounds__(THREADS) void verify_final_kernel(VerifyArgs a, int
                                                                int64_t seq0, const RowChunk* __restrict__ stats,
                                                                FinalPart* __restrict__ finals,
                                                                uint32_t* __restrict__ arrived) {
-  __shared__ FinalSmem<THREADS> sm;
+  __shared__ FinalSmem<DT, THREADS, MODE> sm;
   constexpr bool greedy = MODE == kGreedy;
   const int tid = threadIdx.x;
   const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(groups));
   const int64_t seq = seq0 + blockIdx.x / static_cast<unsigned>(groups);
-  const Walk w = walk<DT, MODE, THREADS>(a, stats, chunks, a.D + 1, seq, sm.walk);
+  if constexpr (kTabled<DT, THREADS> && MODE != kGreedy) {
+    if (tid >= kT) fill_table<kT, THREADS>(sm.table);  // while the others go down the path
+  }
+  const Walk w = walk<DT, MODE>(a, stats, chunks, a.D + 1, seq, sm.walk);
   int32_t* tokens = a.out_tokens + seq * (a.D + 1);
   const bool draws = !greedy && w.kind != kNone;
   if (group == 0) {
@@ -1171,13 +1327,14 @@ struct Cut {
 };
 Cut cut_of(int64_t N, int V) {
   const int64_t all = V > 0 ? ceil_div(V, kPiece) : 1;
-  if (N * ceil_div(all, kFew / kWave) <= kFewBlocks && all <= kFew)
-    return Cut{kFew, static_cast<int>(ceil_div(all, kFew / kWave)), 1};
+  const int64_t few = ceil_div(all, kFew);  // pieces, for no more parts than threads
+  if (N * ceil_div(all, few * (kFew / kWave)) <= kFewBlocks)
+    return Cut{kFew, static_cast<int>(ceil_div(all, few * (kFew / kWave))), static_cast<int>(few)};
   // one workgroup fills a compute unit: as many for a sequence as take the fewest turns
   constexpr int kWaves = kMany / kWave;
   Cut best{kMany, 1, static_cast<int>(ceil_div(all, kWaves))};
   int64_t least = INT64_MAX;
-  for (int g = 1; g <= kMany / kWaves && (g - 1) * kWaves < all; ++g) {
+  for (int g = 1; g <= kFew / kWaves && (g - 1) * kWaves < all; ++g) {
     const int64_t pieces = ceil_div(all, g * kWaves), cost = ceil_div(N * g, kUnits) * (pieces + kTurnPieces);
     if (cost < least) {
       least = cost;
@@ -1192,7 +1349,7 @@ Cut cut_of(int64_t N, int V) {
 constexpr int64_t kStagedTree = int64_t{32} << 20, kStagedChain = int64_t{256} << 20;
 constexpr int kFirstRows = 3;
 constexpr int kStagedLayers = 16;
-constexpr int kBehindGroups = 32;
+constexpr int kBehindGroups = 64;
 
 // How a call is cut. limit: rows of a sequence that are summed first; D + 1 for all.
 struct Plan {
