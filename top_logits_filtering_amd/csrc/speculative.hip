@@ -64,32 +64,13 @@ struct FinalPart {
   double close;  // of p's terms where p and q are too close to tell which is larger
 };
 
-// exp(x - ref) in 64 bits, 0 for -inf and NaN: 2^t with t cut into a whole number
-// and r in [-1/2, 1/2], 2^r by the polynomial of degree 9 that meets it at the
-// Chebyshev points, within 1.9e-14 of it. 17 instructions; the library's exp takes
-// about 30.
+// exp(x - ref) in 64 bits, 0 for -inf and NaN: 2^(n + r) with n whole and r in
+// [-1/2, 1/2], 2^r by the polynomial of degree 9 that meets it at the Chebyshev
+// points, within 1.9e-14 of it. What is added to round to n leaves n in the low bits.
+// 16 instructions; the library's exp takes about 30.
 __device__ __forceinline__ double exp_from(float x, float ref) {
-  double t = (static_cast<double>(x) - static_cast<double>(ref)) * 1.4426950408889634;
-  t = __builtin_fmax(t, -1100.0);
-  const double n = __builtin_rint(t), r = t - n;
-  double e = 1.0205905413765595e-07;
-  e = __builtin_fma(e, r, 1.325964524488711e-06);
-  e = __builtin_fma(e, r, 1.5252672924850737e-05);
-  e = __builtin_fma(e, r, 0.0001540343375125101);
-  e = __builtin_fma(e, r, 0.0013333558200794592);
-  e = __builtin_fma(e, r, 0.009618129193934313);
-  e = __builtin_fma(e, r, 0.05550410866465167);
-  e = __builtin_fma(e, r, 0.2402265069564034);
-  e = __builtin_fma(e, r, 0.6931471805599462);
-  e = __builtin_fma(e, r, 1.0000000000000135);
-  return __builtin_ldexp(e, static_cast<int>(n));
-}
-
-// exp(x): what is added in rounding t stays in its low bits as a whole number. 15
-// instructions.
-__device__ __forceinline__ double exp_of(float x) {
   constexpr double kLog2e = 1.4426950408889634, kRound = 6755399441055744.0;  // 1.5 * 2^52
-  const double d = static_cast<double>(fmaxf(x, -760.0f));
+  const double d = __builtin_fmax(static_cast<double>(x) - static_cast<double>(ref), -760.0);
   const double t = __builtin_fma(d, kLog2e, kRound);
   const double r = __builtin_fma(d, kLog2e, kRound - t);
   double e = 1.0205905413765595e-07;
@@ -326,9 +307,9 @@ __device__ __forceinline__ void draft_of(const VerifyArgs& a, int64_t seq, int j
   node = parent + 1;
 }
 
-// Goes down a sequence's path, as far as it is within the first `limit` rows (of a
-// tree all rows, or the first one). All threads of the workgroup take part and get
-// the same result; what is one thing after the other is left to the first wave.
+// Goes down a sequence's path, in a tree `limit` drafts far at most: so many of its
+// rows are summed. All threads of the workgroup take part and get the same result;
+// what is one thing after the other is left to the first wave.
 constexpr int kSets = kMaxRows / kWave;
 template <class DT, Mode MODE>
 __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats, int chunks, int limit, int64_t seq, WalkSmem& sm) {
@@ -352,7 +333,8 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
   }
   if (tid == 0) sm.last_u = greedy ? 0.0f : a.uniforms[seq * (D + 1) + D];
   // 16 lanes a row: target rows, then draft rows
-  const int targets = n < limit ? n + 1 : limit, rows = targets + (drawn ? (n < limit ? n : limit) : 0);
+  // (in a tree those that are not summed yet are not looked at)
+  const int targets = n + 1, rows = targets + (drawn ? n : 0);
   for (int i = tid < kT ? tid / 16 : rows + 3; i < (rows + 3) / 4 * 4; i += kT / 16) {
     const int r = i < rows ? i : 0;
     const bool target = r < targets;
@@ -383,7 +365,7 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
       return left < right;
     };
     if (mine) {
-      if (token >= 0 && tid < limit) {
+      if (token >= 0) {
         if constexpr (greedy) {
           stays = token == best_token(sm.best[tid]);
         } else {
@@ -436,9 +418,7 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
       __syncthreads();
     }
     w.node = w.count = at;
-    w.open = at >= limit;
-    if (w.open) {
-    } else if constexpr (greedy) {
+    if constexpr (greedy) {
       w.best = sm.best[at];
     } else {
       w.p = RowSum{sm.sum[0][at], sm.ref[0][at]};
@@ -454,7 +434,7 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
     }
   } else if constexpr (!drawn) {
     // A tree: from node to node, out of the drafts' terms in their rows.
-    if (mine && !greedy) sm.term[tid] = token >= 0 && node < limit ? exp_from(x, sm.ref[0][node]) : 0.0;
+    if (mine && !greedy) sm.term[tid] = token >= 0 ? exp_from(x, sm.ref[0][node]) : 0.0;
     __syncthreads();
     bool exact = false;  // the sum of the node's row is in 64 bits
     for (;;) {
@@ -513,7 +493,7 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
           ++w.count;
           w.node = taken + 1;
           exact = false;
-          w.open = w.node >= limit;
+          w.open = w.count >= limit;
           if (w.open) break;
         }
         if (lane == 0) {
@@ -712,13 +692,13 @@ __device__ __forceinline__ void put_chunk(const VerifyArgs& a, int64_t seq, bool
   if (threadIdx.x == 0) *out = c;
 }
 
-// Chunks of the first `limit` rows. Workgroups of a sequence: its target rows, then
-// its draft rows.
+// Chunks of rows. Workgroups of a sequence: its first `targets` target rows, then its
+// draft rows, if there are any.
 template <class DT, bool GREEDY>
-__global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, Split split, int limit, int64_t seq0,
+__global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, Split split, int targets, int64_t seq0,
                                                          RowChunk* __restrict__ stats, uint32_t* __restrict__ arrived) {
   __shared__ ChunkSmem sm;
-  const int targets = limit, rows = targets + (a.draft_logits == nullptr ? 0 : (limit < a.D ? limit : a.D));
+  const int rows = targets + (a.draft_logits == nullptr ? 0 : a.D);
   const unsigned b = blockIdx.x;
   const int ch = static_cast<int>(b % static_cast<unsigned>(split.chunks));
   const unsigned item = b / static_cast<unsigned>(split.chunks);
@@ -1245,26 +1225,21 @@ __device__ __forceinline__ int list_behind(int node, int n, BehindSmem& sm) {
   return all;
 }
 
-// Of a sequence that goes on behind the first `limit` rows, chunks of the others that
-// may be on its path: the target rows from where it stands on (of a tree, those that
-// are behind that), then their draft rows.
+// Of a tree whose path goes on after `limit` drafts, chunks of the row where it
+// stands, or (all) of that and the rows behind it.
 template <class DT, Mode MODE>
-__global__ __launch_bounds__(kT, DT::kPerVec == 4 ? 4 : 5) void verify_behind_kernel(VerifyArgs a, Split split, int limit, int groups, int64_t seq0,
-                                                           RowChunk* stats) {
+__global__ __launch_bounds__(kT, DT::kPerVec == 4 ? 4 : 5) void verify_behind_kernel(VerifyArgs a, Split split, int limit,
+                                                                                     bool all, int groups, int64_t seq0,
+                                                                                     RowChunk* stats) {
   __shared__ BehindSmem sm;
   const int group = static_cast<int>(blockIdx.x % static_cast<unsigned>(groups));
   const int64_t seq = seq0 + blockIdx.x / static_cast<unsigned>(groups);
   const Walk w = walk<DT, MODE>(a, stats, split.chunks, limit, seq, sm.walk);
   if (!w.open) return;
-  const int n = draft_count(a, seq);
-  const bool chain = MODE == kDrawn || a.parents == nullptr;
-  const int rows = chain ? n + 1 - w.node : list_behind(w.node, n, sm);
-  const int items = (rows + (MODE == kDrawn ? rows - 1 : 0)) * split.chunks;
-  for (int i = group; i < items; i += groups) {
+  const int rows = all ? list_behind(w.node, draft_count(a, seq), sm) : 1;
+  for (int i = group; i < rows * split.chunks; i += groups) {
     const int k = i / split.chunks, ch = i - k * split.chunks;
-    const bool target = k < rows;
-    const int r = chain ? w.node + (target ? k : k - rows) : sm.rows[k];
-    put_chunk<DT, MODE == kGreedy>(a, seq, target, r, ch, split, stats, sm.chunk);
+    put_chunk<DT, MODE == kGreedy>(a, seq, true, all ? sm.rows[k] : w.node, ch, split, stats, sm.chunk);
   }
 }
 
@@ -1346,32 +1321,28 @@ Cut cut_of(int64_t N, int V) {
 }
 
 
-constexpr int64_t kStagedTree = int64_t{32} << 20, kStagedChain = int64_t{256} << 20;
-constexpr int kFirstRows = 3;
-constexpr int kStagedLayers = 16;
-constexpr int kBehindGroups = 64;
+// A path through a tree needs few of its rows. Where there is much to read, the first
+// rows are summed before, then the one that each path goes on at, then what is left
+// behind that: 32 trees of 39 drafts, three behind each, V 151936 bf16, take 55 us so,
+// 64 without the second step, 63 with one more like it, and 90 with all rows read.
+// (Chains do not gain: 64 of 4 drafts with draft logits take 59 us with half of their
+// rows read first, 54 all at once; 128 of 3 drafts, V 128256 fp32, 113 both ways.)
+constexpr int64_t kStagedBytes = int64_t{32} << 20;
+constexpr int kStagedElements = 16384;  // of a chunk
+constexpr int kBehindGroups = 64;       // workgroups for all that is left of a sequence
 
-// How a call is cut. limit: rows of a sequence that are summed first; D + 1 for all.
+// How a call is cut.
 struct Plan {
-  int limit, behind;  // workgroups of a sequence that sum the rows behind them
+  bool staged;
   Split split;
   Cut cut;
 };
 Plan plan_of(int dtype, int64_t N, int D, int V, bool draft, bool tree) {
   const int64_t rows = N * (D + 1 + (draft ? D : 0)), bytes = rows * V * (dtype == 0 ? 4 : 2);
-  Plan p;
-  p.limit = D + 1;
-  p.behind = 0;
-  p.cut = cut_of(N, V);
-  p.split = split_of(dtype, rows, V);
-  if (D > 0 && bytes > (tree ? kStagedTree : kStagedChain)) {
-    p.limit = tree ? 1 : (D + 1) / 2;
-    if (p.limit > kFirstRows) p.limit = kFirstRows;
-    const int64_t per = dtype == 0 ? 4 : 8, nv = V / per, c = ceil_div(nv, kT * kStagedLayers);
-    p.split.chunks = static_cast<int>(c > 1 ? c : 1);
-    p.split.vecs = static_cast<int>(ceil_div(nv, p.split.chunks));
-    const int64_t left = (D + 1 - p.limit) * (draft ? 2 : 1) * p.split.chunks;
-    p.behind = static_cast<int>(left < kBehindGroups ? left : kBehindGroups);
+  Plan p{tree && D > 0 && bytes > kStagedBytes, split_of(dtype, rows, V), cut_of(N, V)};
+  if (p.staged) {
+    const int64_t nv = V / (dtype == 0 ? 4 : 8), c = ceil_div(V, kStagedElements);
+    p.split = Split{static_cast<int>(c), static_cast<int>(ceil_div(nv, c))};
   }
   return p;
 }
@@ -1398,22 +1369,25 @@ hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
   RowChunk* stats = reinterpret_cast<RowChunk*>(ws + l.stats);
   FinalPart* finals = reinterpret_cast<FinalPart*>(ws + l.finals);
   uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
-  const int rows = p.limit + (draft ? (p.limit < a.D ? p.limit : a.D) : 0), groups = greedy ? 1 : p.cut.groups;
+  const int targets = p.staged ? 1 : a.D + 1, groups = greedy ? 1 : p.cut.groups;
   // a launch holds at most 2^22 workgroups
-  const int64_t of_rows = static_cast<int64_t>(rows) * p.split.chunks;
+  const int64_t of_rows = static_cast<int64_t>(targets + (draft ? a.D : 0)) * p.split.chunks;
   int64_t per = of_rows > groups ? of_rows : groups;
-  per = per > p.behind ? per : p.behind;
+  if (p.staged && per < kBehindGroups) per = kBehindGroups;
   const int64_t step = (int64_t{1} << 22) / per > 0 ? (int64_t{1} << 22) / per : 1;
   for (int64_t i = 0; i < a.N; i += step) {
     const int64_t n = a.N - i < step ? a.N - i : step;
     auto grid = [&](int64_t of) { return dim3(static_cast<unsigned>(n * of)); };
-    hipLaunchKernelGGL((verify_rows_kernel<DT, greedy>), grid(of_rows), dim3(kT), 0, stream, a, p.split, p.limit, i, stats,
+    hipLaunchKernelGGL((verify_rows_kernel<DT, greedy>), grid(of_rows), dim3(kT), 0, stream, a, p.split, targets, i, stats,
                        arrived);
     if (const hipError_t e = hipGetLastError()) return e;
-    if (p.behind > 0) {
-      hipLaunchKernelGGL((verify_behind_kernel<DT, MODE>), grid(p.behind), dim3(kT), 0, stream, a, p.split, p.limit,
-                         p.behind, i, stats);
-      if (const hipError_t e = hipGetLastError()) return e;
+    if constexpr (!draft) {
+      for (int limit = 1; p.staged && limit <= 2; ++limit) {
+        const int of = limit == 1 ? p.split.chunks : kBehindGroups;
+        hipLaunchKernelGGL((verify_behind_kernel<DT, MODE>), grid(of), dim3(kT), 0, stream, a, p.split, limit, limit == 2,
+                           of, i, stats);
+        if (const hipError_t e = hipGetLastError()) return e;
+      }
     }
     if (greedy || p.cut.threads == kFew)
       hipLaunchKernelGGL((verify_final_kernel<DT, MODE, kFew>), grid(groups), dim3(kFew), 0, stream, a, p.split.chunks,
@@ -1437,7 +1411,7 @@ hipError_t launch_typed(int dtype, const VerifyArgs& a, hipStream_t stream) {
 
 int64_t verify_workspace(int dtype, int64_t N, int D, int V, bool draft_logits) {
   const int64_t chain = layout_of(plan_of(dtype, N, D, V, draft_logits, false), N, D, draft_logits).bytes;
-  const int64_t tree = layout_of(plan_of(dtype, N, D, V, draft_logits, true), N, D, draft_logits).bytes;
+  const int64_t tree = draft_logits ? 0 : layout_of(plan_of(dtype, N, D, V, false, true), N, D, false).bytes;
   return chain > tree ? chain : tree;
 }
 
