@@ -61,7 +61,19 @@ struct FinalPart {
   double left;   // of what is left: p's terms without the rejected tokens', or ratio * p's less q's where that is above 0
   double kept;   // of p's terms where it is
   double draft;  // of q's terms
-  double close;  // of p's terms where p and q are too close to tell which is larger
+};
+// Elements whose terms of p and q are too close to tell which is larger by the ratio
+// at hand are set apart, so many of a sequence.
+constexpr int kMaxClose = 64;
+struct Close {
+  double p, q;
+  double at;  // the element
+};
+// Where workgroups of a sequence meet.
+struct Meeting {
+  FinalPart* parts;   // of all workgroups' waves
+  Close* close;       // [kMaxClose]
+  uint32_t* arrived;  // workgroups that are done, elements set apart
 };
 
 // exp(x - ref) in 64 bits, 0 for -inf and NaN: 2^(n + r) with n whole and r in
@@ -294,7 +306,7 @@ struct WalkSmem {
 // that take: both sums again in 64 bits.
 constexpr double kClose = 1e-6;
 // Elements whose terms of p and q, by the ratio of such sums, differ by no more.
-constexpr double kBand = 4e-7;
+constexpr double kBand = 1e-6;
 
 // Draft j's token and the row that it follows; -1: it counts as not there.
 __device__ __forceinline__ void draft_of(const VerifyArgs& a, int64_t seq, int j, int n, int& token, int& node) {
@@ -704,7 +716,7 @@ __global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, Split spl
   const unsigned item = b / static_cast<unsigned>(split.chunks);
   const int r = static_cast<int>(item % static_cast<unsigned>(rows));
   const int64_t seq = seq0 + item / static_cast<unsigned>(rows);
-  if (r == 0 && ch == 0 && threadIdx.x == 0) arrived[seq] = 0;
+  if (r == 0 && ch == 0 && threadIdx.x < 2) arrived[2 * seq + threadIdx.x] = 0;
   const bool target = r < targets;
   const int w = target ? r : r - targets;
   const int n = draft_count(a, seq);
@@ -727,6 +739,7 @@ struct FinalSmem : std::conditional_t<kTabled<DT, THREADS> && MODE != kGreedy, T
   int outs;
   double sum[4][kWaves];
   double parts[kFew];  // where summed again
+  Close close[kMaxClose];
   uint64_t is[kWaves], may[kWaves];
   double below;
   int last;
@@ -843,8 +856,9 @@ __device__ __forceinline__ double if_or_none(bool is, double v) {
   return __builtin_bit_cast(double, (static_cast<uint64_t>(high) << 32) | static_cast<uint32_t>(u));
 }
 
-// Eight elements' share of a part's sums; p > q where near * p's term > q's.
-__device__ __forceinline__ void add_terms(FinalPart& mine, const Terms& t, double near) {
+// Eight elements' share of a part's sums, v the first of them; p > q where near * p's
+// term > q's.
+__device__ __forceinline__ void add_terms(FinalPart& mine, const Terms& t, double near, int v, const Meeting& meet) {
   bool close = false;
 #pragma unroll
   for (int j = 0; j < kBlock; ++j) {
@@ -864,7 +878,20 @@ __device__ __forceinline__ void add_terms(FinalPart& mine, const Terms& t, doubl
         p = j == k ? t.p[k] : p;
         q = j == k ? t.q[k] : q;
       }
-      if (__builtin_fabs(__builtin_fma(near, p, -q)) < kBand * q) mine.close += p;
+      const double more = __builtin_fma(near, p, -q);
+      if (__builtin_fabs(more) < kBand * q) {
+        if (more > 0.0) {
+          mine.left -= more;
+          mine.kept -= p;
+        }
+        const uint32_t at =
+            __hip_atomic_fetch_add(&meet.arrived[1], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (at < kMaxClose) {
+          put_far(&meet.close[at].p, p);
+          put_far(&meet.close[at].q, q);
+          put_far(&meet.close[at].at, static_cast<double>(v + j));
+        }
+      }
     }
   }
 }
@@ -872,8 +899,8 @@ __device__ __forceinline__ void add_terms(FinalPart& mine, const Terms& t, doubl
 // Sums over a wave's part of the row, of every lane's elements.
 template <class DT, Mode MODE, class Smem>
 __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, const typename DT::raw_t* qrow, int first,
-                                             int pieces, int V, const Walk& w, const Smem& sm) {
-  FinalPart mine{0.0, 0.0, 0.0, 0.0, 0.0};
+                                             int pieces, int V, const Walk& w, const Smem& sm, const Meeting& meet) {
+  FinalPart mine{0.0, 0.0, 0.0, 0.0};
   const Rows least = least_of(w);
   const int lane = threadIdx.x % kWave;
   if (MODE == kDrawn && w.kind == kResidual) {
@@ -883,7 +910,7 @@ __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, con
       const int v = first + i * kPiece + lane * kBlock;
       Terms t;
       if (!terms_at<DT>(prow, qrow, v, V, w, least, true, t)) continue;
-      add_terms(mine, t, near);
+      add_terms(mine, t, near, v, meet);
     }
   } else {
     const bool outs = MODE != kDrawn && w.kind == kWithout && sm.outs != 0;
@@ -963,8 +990,9 @@ __device__ __forceinline__ bool all_masked(const vec_t& q) {
 }
 template <Mode MODE, class Smem>
 __device__ __forceinline__ FinalPart part_by_table(const uint16_t* prow, const uint16_t* qrow, int first, int pieces, int V,
-                                                   const Walk& w, const Smem& sm, const double (&table)[kTable]) {
-  FinalPart mine{0.0, 0.0, 0.0, 0.0, 0.0};
+                                                   const Walk& w, const Smem& sm, const double (&table)[kTable],
+                                                   const Meeting& meet) {
+  FinalPart mine{0.0, 0.0, 0.0, 0.0};
   const int lane = threadIdx.x % kWave;
   const bool two = MODE == kDrawn && w.kind == kResidual;
   const bool outs = MODE != kDrawn && w.kind == kWithout && sm.outs != 0;
@@ -986,7 +1014,7 @@ __device__ __forceinline__ FinalPart part_by_table(const uint16_t* prow, const u
     if (two) {
 #pragma unroll
       for (int j = 0; j < kBlock; j += 2) look_up(table, vword(yn, j / 2), t.q[j], t.q[j + 1]);
-      add_terms(mine, t, near);
+      add_terms(mine, t, near, v, meet);
     } else {
       double sum = 0.0;
 #pragma unroll
@@ -1042,36 +1070,54 @@ __device__ __forceinline__ int first_or_last(bool is, bool may, Smem& sm) {
 // Finds the token out of the parts' sums, by the first kFew threads (the other waves
 // have ended, and barriers wait for none of them).
 template <class DT, Mode MODE, class Smem>
-__device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, const FinalPart* slots, int parts, int pieces,
+__device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, const Meeting& meet, int parts, int pieces,
                                         const typename DT::raw_t* prow, const typename DT::raw_t* qrow,
                                         Smem& sm) {
   constexpr int THREADS = kFew, kWaves = THREADS / kWave;
   const int tid = threadIdx.x, span = pieces * kPiece;
   const bool two = MODE == kDrawn && w.kind == kResidual;
   const Rows least = least_of(w);
-  FinalPart p{0.0, 0.0, 0.0, 0.0, 0.0};
+  FinalPart p{0.0, 0.0, 0.0, 0.0};
+  uint32_t close = 0;
+  if (two) close = __hip_atomic_load(&meet.arrived[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   if (tid < parts) {
-    const FinalPart* from = slots + tid;
+    const FinalPart* from = meet.parts + tid;
     p.all = get_far(&from->all);
     p.left = get_far(&from->left);
     if (two) {
       p.kept = get_far(&from->kept);
       p.draft = get_far(&from->draft);
-      p.close = get_far(&from->close);
     }
   }
-  double total[3] = {p.all, p.draft, p.close};
+  double total[2] = {p.all, p.draft};
   block_sums(total, sm.sum);
   Weights weights{two ? total[1] / total[0] : 1.0, two, MODE != kDrawn && w.kind == kWithout};
   const double near = two ? w.q.sum / w.p.sum : 1.0, off = weights.scale - near;
-  double part = __builtin_fmax(two ? __builtin_fma(off, p.kept, p.left) : p.left, 0.0);
+  double part = two ? __builtin_fma(off, p.kept, p.left) : p.left;
+  if (two && close != 0) {
+    if (close <= kMaxClose && __builtin_fabs(off) <= 0.5 * kBand * near) {
+      // what was set apart, in the order of the elements
+      if (tid < static_cast<int>(close)) sm.close[tid] = Close{get_far(&meet.close[tid].p), get_far(&meet.close[tid].q),
+                                                               get_far(&meet.close[tid].at)};
+      __syncthreads();
+      double done = -1.0;
+      for (;;) {
+        int next = -1;
+        for (int i = 0; i < static_cast<int>(close); ++i) {
+          const double at = sm.close[i].at;
+          if (at > done && static_cast<int>(at) / span == tid && (next < 0 || at < sm.close[next].at)) next = i;
+        }
+        if (next < 0) break;
+        done = sm.close[next].at;
+        part += __builtin_fmax(__builtin_fma(weights.scale, sm.close[next].p, -sm.close[next].q), 0.0);
+      }
+      close = 0;
+    }
+  }
+  part = __builtin_fmax(part, 0.0);
   double below, upto, all;
-  block_scan(part, below, upto, all, sm.sum);
-  // Elements between the parts' ratio of the sums and the one in 64 bits are taken
-  // in or left out by mistake, each with no more than their difference. That is
-  // next to nothing (some 1e-8 of some 1e-7 of the mass) unless the rows are alike;
-  // then the parts are summed again.
-  if (two && (__builtin_fabs(off) * total[2] > 0x1p-43 * all || __builtin_fabs(off) > 0.5 * kBand * near)) {
+  if (two && (close != 0 || __builtin_fabs(off) > 0.5 * kBand * near)) {
+    // the rows are alike: the parts are summed again with the ratio of the sums in 64 bits
     for (int c0 = 0; c0 < parts; c0 += kWaves) {
       const int c = c0 + tid / kWave;
       double sum = 0.0;
@@ -1096,8 +1142,8 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
     }
     __syncthreads();
     part = tid < parts ? sm.parts[tid] : 0.0;
-    block_scan(part, below, upto, all, sm.sum);
   }
+  block_scan(part, below, upto, all, sm.sum);
   if (w.kind != kPlain && !(all > kLeast * (two ? total[1] : total[0]))) {
     weights.residual = weights.without = false;
     part = p.all;
@@ -1156,7 +1202,7 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
 // of a sequence's `groups` workgroups finds the token; -2 for the others.
 template <class DT, Mode MODE, int THREADS>
 __device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w, int64_t seq, int group, int groups,
-                                              int pieces, FinalPart* slots, uint32_t* arrived,
+                                              int pieces, const Meeting& meet,
                                               FinalSmem<DT, THREADS, MODE>& sm) {
   using raw_t = typename DT::raw_t;
   constexpr int kWaves = THREADS / kWave;
@@ -1170,31 +1216,29 @@ __device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w
   FinalPart mine;
   if constexpr (kTabled<DT, THREADS>) {
     if (w.p.ref == 0.0f && (!two || w.q.ref == 0.0f)) {
-      mine = part_by_table<MODE>(prow, qrow, c * span, pieces, a.V, w, sm, sm.table);
+      mine = part_by_table<MODE>(prow, qrow, c * span, pieces, a.V, w, sm, sm.table, meet);
     } else {
-      mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm);
+      mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm, meet);
     }
   } else {
-    mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm);
+    mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm, meet);
   }
   mine.all = wave_sum_f64(mine.all);
   mine.left = wave_sum_f64(mine.left);
   if (two) {
     mine.kept = wave_sum_f64(mine.kept);
     mine.draft = wave_sum_f64(mine.draft);
-    if (__ballot(mine.close != 0.0) != 0) mine.close = wave_sum_f64(mine.close);
   }
   if (tid % kWave == 0) {
-    put_far(&slots[c].all, mine.all);
-    put_far(&slots[c].left, mine.left);
+    put_far(&meet.parts[c].all, mine.all);
+    put_far(&meet.parts[c].left, mine.left);
     if (two) {
-      put_far(&slots[c].kept, mine.kept);
-      put_far(&slots[c].draft, mine.draft);
-      put_far(&slots[c].close, mine.close);
+      put_far(&meet.parts[c].kept, mine.kept);
+      put_far(&meet.parts[c].draft, mine.draft);
     }
   }
-  if (!last_of(arrived, groups, sm.last) || tid >= kFew) return -2;
-  return token_of<DT, MODE>(a, w, slots, parts, pieces, prow, qrow, sm);
+  if (!last_of(meet.arrived, groups, sm.last) || tid >= kFew) return -2;
+  return token_of<DT, MODE>(a, w, meet, parts, pieces, prow, qrow, sm);
 }
 
 struct BehindSmem {
@@ -1247,8 +1291,7 @@ __global__ __launch_bounds__(kT, DT::kPerVec == 4 ? 4 : 5) void verify_behind_ke
 template <class DT, Mode MODE, int THREADS>
 __global__ __launch_bounds__(THREADS) void verify_final_kernel(VerifyArgs a, int chunks, int groups, int pieces,
                                                                int64_t seq0, const RowChunk* __restrict__ stats,
-                                                               FinalPart* __restrict__ finals,
-                                                               uint32_t* __restrict__ arrived) {
+                                                               Meeting all) {
   __shared__ FinalSmem<DT, THREADS, MODE> sm;
   constexpr bool greedy = MODE == kGreedy;
   const int tid = threadIdx.x;
@@ -1269,8 +1312,8 @@ __global__ __launch_bounds__(THREADS) void verify_final_kernel(VerifyArgs a, int
   }
   if constexpr (!greedy) {
     if (!draws) return;
-    const int token = token_by_parts<DT, MODE, THREADS>(a, w, seq, group, groups, pieces,
-                                                        finals + seq * groups * (THREADS / kWave), &arrived[seq], sm);
+    const Meeting meet{all.parts + seq * groups * (THREADS / kWave), all.close + seq * kMaxClose, all.arrived + 2 * seq};
+    const int token = token_by_parts<DT, MODE, THREADS>(a, w, seq, group, groups, pieces, meet, sm);
     if (tid == 0 && token >= -1) tokens[w.count] = token;
   }
 }
@@ -1348,15 +1391,16 @@ Plan plan_of(int dtype, int64_t N, int D, int V, bool draft, bool tree) {
 }
 
 struct Layout {
-  int64_t stats, finals, arrived, bytes;
+  int64_t stats, finals, close, arrived, bytes;
 };
 Layout layout_of(const Plan& p, int64_t N, int D, bool draft) {
   const int64_t rows = N * (D + 1 + (draft ? D : 0));
   Layout l;
   l.stats = 0;
   l.finals = l.stats + rows * p.split.chunks * static_cast<int64_t>(sizeof(RowChunk));
-  l.arrived = l.finals + N * p.cut.groups * (p.cut.threads / kWave) * static_cast<int64_t>(sizeof(FinalPart));
-  l.bytes = l.arrived + N * 4;
+  l.close = l.finals + N * p.cut.groups * (p.cut.threads / kWave) * static_cast<int64_t>(sizeof(FinalPart));
+  l.arrived = l.close + (draft ? N * kMaxClose * static_cast<int64_t>(sizeof(Close)) : 0);
+  l.bytes = l.arrived + N * 8;
   return l;
 }
 
@@ -1367,8 +1411,8 @@ hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
   const Layout l = layout_of(p, a.N, a.D, draft);
   char* ws = static_cast<char*>(a.workspace);
   RowChunk* stats = reinterpret_cast<RowChunk*>(ws + l.stats);
-  FinalPart* finals = reinterpret_cast<FinalPart*>(ws + l.finals);
-  uint32_t* arrived = reinterpret_cast<uint32_t*>(ws + l.arrived);
+  const Meeting meet{reinterpret_cast<FinalPart*>(ws + l.finals), reinterpret_cast<Close*>(ws + l.close),
+                     reinterpret_cast<uint32_t*>(ws + l.arrived)};
   const int targets = p.staged ? 1 : a.D + 1, groups = greedy ? 1 : p.cut.groups;
   // a launch holds at most 2^22 workgroups
   const int64_t of_rows = static_cast<int64_t>(targets + (draft ? a.D : 0)) * p.split.chunks;
@@ -1379,7 +1423,7 @@ hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
     const int64_t n = a.N - i < step ? a.N - i : step;
     auto grid = [&](int64_t of) { return dim3(static_cast<unsigned>(n * of)); };
     hipLaunchKernelGGL((verify_rows_kernel<DT, greedy>), grid(of_rows), dim3(kT), 0, stream, a, p.split, targets, i, stats,
-                       arrived);
+                       meet.arrived);
     if (const hipError_t e = hipGetLastError()) return e;
     if constexpr (!draft) {
       for (int limit = 1; p.staged && limit <= 2; ++limit) {
@@ -1391,10 +1435,10 @@ hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
     }
     if (greedy || p.cut.threads == kFew)
       hipLaunchKernelGGL((verify_final_kernel<DT, MODE, kFew>), grid(groups), dim3(kFew), 0, stream, a, p.split.chunks,
-                         groups, p.cut.pieces, i, stats, finals, arrived);
+                         groups, p.cut.pieces, i, stats, meet);
     else if constexpr (!greedy)
       hipLaunchKernelGGL((verify_final_kernel<DT, MODE, kMany>), grid(groups), dim3(kMany), 0, stream, a, p.split.chunks,
-                         groups, p.cut.pieces, i, stats, finals, arrived);
+                         groups, p.cut.pieces, i, stats, meet);
     if (const hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
