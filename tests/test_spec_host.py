@@ -64,10 +64,11 @@ def test_verify_workspace(lib):
         assert f(*bad) == -1 and tk.last_error()
     assert f(0, 0, 1, 10, 0) >= 16 and f(0, 1, 0, 0, 0) >= 16
     assert tk.speculative_verify_workspace(torch.bfloat16, 64, 4, 151936, True) == f(2, 64, 4, 151936, 1)
-    assert f(2, 64, 4, 151936, 0) < f(2, 64, 4, 151936, 1)
+    assert f(2, 64, 4, 151936, 0) > 16 and f(2, 64, 4, 151936, 1) > f(2, 63, 4, 151936, 1)
     with pytest.raises(tk.TopKTopPError):
         tk.speculative_verify_workspace(torch.float32, 1, 300, 10)
-    assert 0 < f(0, (1 << 31) // 511 - 1, 255, 1 << 20, 0) < f(0, (1 << 31) // 511 - 1, 255, 1 << 20, 1)
+    # the largest sizes stay within an int64
+    assert f(0, (1 << 31) // 511 - 1, 255, 1 << 20, 0) > 1 << 32 and f(0, (1 << 31) // 511 - 1, 255, 1 << 20, 1) > 1 << 32
 
 
 def fork(lib, **kw):

@@ -672,16 +672,28 @@ def _row_strided(t, name, shape, dtype, device):
     return shape[1] if shape[0] <= 1 else ld
 
 
+@functools.lru_cache(maxsize=256)
+def _verify_bytes(dtype, N, D, V, draft_logits):
+    size = load_library().speculative_verify_workspace(dtype, N, D, V, draft_logits)
+    if size < 0:
+        raise TopKTopPError(2, last_error())
+    return size
+
+
+@functools.lru_cache(maxsize=256)
+def _resize_bytes(R, P):
+    size = load_library().cache_pages_resize_workspace(R, P)
+    if size < 0:
+        raise TopKTopPError(2, last_error())
+    return size
+
+
 def speculative_verify_workspace(dtype, N, D, V, draft_logits=False):
     """Bytes of the workspace that speculative_verify takes for N sequences of
     D drafts, V tokens and torch dtype `dtype`, with draft logits or without."""
     import torch
 
-    size = load_library().speculative_verify_workspace(
-        _dtype_code(torch.empty(0, dtype=dtype)), int(N), int(D), int(V), int(bool(draft_logits)))
-    if size < 0:
-        raise TopKTopPError(2, last_error())
-    return size
+    return _verify_bytes(_dtype_code(torch.empty(0, dtype=dtype)), int(N), int(D), int(V), int(bool(draft_logits)))
 
 
 def speculative_verify(logits, drafts, uniforms=None, draft_logits=None, parents=None, lengths=None, out=None,
@@ -751,9 +763,7 @@ def speculative_verify(logits, drafts, uniforms=None, draft_logits=None, parents
         if path is not None:
             _check_dense(path, (N, D), torch.int32, "out path", dev)
         if workspace is None:
-            size = lib.speculative_verify_workspace(dtype, N, D, V, int(p_draft is not None))
-            if size < 0:
-                raise TopKTopPError(2, last_error())
+            size = _verify_bytes(dtype, N, D, V, int(p_draft is not None))
             workspace = torch.empty(size, dtype=torch.uint8, device=logits.device)
         else:
             size = workspace.numel()
@@ -791,21 +801,29 @@ def _page_caches(caches, P, page_size, page_dim, slot_dim, dev):
     import torch
 
     tensors = [caches] if isinstance(caches, torch.Tensor) else list(caches)
+    recorded = torch.is_grad_enabled()
     descs = []
+    shape = stride = dtype = desc = None
     for t in tensors:
         if t.get_device() != dev:
             raise ValueError(f"tensors must share one device: a cache is on {t.device}")
-        if t.is_neg() or (t.is_complex() and t.is_conj()):
-            raise ValueError("a cache must not be a lazily conjugated or negated view")
-        if t.requires_grad and torch.is_grad_enabled():
+        if recorded and t.requires_grad:
             raise ValueError("a cache that requires grad can only be changed under no_grad")
-        dims = t.dim()
-        if not (-dims <= page_dim < dims and -dims <= slot_dim < dims) or (page_dim - slot_dim) % dims == 0:
-            raise ValueError(f"a cache of {dims} axes has no page_dim {page_dim} and slot_dim {slot_dim}")
-        if t.shape[page_dim] != P or t.shape[slot_dim] != page_size:
-            raise ValueError(f"a cache must have {P} pages of {page_size} slots, got shape {tuple(t.shape)}")
+        if t.is_neg():
+            raise ValueError("a cache must not be a lazily negated view")
+        # the caches of a model's layers are alike: one description for all
+        if t.dtype != dtype or t.shape != shape or t.stride() != stride or t.is_complex():
+            shape, stride, dtype = t.shape, t.stride(), t.dtype
+            if t.is_conj():
+                raise ValueError("a cache must not be a lazily conjugated view")
+            dims = t.dim()
+            if not (-dims <= page_dim < dims and -dims <= slot_dim < dims) or (page_dim - slot_dim) % dims == 0:
+                raise ValueError(f"a cache of {dims} axes has no page_dim {page_dim} and slot_dim {slot_dim}")
+            if shape[page_dim] != P or shape[slot_dim] != page_size:
+                raise ValueError(f"a cache must have {P} pages of {page_size} slots, got shape {tuple(shape)}")
+            desc = _state_bytes(shape, stride, t.element_size(), page_dim, slot_dim, P)
         descs.append(_pack_pointer(t.data_ptr()))
-        descs.append(_state_bytes(t.shape, t.stride(), t.element_size(), page_dim, slot_dim, P))
+        descs.append(desc)
     return tensors, b"".join(descs)
 
 
@@ -838,10 +856,7 @@ def cache_pages_fork(tables, lengths, parents, uses, page_size, stream=None):
 
 def cache_pages_resize_workspace(R, P):
     """Bytes of the workspace that cache_pages_resize takes for R rows and P pages."""
-    size = load_library().cache_pages_resize_workspace(int(R), int(P))
-    if size < 0:
-        raise TopKTopPError(2, last_error())
-    return size
+    return _resize_bytes(int(R), int(P))
 
 
 def cache_pages_resize(tables, lengths, new_lengths, uses, page_size, caches=None, page_dim=0, slot_dim=1,
@@ -879,7 +894,7 @@ def cache_pages_resize(tables, lengths, new_lengths, uses, page_size, caches=Non
     handle, scope = _scope(stream, tables.device)
     with scope:
         if workspace is None:
-            size = cache_pages_resize_workspace(R, P)
+            size = _resize_bytes(R, P)
             workspace = torch.empty(size, dtype=torch.uint8, device=tables.device)
         else:
             size = workspace.numel()

@@ -88,9 +88,10 @@ __global__ __launch_bounds__(kMaxBeams) void pages_fork_lengths_kernel(PageTable
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / kWave;
-constexpr int kScan = 16;      // pages of a thread in one step through the pool
-constexpr int kFewPages = 4;   // more pages of a row are handled by the whole workgroup
-constexpr int kManyRows = 64;  // such rows at a time
+constexpr int kScan = 16;     // pages of a thread in a group, which a step through the pool has four of
+constexpr int kScanGroups = 4;
+static_assert(kPlanThreads * kScan < 1 << 16);
+constexpr int kFewPages = 4;  // more pages of a row are handled by the whole workgroup
 
 // One page copied: `slots` slots of page `from` to page `to`.
 struct PageCopy {
@@ -101,43 +102,49 @@ struct ResizePlan {
   int32_t pad[3];
 };
 
+enum Tail : int32_t { kNoTail = 0, kOwn = 1, kKeeps = 2, kCopies = 3 };
 struct RowPlan {
   int32_t old_len, new_len;
   int32_t old_pages, new_pages;
-  int32_t tail;      // the last page, if the row is going to write into it; -1
-  int32_t first;     // place of its first new page among the free ones
-  int32_t copies;    // 1: its tail is copied
-  int32_t keeps;     // 1: its tail is left to it by the others that share it
+  int32_t page;   // the last page, if the row is going to write into it
+  int32_t tail;   // kOwn: nobody else uses it; kKeeps: the others leave it to this row; kCopies: they do not
+  int32_t first;  // place of its first new page among the free ones
+  int32_t serve;  // 1: the row gets what it needs
 };
 
 struct PlanSmem {
-  uint32_t scan[kPlanWaves];
-  int32_t many[kManyRows];
-  int32_t many_count;
+  uint64_t scan[kPlanWaves];
+  int32_t many[2][kPlanThreads];  // rows that give back or get many pages
+  int32_t many_count[2];
+  int32_t shared;   // 1: a row writes into a page that is not its own
   int32_t blocked;  // the first row that would have to copy where nothing can be
   int32_t copies;
 };
 
 // The sum of v over the threads below, and of all.
-__device__ __forceinline__ uint32_t plan_below(uint32_t v, uint32_t& all, PlanSmem& sm) {
+__device__ __forceinline__ uint64_t plan_below(uint64_t v, uint64_t& all, PlanSmem& sm) {
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-  const uint32_t upto = wave_incl_scan_u32(v);
+  const uint64_t upto = wave_incl_scan_u64(v);
   __syncthreads();
   if (lane == kWave - 1) sm.scan[wave] = upto;
   __syncthreads();
-  const uint32_t of = lane < kPlanWaves ? sm.scan[lane] : 0u;
-  const uint32_t sums = wave_incl_scan_u32(of);
-  all = readlane_u32(sums, kPlanWaves - 1);
-  const uint32_t before = wave == 0 ? 0u : readlane_u32(sums, wave - 1);
+  const uint64_t of = lane < kPlanWaves ? sm.scan[lane] : 0ull;
+  const uint64_t sums = wave_incl_scan_u64(of);
+  all = readlane_u64(sums, kPlanWaves - 1);
+  const uint64_t before = wave == 0 ? 0ull : readlane_u64(sums, wave - 1);
   return before + upto - v;
 }
 
 __device__ __forceinline__ int32_t load_now(const int32_t* p) {
   return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
+__device__ __forceinline__ void store_now(int32_t* p, int32_t v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
 
-// Everything but the copies, by one workgroup: releases, tails, needs, free pages,
-// tables. ONE: a row for each thread, which keeps its plan in registers.
+// Everything but the copies, by one workgroup: releases, last pages, needs, free
+// pages, tables. It is a chain of dependent steps: lengths, last page, its uses, the
+// free pages. ONE: a row for each thread, which keeps its plan in registers.
 template <bool ONE>
 __global__ __launch_bounds__(kPlanThreads) void pages_resize_kernel(PageTable t, const int32_t* __restrict__ new_lengths,
                                                                    bool can_copy, RowPlan* __restrict__ plans,
@@ -155,165 +162,163 @@ __global__ __launch_bounds__(kPlanThreads) void pages_resize_kernel(PageTable t,
       for (int64_t r = tid; r < t.R; r += kPlanThreads) f(r, plans[r]);
     }
   };
-  // f(r, i) for every i below count(r) of the rows, by the whole workgroup where that is more than a few
-  auto each_page = [&](auto count, auto f) {
-    const int64_t end = ONE ? kPlanThreads : (t.R + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
-    for (int64_t r0 = 0; r0 < end; r0 += kPlanThreads) {
-      const int64_t r = r0 + tid;
-      const int n = r < t.R ? count(r) : 0;
-      bool left = n > kFewPages;
-      if (!left)
-        for (int i = 0; i < n; ++i) f(r, i, n);
-      for (;;) {
-        __syncthreads();
-        if (tid == 0) sm.many_count = 0;
-        __syncthreads();
-        if (left) {
-          const int at = atomicAdd(&sm.many_count, 1);
-          if (at < kManyRows) {
-            sm.many[at] = tid;
-            left = false;
-          }
-        }
-        __syncthreads();
-        const int listed = sm.many_count < kManyRows ? sm.many_count : kManyRows;
-        if (sm.many_count == 0) break;
-        for (int k = 0; k < listed; ++k) {
-          const int64_t q = r0 + sm.many[k];
-          const int m = count(q);
-          for (int i = tid; i < m; i += kPlanThreads) f(q, i, m);
-        }
+  // f(r, plan, i) for every page i below count(plan) of the rows: by their threads
+  // where these are few, else by a wave or, of few such rows, all waves, which need
+  // the plan in memory
+  auto each_page = [&](int which, auto count, auto f) {
+    rows([&](int64_t r, RowPlan& p) {
+      const int n = count(p);
+      int at = kPlanThreads;
+      if (n > kFewPages) at = atomicAdd(&sm.many_count[which], 1);
+      if (at < kPlanThreads) {
+        if constexpr (ONE) plans[r] = p;
+        sm.many[which][at] = static_cast<int32_t>(r);
+      } else {
+        for (int i = 0; i < n; ++i) f(r, p, i);
       }
+    });
+    __syncthreads();
+    const int n = sm.many_count[which] < kPlanThreads ? sm.many_count[which] : kPlanThreads;
+    const int lanes = n < kPlanWaves ? kPlanThreads : kWave;
+    for (int k = tid / lanes; k < n; k += kPlanThreads / lanes) {
+      const int64_t r = sm.many[which][k];
+      const RowPlan p = plans[r];
+      const int m = count(p);
+#pragma unroll 4
+      for (int i = tid % lanes; i < m; i += lanes) f(r, p, i);
     }
-  };
-  // what other threads need to know of a row comes from memory
-  auto lens = [&](int64_t r, int& old_len, int& new_len) -> bool {
-    old_len = t.lengths[r];
-    new_len = new_lengths[r];
-    const int64_t most = static_cast<int64_t>(t.C) * t.S;
-    return old_len >= 0 && old_len <= most && new_len >= 0 && new_len <= most;
   };
 
   if (tid == 0) {
+    sm.many_count[0] = sm.many_count[1] = 0;
+    sm.shared = 0;
     sm.blocked = 0x7FFFFFFF;
     sm.copies = 0;
   }
   rows([&](int64_t r, RowPlan& p) {
     p = RowPlan{};
-    p.tail = -1;
-    if (!lens(r, p.old_len, p.new_len)) p.old_len = p.new_len = 0;
+    p.old_len = t.lengths[r];
+    p.new_len = new_lengths[r];
+    const int64_t most = static_cast<int64_t>(t.C) * t.S;
+    if (p.old_len < 0 || p.old_len > most || p.new_len < 0 || p.new_len > most) p.old_len = p.new_len = 0;
     p.old_pages = pages_of(p.old_len, t.S, t.C);
     p.new_pages = pages_of(p.new_len, t.S, t.C);
-    if (p.new_len > p.old_len && p.old_len % t.S != 0) {
-      const int32_t page = t.tables[r * t.ld + p.old_pages - 1];
-      if (is_page(page, t.P)) p.tail = page;
+    p.page = -1;
+    if (p.new_len > p.old_len && p.old_len % t.S != 0) p.page = t.tables[r * t.ld + p.old_pages - 1];
+  });
+  __syncthreads();
+  // pages behind the rows' new ends
+  each_page(
+      0, [](const RowPlan& p) { return p.new_len < p.old_len ? p.old_pages - p.new_pages : 0; },
+      [&](int64_t r, const RowPlan& p, int i) {
+        int32_t* entry = t.tables + r * t.ld + p.new_pages + i;
+        if (is_page(*entry, t.P)) atomicSub(&t.uses[*entry], 1);
+        *entry = -1;
+      });
+  // Rows that write into a page leave it. Where none stays, the last of them takes it
+  // again, marked by -1 - row. If every row was its page's only user that is all;
+  // else the last one is found by the smallest of the marks.
+  rows([&](int64_t, RowPlan& p) {
+    if (!is_page(p.page, t.P)) return;
+    p.tail = kCopies;
+    if (atomicSub(&t.uses[p.page], 1) != 1) sm.shared = 1;
+  });
+  __syncthreads();
+  const bool shared = sm.shared != 0;
+  rows([&](int64_t r, RowPlan& p) {
+    if (p.tail == kNoTail) return;
+    if (!shared) {
+      p.tail = kOwn;
+      store_now(&t.uses[p.page], static_cast<int32_t>(-1 - r));
+    } else if (load_now(&t.uses[p.page]) <= 0) {
+      atomicMin(&t.uses[p.page], static_cast<int32_t>(-1 - r));
     }
   });
-  // pages behind the rows' new ends
-  auto released = [&](int64_t r) -> int {
-    int a, b;
-    return lens(r, a, b) && b < a ? pages_of(a, t.S, t.C) - pages_of(b, t.S, t.C) : 0;
-  };
-  each_page(released, [&](int64_t r, int i, int n) {
-    int32_t* entry = t.tables + r * t.ld + pages_of(t.lengths[r], t.S, t.C) - n + i;
-    if (is_page(*entry, t.P)) atomicSub(&t.uses[*entry], 1);
-    *entry = -1;
-  });
-  // Rows that write into a page leave it; where none stays, the last of them takes
-  // it again, marked by -1 - row while it is found.
-  rows([&](int64_t, RowPlan& p) {
-    if (p.tail >= 0) atomicSub(&t.uses[p.tail], 1);
-  });
-  __syncthreads();
-  rows([&](int64_t r, RowPlan& p) {
-    if (p.tail >= 0 && load_now(&t.uses[p.tail]) <= 0) atomicMin(&t.uses[p.tail], static_cast<int32_t>(-1 - r));
-  });
-  __syncthreads();
-  rows([&](int64_t r, RowPlan& p) {
-    if (p.tail < 0) return;
-    p.keeps = load_now(&t.uses[p.tail]) == static_cast<int32_t>(-1 - r) ? 1 : 0;
-    p.copies = 1 - p.keeps;
-    if (p.copies && !can_copy) atomicMin(&sm.blocked, static_cast<int32_t>(r));
-  });
+  if (shared) {
+    __syncthreads();
+    rows([&](int64_t r, RowPlan& p) {
+      if (p.tail != kCopies) return;
+      if (load_now(&t.uses[p.page]) == static_cast<int32_t>(-1 - r)) p.tail = kKeeps;
+      else if (!can_copy) atomicMin(&sm.blocked, static_cast<int32_t>(r));
+    });
+  }
   // what the rows need, one behind the other
-  uint32_t need_all = 0;
+  const uint64_t cap = static_cast<uint64_t>(t.P) + 1;  // more than there can be
+  uint64_t need_all = 0;
   const int64_t end = ONE ? kPlanThreads : (t.R + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
   auto need_of = [](const RowPlan& p) -> uint32_t {
-    return p.new_len > p.old_len ? static_cast<uint32_t>(p.new_pages - p.old_pages + p.copies) : 0u;
+    return p.new_len > p.old_len ? static_cast<uint32_t>(p.new_pages - p.old_pages) + (p.tail == kCopies ? 1u : 0u) : 0u;
   };
-  const uint32_t cap = static_cast<uint32_t>(t.P) + 1u;  // more than there can be
   for (int64_t r0 = 0; r0 < end; r0 += kPlanThreads) {
     const int64_t r = r0 + tid;
     RowPlan* p = nullptr;
     if constexpr (ONE) p = &held;
     else if (r < t.R) p = &plans[r];
-    uint32_t need = p != nullptr && r < t.R ? need_of(*p) : 0u;
-    need = need < cap ? need : cap;
-    uint32_t all;
-    uint32_t below = plan_below(need, all, sm);
-    below = below < cap - need_all ? need_all + below : cap;
-    if (p != nullptr && r < t.R) p->first = static_cast<int32_t>(below);
-    need_all = all < cap - need_all ? need_all + all : cap;
+    const bool is = p != nullptr && r < t.R;
+    uint64_t all;
+    const uint64_t below = need_all + plan_below(is ? need_of(*p) : 0u, all, sm);
+    if (is) p->first = static_cast<int32_t>(below < cap ? below : cap);
+    need_all += all;
   }
   // the free pages, from the lowest on
-  __threadfence();
-  __syncthreads();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
   uint32_t found = 0;
-  for (int64_t p0 = 0; p0 < t.P && found < need_all; p0 += static_cast<int64_t>(kPlanThreads) * kScan) {
-    const int64_t base = p0 + static_cast<int64_t>(tid) * kScan;
-    uint32_t mask = 0;
-    if (base + kScan <= t.P) {
-      int32_t u[kScan];
-      __builtin_memcpy(u, t.uses + base, sizeof(u));
+  for (int64_t p0 = 0; p0 < t.P && found < need_all; p0 += int64_t{kScanGroups} * kPlanThreads * kScan) {
+    uint32_t mask[kScanGroups];
+    uint64_t counts = 0;  // of the groups, 16 bits each: a group has kPlanThreads * kScan pages
 #pragma unroll
-      for (int i = 0; i < kScan; ++i) mask |= (u[i] == 0 ? 1u : 0u) << i;
-    } else {
-      for (int i = 0; i < kScan; ++i)
-        if (base + i < t.P && t.uses[base + i] == 0) mask |= 1u << i;
+    for (int g = 0; g < kScanGroups; ++g) {
+      const int64_t base = p0 + (static_cast<int64_t>(g) * kPlanThreads + tid) * kScan;
+      mask[g] = 0;
+      if (base + kScan <= t.P) {
+        int32_t u[kScan];
+        __builtin_memcpy(u, t.uses + base, sizeof(u));
+#pragma unroll
+        for (int i = 0; i < kScan; ++i) mask[g] |= (u[i] == 0 ? 1u : 0u) << i;
+      } else {
+        for (int i = 0; i < kScan; ++i)
+          if (base + i < t.P && t.uses[base + i] == 0) mask[g] |= 1u << i;
+      }
+      counts |= static_cast<uint64_t>(__builtin_popcount(mask[g])) << (16 * g);
     }
-    uint32_t all;
-    uint32_t at = found + plan_below(__builtin_popcount(mask), all, sm);
-    for (; mask != 0 && at < need_all; mask &= mask - 1, ++at)
-      pool[at] = static_cast<int32_t>(base + __builtin_ctz(mask));
-    found += all;
+    uint64_t all;
+    const uint64_t below = plan_below(counts, all, sm);
+#pragma unroll
+    for (int g = 0; g < kScanGroups; ++g) {
+      uint32_t at = found + static_cast<uint32_t>(below >> (16 * g) & 0xFFFFu);
+      const int64_t base = p0 + (static_cast<int64_t>(g) * kPlanThreads + tid) * kScan;
+      for (uint32_t m = mask[g]; m != 0 && at < need_all; m &= m - 1, ++at)
+        pool[at] = static_cast<int32_t>(base + __builtin_ctz(m));
+      found += static_cast<uint32_t>(all >> (16 * g) & 0xFFFFu);
+    }
   }
   __syncthreads();
   const int64_t blocked = sm.blocked;
-  auto served = [&](int64_t r, const RowPlan& p) -> bool {
-    return p.new_len > p.old_len && r < blocked && static_cast<uint32_t>(p.first) + need_of(p) <= found;
-  };
-  rows([&](int64_t, RowPlan& p) {
-    if (p.keeps) __hip_atomic_store(&t.uses[p.tail], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  });
-  __syncthreads();
+  if (shared) {
+    rows([&](int64_t, RowPlan& p) {
+      if (p.tail == kKeeps) store_now(&t.uses[p.page], 0);
+    });
+    __syncthreads();
+  }
   rows([&](int64_t r, RowPlan& p) {
-    const bool go = served(r, p);
-    if (p.tail >= 0 && (p.keeps || !go)) atomicAdd(&t.uses[p.tail], 1);
-    if (go && p.copies) {
-      const int32_t page = pool[p.first];
+    p.serve = p.new_len > p.old_len && r < blocked && static_cast<uint64_t>(p.first) + need_of(p) <= found ? 1 : 0;
+    if (p.tail == kOwn) store_now(&t.uses[p.page], 1);
+    else if (p.tail == kKeeps || (p.tail == kCopies && !p.serve)) atomicAdd(&t.uses[p.page], 1);
+    if (p.serve && p.tail == kCopies) {
+      const int32_t page = pool[p.first++];
       t.tables[r * t.ld + p.old_pages - 1] = page;
-      __hip_atomic_store(&t.uses[page], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      copies[atomicAdd(&sm.copies, 1)] = PageCopy{p.tail, page, p.old_len % t.S};
+      store_now(&t.uses[page], 1);
+      copies[atomicAdd(&sm.copies, 1)] = PageCopy{p.page, page, p.old_len % t.S};
     }
-    // for the pages behind: where they lie in the pool, or -1
-    plans[r].first = go ? p.first + p.copies : -1;
-    plans[r].old_pages = p.old_pages;
+    if (p.serve || p.new_len < p.old_len) t.lengths[r] = p.new_len;
   });
-  __threadfence_block();
-  __syncthreads();
-  auto added = [&](int64_t r) -> int {
-    int a, b;
-    return plans[r].first >= 0 && lens(r, a, b) && b > a ? pages_of(b, t.S, t.C) - pages_of(a, t.S, t.C) : 0;
-  };
-  each_page(added, [&](int64_t r, int i, int) {
-    const int32_t page = pool[plans[r].first + i];
-    t.tables[r * t.ld + plans[r].old_pages + i] = page;
-    __hip_atomic_store(&t.uses[page], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-  });
-  __syncthreads();
-  rows([&](int64_t r, RowPlan& p) {
-    if (p.new_len < p.old_len || plans[r].first >= 0) t.lengths[r] = p.new_len;
-  });
+  each_page(
+      1, [](const RowPlan& p) { return p.serve ? p.new_pages - p.old_pages : 0; },
+      [&](int64_t r, const RowPlan& p, int i) {
+        const int32_t page = pool[p.first + i];
+        t.tables[r * t.ld + p.old_pages + i] = page;
+        store_now(&t.uses[page], 1);
+      });
   if (tid == 0) out->copies = sm.copies;
 }
 
@@ -402,14 +407,19 @@ __global__ __launch_bounds__(kCompactThreads) void pages_compact_kernel(PageCach
   const unsigned tile = blockIdx.x % static_cast<unsigned>(tiles), item = blockIdx.x / static_cast<unsigned>(tiles);
   char* data = c.data[item % static_cast<unsigned>(c.count)];
   const int64_t seq = seq0 + item / static_cast<unsigned>(c.count);
+  // all that does not hang on one another at once
   int n = a.counts[seq];
+  const int64_t start = a.starts[seq], most = static_cast<int64_t>(a.C) * a.S;
+  int32_t at = tid < a.D ? a.path[seq * a.D + tid] : -1, before = tid > 0 && tid < a.D ? a.path[seq * a.D + tid - 1] : -1;
   n = n < a.D ? n : a.D;
   if (n <= 0) return;
-  const int64_t start = a.starts[seq], most = static_cast<int64_t>(a.C) * a.S;
   if (tid == 0) stop = n;
   __syncthreads();
   for (int j = tid; j < n; j += kCompactThreads) {
-    const int32_t at = a.path[seq * a.D + j], before = j > 0 ? a.path[seq * a.D + j - 1] : -1;
+    if (j >= kCompactThreads) {
+      at = a.path[seq * a.D + j];
+      before = a.path[seq * a.D + j - 1];
+    }
     const int64_t from = start + at, to = start + j;
     from_page[j] = to_page[j] = -1;
     if (at <= before || start < 0 || from >= most) {
