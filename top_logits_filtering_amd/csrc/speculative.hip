@@ -803,11 +803,16 @@ __device__ __forceinline__ void list_out(const VerifyArgs& a, const Walk& w, int
   }
   __syncthreads();
 }
+// Which of the elements v .. v + 7 are among them: bits.
 template <class Smem>
-__device__ __forceinline__ bool is_out(int v, const Smem& sm) {
-  bool out = false;
-  for (int i = 0; i < sm.outs; ++i) out |= sm.out[i] == v;
-  return out;
+__device__ __forceinline__ uint32_t outs_at(int v, const Smem& sm) {
+  uint32_t mask = 0;
+  const int n = sm.outs;
+  for (int i = 0; i < n; ++i) {
+    const uint32_t at = static_cast<uint32_t>(sm.out[i] - v);
+    if (at < kBlock) mask |= 1u << at;
+  }
+  return mask;
 }
 
 // The workgroup's sums of v[0 .. COUNT), in all threads.
@@ -924,9 +929,10 @@ __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, con
       for (int j = 0; j < kBlock; ++j) sum += t.p[j];
       mine.all += sum;
       if (outs) {
+        const uint32_t gone = outs_at(v, sm);
         sum = 0.0;
 #pragma unroll
-        for (int j = 0; j < kBlock; ++j) sum += is_out(v + j, sm) ? 0.0 : t.p[j];
+        for (int j = 0; j < kBlock; ++j) sum += (gone >> j & 1u) != 0 ? 0.0 : t.p[j];
       }
       mine.left += sum;
     }
@@ -1021,9 +1027,10 @@ __device__ __forceinline__ FinalPart part_by_table(const uint16_t* prow, const u
       for (int j = 0; j < kBlock; ++j) sum += t.p[j];
       mine.all += sum;
       if (outs) {
+        const uint32_t gone = outs_at(v, sm);
         sum = 0.0;
 #pragma unroll
-        for (int j = 0; j < kBlock; ++j) sum += is_out(v + j, sm) ? 0.0 : t.p[j];
+        for (int j = 0; j < kBlock; ++j) sum += (gone >> j & 1u) != 0 ? 0.0 : t.p[j];
       }
       mine.left += sum;
     }
@@ -1036,12 +1043,14 @@ struct Weights {
   double scale;
   bool residual, without;
   template <class Smem>
-  __device__ __forceinline__ double of(const Terms& t, int j, int v, const Smem& sm) const {
-    if (residual) {
-      const double more = __builtin_fma(scale, t.p[j], -t.q[j]);
-      return more > 0.0 ? more : 0.0;
+  __device__ __forceinline__ void of(const Terms& t, int v, const Smem& sm, double (&wt)[kBlock]) const {
+    uint32_t gone = 0;
+    if (without) gone = outs_at(v, sm);
+#pragma unroll
+    for (int j = 0; j < kBlock; ++j) {
+      const double more = residual ? __builtin_fma(scale, t.p[j], -t.q[j]) : t.p[j];
+      wt[j] = more > 0.0 && (gone >> j & 1u) == 0 ? more : 0.0;
     }
-    return without && is_out(v, sm) ? 0.0 : t.p[j];
   }
 };
 
@@ -1165,9 +1174,9 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
     int last = -1;  // the last element of any weight
     Terms t;
     if (terms_at<DT>(prow, qrow, v, a.V, w, least, two, t)) {
+      weights.of(t, v, sm, wt);
 #pragma unroll
       for (int j = 0; j < kBlock; ++j) {
-        wt[j] = weights.of(t, j, v + j, sm);
         sum += wt[j];
         if (wt[j] > 0.0) last = v + j;
       }
@@ -1372,7 +1381,14 @@ Cut cut_of(int64_t N, int V) {
 // rows read first, 54 all at once; 128 of 3 drafts, V 128256 fp32, 113 both ways.)
 constexpr int64_t kStagedBytes = int64_t{32} << 20;
 constexpr int kStagedElements = 16384;  // of a chunk
-constexpr int kBehindGroups = 64;       // workgroups for all that is left of a sequence
+// Workgroups for all that is left, as many as run at a time.
+constexpr int kBehindBlocks = 1280;
+int behind_groups(int64_t N, int D, const Split& split) {
+  const int64_t most = static_cast<int64_t>(D) * split.chunks;
+  int64_t g = kBehindBlocks / N;
+  g = g > split.chunks ? g : split.chunks;
+  return static_cast<int>(g < most ? g : most);
+}
 
 // How a call is cut.
 struct Plan {
@@ -1417,7 +1433,8 @@ hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
   // a launch holds at most 2^22 workgroups
   const int64_t of_rows = static_cast<int64_t>(targets + (draft ? a.D : 0)) * p.split.chunks;
   int64_t per = of_rows > groups ? of_rows : groups;
-  if (p.staged && per < kBehindGroups) per = kBehindGroups;
+  const int behind = p.staged ? behind_groups(a.N, a.D, p.split) : 0;
+  per = per > behind ? per : behind;
   const int64_t step = (int64_t{1} << 22) / per > 0 ? (int64_t{1} << 22) / per : 1;
   for (int64_t i = 0; i < a.N; i += step) {
     const int64_t n = a.N - i < step ? a.N - i : step;
@@ -1427,7 +1444,7 @@ hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
     if (const hipError_t e = hipGetLastError()) return e;
     if constexpr (!draft) {
       for (int limit = 1; p.staged && limit <= 2; ++limit) {
-        const int of = limit == 1 ? p.split.chunks : kBehindGroups;
+        const int of = limit == 1 ? p.split.chunks : behind;
         hipLaunchKernelGGL((verify_behind_kernel<DT, MODE>), grid(of), dim3(kT), 0, stream, a, p.split, limit, limit == 2,
                            of, i, stats);
         if (const hipError_t e = hipGetLastError()) return e;
