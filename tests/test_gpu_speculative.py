@@ -360,6 +360,65 @@ def test_close_decisions(V, dtype):
     assert 0 < a.sum() < N and 0 < b.sum() < N
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N", [3, 600])
+@pytest.mark.parametrize("mode", ["far", "alike"])
+def test_uniforms_at_the_ends(mode, N, dtype):
+    """Uniforms of 0, next to 1 and of 1, where the row begins and ends with tokens of next to no weight (far), or
+    where p and q are the same but for two tokens, so that the others' residuals are nothing but roundings. The token
+    has to be there, and its piece of [0, 1) to reach the uniform but for roundings: terms are off by up to 4e-14,
+    those of both rows together by 8e-14 of 1, of which the residual is a part m only: 1e-13 / m. The reference's sums
+    of 20000 terms are within 20000 2^-53 < 1e-11."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    rng = np.random.default_rng(N)
+    V, D = 20000, 1
+    base = head(rng, (N, D + 1, V), high=4.0)
+    drafts, y = np.zeros((N, D), np.int32), None
+    u = np.tile(np.array([[0.0, 0.0], [1 - 2.0 ** -24, 1 - 2.0 ** -24], [1.0, 1.0]]), (N // 3, 1))
+    lengths = None
+    t = getattr(torch, dtype)
+    if mode == "far":
+        base[:, :, :9000] = -100.0
+        base[:, :, -4000:] = -100.0
+        lengths = torch.zeros(N, dtype=torch.int32, device="cuda")
+    else:
+        # two of forty tokens swap their weights; the draft, the one that q has more of, is rejected
+        keep = np.argpartition(-base[:, 0] + 20 * (rng.random((N, V)) < 0.5), 40, axis=1)[:, :40]
+        few = np.full((N, V), -np.inf)
+        np.put_along_axis(few, keep, np.take_along_axis(base[:, 0], keep, 1), 1)
+        few[np.arange(N), keep[:, 5]] = 4.0
+        few[np.arange(N), keep[:, 6]] = 2.0
+        base[:, 0] = few
+        other = few.copy()
+        other[np.arange(N), keep[:, 5]] = 2.0
+        other[np.arange(N), keep[:, 6]] = 4.0
+        drafts[:, 0] = keep[:, 6]
+        u[:, 0] = 1 - 2.0 ** -24
+        y = on_gpu(torch, other, t)
+    x = on_gpu(torch, base.reshape(-1, V), t)
+    tokens, accepted, _ = tk.speculative_verify(x, torch.from_numpy(drafts).cuda(),
+                                                torch.from_numpy(np.float32(u)).cuda(), draft_logits=y, lengths=lengths)
+    got = tokens.cpu().numpy()
+    assert (accepted == 0).all() and (got[:, 0] >= 0).all() and (got[:, 0] < V).all()
+    xs = back(x).reshape(N, D + 1, V)[:, 0]
+    e = np.exp(xs - xs.max(1, keepdims=True))
+    r, m = e / e.sum(1, keepdims=True), np.ones(N)
+    if y is not None:
+        ys = back(y)
+        q = np.exp(ys - ys.max(1, keepdims=True))
+        r = np.maximum(r - q / q.sum(1, keepdims=True), 0.0)
+        m = r.sum(1)
+        assert m.min() > 1e-6
+        r /= m[:, None]
+    upto = np.cumsum(r, 1)
+    at = np.minimum(np.float32(u[:, D]).astype(np.float64), 1.0)
+    i = np.arange(N)
+    end, off = upto[i, got[:, 0]], 1e-11 + 1e-13 / m
+    assert (end - r[i, got[:, 0]] <= at + off).all() and (end >= at - off).all()
+
+
 def test_every_token_is_drawn_in_its_place():
     """One row, uniforms over all of [0, 1): each token's share, at the borders as well."""
     torch = need_gpu()

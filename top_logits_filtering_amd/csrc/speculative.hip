@@ -283,7 +283,6 @@ struct Walk {
   uint64_t best;
 };
 
-
 struct WalkSmem {
   int32_t token[kMaxRows];   // -1: the draft counts as not there
   int32_t node[kMaxRows];    // the row that it follows
@@ -1161,49 +1160,56 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
   }
   const double at = static_cast<double>(sm.walk.last_u) * all;
   // the part that `at` lies in; for a uniform out of range the first or the last one of any weight
-  const int c = first_or_last(upto > at && upto > below, upto > below, sm);
-  if (c < 0) return -1;
-  if (tid == c) sm.below = below;
-  __syncthreads();
-  double base = sm.below;
-  if constexpr (MODE == kProposed) list_out(a, w, c * span, (c + 1) * span, sm);
+  bool is = upto > at && upto > below, may = upto > below;
+  const double begin = below;
   int last_seen = -1;
+  for (;;) {
+    const int c = first_or_last(is, may, sm);
+    if (c < 0) break;
+    if (tid == c) sm.below = begin;
+    __syncthreads();
+    double base = sm.below;
+    if constexpr (MODE == kProposed) list_out(a, w, c * span, (c + 1) * span, sm);
 #pragma unroll 1
-  for (int i = 0; i < span; i += THREADS * kBlock) {
-    const int v = i + tid * kBlock < span ? c * span + i + tid * kBlock : a.V;
-    double wt[kBlock], sum = 0.0;
-    int last = -1;  // the last element of any weight
-    Terms t;
-    if (terms_at<DT>(prow, qrow, v, a.V, w, least, two, t)) {
-      weights.of(t, v, sm, wt);
-#pragma unroll
-      for (int j = 0; j < kBlock; ++j) {
-        sum += wt[j];
-        if (wt[j] > 0.0) last = v + j;
-      }
-    }
-    block_scan(sum, below, upto, all, sm.sum);
-    const bool here = last >= 0 && base + upto > at;
-    const int finder = first_or_last(here, last >= 0, sm);
-    if (finder >= 0) {
-      if (tid == finder) {
-        int token = last;
-        double reach = base + below;
+    for (int i = 0; i < span; i += THREADS * kBlock) {
+      const int v = i + tid * kBlock < span ? c * span + i + tid * kBlock : a.V;
+      double wt[kBlock], sum = 0.0;
+      int last = -1;  // the last element of any weight
+      Terms t;
+      if (terms_at<DT>(prow, qrow, v, a.V, w, least, two, t)) {
+        weights.of(t, v, sm, wt);
 #pragma unroll
         for (int j = 0; j < kBlock; ++j) {
-          reach += wt[j];
-          if (wt[j] > 0.0 && reach > at) token = token < v + j ? token : v + j;
+          sum += wt[j];
+          if (wt[j] > 0.0) last = v + j;
         }
-        sm.found = token;
-        sm.last = here ? 1 : 0;
       }
-      __syncthreads();
-      last_seen = sm.found;
-      const bool done = sm.last != 0;
-      __syncthreads();
-      if (done) break;
+      block_scan(sum, below, upto, all, sm.sum);
+      const bool here = last >= 0 && base + upto > at;
+      const int finder = first_or_last(here, last >= 0, sm);
+      if (finder >= 0) {
+        if (tid == finder) {
+          int token = last;
+          double reach = base + below;
+#pragma unroll
+          for (int j = 0; j < kBlock; ++j) {
+            reach += wt[j];
+            if (wt[j] > 0.0 && reach > at) token = token < v + j ? token : v + j;
+          }
+          sm.found = token;
+          sm.last = here ? 1 : 0;
+        }
+        __syncthreads();
+        last_seen = sm.found;
+        const bool done = sm.last != 0;
+        __syncthreads();
+        if (done) break;
+      }
+      base += all;
     }
-    base += all;
+    if (last_seen >= 0) break;
+    // its weight was but roundings, or elements that count as 0 here
+    if (tid == c) is = may = false;
   }
   return last_seen;
 }
@@ -1372,7 +1378,6 @@ Cut cut_of(int64_t N, int V) {
   }
   return best;
 }
-
 
 // A path through a tree needs few of its rows. Where there is much to read, the first
 // rows are summed before, then the one that each path goes on at, then what is left
