@@ -127,8 +127,8 @@ __device__ __forceinline__ void load_block(const typename DT::raw_t* row, int v,
 
 // What workgroups of one kernel tell each other goes past the caches of their dies:
 // stores and loads of device scope, in order by waiting for the stores. (A fence
-// of device scope writes back a die's whole cache: with one in every wave the
-// second kernel took 488 us instead of 35 for 128 rows of 128256 fp32.)
+// of device scope writes back a die's whole cache: with one in every wave the last
+// kernel took ten times as long.)
 __device__ __forceinline__ void put_far(double* to, double v) {
   __hip_atomic_store(to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -1336,23 +1336,31 @@ __global__ __launch_bounds__(THREADS) void verify_final_kernel(VerifyArgs a, int
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-constexpr int kTargetBlocks = 512;  // chunks wanted where rows are few
-constexpr int kMaxLayers = 32;      // vectors of a thread at most, 16-bit types (fp32: twice)
+constexpr int kUnits = 256;     // compute units
+constexpr int kMaxLayers = 32;  // vectors of a thread at most, 16-bit types (fp32: twice)
 
+// Chunks of few rows: no more of all than compute units, and none of less than a
+// group of vectors. (16 sequences of 4 drafts with draft logits, V 151936 bf16, take
+// 24.7 us, and 25.8 with twice as many chunks; 24 of 3, V 128256 fp32, 23.0 and 25.3.)
 Split split_of(int dtype, int64_t rows, int V) {
   const int64_t per = dtype == 0 ? 4 : 8;
   const int64_t nv = V / per;
   const int64_t largest = kT * kMaxLayers * 8 / per, smallest = kT * 32 / per;
   const int64_t least = ceil_div(nv, largest), most = ceil_div(nv, smallest);
-  int64_t c = rows > 0 ? ceil_div(kTargetBlocks, rows) : 1;
+  int64_t c = rows > 0 ? kUnits / rows : 1;
   c = c < most ? c : most;
   c = c > least ? c : least;
   c = c > 1 ? c : 1;
   return Split{static_cast<int>(c), static_cast<int>(ceil_div(nv, c))};
 }
 
-constexpr int kUnits = 256;      // compute units
+// Up to so many workgroups of kFew threads run at a time with what they hold of
+// shared memory, and one sequence alone is done sooner by them (V 151936 bf16, 5
+// drafts: 15.5 us and 16.7); beyond, kMany threads share one look at the path: 64
+// sequences of 4 drafts 52 us and 71, 128 of 3, V 128256 fp32, 113 and 156.
 constexpr int kFewBlocks = 512;
+// What a workgroup does besides, in pieces of a wave (counting none, 420 sequences
+// of 2 proposals, V 151936 bf16, are cut in 7 and take 217 us instead of 122).
 constexpr int kTurnPieces = 3;
 // Workgroups for the row where a sequence's path ends, their threads, and pieces of
 // their waves.
@@ -1380,12 +1388,14 @@ Cut cut_of(int64_t N, int V) {
 }
 
 // A path through a tree needs few of its rows. Where there is much to read, the first
-// rows are summed before, then the one that each path goes on at, then what is left
-// behind that: 32 trees of 39 drafts, three behind each, V 151936 bf16, take 55 us so,
-// 64 without the second step, 63 with one more like it, and 90 with all rows read.
+// rows are summed before, then (kStagedBytes) what is left behind the one that each
+// path goes on at, or (kTwiceBytes) first that one alone. Trees of 39 drafts, three
+// behind each, V 151936 bf16, with all rows read at once, one step and two: 4 of them
+// (49 MB) 24.8, 26.9 and 33.2 us, 8 (97 MB) 34.6, 31.0 and 35.2, 16 (194 MB) 49.1, 38.0
+// and 37.4, 32 80, 51 and 43.
 // (Chains do not gain: 64 of 4 drafts with draft logits take 59 us with half of their
 // rows read first, 54 all at once; 128 of 3 drafts, V 128256 fp32, 113 both ways.)
-constexpr int64_t kStagedBytes = int64_t{32} << 20;
+constexpr int64_t kStagedBytes = int64_t{80} << 20, kTwiceBytes = int64_t{160} << 20;
 constexpr int kStagedElements = 16384;  // of a chunk
 // Workgroups for all that is left, as many as run at a time.
 constexpr int kBehindBlocks = 1280;
@@ -1398,21 +1408,21 @@ int behind_groups(int64_t N, int D, const Split& split) {
 
 // How a call is cut.
 struct Plan {
-  bool staged;
+  int steps;  // of a tree, behind its first rows; 0: all rows at once
   Split split;
   Cut cut;
 };
 Plan plan_of(int dtype, int64_t N, int D, int V, bool draft, bool tree) {
   const int64_t rows = N * (D + 1 + (draft ? D : 0)), bytes = rows * V * (dtype == 0 ? 4 : 2);
-  Plan p{tree && D > 0 && bytes > kStagedBytes, split_of(dtype, rows, V), cut_of(N, V)};
-  if (p.staged) {
+  Plan p{tree && D > 0 ? (bytes > kStagedBytes) + (bytes > kTwiceBytes) : 0, split_of(dtype, rows, V), cut_of(N, V)};
+  if (p.steps > 0) {
     const int64_t nv = V / (dtype == 0 ? 4 : 8), c = ceil_div(V, kStagedElements);
     p.split = Split{static_cast<int>(c), static_cast<int>(ceil_div(nv, c))};
   }
   return p;
 }
 
-int targets_of(const Plan& p, int D) { return p.staged ? 1 : D + 1; }
+int targets_of(const Plan& p, int D) { return p.steps > 0 ? 1 : D + 1; }
 
 // Rows of no more than the last-level cache are left there: 64 sequences of 4 drafts,
 // 175 MB, take 54.0 us so and 56.3 past it, 128 of 3 drafts, 460 MB, 113.4 and 111.7.
@@ -1446,7 +1456,7 @@ hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
   // a launch holds at most 2^22 workgroups
   const int64_t of_rows = static_cast<int64_t>(targets + (draft ? a.D : 0)) * p.split.chunks;
   int64_t per = of_rows > groups ? of_rows : groups;
-  const int behind = p.staged ? behind_groups(a.N, a.D, p.split) : 0;
+  const int behind = p.steps > 0 ? behind_groups(a.N, a.D, p.split) : 0;
   per = per > behind ? per : behind;
   const int64_t step = (int64_t{1} << 22) / per > 0 ? (int64_t{1} << 22) / per : 1;
   for (int64_t i = 0; i < a.N; i += step) {
@@ -1460,10 +1470,11 @@ hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
                          i, stats, meet.arrived);
     if (const hipError_t e = hipGetLastError()) return e;
     if constexpr (!draft) {
-      for (int limit = 1; p.staged && limit <= 2; ++limit) {
-        const int of = limit == 1 ? p.split.chunks : behind;
-        hipLaunchKernelGGL((verify_behind_kernel<DT, MODE>), grid(of), dim3(kT), 0, stream, a, p.split, limit, limit == 2,
-                           of, i, stats);
+      for (int limit = 1; limit <= p.steps; ++limit) {
+        const bool all = limit == p.steps;
+        const int of = all ? behind : p.split.chunks;
+        hipLaunchKernelGGL((verify_behind_kernel<DT, MODE>), grid(of), dim3(kT), 0, stream, a, p.split, limit, all, of, i,
+                           stats);
         if (const hipError_t e = hipGetLastError()) return e;
       }
     }
