@@ -363,6 +363,24 @@ def test_beam_steps():
     assert int((uses > 0).sum()) < R * 5  # the beams of a prompt share their beginning
 
 
+def test_fork_of_a_long_row():
+    """More columns than one launch's threads; only the last ones and the first hold pages."""
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    C = (1 << 28) + 77
+    tables = torch.full((2, C), -1, dtype=torch.int32, device="cuda")
+    uses = torch.zeros(200, dtype=torch.int32, device="cuda")
+    at = torch.cat([torch.arange(3, device="cuda"), torch.arange(C - 150, C, device="cuda")])
+    tables[0, at] = torch.arange(153, dtype=torch.int32, device="cuda")
+    uses[:153] = 1
+    lengths = torch.tensor([C, 5], dtype=torch.int32, device="cuda")
+    tk.cache_pages_fork(tables, lengths, torch.zeros(1, 2, dtype=torch.int32, device="cuda"), uses, 1)
+    assert bool((tables[1] == tables[0]).all()) and bool((lengths == C).all())
+    assert bool((tables[0, at] == torch.arange(153, device="cuda")).all()) and int((tables[0] >= 0).sum()) == 153
+    assert bool((uses[:153] == 2).all()) and bool((uses[153:] == 0).all())
+
+
 def test_captured_steps():
     """Resize, compact and fork in a graph, replayed between eager work on the same pool."""
     torch = need_gpu()

@@ -26,11 +26,11 @@ __device__ __forceinline__ int pages_of(int length, int S, int C) {
 __device__ __forceinline__ bool is_page(int32_t page, int64_t P) { return page >= 0 && page < P; }
 
 // 64 columns of one prompt's rows. They pass through shared memory, as any row may
-// follow any other. LENGTHS: the prompt has no other workgroup, which would still
+// follow any other. The prompt's workgroups here begin at column tile0 * 64. LENGTHS: the prompt has no other workgroup, which would still
 // have to read the lengths.
 template <bool LENGTHS>
 __global__ __launch_bounds__(kForkThreads) void pages_fork_kernel(PageTable t, const int32_t* __restrict__ parents, int K,
-                                                                  int tiles, int64_t item0) {
+                                                                  int tiles, int tile0, int64_t item0) {
   __shared__ int32_t held[kMaxBeams][kForkCols];
   __shared__ int32_t parent[kMaxBeams];
   __shared__ int32_t pages[kMaxBeams];
@@ -38,7 +38,7 @@ __global__ __launch_bounds__(kForkThreads) void pages_fork_kernel(PageTable t, c
   __shared__ int32_t kids[kMaxBeams];
   __shared__ uint64_t apart[kForkWaves];  // columns whose entries are not all the same page
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  const int tile = static_cast<int>(blockIdx.x % static_cast<unsigned>(tiles));
+  const int tile = tile0 + static_cast<int>(blockIdx.x % static_cast<unsigned>(tiles));
   const int64_t item = item0 + blockIdx.x / static_cast<unsigned>(tiles);
   if (tid < K) {
     const int p = parents[item * K + tid];
@@ -368,11 +368,16 @@ template <int W>
 __global__ __launch_bounds__(kCopyThreads) void pages_copy_kernel(PageCaches c, const PageCopy* __restrict__ copies,
                                                                   const ResizePlan* __restrict__ plan) {
   using col_t = typename Bytes<W>::type;
-  const uint32_t total = static_cast<uint32_t>(plan->copies) * static_cast<uint32_t>(c.count);
-  for (uint32_t i = blockIdx.x; i < total; i += gridDim.x) {
-    const uint32_t k = i / static_cast<uint32_t>(c.count);
+  const uint32_t total = static_cast<uint32_t>(plan->copies), count = static_cast<uint32_t>(c.count);
+  const uint32_t step = gridDim.x / count, step_cache = gridDim.x - step * count;
+  uint32_t k = blockIdx.x / count, cache = blockIdx.x - k * count;
+  for (; k < total; k += step, cache += step_cache) {
+    if (cache >= count) {
+      cache -= count;
+      if (++k >= total) break;
+    }
     const PageCopy one = copies[k];
-    char* data = c.data[i - k * static_cast<uint32_t>(c.count)];
+    char* data = c.data[cache];
     const char* from = data + one.from * c.shape.page_stride;
     char* to = data + one.to * c.shape.page_stride;
     const uint32_t runs = c.shape.run.d, per = runs * static_cast<uint32_t>(one.slots);
@@ -486,7 +491,9 @@ bool same_shape(const BeamState& a, const BeamState& b) {
   return same;
 }
 
-// f(caches, bytes of a column) for runs of caches of one shape.
+// f(caches, bytes of a column) for runs of caches of one shape, of no more than
+// kMaxColumns columns together (or one cache).
+constexpr uint64_t kMaxColumns = uint64_t{1} << 31;
 template <class F>
 hipError_t by_shape(const BeamState* caches, int64_t count, F f) {
   for (int64_t i = 0; i < count;) {
@@ -494,7 +501,10 @@ hipError_t by_shape(const BeamState* caches, int64_t count, F f) {
     PageCaches c{};
     c.shape = shape_of(caches[i], w);
     int64_t j = i;
-    for (; j < count && c.count < kMaxCaches && same_shape(caches[i], caches[j]); ++j) c.data[c.count++] = caches[j].data;
+    for (; j < count && c.count < kMaxCaches && same_shape(caches[i], caches[j]) &&
+           (c.count == 0 || (static_cast<uint64_t>(c.count) + 1) * c.shape.columns <= kMaxColumns);
+         ++j)
+      c.data[c.count++] = caches[j].data;
     if (const hipError_t e = f(c, w)) return e;
     i = j;
   }
@@ -515,16 +525,22 @@ bool page_state_fits(const BeamState& s) {
 }
 
 hipError_t launch_pages_fork(const PageTable& t, const int32_t* parents, int64_t N, int K, hipStream_t stream) {
-  const int tiles = t.C > 0 ? (t.C + kForkCols - 1) / kForkCols : 1;
-  const int64_t step = (int64_t{1} << 22) / tiles > 0 ? (int64_t{1} << 22) / tiles : 1;
+  // a launch holds at most 2^22 workgroups
+  constexpr int64_t kMost = int64_t{1} << 22;
+  const int64_t tiles = t.C > 0 ? (static_cast<int64_t>(t.C) + kForkCols - 1) / kForkCols : 1;
+  const int64_t step = kMost / tiles > 0 ? kMost / tiles : 1;
   for (int64_t i = 0; i < N; i += step) {
     const int64_t n = N - i < step ? N - i : step;
-    const dim3 grid(static_cast<unsigned>(n * tiles));
     if (tiles == 1) {
-      hipLaunchKernelGGL((pages_fork_kernel<true>), grid, dim3(kForkThreads), 0, stream, t, parents, K, tiles, i);
+      hipLaunchKernelGGL((pages_fork_kernel<true>), dim3(static_cast<unsigned>(n)), dim3(kForkThreads), 0, stream, t,
+                         parents, K, 1, 0, i);
     } else {
-      hipLaunchKernelGGL((pages_fork_kernel<false>), grid, dim3(kForkThreads), 0, stream, t, parents, K, tiles, i);
-      if (const hipError_t e = hipGetLastError()) return e;
+      for (int64_t j = 0; j < tiles; j += kMost) {
+        const int64_t of = tiles - j < kMost ? tiles - j : kMost;
+        hipLaunchKernelGGL((pages_fork_kernel<false>), dim3(static_cast<unsigned>(n * of)), dim3(kForkThreads), 0, stream,
+                           t, parents, K, static_cast<int>(of), static_cast<int>(j), i);
+        if (const hipError_t e = hipGetLastError()) return e;
+      }
       hipLaunchKernelGGL(pages_fork_lengths_kernel, dim3(static_cast<unsigned>(n)), dim3(kMaxBeams), 0, stream, t,
                          parents, K, i);
     }
