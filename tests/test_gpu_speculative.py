@@ -419,6 +419,41 @@ def test_uniforms_at_the_ends(mode, N, dtype):
     assert (end - r[i, got[:, 0]] <= at + off).all() and (end >= at - off).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N", [4, 400])
+@pytest.mark.parametrize("count", [5, 5000])
+def test_residuals_of_alike_rows(count, N, dtype):
+    """Rows p and q that are the same in `count` tokens and permuted in 40 others, so that the ratio of their sums is 1
+    but for roundings and no sum in 32 bits tells which of the equal tokens is larger; uniforms anywhere and next to the
+    borders of the residual's tokens."""
+    torch = need_gpu()
+    rng = np.random.default_rng(count + N)
+    V, D = 20000, 1
+    t = getattr(torch, dtype)
+    p = np.full((N, D + 1, V), -np.inf)
+    q = np.full((N, D, V), -np.inf)
+    drafts = np.empty((N, D), np.int32)
+    for i in range(N):
+        at = rng.choice(V, count + 40, replace=False)
+        p[i, 0, at] = rng.standard_normal(count + 40) * 2
+        q[i, 0, at] = p[i, 0, at]
+        few = at[:40]
+        p[i, 0, few] += 4.0
+        q[i, 0, few] = np.roll(p[i, 0, few], 1)
+        drafts[i, 0] = few[np.argmax(q[i, 0, few] - p[i, 0, few])]
+    x, y = on_gpu(torch, p.reshape(-1, V), t), on_gpu(torch, q.reshape(-1, V), t)
+    u = rng.random((N, D + 1))
+    u[:, 0] = 1 - 2.0 ** -24
+    xs, ys = back(x).reshape(N, D + 1, V), back(y)
+    for i in range(0, N, 2):
+        r = np.maximum(spec_ref.softmax(xs[i, 0]) - spec_ref.softmax(ys[i]), 0)
+        edges = np.cumsum(r) / r.sum()
+        edge = np.float32(edges[rng.choice(np.nonzero(r > 1e-6)[0])])
+        u[i, D] = min(np.nextafter(edge, np.float32(i % 4), dtype=np.float32) if i % 8 < 4 else edge, 1 - 2.0 ** -24)
+    acc, _ = check(torch, x, drafts, u, y)
+    assert (acc == 0).all()
+
+
 def test_every_token_is_drawn_in_its_place():
     """One row, uniforms over all of [0, 1): each token's share, at the borders as well."""
     torch = need_gpu()

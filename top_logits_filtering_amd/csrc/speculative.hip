@@ -61,19 +61,12 @@ struct FinalPart {
   double left;   // of what is left: p's terms without the rejected tokens', or ratio * p's less q's where that is above 0
   double kept;   // of p's terms where it is
   double draft;  // of q's terms
-};
-// Elements whose terms of p and q are too close to tell which is larger by the ratio
-// at hand are set apart, so many of a sequence.
-constexpr int kMaxClose = 64;
-struct Close {
-  double p, q;
-  double at;  // the element
+  double close;  // of q's terms where they are too close to p's to tell which is larger: not in left and kept
 };
 // Where workgroups of a sequence meet.
 struct Meeting {
   FinalPart* parts;   // of all workgroups' waves
-  Close* close;       // [kMaxClose]
-  uint32_t* arrived;  // workgroups that are done, elements set apart
+  uint32_t* arrived;  // workgroups that are done
 };
 
 // exp(x - ref) in 64 bits, 0 for -inf and NaN: 2^(n + r) with n whole and r in
@@ -716,7 +709,7 @@ __global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, Split spl
   const unsigned item = b / static_cast<unsigned>(split.chunks);
   const int r = static_cast<int>(item % static_cast<unsigned>(rows));
   const int64_t seq = seq0 + item / static_cast<unsigned>(rows);
-  if (r == 0 && ch == 0 && threadIdx.x < 2) arrived[2 * seq + threadIdx.x] = 0;
+  if (r == 0 && ch == 0 && threadIdx.x == 0) arrived[seq] = 0;
   const bool target = r < targets;
   const int w = target ? r : r - targets;
   const int n = draft_count(a, seq);
@@ -739,11 +732,10 @@ struct FinalSmem : std::conditional_t<kTabled<DT, THREADS> && MODE != kGreedy, T
   int outs;
   double sum[4][kWaves];
   double parts[kFew];  // where summed again
-  Close close[kMaxClose];
   uint64_t is[kWaves], may[kWaves];
   double below;
   int last;
-  int found;
+  int found, sure;
 };
 
 // The terms of eight neighbouring elements: p's, and q's.
@@ -861,9 +853,8 @@ __device__ __forceinline__ double if_or_none(bool is, double v) {
   return __builtin_bit_cast(double, (static_cast<uint64_t>(high) << 32) | static_cast<uint32_t>(u));
 }
 
-// Eight elements' share of a part's sums, v the first of them; p > q where near * p's
-// term > q's.
-__device__ __forceinline__ void add_terms(FinalPart& mine, const Terms& t, double near, int v, const Meeting& meet) {
+// Eight elements' share of a part's sums; p > q where near * p's term > q's.
+__device__ __forceinline__ void add_terms(FinalPart& mine, const Terms& t, double near) {
   bool close = false;
 #pragma unroll
   for (int j = 0; j < kBlock; ++j) {
@@ -889,13 +880,7 @@ __device__ __forceinline__ void add_terms(FinalPart& mine, const Terms& t, doubl
           mine.left -= more;
           mine.kept -= p;
         }
-        const uint32_t at =
-            __hip_atomic_fetch_add(&meet.arrived[1], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (at < kMaxClose) {
-          put_far(&meet.close[at].p, p);
-          put_far(&meet.close[at].q, q);
-          put_far(&meet.close[at].at, static_cast<double>(v + j));
-        }
+        mine.close += q;
       }
     }
   }
@@ -904,8 +889,8 @@ __device__ __forceinline__ void add_terms(FinalPart& mine, const Terms& t, doubl
 // Sums over a wave's part of the row, of every lane's elements.
 template <class DT, Mode MODE, class Smem>
 __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, const typename DT::raw_t* qrow, int first,
-                                             int pieces, int V, const Walk& w, const Smem& sm, const Meeting& meet) {
-  FinalPart mine{0.0, 0.0, 0.0, 0.0};
+                                             int pieces, int V, const Walk& w, const Smem& sm) {
+  FinalPart mine{};
   const Rows least = least_of(w);
   const int lane = threadIdx.x % kWave;
   if (MODE == kDrawn && w.kind == kResidual) {
@@ -915,7 +900,7 @@ __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, con
       const int v = first + i * kPiece + lane * kBlock;
       Terms t;
       if (!terms_at<DT>(prow, qrow, v, V, w, least, true, t)) continue;
-      add_terms(mine, t, near, v, meet);
+      add_terms(mine, t, near);
     }
   } else {
     const bool outs = MODE != kDrawn && w.kind == kWithout && sm.outs != 0;
@@ -996,9 +981,8 @@ __device__ __forceinline__ bool all_masked(const vec_t& q) {
 }
 template <Mode MODE, class Smem>
 __device__ __forceinline__ FinalPart part_by_table(const uint16_t* prow, const uint16_t* qrow, int first, int pieces, int V,
-                                                   const Walk& w, const Smem& sm, const double (&table)[kTable],
-                                                   const Meeting& meet) {
-  FinalPart mine{0.0, 0.0, 0.0, 0.0};
+                                                   const Walk& w, const Smem& sm, const double (&table)[kTable]) {
+  FinalPart mine{};
   const int lane = threadIdx.x % kWave;
   const bool two = MODE == kDrawn && w.kind == kResidual;
   const bool outs = MODE != kDrawn && w.kind == kWithout && sm.outs != 0;
@@ -1020,7 +1004,7 @@ __device__ __forceinline__ FinalPart part_by_table(const uint16_t* prow, const u
     if (two) {
 #pragma unroll
       for (int j = 0; j < kBlock; j += 2) look_up(table, vword(yn, j / 2), t.q[j], t.q[j + 1]);
-      add_terms(mine, t, near, v, meet);
+      add_terms(mine, t, near);
     } else {
       double sum = 0.0;
 #pragma unroll
@@ -1078,6 +1062,12 @@ __device__ __forceinline__ int first_or_last(bool is, bool may, Smem& sm) {
 
 // Finds the token out of the parts' sums, by the first kFew threads (the other waves
 // have ended, and barriers wait for none of them).
+//
+// Parts were summed with near, the ratio of q's sum and p's out of the chunks; scale is
+// that ratio in 64 bits. For elements that are not close both tell the same one of p
+// and q to be larger, and left + (scale - near) kept is what they add up to. The close
+// ones add up to at most `more`: where that could move the token, and where scale is
+// not as near as that, the parts are summed again with scale.
 template <class DT, Mode MODE, class Smem>
 __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, const Meeting& meet, int parts, int pieces,
                                         const typename DT::raw_t* prow, const typename DT::raw_t* qrow,
@@ -1086,9 +1076,7 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
   const int tid = threadIdx.x, span = pieces * kPiece;
   const bool two = MODE == kDrawn && w.kind == kResidual;
   const Rows least = least_of(w);
-  FinalPart p{0.0, 0.0, 0.0, 0.0};
-  uint32_t close = 0;
-  if (two) close = __hip_atomic_load(&meet.arrived[1], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  FinalPart p{};
   if (tid < parts) {
     const FinalPart* from = meet.parts + tid;
     p.all = get_far(&from->all);
@@ -1096,122 +1084,131 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
     if (two) {
       p.kept = get_far(&from->kept);
       p.draft = get_far(&from->draft);
+      p.close = get_far(&from->close);
     }
   }
-  double total[2] = {p.all, p.draft};
+  double total[MODE == kDrawn ? 3 : 1];
+  total[0] = p.all;
+  if constexpr (MODE == kDrawn) {
+    total[1] = p.draft;
+    total[2] = p.close;
+  }
   block_sums(total, sm.sum);
-  Weights weights{two ? total[1] / total[0] : 1.0, two, MODE != kDrawn && w.kind == kWithout};
-  const double near = two ? w.q.sum / w.p.sum : 1.0, off = weights.scale - near;
-  double part = two ? __builtin_fma(off, p.kept, p.left) : p.left;
-  if (two && close != 0) {
-    if (close <= kMaxClose && __builtin_fabs(off) <= 0.5 * kBand * near) {
-      // what was set apart, in the order of the elements
-      if (tid < static_cast<int>(close)) sm.close[tid] = Close{get_far(&meet.close[tid].p), get_far(&meet.close[tid].q),
-                                                               get_far(&meet.close[tid].at)};
-      __syncthreads();
-      double done = -1.0;
-      for (;;) {
-        int next = -1;
-        for (int i = 0; i < static_cast<int>(close); ++i) {
-          const double at = sm.close[i].at;
-          if (at > done && static_cast<int>(at) / span == tid && (next < 0 || at < sm.close[next].at)) next = i;
-        }
-        if (next < 0) break;
-        done = sm.close[next].at;
-        part += __builtin_fmax(__builtin_fma(weights.scale, sm.close[next].p, -sm.close[next].q), 0.0);
-      }
-      close = 0;
+  double part = p.left, scale = 1.0, more = 0.0, least_mass = kLeast * total[0];
+  bool again = false;
+  if constexpr (MODE == kDrawn) {
+    if (two) {
+      scale = total[1] / total[0];
+      const double near = w.q.sum / w.p.sum, off = scale - near;
+      part = __builtin_fmax(__builtin_fma(off, p.kept, part), 0.0);
+      more = 2.0 * kBand * total[2];
+      least_mass = kLeast * total[1];
+      again = __builtin_fabs(off) > 0.5 * kBand * near;
     }
   }
-  part = __builtin_fmax(part, 0.0);
-  double below, upto, all;
-  if (two && (close != 0 || __builtin_fabs(off) > 0.5 * kBand * near)) {
-    // the rows are alike: the parts are summed again with the ratio of the sums in 64 bits
-    for (int c0 = 0; c0 < parts; c0 += kWaves) {
-      const int c = c0 + tid / kWave;
-      double sum = 0.0;
+  for (;;) {
+    if (again) {
+      for (int c0 = 0; c0 < parts; c0 += kWaves) {
+        const int c = c0 + tid / kWave;
+        double sum = 0.0;
 #pragma unroll 1
-      for (int i = 0; i < pieces; ++i) {
-        const int v = c * span + i * kPiece + tid % kWave * kBlock;
-        float x[kBlock], y[kBlock];
-        load_block<DT>(prow, v, a.V, x);
-        load_block<DT>(qrow, v, a.V, y);
+        for (int i = 0; i < pieces; ++i) {
+          const int v = c * span + i * kPiece + tid % kWave * kBlock;
+          float x[kBlock], y[kBlock];
+          load_block<DT>(prow, v, a.V, x);
+          load_block<DT>(qrow, v, a.V, y);
 #pragma unroll 1
-        for (int j = 0; j < kBlock; ++j) {  // one after the other: rarely taken
-          sum += __builtin_fmax(__builtin_fma(weights.scale, exp_from(x[0], w.p.ref), -exp_from(y[0], w.q.ref)), 0.0);
+          for (int j = 0; j < kBlock; ++j) {  // one after the other: rarely taken
+            sum += __builtin_fmax(__builtin_fma(scale, exp_from(x[0], w.p.ref), -exp_from(y[0], w.q.ref)), 0.0);
 #pragma unroll
-          for (int k = 0; k + 1 < kBlock; ++k) {
-            x[k] = x[k + 1];
-            y[k] = y[k + 1];
+            for (int k = 0; k + 1 < kBlock; ++k) {
+              x[k] = x[k + 1];
+              y[k] = y[k + 1];
+            }
           }
         }
+        sum = wave_sum_f64(sum);
+        if (c < parts && tid % kWave == 0) sm.parts[c] = sum;
       }
-      sum = wave_sum_f64(sum);
-      if (c < parts && tid % kWave == 0) sm.parts[c] = sum;
+      __syncthreads();
+      part = tid < parts ? sm.parts[tid] : 0.0;
+      more = 0.0;
     }
-    __syncthreads();
-    part = tid < parts ? sm.parts[tid] : 0.0;
-  }
-  block_scan(part, below, upto, all, sm.sum);
-  if (w.kind != kPlain && !(all > kLeast * (two ? total[1] : total[0]))) {
-    weights.residual = weights.without = false;
-    part = p.all;
+    Weights weights{scale, two, MODE != kDrawn && w.kind == kWithout};
+    double below, upto, all;
     block_scan(part, below, upto, all, sm.sum);
-  }
-  const double at = static_cast<double>(sm.walk.last_u) * all;
-  // the part that `at` lies in; for a uniform out of range the first or the last one of any weight
-  bool is = upto > at && upto > below, may = upto > below;
-  const double begin = below;
-  int last_seen = -1;
-  for (;;) {
-    const int c = first_or_last(is, may, sm);
-    if (c < 0) break;
-    if (tid == c) sm.below = begin;
-    __syncthreads();
-    double base = sm.below;
-    if constexpr (MODE == kProposed) list_out(a, w, c * span, (c + 1) * span, sm);
-#pragma unroll 1
-    for (int i = 0; i < span; i += THREADS * kBlock) {
-      const int v = i + tid * kBlock < span ? c * span + i + tid * kBlock : a.V;
-      double wt[kBlock], sum = 0.0;
-      int last = -1;  // the last element of any weight
-      Terms t;
-      if (terms_at<DT>(prow, qrow, v, a.V, w, least, two, t)) {
-        weights.of(t, v, sm, wt);
-#pragma unroll
-        for (int j = 0; j < kBlock; ++j) {
-          sum += wt[j];
-          if (wt[j] > 0.0) last = v + j;
-        }
+    if (w.kind != kPlain && !(all > least_mass)) {
+      if (more > 0.0) {
+        again = true;
+        continue;
       }
-      block_scan(sum, below, upto, all, sm.sum);
-      const bool here = last >= 0 && base + upto > at;
-      const int finder = first_or_last(here, last >= 0, sm);
-      if (finder >= 0) {
-        if (tid == finder) {
-          int token = last;
-          double reach = base + below;
+      weights.residual = weights.without = false;
+      block_scan(p.all, below, upto, all, sm.sum);
+    }
+    const double at = static_cast<double>(sm.walk.last_u) * all;
+    // the part that `at` lies in; for a uniform out of range the first or the last one of any weight
+    bool is = upto > at && upto > below, may = upto > below;
+    const double begin = below;
+    int last_seen = -1;
+    bool sure = more == 0.0;
+    for (;;) {
+      const int c = first_or_last(is, may, sm);
+      if (c < 0) break;
+      if (tid == c) sm.below = begin;
+      __syncthreads();
+      double base = sm.below;
+      if constexpr (MODE == kProposed) list_out(a, w, c * span, (c + 1) * span, sm);
+#pragma unroll 1
+      for (int i = 0; i < span; i += THREADS * kBlock) {
+        const int v = i + tid * kBlock < span ? c * span + i + tid * kBlock : a.V;
+        double wt[kBlock], sum = 0.0;
+        int last = -1;  // the last element of any weight
+        Terms t;
+        if (terms_at<DT>(prow, qrow, v, a.V, w, least, two, t)) {
+          weights.of(t, v, sm, wt);
 #pragma unroll
           for (int j = 0; j < kBlock; ++j) {
-            reach += wt[j];
-            if (wt[j] > 0.0 && reach > at) token = token < v + j ? token : v + j;
+            sum += wt[j];
+            if (wt[j] > 0.0) last = v + j;
           }
-          sm.found = token;
-          sm.last = here ? 1 : 0;
         }
-        __syncthreads();
-        last_seen = sm.found;
-        const bool done = sm.last != 0;
-        __syncthreads();
-        if (done) break;
+        block_scan(sum, below, upto, all, sm.sum);
+        const bool here = last >= 0 && base + upto > at;
+        const int finder = first_or_last(here, last >= 0, sm);
+        if (finder >= 0) {
+          if (tid == finder) {
+            int token = -1;
+            double reach = base + below;
+            bool clear = false;
+#pragma unroll
+            for (int j = 0; j < kBlock; ++j) {
+              const double from = reach;
+              reach += wt[j];
+              if (token < 0 && wt[j] > 0.0 && reach > at) {
+                token = v + j;
+                clear = from + more <= at && at + more < reach;
+              }
+            }
+            sm.found = token >= 0 ? token : last;
+            sm.last = here ? 1 : 0;
+            sm.sure = clear ? 1 : 0;
+          }
+          __syncthreads();
+          last_seen = sm.found;
+          sure = more == 0.0 || sm.sure != 0;
+          const bool done = sm.last != 0;
+          __syncthreads();
+          if (done) break;
+        }
+        base += all;
       }
-      base += all;
+      if (last_seen >= 0) break;
+      // its weight was but roundings, or elements that count as 0 here
+      if (tid == c) is = may = false;
     }
-    if (last_seen >= 0) break;
-    // its weight was but roundings, or elements that count as 0 here
-    if (tid == c) is = may = false;
+    if (sure) return last_seen;
+    again = true;
   }
-  return last_seen;
 }
 
 // A group's parts of the row where the path ends, one of each wave. Then the last
@@ -1232,18 +1229,19 @@ __device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w
   FinalPart mine;
   if constexpr (kTabled<DT, THREADS>) {
     if (w.p.ref == 0.0f && (!two || w.q.ref == 0.0f)) {
-      mine = part_by_table<MODE>(prow, qrow, c * span, pieces, a.V, w, sm, sm.table, meet);
+      mine = part_by_table<MODE>(prow, qrow, c * span, pieces, a.V, w, sm, sm.table);
     } else {
-      mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm, meet);
+      mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm);
     }
   } else {
-    mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm, meet);
+    mine = part_of<DT, MODE>(prow, qrow, c * span, pieces, a.V, w, sm);
   }
   mine.all = wave_sum_f64(mine.all);
   mine.left = wave_sum_f64(mine.left);
   if (two) {
     mine.kept = wave_sum_f64(mine.kept);
     mine.draft = wave_sum_f64(mine.draft);
+    if (__ballot(mine.close > 0.0) != 0) mine.close = wave_sum_f64(mine.close);
   }
   if (tid % kWave == 0) {
     put_far(&meet.parts[c].all, mine.all);
@@ -1251,6 +1249,7 @@ __device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w
     if (two) {
       put_far(&meet.parts[c].kept, mine.kept);
       put_far(&meet.parts[c].draft, mine.draft);
+      put_far(&meet.parts[c].close, mine.close);
     }
   }
   if (!last_of(meet.arrived, groups, sm.last) || tid >= kFew) return -2;
@@ -1328,7 +1327,7 @@ __global__ __launch_bounds__(THREADS) void verify_final_kernel(VerifyArgs a, int
   }
   if constexpr (!greedy) {
     if (!draws) return;
-    const Meeting meet{all.parts + seq * groups * (THREADS / kWave), all.close + seq * kMaxClose, all.arrived + 2 * seq};
+    const Meeting meet{all.parts + seq * groups * (THREADS / kWave), all.arrived + seq};
     const int token = token_by_parts<DT, MODE, THREADS>(a, w, seq, group, groups, pieces, meet, sm);
     if (tid == 0 && token >= -1) tokens[w.count] = token;
   }
@@ -1429,16 +1428,15 @@ int targets_of(const Plan& p, int D) { return p.steps > 0 ? 1 : D + 1; }
 constexpr int64_t kKeptBytes = int64_t{256} << 20;
 
 struct Layout {
-  int64_t stats, finals, close, arrived, bytes;
+  int64_t stats, finals, arrived, bytes;
 };
 Layout layout_of(const Plan& p, int64_t N, int D, bool draft) {
   const int64_t rows = N * (D + 1 + (draft ? D : 0));
   Layout l;
   l.stats = 0;
   l.finals = l.stats + rows * p.split.chunks * static_cast<int64_t>(sizeof(RowChunk));
-  l.close = l.finals + N * p.cut.groups * (p.cut.threads / kWave) * static_cast<int64_t>(sizeof(FinalPart));
-  l.arrived = l.close + (draft ? N * kMaxClose * static_cast<int64_t>(sizeof(Close)) : 0);
-  l.bytes = l.arrived + N * 8;
+  l.arrived = l.finals + N * p.cut.groups * (p.cut.threads / kWave) * static_cast<int64_t>(sizeof(FinalPart));
+  l.bytes = l.arrived + N * 4;
   return l;
 }
 
@@ -1449,8 +1447,7 @@ hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
   const Layout l = layout_of(p, a.N, a.D, draft);
   char* ws = static_cast<char*>(a.workspace);
   RowChunk* stats = reinterpret_cast<RowChunk*>(ws + l.stats);
-  const Meeting meet{reinterpret_cast<FinalPart*>(ws + l.finals), reinterpret_cast<Close*>(ws + l.close),
-                     reinterpret_cast<uint32_t*>(ws + l.arrived)};
+  const Meeting meet{reinterpret_cast<FinalPart*>(ws + l.finals), reinterpret_cast<uint32_t*>(ws + l.arrived)};
   const bool keep = a.N * (targets_of(p, a.D) + (draft ? a.D : 0)) * a.V * (dtype == 0 ? 4 : 2) <= kKeptBytes;
   const int targets = targets_of(p, a.D), groups = greedy ? 1 : p.cut.groups;
   // a launch holds at most 2^22 workgroups
