@@ -866,22 +866,13 @@ __device__ __forceinline__ void add_terms(FinalPart& mine, const Terms& t, doubl
     close |= __builtin_fabs(more) < kBand * t.q[j];
   }
   if (__ballot(close) != 0) {
-#pragma unroll 1
-    for (int j = 0; j < kBlock; ++j) {
-      double p = 0.0, q = 0.0;
 #pragma unroll
-      for (int k = 0; k < kBlock; ++k) {
-        p = j == k ? t.p[k] : p;
-        q = j == k ? t.q[k] : q;
-      }
-      const double more = __builtin_fma(near, p, -q);
-      if (__builtin_fabs(more) < kBand * q) {
-        if (more > 0.0) {
-          mine.left -= more;
-          mine.kept -= p;
-        }
-        mine.close += q;
-      }
+    for (int j = 0; j < kBlock; ++j) {
+      const double more = __builtin_fma(near, t.p[j], -t.q[j]);
+      const bool is = __builtin_fabs(more) < kBand * t.q[j];
+      mine.left -= if_or_none(is && more > 0.0, more);
+      mine.kept -= if_or_none(is && more > 0.0, t.p[j]);
+      mine.close += if_or_none(is, t.q[j]);
     }
   }
 }
