@@ -8,9 +8,11 @@ falling back to anything else.
 
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import functools
+import operator
 import os
 import struct
 from typing import Optional
@@ -399,6 +401,7 @@ def top_k_top_p_sorted_survivors(logits, p=None, k=None, min_p=None, cap=1024, w
 
 
 _pack_pointer = struct.Struct("=Q").pack
+_NO_POINTER = bytes(8)
 _NULL_SCOPE = contextlib.nullcontext()
 
 
@@ -796,35 +799,40 @@ def _page_table(tables, lengths, uses, R):
     return ld, C, uses.shape[0]
 
 
+_shape_of, _dtype_of, _requires_grad_of = map(operator.attrgetter, ("shape", "dtype", "requires_grad"))
+
+
 def _page_caches(caches, P, page_size, page_dim, slot_dim, dev):
     """(tensors, their descriptions) of caches of P pages."""
     import torch
 
-    tensors = [caches] if isinstance(caches, torch.Tensor) else list(caches)
-    recorded = torch.is_grad_enabled()
-    descs = []
-    shape = stride = dtype = desc = None
-    for t in tensors:
-        if t.get_device() != dev:
-            raise ValueError(f"tensors must share one device: a cache is on {t.device}")
-        if recorded and t.requires_grad:
-            raise ValueError("a cache that requires grad can only be changed under no_grad")
-        if t.is_neg():
-            raise ValueError("a cache must not be a lazily negated view")
-        # the caches of a model's layers are alike: one description for all
-        if t.dtype != dtype or t.shape != shape or t.stride() != stride or t.is_complex():
-            shape, stride, dtype = t.shape, t.stride(), t.dtype
-            if t.is_conj():
-                raise ValueError("a cache must not be a lazily conjugated view")
-            dims = t.dim()
-            if not (-dims <= page_dim < dims and -dims <= slot_dim < dims) or (page_dim - slot_dim) % dims == 0:
-                raise ValueError(f"a cache of {dims} axes has no page_dim {page_dim} and slot_dim {slot_dim}")
-            if shape[page_dim] != P or shape[slot_dim] != page_size:
-                raise ValueError(f"a cache must have {P} pages of {page_size} slots, got shape {tuple(shape)}")
-            desc = _state_bytes(shape, stride, t.element_size(), page_dim, slot_dim, P)
-        descs.append(_pack_pointer(t.data_ptr()))
-        descs.append(desc)
-    return tensors, b"".join(descs)
+    Tensor = torch.Tensor
+    tensors = [caches] if isinstance(caches, Tensor) else list(caches)
+    # maps and sets, as a step of the interpreter for each property of each tensor takes longer than the call
+    if set(map(Tensor.get_device, tensors)) - {dev}:
+        raise ValueError("tensors must share one device: a cache is on another")
+    if torch.is_grad_enabled() and any(map(_requires_grad_of, tensors)):
+        raise ValueError("a cache that requires grad can only be changed under no_grad")
+    if any(map(Tensor.is_neg, tensors)):
+        raise ValueError("a cache must not be a lazily negated view")
+    shapes, strides, dtypes = set(map(_shape_of, tensors)), set(map(Tensor.stride, tensors)), set(map(_dtype_of, tensors))
+    for dtype in dtypes:
+        if dtype.is_complex and any(map(Tensor.is_conj, tensors)):
+            raise ValueError("a cache must not be a lazily conjugated view")
+    for shape in shapes:
+        dims = len(shape)
+        if not (-dims <= page_dim < dims and -dims <= slot_dim < dims) or (page_dim - slot_dim) % dims == 0:
+            raise ValueError(f"a cache of {dims} axes has no page_dim {page_dim} and slot_dim {slot_dim}")
+        if shape[page_dim] != P or shape[slot_dim] != page_size:
+            raise ValueError(f"a cache must have {P} pages of {page_size} slots, got shape {tuple(shape)}")
+    if len(shapes) == len(strides) == len(dtypes) == 1:  # the caches of a model's layers: one description for all
+        t = tensors[0]
+        descs = _NO_POINTER + _state_bytes(t.shape, t.stride(), t.element_size(), page_dim, slot_dim, P)
+        words = memoryview(bytearray(descs * len(tensors))).cast("q")
+        words[::len(descs) // 8] = array.array("q", map(Tensor.data_ptr, tensors))
+        return tensors, bytes(words)
+    return tensors, b"".join(_pack_pointer(t.data_ptr()) +
+                             _state_bytes(t.shape, t.stride(), t.element_size(), page_dim, slot_dim, P) for t in tensors)
 
 
 def cache_pages_fork(tables, lengths, parents, uses, page_size, stream=None):
