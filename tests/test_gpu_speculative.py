@@ -454,6 +454,40 @@ def test_residuals_of_alike_rows(count, N, dtype):
     assert (acc == 0).all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_what_is_left_may_be_little(dtype):
+    """Proposals that have next to all of their row are rejected: the token comes from the rest, of which most lies far
+    below the row's largest."""
+    torch = need_gpu()
+    rng = np.random.default_rng(11)
+    N, D, V = 700, 1, 12000
+    base = np.empty((N, D + 1, V))
+    base[:, :, : V // 2] = -26.0 - 3.0 * rng.random((N, D + 1, V // 2))
+    base[:, :, V // 2:] = -52.0 - rng.random((N, D + 1, V - V // 2))
+    base[:, :, 7] = 0.0
+    x = on_gpu(torch, base.reshape(-1, V), getattr(torch, dtype))
+    u = rng.random((N, D + 1))
+    u[:, 0] = 1.0  # not below p(7), which no uniform below 1 reaches here
+    u[: N // 2, D] = 1 - 2.0 ** -24
+    u[: N // 4, D] = 0.0
+    drafts = np.full((N, D), 7, np.int32)
+    acc, _ = check(torch, x, drafts, u)
+    assert (acc == 0).all()
+
+
+def test_no_vocabulary():
+    torch = need_gpu()
+    import top_logits_filtering_amd as tk
+
+    for D in (0, 3):
+        x, drafts = torch.zeros(2 * (D + 1), 0, device="cuda"), torch.zeros(2, D, dtype=torch.int32, device="cuda")
+        u = torch.rand(2, D + 1, device="cuda")
+        for kw in ({}, dict(uniforms=u), dict(uniforms=u, draft_logits=torch.zeros(2 * D, 0, device="cuda")),
+                   dict(uniforms=u, parents=torch.full((2, D), -1, dtype=torch.int32, device="cuda"))):
+            tokens, accepted, _ = tk.speculative_verify(x, drafts, **kw)
+            assert (tokens == -1).all() and (accepted == 0).all()
+
+
 def test_every_token_is_drawn_in_its_place():
     """One row, uniforms over all of [0, 1): each token's share, at the borders as well."""
     torch = need_gpu()

@@ -751,9 +751,10 @@ struct FinalSmem : std::conditional_t<kTabled<DT, THREADS> && MODE != kGreedy, T
 struct Terms {
   double p[kBlock], q[kBlock];
 };
-// Elements of no more than exp(-50) of the row, so a 2^-52nd of it all together,
-// count as 0 where a whole wave has none but them: rows that were filtered.
-constexpr float kFar = 50.0f;
+// Elements of no more than exp(-70) of the row, so below 2^-80 of it all together, count
+// as 0 where a whole wave has none but them: rows that were filtered. (What is left of a
+// row without its rejected tokens is at least the 2^-24th that a uniform can be below 1.)
+constexpr float kFar = 70.0f;
 struct Rows {
   float p_least, q_least;
 };
