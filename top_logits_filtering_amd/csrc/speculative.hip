@@ -72,10 +72,14 @@ struct FinalPart {
   double draft;  // of q's terms
   double close;  // of q's terms where they are too close to p's to tell which is larger: not in left and kept
 };
-// Where workgroups of a sequence meet.
+constexpr int kSums = sizeof(FinalPart) / sizeof(double);
+// Where workgroups of a sequence meet. Each one's counter has 64 bytes of its own:
+// counters side by side wait for one another (8 sequences of 4 proposals, V 151936 bf16,
+// 18.0 us instead of 15.9).
+constexpr int kApart = 16;
 struct Meeting {
-  FinalPart* parts;   // of all workgroups' waves
-  uint32_t* arrived;  // workgroups that are done
+  double* sums;       // [kSums][parts], those of all workgroups' waves as in FinalPart
+  uint32_t* arrived;  // workgroups that are done, kApart counters apart
 };
 
 // exp(x - ref) in 64 bits, 0 for -inf and NaN: 2^(n + r) with n whole and r in
@@ -718,7 +722,7 @@ __global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, Split spl
   const unsigned item = b / static_cast<unsigned>(split.chunks);
   const int r = static_cast<int>(item % static_cast<unsigned>(rows));
   const int64_t seq = seq0 + item / static_cast<unsigned>(rows);
-  if (r == 0 && ch == 0 && threadIdx.x == 0) arrived[seq] = 0;
+  if (r == 0 && ch == 0 && threadIdx.x == 0) arrived[kApart * seq] = 0;
   const bool target = r < targets;
   const int w = target ? r : r - targets;
   const int n = draft_count(a, seq);
@@ -1081,13 +1085,13 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
   const Rows least = least_of(w);
   FinalPart p{};
   if (tid < parts) {
-    const FinalPart* from = meet.parts + tid;
-    p.all = get_far(&from->all);
-    p.left = get_far(&from->left);
+    const double* from = meet.sums + tid;
+    p.all = get_far(from);
+    p.left = get_far(from + parts);
     if (two) {
-      p.kept = get_far(&from->kept);
-      p.draft = get_far(&from->draft);
-      p.close = get_far(&from->close);
+      p.kept = get_far(from + 2 * parts);
+      p.draft = get_far(from + 3 * parts);
+      p.close = get_far(from + 4 * parts);
     }
   }
   double total[MODE == kDrawn ? 3 : 1];
@@ -1110,7 +1114,7 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
     }
   }
   for (;;) {
-    if (again) {
+    if (MODE == kDrawn && again) {
       for (int c0 = 0; c0 < parts; c0 += kWaves) {
         const int c = c0 + tid / kWave;
         double sum = 0.0;
@@ -1141,7 +1145,7 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
     double below, upto, all;
     block_scan(part, below, upto, all, sm.sum);
     if (w.kind != kPlain && !(all > least_mass)) {
-      if (more > 0.0) {
+      if (MODE == kDrawn && more > 0.0) {
         again = true;
         continue;
       }
@@ -1185,20 +1189,20 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
             bool clear = false;
 #pragma unroll
             for (int j = 0; j < kBlock; ++j) {
-              const double from = reach;
+              [[maybe_unused]] const double from = reach;
               reach += wt[j];
               if (token < 0 && wt[j] > 0.0 && reach > at) {
                 token = v + j;
-                clear = from + more <= at && at + more < reach;
+                if constexpr (MODE == kDrawn) clear = from + more <= at && at + more < reach;
               }
             }
             sm.found = token >= 0 ? token : last;
             sm.last = here ? 1 : 0;
-            sm.sure = clear ? 1 : 0;
+            if constexpr (MODE == kDrawn) sm.sure = clear ? 1 : 0;
           }
           __syncthreads();
           last_seen = sm.found;
-          sure = more == 0.0 || sm.sure != 0;
+          if constexpr (MODE == kDrawn) sure = more == 0.0 || sm.sure != 0;
           const bool done = sm.last != 0;
           __syncthreads();
           if (done) break;
@@ -1209,7 +1213,7 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
       // its weight was but roundings, or elements that count as 0 here
       if (tid == c) is = may = false;
     }
-    if (sure) return last_seen;
+    if (MODE != kDrawn || sure) return last_seen;
     again = true;
   }
 }
@@ -1247,12 +1251,13 @@ __device__ __forceinline__ int token_by_parts(const VerifyArgs& a, const Walk& w
     if (__ballot(mine.close > 0.0) != 0) mine.close = wave_sum_f64(mine.close);
   }
   if (tid % kWave == 0) {
-    put_far(&meet.parts[c].all, mine.all);
-    put_far(&meet.parts[c].left, mine.left);
+    double* to = meet.sums + c;
+    put_far(to, mine.all);
+    put_far(to + parts, mine.left);
     if (two) {
-      put_far(&meet.parts[c].kept, mine.kept);
-      put_far(&meet.parts[c].draft, mine.draft);
-      put_far(&meet.parts[c].close, mine.close);
+      put_far(to + 2 * parts, mine.kept);
+      put_far(to + 3 * parts, mine.draft);
+      put_far(to + 4 * parts, mine.close);
     }
   }
   if (!last_of(meet.arrived, groups, sm.last) || tid >= kFew) return -2;
@@ -1330,7 +1335,7 @@ __global__ __launch_bounds__(THREADS) void verify_final_kernel(VerifyArgs a, int
   }
   if constexpr (!greedy) {
     if (!draws) return;
-    const Meeting meet{all.parts + seq * groups * (THREADS / kWave), all.arrived + seq};
+    const Meeting meet{all.sums + seq * groups * (THREADS / kWave) * kSums, all.arrived + kApart * seq};
     const int token = token_by_parts<DT, MODE, THREADS>(a, w, seq, group, groups, pieces, meet, sm);
     if (tid == 0 && token >= -1) tokens[w.count] = token;
   }
@@ -1439,7 +1444,7 @@ Layout layout_of(const Plan& p, int64_t N, int D, bool draft) {
   l.stats = 0;
   l.finals = l.stats + rows * p.split.chunks * static_cast<int64_t>(sizeof(RowChunk));
   l.arrived = l.finals + N * p.cut.groups * (p.cut.threads / kWave) * static_cast<int64_t>(sizeof(FinalPart));
-  l.bytes = l.arrived + N * 4;
+  l.bytes = l.arrived + N * kApart * 4;
   return l;
 }
 
@@ -1450,7 +1455,7 @@ hipError_t launch_mode(int dtype, const VerifyArgs& a, hipStream_t stream) {
   const Layout l = layout_of(p, a.N, a.D, draft);
   char* ws = static_cast<char*>(a.workspace);
   RowChunk* stats = reinterpret_cast<RowChunk*>(ws + l.stats);
-  const Meeting meet{reinterpret_cast<FinalPart*>(ws + l.finals), reinterpret_cast<uint32_t*>(ws + l.arrived)};
+  const Meeting meet{reinterpret_cast<double*>(ws + l.finals), reinterpret_cast<uint32_t*>(ws + l.arrived)};
   const bool keep = a.N * (targets_of(p, a.D) + (draft ? a.D : 0)) * a.V * (dtype == 0 ? 4 : 2) <= kKeptBytes;
   const int targets = targets_of(p, a.D), groups = greedy ? 1 : p.cut.groups;
   // a launch holds at most 2^22 workgroups
