@@ -1415,8 +1415,8 @@ Cut cut_of(int64_t N, int V) {
 // rows are summed before, then (kStagedBytes) what is left behind the one that each
 // path goes on at, or (kTwiceBytes) first that one alone. Trees of 39 drafts, three
 // behind each, V 151936 bf16, with all rows read at once, one step and two: 4 of them
-// (49 MB) 24.8, 26.9 and 33.2 us, 8 (97 MB) 34.6, 31.0 and 35.2, 16 (194 MB) 49.1, 38.0
-// and 37.4, 32 80, 51 and 43.
+// (49 MB) 24.0, 26.5 and 32.5 us, 8 (97 MB) 34.1, 30.7 and 34.8, 16 (194 MB) 48.7, 37.6
+// and 37.4, 32 81, 50 and 42.
 // (Chains do not gain: 64 of 4 drafts with draft logits take 59 us with half of their
 // rows read first, 54 all at once; 128 of 3 drafts, V 128256 fp32, 113 both ways.)
 constexpr int64_t kStagedBytes = int64_t{80} << 20, kTwiceBytes = int64_t{160} << 20;
