@@ -33,6 +33,7 @@
 #include <type_traits>
 
 #include "device_common.h"
+#include "draft_tree.h"
 #include "exp_sum.h"
 #include "reg_tile.h"
 #include "speculative.h"
@@ -292,7 +293,7 @@ struct Walk {
 
 struct WalkSmem {
   int32_t token[kMaxRows];   // -1: the draft counts as not there
-  int32_t node[kMaxRows];    // the row that it follows
+  int32_t node[kMaxRows];    // the row that it follows, -1 if it is not there
   float u[kMaxRows];
   double term[kMaxRows];     // its term in that row
   union {
@@ -314,15 +315,9 @@ constexpr double kClose = 1e-6;
 // Elements whose terms of p and q, by the ratio of such sums, differ by no more.
 constexpr double kBand = 1e-6;
 
-// Draft j's token and the row that it follows; -1: it counts as not there.
-__device__ __forceinline__ void draft_of(const VerifyArgs& a, int64_t seq, int j, int n, int& token, int& node) {
-  token = -1;
-  node = 0;
-  if (j >= n) return;
-  token = a.drafts[seq * a.D + j];
-  const int parent = a.parents == nullptr ? j - 1 : a.parents[seq * a.D + j];
-  if (token < 0 || token >= a.V || parent < -1 || parent >= j) token = -1;
-  node = parent + 1;
+__device__ __forceinline__ DraftPlace draft_of(const VerifyArgs& a, int64_t seq, int j, int n) {
+  if (j >= n) return DraftPlace{-1, -1};
+  return draft_place(j, a.drafts[seq * a.D + j], a.parents == nullptr ? j - 1 : a.parents[seq * a.D + j], a.V);
 }
 
 // Goes down a sequence's path, in a tree `limit` drafts far at most: so many of its
@@ -336,10 +331,12 @@ __device__ __forceinline__ Walk walk(const VerifyArgs& a, const RowChunk* stats,
   constexpr bool greedy = MODE == kGreedy, drawn = MODE == kDrawn;
   const bool chain = drawn || a.parents == nullptr;
   const bool mine = wave * kWave <= n;  // waves that have drafts to look at: the first kSets at most
-  int token = -1, node = 0;
+  int token = -1, node = -1;
   float x = -INFINITY, y = -INFINITY;
   if (mine) {
-    draft_of(a, seq, tid, n, token, node);
+    const DraftPlace at = draft_of(a, seq, tid, n);
+    token = at.token;
+    node = at.node;
     if (token >= 0 && !greedy) x = DT::value(target_row<DT>(a, seq, node)[token]);
     if (token >= 0 && drawn) y = DT::value(draft_row<DT>(a, seq, tid)[token]);
     sm.u[tid] = !greedy && tid <= n ? a.uniforms[seq * (D + 1) + tid] : 0.0f;
@@ -1290,11 +1287,7 @@ struct BehindSmem {
 // The rows of a tree at and behind row `node`, in sm.rows; how many.
 __device__ __forceinline__ int list_behind(int node, int n, BehindSmem& sm) {
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave;
-  int r = tid;  // row; draft tid - 1
-  bool in = tid <= n && (tid == 0 || sm.walk.token[tid - 1] >= 0);
-  if (in)
-    while (r > node) r = sm.walk.node[r - 1];
-  in = in && r == node;
+  const bool in = tid <= n && row_behind(tid, node, sm.walk.token, sm.walk.node);
   const uint64_t mask = __ballot(in);
   if (lane == 0) sm.is[wave] = mask;
   __syncthreads();
