@@ -34,6 +34,7 @@
 
 #include "device_common.h"
 #include "draft_tree.h"
+#include "exp64.h"
 #include "exp_sum.h"
 #include "reg_tile.h"
 #include "speculative.h"
@@ -80,28 +81,6 @@ struct Meeting {
   double* sums;       // [kSums][parts], those of all workgroups' waves as in FinalPart
   uint32_t* arrived;  // workgroups that are done, kApart counters apart
 };
-
-// exp(x - ref) in 64 bits, 0 for -inf and NaN: 2^(n + r) with n whole and r in
-// [-1/2, 1/2], 2^r by the polynomial of degree 9 that meets it at the Chebyshev
-// points, within 1.9e-14 of it. What is added to round to n leaves n in the low bits.
-// 16 instructions; the library's exp takes about 30.
-__device__ __forceinline__ double exp_from(float x, float ref) {
-  constexpr double kLog2e = 1.4426950408889634, kRound = 6755399441055744.0;  // 1.5 * 2^52
-  const double d = __builtin_fmax(static_cast<double>(x) - static_cast<double>(ref), -760.0);
-  const double t = __builtin_fma(d, kLog2e, kRound);
-  const double r = __builtin_fma(d, kLog2e, kRound - t);
-  double e = 1.0205905413765595e-07;
-  e = __builtin_fma(e, r, 1.325964524488711e-06);
-  e = __builtin_fma(e, r, 1.5252672924850737e-05);
-  e = __builtin_fma(e, r, 0.0001540343375125101);
-  e = __builtin_fma(e, r, 0.0013333558200794592);
-  e = __builtin_fma(e, r, 0.009618129193934313);
-  e = __builtin_fma(e, r, 0.05550410866465167);
-  e = __builtin_fma(e, r, 0.2402265069564034);
-  e = __builtin_fma(e, r, 0.6931471805599462);
-  e = __builtin_fma(e, r, 1.0000000000000135);
-  return __builtin_ldexp(e, static_cast<int>(static_cast<uint32_t>(__builtin_bit_cast(uint64_t, t))));
-}
 
 __device__ __forceinline__ double wave_incl_scan_f64(double v) {
   auto step = [&](uint64_t moved) { v += __builtin_bit_cast(double, moved); };
@@ -741,7 +720,6 @@ __global__ __launch_bounds__(kT) void verify_rows_kernel(VerifyArgs a, Split spl
 
 template <class DT, int THREADS>
 constexpr bool kTabled = THREADS == kMany && DT::kPerVec == 8 && DT::kNegInf == 0xFF80u;
-constexpr int kTable = 8192 + ((134 - 83) << 7) + 1;
 struct NoTable {};
 struct Table {
   double table[kTable];
@@ -940,33 +918,14 @@ __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, con
 }
 
 // bf16 rows whose references are 0, as a model's logits have: there are so few
-// values that exp of all of them fits shared memory, 1.0 below 2^-44 in size and 0
-// from -128 down. A look-up takes 5 instructions and 10 or so cycles of shared
-// memory, where the polynomial takes 17: 52 us and 61 for 64 sequences of 4 drafts with
-// draft logits, V 151936. (Workgroups of kFew threads have too little room and time to
-// fill it.)
-constexpr int kTableLow = 83 << 7, kTableHigh = 134 << 7;  // bits of 2^-44 and 2^7
-constexpr int kTableSign = 8192;                           // entries of the negative ones come behind
-static_assert(kTable == kTableSign + kTableHigh - kTableLow + 1);
-constexpr int kTableNear = 118 << 7;                       // bits of 2^-9: below, four terms of the series are within 2^-52
+// values that exp of all of them fits shared memory. A look-up takes 5 instructions
+// and 10 or so cycles of shared memory, where the polynomial takes 17: 52 us and 61 for
+// 64 sequences of 4 drafts with draft logits, V 151936. (Workgroups of kFew threads have
+// too little room and time to fill it.)
 template <int FIRST, int THREADS>
 __device__ __forceinline__ void fill_table(double (&table)[kTable]) {  // by threads FIRST and up
-  for (int m = kTableLow + threadIdx.x - FIRST; m <= kTableHigh; m += THREADS - FIRST) {
-    const float x = __uint_as_float(static_cast<uint32_t>(m) << 16);
-    double up, down;
-    if (m < kTableNear) {
-      const double d = x;
-      const double even = __builtin_fma(d * d, __builtin_fma(d * d, 1.0 / 24, 0.5), 1.0);
-      const double odd = __builtin_fma(d * d, 1.0 / 6, 1.0) * d;
-      up = even + odd;
-      down = even - odd;
-    } else {
-      up = exp_from(x, 0.0f);
-      down = exp_from(-x, 0.0f);
-    }
-    table[m - kTableLow] = up;
-    table[kTableSign + m - kTableLow] = m == kTableHigh ? 0.0 : down;
-  }
+  for (int m = kTableLow + threadIdx.x - FIRST; m <= kTableHigh; m += THREADS - FIRST)
+    table_pair(m, table[m - kTableLow], table[kTableSign + m - kTableLow]);
 }
 using pair_t = uint16_t __attribute__((ext_vector_type(2)));
 // The terms of two elements of a row.
