@@ -746,6 +746,8 @@ struct Terms {
 // as 0 where a whole wave has none but them: rows that were filtered. (What is left of a
 // row without its rejected tokens is at least the 2^-24th that a uniform can be below 1.)
 constexpr float kFar = 70.0f;
+// The least that count otherwise: where the logits are so large that these are no
+// less than the largest, that one counts.
 struct Rows {
   float p_least, q_least;
 };
@@ -754,8 +756,8 @@ __device__ __forceinline__ float log_below(double sum) {  // no more than ln 2 b
 }
 __device__ __forceinline__ Rows least_of(const Walk& w) {
   Rows r;
-  r.p_least = w.p.ref + log_below(w.p.sum) - kFar;
-  r.q_least = w.kind == kResidual ? w.q.ref + log_below(w.q.sum) - kFar : INFINITY;
+  r.p_least = w.p.ref + (log_below(w.p.sum) - kFar);
+  r.q_least = w.kind == kResidual ? w.q.ref + (log_below(w.q.sum) - kFar) : INFINITY;
   return r;
 }
 __device__ __forceinline__ float largest(const float (&x)[kBlock]) {
@@ -767,10 +769,10 @@ __device__ __forceinline__ bool terms_at(const typename DT::raw_t* prow, const t
                                          const Walk& w, const Rows& least, bool two, Terms& t) {
   float x[kBlock], y[kBlock];
   load_block<DT>(prow, v, V, x);
-  bool some = largest(x) > least.p_least;
+  bool some = largest(x) >= least.p_least;
   if (two) {
     load_block<DT>(qrow, v, V, y);
-    some |= largest(y) > least.q_least;
+    some |= largest(y) >= least.q_least;
   }
   if (__ballot(some) == 0) return false;
 #pragma unroll
