@@ -459,7 +459,10 @@ topktopp_status beam_backtrace(const int32_t* tokens, const int32_t* parents, in
  * Numerics. The sums of exp behind an acceptance have a relative error below
  * 1e-6; a decision that this could turn is made again with sums in 64 bits, as
  * are all sums behind a drawn token. Of two outcomes that only the roundings of
- * 64 bits tell apart, either may come. Results are deterministic.
+ * 64 bits tell apart, either may come. Every logit above -inf has weight, so a
+ * uniform of 0 draws the first such token, however far it lies below the others;
+ * only beyond what 64 bits hold (650 below the row's largest, or more) may it count
+ * as 0. Results are deterministic.
  *
  * Errors: ERR_NULLPTR for logits (unless V is 0), drafts (unless D is 0),
  * out_tokens, out_accepted or the workspace NULL; ERR_INVALID for a dtype, N < 0,

@@ -64,3 +64,66 @@ def test_rows_of_the_largest_sizes(kind, V, N, dtype):
             want = k + (k >= out)
         got, accepted = drawn(torch, x, np.repeat(u, 2, 1), y, out[:, None])
         assert (accepted == 0).all() and (got == want).all()
+
+
+FAR = (0.0, 1e-45, 1.1e-30, 2.5e-29, 0.3, 1 - 2.0 ** -24, 1.0)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("N", [7, 700])  # few workgroups and many
+@pytest.mark.parametrize("far", [-64.0, -100.0, -600.0])
+@pytest.mark.parametrize("mode", ["plain", "proposal", "tree", "drawn", "drawn from masked"])
+def test_tokens_far_below_the_others(mode, far, N, dtype):
+    """Rows that begin and end with tokens far below the others, which no sum in 64 bits of the whole row shows, and
+    uniforms that fall on them: 0 on the first token of any weight, 1 on the last, and others between.
+
+    Weights are within 2e-14 of themselves and those of a draw within m 4e-14 of what is left, 1 / m of the row (m < 2000
+    here: the drafts' share is above 1 / 2000): cumulative sums are sure to 1e-10 of themselves."""
+    torch = need_gpu()
+    say("far", mode, far, N, dtype)
+    rng = np.random.default_rng(N + int(-far) + len(mode))
+    V, D, t = 20000, 0 if mode == "plain" else 1, getattr(torch, dtype)
+    base = rng.random((N, D + 1, V)).astype(np.float64)
+    base[:, :, :9000] = base[:, :, -4000:] = far
+    base[:, 0, 3] = base[:, 0, V - 2] = -np.inf
+    base[1::2, 0, :2] = -np.inf  # the first token of any weight is another one
+    draft = rng.integers(9000, V - 4000, N)
+    i = np.arange(N)
+    if D:
+        base[i, 0, draft] = 4.0
+    x = torch.from_numpy(base.reshape(-1, V)).cuda().to(t)
+    xs = x.double().cpu().numpy().reshape(N, D + 1, V)[:, 0].astype(np.longdouble)
+    softmax = lambda a: (lambda e: e / e.sum(1, keepdims=True))(np.exp(a - a.max(1, keepdims=True)))
+    r = softmax(xs)
+    u = np.full((N, D + 1), 1 - 2.0 ** -24)
+    u[:, D] = np.resize(FAR, N)
+    y = None
+    if mode in ("proposal", "tree"):
+        r[i, draft] = 0
+    elif D:
+        other = base[:, 0].copy()
+        other[i, draft] = 7.0
+        if mode == "drawn from masked":
+            other[other < 0] = -np.inf
+        y = torch.from_numpy(other).cuda().to(t)
+        q = softmax(y.double().cpu().numpy().astype(np.longdouble))
+        assert (q[i, draft] > r[i, draft]).all()
+        r = np.maximum(r - q, 0)
+        r[i, draft] = 0
+        assert (r.sum(1) > 1 / 2000).all()
+    got, accepted = drawn(torch, x, u, y, draft[:, None] if D else None, np.full((N, 1), -1) if mode == "tree" else None)
+    assert (accepted == 0).all()
+    upto = np.cumsum(r, 1)
+    for k in range(N):
+        uk = np.longdouble(np.float32(u[k, D]))
+        weight = np.nonzero(r[k] > 0)[0]
+        if uk >= 1:
+            assert got[k] == weight[-1], k
+            continue
+        at = uk * upto[k, -1]
+        want = weight[upto[k, weight] > at][0]
+        if uk > 0:
+            near = np.abs(upto[k, weight] - at) <= 1e-10 * at
+            if near.any():
+                continue
+        assert got[k] == want, (k, float(uk), got[k], want)

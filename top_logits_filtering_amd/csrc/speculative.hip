@@ -731,7 +731,7 @@ struct FinalSmem : std::conditional_t<kTabled<DT, THREADS> && MODE != kGreedy, T
   int32_t out[kMaxRows];  // rejected tokens within the range
   int outs;
   double sum[4][kWaves];
-  double parts[kFew];  // where summed again
+  double parts[2][kFew];  // sums of the parts: of what is left, where summed again, and of p
   uint64_t is[kWaves], may[kWaves];
   double below;
   int last;
@@ -742,12 +742,14 @@ struct FinalSmem : std::conditional_t<kTabled<DT, THREADS> && MODE != kGreedy, T
 struct Terms {
   double p[kBlock], q[kBlock];
 };
-// Elements of no more than exp(-70) of the row, so below 2^-80 of it all together, count
-// as 0 where a whole wave has none but them: rows that were filtered. (What is left of a
-// row without its rejected tokens is at least the 2^-24th that a uniform can be below 1.)
+// Elements of less than exp(-70) of the row are left out where a whole wave has none but
+// them: rows that were filtered. All together they are below kFarShare of the row an
+// element, and only a uniform closer than that to a token's border, as 0 is to the first
+// one's, has the row summed again with them.
+// The least that count: where the logits are so large that 70 less is the same number,
+// that of the largest.
 constexpr float kFar = 70.0f;
-// The least that count otherwise: where the logits are so large that these are no
-// less than the largest, that one counts.
+constexpr double kFarShare = 0x1p-100;  // exp(-70) is 2^-100.99
 struct Rows {
   float p_least, q_least;
 };
@@ -763,13 +765,13 @@ __device__ __forceinline__ Rows least_of(const Walk& w) {
 __device__ __forceinline__ float largest(const float (&x)[kBlock]) {
   return fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
 }
-// False if they are all 0, for the whole wave.
+// False if they are all left out, for the whole wave; all: none are.
 template <class DT>
 __device__ __forceinline__ bool terms_at(const typename DT::raw_t* prow, const typename DT::raw_t* qrow, int v, int V,
-                                         const Walk& w, const Rows& least, bool two, Terms& t) {
+                                         const Walk& w, const Rows& least, bool all, bool two, Terms& t) {
   float x[kBlock], y[kBlock];
   load_block<DT>(prow, v, V, x);
-  bool some = largest(x) >= least.p_least;
+  bool some = all || largest(x) >= least.p_least;
   if (two) {
     load_block<DT>(qrow, v, V, y);
     some |= largest(y) >= least.q_least;
@@ -893,7 +895,7 @@ __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, con
     for (int i = 0; i < pieces; ++i) {
       const int v = first + i * kPiece + lane * kBlock;
       Terms t;
-      if (!terms_at<DT>(prow, qrow, v, V, w, least, true, t)) continue;
+      if (!terms_at<DT>(prow, qrow, v, V, w, least, false, true, t)) continue;
       add_terms(mine, t, near);
     }
   } else {
@@ -902,7 +904,7 @@ __device__ __forceinline__ FinalPart part_of(const typename DT::raw_t* prow, con
     for (int i = 0; i < pieces; ++i) {
       const int v = first + i * kPiece + lane * kBlock;
       Terms t;
-      if (!terms_at<DT>(prow, qrow, v, V, w, least, false, t)) continue;
+      if (!terms_at<DT>(prow, qrow, v, V, w, least, false, false, t)) continue;
       double sum = 0.0;
 #pragma unroll
       for (int j = 0; j < kBlock; ++j) sum += t.p[j];
@@ -1043,8 +1045,9 @@ __device__ __forceinline__ int first_or_last(bool is, bool may, Smem& sm) {
 // Parts were summed with near, the ratio of q's sum and p's out of the chunks; scale is
 // that ratio in 64 bits. For elements that are not close both tell the same one of p
 // and q to be larger, and left + (scale - near) kept is what they add up to. The close
-// ones add up to at most `more`: where that could move the token, and where scale is
-// not as near as that, the parts are summed again with scale.
+// ones and those that are too far below the row's largest add up to at most `more`:
+// where that could move the token, and where scale is not as near as that, the parts
+// are summed again, with scale and of all elements.
 template <class DT, Mode MODE, class Smem>
 __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, const Meeting& meet, int parts, int pieces,
                                         const typename DT::raw_t* prow, const typename DT::raw_t* qrow,
@@ -1070,61 +1073,85 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
     total[1] = p.draft;
     total[2] = p.close;
   }
+  sm.parts[1][tid] = p.all;
   block_sums(total, sm.sum);
   double part = p.left, scale = 1.0, more = 0.0, least_mass = kLeast * total[0];
   bool again = false;
   if constexpr (MODE == kDrawn) {
+    more = a.V * kFarShare * total[0];
     if (two) {
       scale = total[1] / total[0];
       const double near = w.q.sum / w.p.sum, off = scale - near;
       part = __builtin_fmax(__builtin_fma(off, p.kept, part), 0.0);
-      more = 2.0 * kBand * total[2];
+      more = 2.0 * kBand * total[2] + a.V * kFarShare * total[1];
       least_mass = kLeast * total[1];
       again = __builtin_fabs(off) > 0.5 * kBand * near;
     }
   }
   for (;;) {
-    if (MODE == kDrawn && again) {
+    if (again) {
+      if constexpr (MODE == kProposed) list_out(a, w, 0, a.V, sm);
+      const bool outs = MODE != kDrawn && w.kind == kWithout;
       for (int c0 = 0; c0 < parts; c0 += kWaves) {
         const int c = c0 + tid / kWave;
-        double sum = 0.0;
+        double sum = 0.0, whole = 0.0;
 #pragma unroll 1
         for (int i = 0; i < pieces; ++i) {
           const int v = c * span + i * kPiece + tid % kWave * kBlock;
           float x[kBlock], y[kBlock];
           load_block<DT>(prow, v, a.V, x);
-          load_block<DT>(qrow, v, a.V, y);
+          if constexpr (MODE == kDrawn) load_block<DT>(qrow, v, a.V, y);
+          const uint32_t gone = outs ? outs_at(v, sm) : 0u;
 #pragma unroll 1
           for (int j = 0; j < kBlock; ++j) {  // one after the other: rarely taken
-            sum += __builtin_fmax(__builtin_fma(scale, exp_from(x[0], w.p.ref), -exp_from(y[0], w.q.ref)), 0.0);
+            const double one = exp_from(x[0], w.p.ref);
+            double left = (gone >> j & 1u) != 0 ? 0.0 : one;
+            if constexpr (MODE == kDrawn) {
+              const double more_than_q = __builtin_fmax(__builtin_fma(scale, one, -exp_from(y[0], w.q.ref)), 0.0);
+              left = two ? more_than_q : one;
+            }
+            whole += one;
+            sum += left;
 #pragma unroll
             for (int k = 0; k + 1 < kBlock; ++k) {
               x[k] = x[k + 1];
-              y[k] = y[k + 1];
+              if constexpr (MODE == kDrawn) y[k] = y[k + 1];
             }
           }
         }
         sum = wave_sum_f64(sum);
-        if (c < parts && tid % kWave == 0) sm.parts[c] = sum;
+        whole = wave_sum_f64(whole);
+        if (tid % kWave == 0) {
+          sm.parts[0][c] = sum;
+          sm.parts[1][c] = whole;
+        }
       }
       __syncthreads();
-      part = tid < parts ? sm.parts[tid] : 0.0;
+      part = tid < parts ? sm.parts[0][tid] : 0.0;
       more = 0.0;
     }
     Weights weights{scale, two, MODE != kDrawn && w.kind == kWithout};
     double below, upto, all;
     block_scan(part, below, upto, all, sm.sum);
     if (w.kind != kPlain && !(all > least_mass)) {
-      if (MODE == kDrawn && more > 0.0) {
+      if (!again) {
         again = true;
         continue;
       }
       weights.residual = weights.without = false;
-      block_scan(p.all, below, upto, all, sm.sum);
+      part = tid < parts ? sm.parts[1][tid] : 0.0;
+      block_scan(part, below, upto, all, sm.sum);
     }
-    const double at = static_cast<double>(sm.walk.last_u) * all;
-    // the part that `at` lies in; for a uniform out of range the first or the last one of any weight
-    bool is = upto > at && upto > below, may = upto > below;
+    // from a uniform of 1 on the last token of any weight, which roundings of the sums must not hide
+    const double at = sm.walk.last_u < 1.0f ? static_cast<double>(sm.walk.last_u) * all : INFINITY;
+    // Without q what is left out moves a border by less than the roundings of one at
+    // 2^-26 of the row, so that only uniforms below that or from 1 on need all elements.
+    if (MODE != kDrawn && !again && !(at >= 0x1p-26 * total[0] && at < all)) {
+      again = true;
+      continue;
+    }
+    // the part that `at` lies in, else the last one of any weight
+    bool is = part > 0.0 && upto > at, may = part > 0.0;
     const double begin = below;
     int last_seen = -1;
     bool sure = more == 0.0;
@@ -1141,7 +1168,7 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
         double wt[kBlock], sum = 0.0;
         int last = -1;  // the last element of any weight
         Terms t;
-        if (terms_at<DT>(prow, qrow, v, a.V, w, least, two, t)) {
+        if (terms_at<DT>(prow, qrow, v, a.V, w, least, again, two, t)) {
           weights.of(t, v, sm, wt);
 #pragma unroll
           for (int j = 0; j < kBlock; ++j) {
@@ -1180,10 +1207,10 @@ __device__ __forceinline__ int token_of(const VerifyArgs& a, const Walk& w, cons
         base += all;
       }
       if (last_seen >= 0) break;
-      // its weight was but roundings, or elements that count as 0 here
+      // its weight was but roundings, or elements that are left out
       if (tid == c) is = may = false;
     }
-    if (MODE != kDrawn || sure) return last_seen;
+    if (sure) return last_seen;
     again = true;
   }
 }
