@@ -521,17 +521,20 @@ topktopp_status cache_pages_fork(int32_t* tables, int64_t ld_tables, int64_t C, 
  * C * page_size. lengths[r] becomes new_lengths[r] for all others.
  *   caches     host array of `count` descriptions as for beam_reorder_states,
  *              read during the call, with P rows (the pages) and page_size
- *              positions (the slots); disjoint. With count 0 nothing can be
- *              copied: the first row that would have to and the growing rows
- *              behind it stay as they are.
+ *              positions (the slots). From the first byte of one to its last no
+ *              other begins: views that lie between one another's elements, as
+ *              keys and values of one tensor may, go as that tensor. With count 0
+ *              nothing can be copied: the first row that would have to and the
+ *              growing rows behind it stay as they are.
  *   workspace  cache_pages_resize_workspace(R, P) bytes, 16-byte aligned; calls
  *              that may run at the same time need one each.
  * ERR_NULLPTR for tables (unless C is 0), lengths, new_lengths, uses (unless P
  * is 0), the workspace, caches or a cache's data NULL; ERR_INVALID for sizes out
  * of range as above, a cache with other positions than page_size, one whose
  * elements share memory or of more than 2^31 - 1 columns of a page, a workspace
- * too small or not aligned, or buffers that overlap. Nothing is changed if any
- * argument is refused. R == 0 is a successful no-op.
+ * too small or not aligned, or buffers (caches: in the sense above) that
+ * overlap. Nothing is changed if any argument is refused. R == 0 is a successful
+ * no-op.
  */
 topktopp_status cache_pages_resize(int32_t* tables, int64_t ld_tables, int64_t R, int64_t C, int32_t* lengths,
                                    const int32_t* new_lengths, int32_t* uses, int64_t P, int64_t page_size,

@@ -718,7 +718,7 @@ def speculative_verify(logits, drafts, uniforms=None, draft_logits=None, parents
     tokens holds the accepted drafts, the token behind them and -1; path (with
     parents) the accepted drafts' numbers and -1. Draft w behind an accepted one
     stands if u[w] q(d) < p(d); where it does not, the token is drawn from
-    max(p - q, 0). A row with a NaN or +inf or nothing above -inf accepts
+    max(p - q, 0). A chain is faster without parents. A row with a NaN or +inf or nothing above -inf accepts
     nothing and gives -1. out: the three tensors to fill (path None without
     parents, or wherever it is not needed); workspace: a uint8 tensor of
     speculative_verify_workspace() bytes, not used by any other call that may
@@ -883,8 +883,10 @@ def cache_pages_resize(tables, lengths, new_lengths, uses, page_size, caches=Non
 
     tables, lengths, uses: as for cache_pages_fork; new_lengths [R] int32. caches:
     a tensor or a sequence of them, any dtype and strides, with the pages along
-    page_dim and their slots along slot_dim; without, nothing can be copied, and
-    the first row that would have to be counts as not served. workspace: a uint8
+    page_dim and their slots along slot_dim, none beginning within another (views
+    that interleave, as keys and values of one tensor may, go as that tensor);
+    without, nothing can be copied, and the first row that would have to be counts
+    as not served. workspace: a uint8
     tensor of cache_pages_resize_workspace() bytes, not used by any other call that
     may run at the same time. Returns lengths."""
     import torch
@@ -920,12 +922,11 @@ def cache_pages_compact(caches, tables, starts, path, counts, page_dim=0, slot_d
     cache, position starts[i] + j of sequence i becomes what position
     starts[i] + path[i, j] was, for j < counts[i].
 
-    caches: a tensor or a sequence of them, any dtype and strides, with the pages
-    along page_dim and their slots along slot_dim; tables [N, C] int32, rows
-    contiguous: position t lies in page tables[i, t // slots]; starts and counts
-    [N] int32; path [N, D] int32, ascending, as speculative_verify gives it (a
-    path ends before a number that is not larger than the one before). The pages
-    written to must be those of one sequence only. Returns caches."""
+    caches: as for cache_pages_resize; tables [N, C] int32, rows contiguous:
+    position t lies in page tables[i, t // slots]; starts and counts [N] int32;
+    path [N, D] int32, ascending, as speculative_verify gives it (a path ends
+    before a number that is not larger than the one before). The pages written to
+    must be those of one sequence only. Returns caches."""
     import torch
 
     lib = _lib or load_library()

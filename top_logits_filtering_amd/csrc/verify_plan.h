@@ -40,10 +40,17 @@ inline Split split_of(int dtype, int64_t rows, int V) {
   return Split{static_cast<int>(c), static_cast<int>(ceil_div(nv, c))};
 }
 
-// Up to so many workgroups of kFew threads run at a time with what they hold of
-// shared memory, and one sequence alone is done sooner by them (V 151936 bf16, 5
-// drafts: 15.5 us and 16.7); beyond, kMany threads share one look at the path: 64
-// sequences of 4 drafts 52 us and 71, 128 of 3, V 128256 fp32, 113 and 156.
+// Up to so many workgroups of kFew threads are taken, beyond them those of kMany, which
+// share one look at the path. Where the two take as long depends on the type and on
+// whether there are draft logits, and lies between 400 and 900 (us, kFew and kMany):
+//   bf16, V 151936, 4 drafts with draft logits: 152 workgroups 17.7 and 19.2, 380 24.6
+//   and 24.5, 532 26.3 and 24.6, 988 34.8 and 30.9;
+//   fp32, V 128256, 3 with draft logits: 378 19.1 and 20.0, 630 22.3 and 22.3, 882 25.6
+//   and 24.1, 2016 44.4 and 37.6;
+//   fp16, V 32003, 4 with draft logits: 256 17.0 and 19.3, 512 20.7 and 21.9, 768 22.6
+//   and 22.2; 2 proposals: 512 14.2 and 15.0, 1024 17.5 and 16.6.
+// (1024 of kFew run at a time, as their registers allow four a SIMD. Short rows of large
+// batches would do better with kFew: 400 sequences, V 5000 fp32, 29.9 and 34.3.)
 constexpr int kFewBlocks = 512;
 // What a workgroup does besides, in pieces of a wave (counting none, 420 sequences
 // of 2 proposals, V 151936 bf16, are cut in 7 and take 217 us instead of 122).
@@ -78,7 +85,11 @@ inline Cut cut_of(int64_t N, int V) {
 // path goes on at, or (kTwiceBytes) first that one alone. Trees of 39 drafts, three
 // behind each, V 151936 bf16, with all rows read at once, one step and two: 4 of them
 // (49 MB) 24.0, 26.5 and 32.5 us, 8 (97 MB) 34.1, 30.7 and 34.8, 16 (194 MB) 48.7, 37.6
-// and 37.4, 32 81, 50 and 42.
+// and 37.4, 32 86, 54 and 43. The same trees in fp32, V 128256: 4 (82 MB) 28.8, 30.6 and
+// 35.2, 8 (164 MB) 44.6, 35.3 and 37.8, 16 66.5, 45.0 and 40.6; V 32003 bf16: 40 (102 MB)
+// 35.6, 31.9 and 37.8, 160 91, 60 and 47. The host does not see what the trees are like:
+// a chain given as parents, of which far more lies behind, loses (32 of 39 drafts, V
+// 151936 bf16, 83, 102 and 105; 128 of 8 85, 98 and 103) and is better given without.
 // (Chains do not gain: 64 of 4 drafts with draft logits take 59 us with half of their
 // rows read first, 54 all at once; 128 of 3 drafts, V 128256 fp32, 113 both ways.)
 constexpr int64_t kStagedBytes = int64_t{80} << 20, kTwiceBytes = int64_t{160} << 20;
